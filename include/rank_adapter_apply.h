@@ -571,6 +571,197 @@ int lora_apply_static_scratch(const void *x, void *y, const int32_t *token_slot_
                               const void *B_pool, const float *scale_dev,
                               const int32_t *rank_dev, void *stream);
 
+/*
+ * The rest of a step over drafted tokens, around the delta of the layers: the
+ * base model's product with 4-bit weights that lora_apply_multi adds to,
+ * rotary positions with the append to a paged key/value cache, attention of
+ * drafted trees over that cache, and the verification of the drafts. (The
+ * source pages have no counterpart to these calls.)
+ *
+ * They need no context. Every call queues its kernels on `stream` (cudaStream_t
+ * as void*), allocates nothing, keeps nothing for a later call, does not
+ * synchronise the host and may be captured into a graph (make the first call of
+ * each before a capture: it loads the device code). All pointers are device
+ * pointers; strides are in elements and the last dimension is contiguous.
+ * dtype is a lora_dtype: LORA_DTYPE_BF16 computes in fp32 with one final
+ * rounding to bf16. A count of zero (tokens, requests) is LORA_OK and queues
+ * nothing. What can only be seen on the device (positions, cache slots, page
+ * ids, lengths, tree parents, token ids) never leads to an access outside the
+ * arrays: each call says what it does with an entry out of range.
+ * Outputs must not overlap inputs, except where a call allows it.
+ */
+
+/*
+ * y[t][i] = sum_k w[i][k] x[t][k],
+ * w[i][k] = scales[i][k / group] * (n[i][k] - zeros[i][k / group]), n in 0..15:
+ * the base projection of a few tokens with 4-bit weights, rounded once.
+ */
+typedef struct {
+    const void *x;            /* [n_tokens][d_in], rows x_stride apart */
+    int64_t x_stride;
+    const uint8_t *qweight;   /* [d_out][d_in / 2], 16-byte aligned: byte j of a row holds n of
+                                 column 2j in its low and of column 2j + 1 in its high four bits */
+    const void *scales;       /* [d_out][d_in / group], type dtype */
+    const uint8_t *zeros;     /* [d_out][d_in / group], 0..255 (0..15 in practice); NULL: 8 everywhere */
+    void *y;                  /* [n_tokens][d_out], rows y_stride apart */
+    int64_t y_stride;
+    int n_tokens, d_in, d_out;
+    int group;                /* 32, 64 or 128; d_in is a multiple of it */
+    int dtype;                /* of x, scales and y */
+} lora_base_linear_desc;
+
+int lora_base_linear(const lora_base_linear_desc *desc, void *stream);
+
+/* Frequencies of rotary positions, pair j of rot_dim / 2: f_j = base^(-2j / rot_dim), then */
+enum lora_rope_scaling {
+    LORA_ROPE_PLAIN = 0,      /* angle = position * f_j */
+    LORA_ROPE_LINEAR = 1,     /* angle = position * f_j / factor */
+    LORA_ROPE_BASE = 2,       /* base raised to base * factor^(rot_dim / (rot_dim - 2)) ("NTK-aware") */
+    LORA_ROPE_PIECES = 3,     /* by wavelength w = 2 pi / f_j: below original / high_freq f_j is kept, above
+                                 original / low_freq it is f_j / factor, and between the two
+                                 (1 - m) f_j / factor + m f_j, m = (original / w - low_freq) / (high_freq - low_freq) */
+    LORA_ROPE_YARN = 4,       /* by the turns a pair makes within `original` positions: with
+                                 c(n) = rot_dim ln(original / (2 pi n)) / (2 ln base), lo = max(floor(c(high_freq)), 0),
+                                 hi = min(ceil(c(low_freq)), rot_dim - 1), ramp = clamp((j - lo) / max(hi - lo, 0.001), 0, 1):
+                                 f_j (1 - ramp) + f_j / factor * ramp; cos and sin times 0.1 ln(factor) + 1 (factor > 1) */
+};
+
+/*
+ * table[p][0 .. rot_dim/2) = cos, table[p][rot_dim/2 .. rot_dim) = sin of the
+ * angles of position p, p = 0 .. n_positions - 1, each computed in double and
+ * rounded once to fp32. rot_dim: even, 2..512 (4.. for LORA_ROPE_BASE). base >
+ * 1. factor >= 1, original >= 1, low_freq < high_freq (both > 0): read where
+ * the formula names them. Built once and kept by the caller.
+ */
+int lora_rope_table(float *table, int n_positions, int rot_dim, int scaling, double base, double factor,
+                    double original, double low_freq, double high_freq, void *stream);
+
+/*
+ * Rotate the first rot_dim elements of every head of q (and k) by the angles
+ * of the token's position: the pair (a, b) becomes (a cos - b sin, a sin + b
+ * cos); pairs are elements (2j, 2j + 1) when interleaved, else (j, j + rot_dim /
+ * 2). Elements past rot_dim are copied. inverse != 0 rotates by the negative
+ * angle: the gradient of the forward rotation (and its undoing). With k, the
+ * rotated k and the unchanged v of token t are written to slot slots[t] of the
+ * paged cache: page slots[t] / page_size, place slots[t] % page_size.
+ * A token whose position is outside the table has none of its rows written; a
+ * slot outside [0, n_pages * page_size) writes no cache row (its q row is).
+ * Two tokens with one slot: which of them stays is not defined. q_out may be q
+ * itself with the same strides.
+ */
+typedef struct {
+    const void *q;            /* [n_tokens][n_heads][head_dim] */
+    int64_t q_token, q_head;  /* strides */
+    void *q_out;              /* like q */
+    int64_t q_out_token, q_out_head;
+    const void *k;            /* [n_tokens][n_kv_heads][head_dim], or NULL with n_kv_heads 0 */
+    int64_t k_token, k_head;
+    const void *v;            /* like k */
+    int64_t v_token, v_head;
+    void *k_cache, *v_cache;  /* [n_pages][page_size][n_kv_heads][head_dim], both with these strides */
+    int64_t cache_page, cache_slot, cache_head;
+    const int64_t *slots;     /* [n_tokens] */
+    int64_t n_pages;
+    const int32_t *positions; /* [n_tokens] */
+    const float *table;       /* [n_positions][rot_dim], lora_rope_table's layout */
+    int n_positions, page_size;
+    int n_tokens, n_heads, n_kv_heads, head_dim;
+    int rot_dim;              /* even, 2..head_dim */
+    int interleaved, inverse, dtype;
+} lora_rope_desc;
+
+int lora_rope(const lora_rope_desc *desc, void *stream);
+
+/*
+ * Attention of drafted trees over a paged cache. Request b owns the query rows
+ * (nodes) node_starts[b] .. node_starts[b + 1) and the cache rows of its page
+ * table: key p is place p % page_size of page page_table[b][p / page_size].
+ * Keys 0 .. ctx_lens[b] - 1 are its context and key ctx_lens[b] + j is node j
+ * of its tree (appended before this call). Node i sees the whole context and
+ * the nodes j whose bit is set in tree_mask[node]: bit j % 64 of word j / 64;
+ * without a tree_mask, the nodes 0..i (a chain; one node: a decode step).
+ *   out = sum_p softmax_p(scale q.k_p) v_p,   lse = ln sum_p exp(scale q.k_p)
+ * over the keys it sees; a row that sees none gets out = 0, lse = -inf. Head h
+ * reads key/value head h / (n_heads / n_kv_heads). Keys past the page table's
+ * row or on a page id outside [0, n_pages) are not seen; what lies there, and
+ * in cache rows that no query sees, has no effect, NaN and infinities included.
+ * A context length below 0 counts as 0; node_starts are clamped to
+ * [0, n_tokens]. Rows that belong to no request are not written.
+ * head_dim: a multiple of 8 up to 128. The q, out and cache pointers and
+ * strides must be multiples of 16 bytes.
+ */
+typedef struct {
+    const void *q;            /* [n_tokens][n_heads][head_dim] */
+    int64_t q_token, q_head;
+    const void *k_cache, *v_cache; /* [n_pages][page_size][n_kv_heads][head_dim], both with these strides */
+    int64_t cache_page, cache_slot, cache_head;
+    int64_t n_pages;
+    const int32_t *page_table; /* [n_requests][table_pages], rows table_stride apart */
+    int64_t table_stride;
+    const int32_t *ctx_lens;  /* [n_requests] */
+    const int32_t *node_starts; /* [n_requests + 1], not decreasing */
+    const uint64_t *tree_mask; /* [n_tokens][mask_words], or NULL */
+    void *out;                /* [n_tokens][n_heads][head_dim] */
+    int64_t out_token, out_head;
+    float *lse;               /* [n_tokens][n_heads], or NULL */
+    void *workspace;          /* lora_tree_attention_workspace_bytes(...), 256-byte aligned; contents not kept */
+    size_t workspace_bytes;
+    float scale;
+    int page_size, table_pages, mask_words;
+    int n_requests, n_tokens, n_heads, n_kv_heads, head_dim, dtype;
+} lora_tree_attention_desc;
+
+/* Bytes of workspace of a lora_tree_attention call (0 for sizes it refuses). */
+size_t lora_tree_attention_workspace_bytes(int n_requests, int n_tokens, int n_heads, int n_kv_heads,
+                                           int head_dim, int dtype);
+
+int lora_tree_attention(const lora_tree_attention_desc *desc, void *stream);
+
+/*
+ * Verify drafted trees against the target's probabilities, from given random
+ * numbers. Request b owns the nodes node_starts[b] .. node_starts[b + 1); node
+ * 0 of a request is its root (the last token that is already accepted), node i
+ * > 0 is a drafted token tokens[i] that follows node parents[i] < i (indices
+ * within the request). target[i] are the target's probabilities after node i;
+ * draft[i] those the children of node i were drawn from. Starting at the root,
+ * the children of the current node are tried in the order of their index:
+ *   S_0 = 1, R_0 = p = target[node], q = draft[node], a_1 = 1, and after the
+ *   i-th rejection  R_i = max(p - a_i q, 0), S_i = sum R_i, a_{i+1} = a_i + S_i;
+ *   child i + 1 with token x is accepted if uniforms[child] * q[x] * S_i < R_i[x].
+ * The first accepted child becomes the current node; if there is none, or
+ * max_path nodes are accepted, the walk ends. The next token is the index of
+ * the largest R[v] / noise[b][v] (the lowest on a tie) of the last node's
+ * rejections (R_0 if its R is all zero or it stopped at max_path): with
+ * uniforms from U[0, 1) and noise from the exponential distribution, the tokens
+ * are distributed as the target's own. Without draft (NULL: drafts chosen
+ * without chance), q is 1 at the child's own token: accept if uniforms[child] *
+ * S < R[x]; a rejection sets R[x] = 0, S = sum R.
+ * path[b] lists the accepted nodes, then -1; n_accepted[b] counts them;
+ * next_token[b] = -1 where no probability is positive (and for a request
+ * without nodes). Nodes with a parent outside [0, own index) or a token outside
+ * [0, vocab) are no one's children; a request's nodes past the first 1024 are
+ * not looked at.
+ */
+typedef struct {
+    const void *target;       /* [n_nodes][vocab], rows target_row apart, type dtype */
+    int64_t target_row;
+    const void *draft;        /* like target, rows draft_row apart, or NULL */
+    int64_t draft_row;
+    const int32_t *tokens;    /* [n_nodes] */
+    const int32_t *parents;   /* [n_nodes] */
+    const int32_t *node_starts; /* [n_requests + 1] */
+    const float *uniforms;    /* [n_nodes] */
+    const float *noise;       /* [n_requests][vocab], rows noise_row apart, > 0 */
+    int64_t noise_row;
+    int32_t *path;            /* [n_requests][max_path] */
+    int32_t *n_accepted;      /* [n_requests] */
+    int32_t *next_token;      /* [n_requests] */
+    int max_path;
+    int n_requests, n_nodes, vocab, dtype;
+} lora_verify_desc;
+
+int lora_verify_drafts(const lora_verify_desc *desc, void *stream);
+
 /* Message for the last failed call on this thread ("" if none; error reporting
  * only, no counterpart on the source pages). */
 const char *lora_last_error(void);

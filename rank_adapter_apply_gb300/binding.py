@@ -38,6 +38,8 @@ EXPORTED = [
     "lora_set_slot_tracking", "lora_load_slots", "lora_assign_batch", "lora_release_batch",
     "lora_selftest_wait_timeout", "lora_assign_tokens", "lora_sync_host", "lora_abort_load",
     "lora_register_host_adapters", "lora_set_warm_set", "lora_serve_step",
+    "lora_base_linear", "lora_rope_table", "lora_rope", "lora_tree_attention_workspace_bytes",
+    "lora_tree_attention", "lora_verify_drafts",
 ]
 
 
@@ -58,6 +60,40 @@ class LoraStats(ctypes.Structure):
 
     def as_dict(self):
         return {k: getattr(self, k) for k, _ in self._fields_}
+
+
+def _fields(spec):
+    """ctypes fields from "name:kind" words (p pointer, l int64, i int, f float, z size_t)."""
+    kinds = {"p": ctypes.c_void_p, "l": ctypes.c_int64, "i": ctypes.c_int, "f": ctypes.c_float, "z": ctypes.c_size_t}
+    return [(w.split(":")[0], kinds[w.split(":")[1]]) for w in spec.split()]
+
+
+class LoraBaseLinearDesc(ctypes.Structure):
+    _fields_ = _fields("x:p x_stride:l qweight:p scales:p zeros:p y:p y_stride:l n_tokens:i d_in:i d_out:i group:i "
+                       "dtype:i")
+
+
+class LoraRopeDesc(ctypes.Structure):
+    _fields_ = _fields("q:p q_token:l q_head:l q_out:p q_out_token:l q_out_head:l k:p k_token:l k_head:l v:p "
+                       "v_token:l v_head:l k_cache:p v_cache:p cache_page:l cache_slot:l cache_head:l slots:p "
+                       "n_pages:l positions:p table:p n_positions:i page_size:i n_tokens:i n_heads:i n_kv_heads:i "
+                       "head_dim:i rot_dim:i interleaved:i inverse:i dtype:i")
+
+
+class LoraTreeAttentionDesc(ctypes.Structure):
+    _fields_ = _fields("q:p q_token:l q_head:l k_cache:p v_cache:p cache_page:l cache_slot:l cache_head:l n_pages:l "
+                       "page_table:p table_stride:l ctx_lens:p node_starts:p tree_mask:p out:p out_token:l out_head:l "
+                       "lse:p workspace:p workspace_bytes:z scale:f page_size:i table_pages:i mask_words:i "
+                       "n_requests:i n_tokens:i n_heads:i n_kv_heads:i head_dim:i dtype:i")
+
+
+class LoraVerifyDesc(ctypes.Structure):
+    _fields_ = _fields("target:p target_row:l draft:p draft_row:l tokens:p parents:p node_starts:p uniforms:p noise:p "
+                       "noise_row:l path:p n_accepted:p next_token:p max_path:i n_requests:i n_nodes:i vocab:i "
+                       "dtype:i")
+
+
+LORA_ROPE_PLAIN, LORA_ROPE_LINEAR, LORA_ROPE_BASE, LORA_ROPE_PIECES, LORA_ROPE_YARN = range(5)
 
 
 class LoraError(RuntimeError):
@@ -123,6 +159,12 @@ def load(path: str = LIB_PATH):
         "lora_set_warm_set": (i32, [vp, i32, P(u64)]),
         "lora_serve_step": (i32, [vp, i32, P(u64), i32, P(i32), P(vp), P(vp), vp, i32, i32, P(u64), P(i32),
                                   P(i32), P(u64), P(i32), P(i32)]),
+        "lora_base_linear": (i32, [P(LoraBaseLinearDesc), vp]),
+        "lora_rope_table": (i32, [vp, i32, i32, i32] + [ctypes.c_double] * 5 + [vp]),
+        "lora_rope": (i32, [P(LoraRopeDesc), vp]),
+        "lora_tree_attention_workspace_bytes": (sz, [i32] * 6),
+        "lora_tree_attention": (i32, [P(LoraTreeAttentionDesc), vp]),
+        "lora_verify_drafts": (i32, [P(LoraVerifyDesc), vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -415,3 +457,30 @@ def lora_serve_step(ctx, adapter_ids, layers=(), x_ptrs=(), y_ptrs=(), idx_bufs=
     dec = [(int(o_ids[i]), int(o_sl[i]), int(o_nd[i]), -1 if o_ev[i] == NO_ID else int(o_ev[i]))
            for i in range(nd.value)]
     return dec, ng.value
+
+
+# --- the drafted-token step (operators.py is the torch-tensor form) ---------------
+
+def lora_base_linear(desc, stream):
+    return check(load().lora_base_linear(desc, stream))
+
+
+def lora_rope_table(table, n_positions, rot_dim, scaling, base, factor, original, low_freq, high_freq, stream):
+    return check(load().lora_rope_table(table, n_positions, rot_dim, scaling, base, factor, original, low_freq,
+                                        high_freq, stream))
+
+
+def lora_rope(desc, stream):
+    return check(load().lora_rope(desc, stream))
+
+
+def lora_tree_attention_workspace_bytes(n_requests, n_tokens, n_heads, n_kv_heads, head_dim, dtype):
+    return int(load().lora_tree_attention_workspace_bytes(n_requests, n_tokens, n_heads, n_kv_heads, head_dim, dtype))
+
+
+def lora_tree_attention(desc, stream):
+    return check(load().lora_tree_attention(desc, stream))
+
+
+def lora_verify_drafts(desc, stream):
+    return check(load().lora_verify_drafts(desc, stream))

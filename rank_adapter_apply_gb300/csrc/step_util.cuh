@@ -1,0 +1,54 @@
+// Shared by the drafted-token step's calls (base_linear.cu, rope.cu,
+// tree_attention.cu, verify_drafts.cu): argument errors, launch errors and
+// element access by type.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdarg>
+#include <cstdint>
+#include <cstdio>
+
+#include "device_util.cuh"
+#include "kernels.cuh"
+#include "rank_adapter_apply.h"
+
+namespace lora {
+namespace step {
+
+// Record a formatted message for lora_last_error() and return `code`.
+inline int fail(int code, const char *fmt, ...) {
+    char buf[256];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return set_last_error(code, buf);
+}
+
+inline int launched(const char *what, cudaError_t e) {
+    if (e == cudaSuccess) return LORA_OK;
+    return fail(LORA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+inline bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+inline bool known_dtype(int dtype) { return dtype == LORA_DTYPE_F32 || dtype == LORA_DTYPE_BF16; }
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+}  // namespace step
+}  // namespace lora
