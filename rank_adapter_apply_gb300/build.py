@@ -17,6 +17,7 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -46,6 +47,25 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+# The tensor form of the drafted-token step's calls: a Python module of its own,
+# which the library does not depend on (and the sanitizer build leaves out).
+TENSOR_CALLS = os.path.join(BUILD, "_tensor_calls.so")
+TENSOR_CALLS_SOURCE = os.path.join(CSRC, "tensor_calls.cpp")
+
+
+def _tensor_calls_command(out: str) -> list[str]:
+    from importlib.util import find_spec
+    torch = os.path.dirname(find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) if os.path.isabs(_nvcc()) else "/usr/local/cuda"
+    include = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
+               os.path.join(torch, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
+               os.path.join(cuda, "include")]
+    lib = os.path.join(torch, "lib")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D_GLIBCXX_USE_CXX11_ABI=1",
+            *[f"-I{d}" for d in include], TENSOR_CALLS_SOURCE, "-o", out, f"-L{lib}", "-ltorch_python", "-ltorch_cuda",
+            "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{lib}"]
+
+
 SANITIZE_FLAGS = ["-Xcompiler", "-fsanitize=address,-fsanitize=undefined,-fno-omit-frame-pointer", "-g"]
 
 
@@ -67,20 +87,27 @@ def build(force: bool = False, verbose: bool = False, sanitize: bool = False) ->
             if src.endswith(".cpp"):
                 cmd = [nvcc, *flags, "-x", "c++", "-c", path, "-o", obj]
             jobs.append(cmd)
+    objects = bool(jobs)
+    calls_tmp = TENSOR_CALLS + f".tmp{os.getpid()}"
+    calls = not sanitize and (force or _stale(TENSOR_CALLS, [TENSOR_CALLS_SOURCE, common_deps[-1]]))
+    if calls:
+        jobs.insert(0, _tensor_calls_command(calls_tmp))
 
     def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
         p = subprocess.run(cmd, capture_output=True, text=True)
         if p.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{p.stdout}\n{p.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n{' '.join(cmd)}\n{p.stdout}\n{p.stderr}")
         return p.stderr
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
         for err in ex.map(run, jobs):
             if verbose and err:
                 print(err, flush=True)
-    if force or jobs or _stale(lib_path, objs):
+    if calls:
+        os.replace(calls_tmp, TENSOR_CALLS)
+    if force or objects or _stale(lib_path, objs):
         tmp = lib_path + f".tmp{os.getpid()}"
         link_extra = ["-Xcompiler", "-fsanitize=address,-fsanitize=undefined"] if sanitize else []
         run([nvcc, *ARCH, "-shared", "-cudart", "static", *objs, *link_extra, "-o", tmp])

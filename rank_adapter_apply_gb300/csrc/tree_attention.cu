@@ -1,6 +1,8 @@
 // lora_tree_attention: attention of drafted trees over a paged cache.
 #include "step_util.cuh"
 
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 
 namespace lora {
@@ -35,14 +37,7 @@ __device__ int request_of(const TreeArgs &a, int t) {
 }
 
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y));
-}
 __device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
-    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-}
 
 // One CTA of four warps for each query row; a warp takes every fourth key, a
 // lane four elements of the head; the running maximum and sum in fp32, the
@@ -116,6 +111,615 @@ __global__ void __launch_bounds__(128) tree_rows_kernel(TreeArgs a) {
     if (a.lse && lane == 0) a.lse[(size_t)t * a.n_heads + h] = top == -INFINITY ? -INFINITY : top + logf(sum);
 }
 
+// ---- bf16: tensor-core tiles over the paged cache --------------------------------
+//
+// A unit is (request, row tile, key/value head): the query rows of one tile (a
+// node's query heads that share the key/value head lie side by side) against all
+// keys of the request in tiles of 64. The key tiles of all units, in a row, are
+// dealt to the CTAs in equal shares: a share is a run of tiles that may start and
+// end inside a unit, so ragged lengths cost nothing, and a unit is split over
+// many CTAs where there are few. A CTA that covers a whole unit writes its result;
+// the others write (O, m, l) to the workspace, and join_kernel joins them.
+constexpr int kTileKeys = 64;
+constexpr int kStages = 3;
+
+struct Plan {                 // workspace regions
+    float *part;              // [2 * ctas][M][DP] unnormalised O
+    float2 *stat;             // [2 * ctas][M] (m, l), m in powers of two
+    int4 *seg;                // [ctas] (request, row tile, head, parts) of the unit that starts in a CTA's share and
+                              // goes on past it; parts = 0: there is none
+    int ctas;
+};
+// Part slots: 2c + 1 holds the first part of the unit that goes on past CTA c's
+// share, 2c the part of the unit that began before it.
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// 16 bytes to shared memory, zeros when !ok (the source is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+struct Request {
+    int start, nodes, row_tiles, key_tiles, ctx, keys;
+};
+
+__device__ Request request(const TreeArgs &a, int b, int m_rows) {
+    Request r;
+    r.start = node_start(a, b);
+    r.nodes = max(node_start(a, b + 1) - r.start, 0);
+    // keys that fit the page table; the largest count is a multiple of the tile below 2^31
+    const long long room = min((long long)a.table_pages * a.page_size, 0x7fffffc0ll);
+    r.ctx = max(a.ctx_lens[b], 0);
+    r.keys = (int)min((long long)r.ctx + r.nodes, room);
+    r.row_tiles = (r.nodes * (a.n_heads / a.n_kv) + m_rows - 1) / m_rows;
+    r.key_tiles = max((r.keys + kTileKeys - 1) / kTileKeys, 1);   // one for rows without keys, too
+    return r;
+}
+
+// Where a CTA is in the run of tiles.
+struct Cursor {
+    Request r;
+    int b, row_tile, head, tile;
+};
+
+__device__ __forceinline__ void next_tile(const TreeArgs &a, Cursor &c, int m_rows) {
+    if (++c.tile < c.r.key_tiles) return;
+    c.tile = 0;
+    if (++c.head < a.n_kv) return;
+    c.head = 0;
+    if (++c.row_tile < c.r.row_tiles) return;
+    c.row_tile = 0;
+    do {
+        if (++c.b >= a.n_requests) return;
+        c.r = request(a, c.b, m_rows);
+    } while (c.r.row_tiles == 0);
+}
+
+// Bits 0..63: which of the tile's keys p0 .. p0 + 63 node i (row `token`) sees.
+__device__ uint64_t seen_keys(const TreeArgs &a, const Request &r, int i, int p0) {
+    const int in_ctx = r.ctx - p0;
+    uint64_t seen = in_ctx >= 64 ? ~0ull : in_ctx <= 0 ? 0ull : (1ull << in_ctx) - 1;
+    if (in_ctx >= 64) return seen;
+    const int j0 = -in_ctx;                             // the node that is the tile's first key
+    if (!a.tree_mask) {
+        const int n = in_ctx + i + 1;                   // keys up to the node itself
+        return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1;
+    }
+    const uint64_t *m = a.tree_mask + (size_t)(r.start + i) * a.mask_words;
+    if (j0 < 0) return seen | m[0] << (-j0);
+    const int w = j0 >> 6, sh = j0 & 63;
+    if (w < a.mask_words) seen = m[w] >> sh;
+    if (sh && w + 1 < a.mask_words) seen |= m[w + 1] << (64 - sh);
+    return seen;
+}
+
+template <int DP, int WM, int WN>
+struct Tile {
+    static constexpr int M = 16 * WM, NK = kTileKeys / WN, kWarps = WM * WN, kThreads = 32 * kWarps;
+    static constexpr int kRowBytes = DP * 2, kHalf = kTileKeys * kRowBytes, kStage = 2 * kHalf;
+    // stages, then a ring of the tiles' key offsets and valid-key masks (one place more than stages: a tile's are
+    // written while the tile one stage-count before it may still be read), then the search's scratch
+    static constexpr int kRing = kStages + 1;
+    static constexpr int kOff = kStages * kStage, kValid = kOff + kRing * kTileKeys * 8;
+    static constexpr int kStart = kValid + kRing * 8, kSmem = kStart + 64;
+};
+
+template <int DP, int WM, int WN>
+__global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan plan) {
+    using T = Tile<DP, WM, WN>;
+    constexpr int kPieces = DP / 8;                     // 16-byte pieces of a row
+    extern __shared__ __align__(128) unsigned char smem[];
+    long long *offs = reinterpret_cast<long long *>(smem + T::kOff);        // element offset of a key's row, -1: none
+    uint32_t *valid = reinterpret_cast<uint32_t *>(smem + T::kValid);       // two words a tile
+    long long *first = reinterpret_cast<long long *>(smem + T::kStart);     // request, tiles before it, total, scratch
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int wm = warp % WM, wn = warp / WM, g4 = lane >> 2, t4 = lane & 3;
+    const int group = a.n_heads / a.n_kv;
+
+    grid_launch_dependents();                            // join_kernel waits for this grid's end itself
+    if (tid == 0) plan.seg[blockIdx.x] = make_int4(0, 0, 0, 0);
+    // ---- this CTA's share: tiles [lo, hi) of the total
+    long long lo, hi, total = 0, used;
+    {
+        long long mine = 0;
+        for (int b = tid; b < a.n_requests; b += T::kThreads) {
+            const Request r = request(a, b, T::M);
+            mine += (long long)r.row_tiles * r.key_tiles * a.n_kv;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        if (lane == 0) first[warp] = mine;
+        __syncthreads();
+        for (int w = 0; w < T::kWarps; ++w) total += first[w];
+        used = min((long long)gridDim.x, total);
+        if (blockIdx.x >= used) return;
+        lo = total * blockIdx.x / used;
+        hi = total * (blockIdx.x + 1) / used;
+        __syncthreads();
+    }
+    Cursor load;
+    {
+        long long before = 0;
+        for (int b0 = 0;; b0 += T::kThreads) {           // ends at the latest in the chunk that holds tile lo < total
+            const int b = b0 + tid;
+            long long n = 0;
+            if (b < a.n_requests) {
+                const Request r = request(a, b, T::M);
+                n = (long long)r.row_tiles * r.key_tiles * a.n_kv;
+            }
+            long long upto = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            if (lane == 31) first[2 + warp] = upto;
+            if (tid == 0) first[0] = -1;
+            __syncthreads();
+            for (int w = 0; w < warp; ++w) upto += first[2 + w];
+            upto += before;
+            if (upto - n <= lo && lo < upto) first[0] = b, first[1] = upto - n;
+            for (int w = 0; w < T::kWarps; ++w) before += first[2 + w];
+            __syncthreads();
+            if (first[0] >= 0 || b0 + T::kThreads >= a.n_requests) break;
+            __syncthreads();
+        }
+        if (first[0] < 0) return;                        // not reached: lo < total
+        load.b = (int)first[0];
+        load.r = request(a, load.b, T::M);
+        long long at = lo - first[1];
+        load.tile = (int)(at % load.r.key_tiles);
+        at /= load.r.key_tiles;
+        load.head = (int)(at % a.n_kv);
+        load.row_tile = (int)(at / a.n_kv);
+    }
+    Cursor c = load;                                     // the tile being computed; `load` runs ahead of it
+    Cursor look = load;                                  // the tile whose page ids are being read: one further ahead
+    const int n_tiles = (int)(hi - lo);
+
+    // Offsets of tile i's keys: read into a register by threads 0..63, stored to the ring at the end of the step.
+    auto read_off = [&](const Cursor &u) -> long long {
+        const int p = u.tile * kTileKeys + tid;
+        if (tid >= kTileKeys || p >= u.r.keys) return -1;
+        const int at = p / a.page_size, id = a.page_table[u.b * a.table_stride + at];
+        return id >= 0 && id < a.n_pages ? id * a.c_page + (p - at * a.page_size) * a.c_slot : -1;
+    };
+    auto store_off = [&](int i, long long off) {
+        if (tid >= kTileKeys) return;
+        offs[i % T::kRing * kTileKeys + tid] = off;
+        const uint32_t ok = __ballot_sync(0xffffffffu, off >= 0);
+        if (lane == 0) valid[i % T::kRing * 2 + warp] = ok;
+    };
+    auto issue = [&](int i, const Cursor &u) {
+        const uint32_t base = smem_u32(smem) + i % kStages * T::kStage;
+        const int piece = tid % kPieces;
+        const bool in_head = piece * 8 < a.head_dim;
+        const long long at0 = u.head * a.c_head + piece * 8;
+#pragma unroll
+        for (int n = 0; n < kTileKeys * kPieces / T::kThreads; ++n) {
+            const int k = tid / kPieces + n * (T::kThreads / kPieces);
+            const long long off = offs[i % T::kRing * kTileKeys + k];
+            const bool ok = off >= 0 && in_head;
+            const long long at = ok ? off + at0 : 0;
+            const uint32_t dst = base + k * T::kRowBytes + ((piece ^ (k & 7)) << 4);
+            copy16(dst, static_cast<const __nv_bfloat16 *>(a.k_cache) + at, ok);
+            copy16(dst + T::kHalf, static_cast<const __nv_bfloat16 *>(a.v_cache) + at, ok);
+        }
+    };
+
+    // fill: offsets of the first tiles, then their copies; one commit group a tile
+    long long pending = -1;
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (i < n_tiles) {
+            store_off(i, read_off(look));
+            next_tile(a, look, T::M);
+        }
+    }
+    __syncthreads();
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (i < n_tiles) {
+            issue(i, load);
+            next_tile(a, load, T::M);
+        }
+        cp_async_commit();
+    }
+    if (kStages - 1 < n_tiles) store_off(kStages - 1, read_off(look));
+
+    uint32_t q[DP / 16][4];
+    float o[DP / 8][4], m[2], l[2];
+    const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale);
+    const float c2 = scale * 1.4426950408889634f;        // scores in powers of two
+    bool fresh = true;
+    int seg_first = c.tile;
+    const uint32_t lm_row = lane & 7, lm_hi = (lane >> 3) & 1, lm_top = lane >> 4;
+
+    for (int i = 0; i < n_tiles; ++i) {
+        if (fresh) {                                     // a new unit: its query rows, straight into fragments
+            const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q);
+#pragma unroll
+            for (int hrow = 0; hrow < 2; ++hrow) {
+                const int row = c.row_tile * T::M + wm * 16 + g4 + hrow * 8;
+                const int node = row / group;
+                const bool ok = node < c.r.nodes;
+                const long long at = ok ? (c.r.start + node) * a.q_token + (c.head * group + row % group) * a.q_head : 0;
+#pragma unroll
+                for (int ks = 0; ks < DP / 16; ++ks)
+#pragma unroll
+                    for (int up = 0; up < 2; ++up) {
+                        const int col = ks * 16 + up * 8 + t4 * 2;
+                        uint32_t v = 0;
+                        if (ok && col < a.head_dim) v = *reinterpret_cast<const uint32_t *>(qp + at + col);
+                        if (a.scale < 0.f) v ^= 0x80008000u;
+                        if (a.scale == 0.f) v = 0;
+                        q[ks][up * 2 + hrow] = v;
+                    }
+            }
+#pragma unroll
+            for (int d = 0; d < DP / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+            m[0] = m[1] = -INFINITY;
+            l[0] = l[1] = 0.f;
+            seg_first = c.tile;
+            fresh = false;
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncthreads();                                 // tile i is here, and everyone is done with tile i - 1
+        if (i + kStages - 1 < n_tiles) {
+            issue(i + kStages - 1, load);
+            next_tile(a, load, T::M);
+            next_tile(a, look, T::M);
+        }
+        cp_async_commit();
+        if (i + kStages < n_tiles) pending = read_off(look);
+
+        // ---- scores of this warp's rows and keys
+        const uint32_t kb = smem_u32(smem) + i % kStages * T::kStage, vb = kb + T::kHalf;
+        float s[T::NK / 8][4];
+#pragma unroll
+        for (int n = 0; n < T::NK / 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < DP / 16; ++ks) {
+#pragma unroll
+            for (int n = 0; n < T::NK / 16; ++n) {
+                uint32_t kf[4];
+                const uint32_t key = wn * T::NK + n * 16 + lm_top * 8 + lm_row;
+                ldsm4(kf, kb + key * T::kRowBytes + (((ks * 2 + lm_hi) ^ (key & 7)) << 4));
+                mma_bf16(s[2 * n], q[ks][0], q[ks][1], q[ks][2], q[ks][3], kf[0], kf[1]);
+                mma_bf16(s[2 * n + 1], q[ks][0], q[ks][1], q[ks][2], q[ks][3], kf[2], kf[3]);
+            }
+        }
+        // ---- keys a row does not see
+        const int p0 = c.tile * kTileKeys;
+        const uint64_t there = valid[i % T::kRing * 2] | (uint64_t)valid[i % T::kRing * 2 + 1] << 32;
+        bool hidden = false;                             // a key that is there but that one of this thread's rows skips
+        const bool masked = there != ~0ull || p0 + kTileKeys > c.r.ctx;
+        if (masked) {
+#pragma unroll
+            for (int hrow = 0; hrow < 2; ++hrow) {
+                const int node = (c.row_tile * T::M + wm * 16 + g4 + hrow * 8) / group;
+                uint64_t seen = 0;
+                if (node < c.r.nodes) {
+                    seen = seen_keys(a, c.r, node, p0) & there;
+                    hidden = hidden || seen != there;
+                }
+                seen >>= wn * T::NK;
+#pragma unroll
+                for (int n = 0; n < T::NK / 8; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (!(seen >> (n * 8 + t4 * 2 + e) & 1)) s[n][hrow * 2 + e] = -INFINITY;
+            }
+        }
+        // ---- running maximum and sum
+        float top[2] = {m[0], m[1]};
+#pragma unroll
+        for (int n = 0; n < T::NK / 8; ++n) {
+            top[0] = fmaxf(top[0], fmaxf(s[n][0], s[n][1]));
+            top[1] = fmaxf(top[1], fmaxf(s[n][2], s[n][3]));
+        }
+#pragma unroll
+        for (int hrow = 0; hrow < 2; ++hrow) {
+            top[hrow] = fmaxf(top[hrow], __shfl_xor_sync(0xffffffffu, top[hrow], 1));
+            top[hrow] = fmaxf(top[hrow], __shfl_xor_sync(0xffffffffu, top[hrow], 2));
+        }
+        const bool moved = top[0] != m[0] || top[1] != m[1];
+        const float base0 = top[0] == -INFINITY ? 0.f : top[0] * c2, base1 = top[1] == -INFINITY ? 0.f : top[1] * c2;
+        if (__any_sync(0xffffffffu, moved)) {
+            const float k0 = exp2_fast(fmaf(m[0], c2, -base0)), k1 = exp2_fast(fmaf(m[1], c2, -base1));
+            l[0] *= k0;
+            l[1] *= k1;
+#pragma unroll
+            for (int d = 0; d < DP / 8; ++d) {
+                o[d][0] *= k0;
+                o[d][1] *= k0;
+                o[d][2] *= k1;
+                o[d][3] *= k1;
+            }
+            m[0] = top[0];
+            m[1] = top[1];
+        }
+        uint32_t pf[T::NK / 8][2];
+#pragma unroll
+        for (int n = 0; n < T::NK / 8; ++n) {
+            const float e0 = exp2_fast(fmaf(s[n][0], c2, -base0)), e1 = exp2_fast(fmaf(s[n][1], c2, -base0));
+            const float e2 = exp2_fast(fmaf(s[n][2], c2, -base1)), e3 = exp2_fast(fmaf(s[n][3], c2, -base1));
+            l[0] += e0 + e1;
+            l[1] += e2 + e3;
+            // weights to bf16 for the second product: 2^-9 relative, below the output's own rounding; their sum
+            // l stays in fp32 and unrounded
+            pf[n][0] = pack_bf16(e0, e1);
+            pf[n][1] = pack_bf16(e2, e3);
+        }
+        // A weight of zero times an infinity or NaN is NaN: where a row skips a key that is there (the whole block
+        // decides alike, in tiles of tree keys only), values that are not finite are looked for, and such a tile
+        // is summed key by key without the zero weights.
+        bool by_key = false;
+        if (masked && __syncthreads_or(hidden)) {
+            uint32_t odd = 0;
+            for (int n = tid; n < T::kHalf / 16; n += T::kThreads) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(smem + i % kStages * T::kStage + T::kHalf + n * 16);
+                odd |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
+                       ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
+            }
+            by_key = __syncthreads_or((odd & 0x80008000u) != 0);
+        }
+        if (by_key) {
+            // the weights go where the keys lay (every warp has its scores by now): [M][64] bf16
+            uint32_t *w = reinterpret_cast<uint32_t *>(smem + i % kStages * T::kStage);
+#pragma unroll
+            for (int n = 0; n < T::NK / 8; ++n)
+#pragma unroll
+                for (int hrow = 0; hrow < 2; ++hrow)
+                    w[(wm * 16 + g4 + hrow * 8) * 32 + (wn * T::NK + n * 8) / 2 + t4] = pf[n][hrow];
+            __syncwarp();
+            for (int k = wn * T::NK; k < (wn + 1) * T::NK; ++k) {
+                const __nv_bfloat16 *wb = reinterpret_cast<const __nv_bfloat16 *>(w);
+                const float w0 = to_f32(wb[(wm * 16 + g4) * 64 + k]), w1 = to_f32(wb[(wm * 16 + g4 + 8) * 64 + k]);
+                const unsigned char *vr = smem + i % kStages * T::kStage + T::kHalf + k * T::kRowBytes + t4 * 4;
+#pragma unroll
+                for (int d = 0; d < DP / 8; ++d) {
+                    const uint32_t v = *reinterpret_cast<const uint32_t *>(vr + ((d ^ (k & 7)) << 4));
+                    if (w0 != 0.f) o[d][0] = fmaf(w0, bf_lo(v), o[d][0]), o[d][1] = fmaf(w0, bf_hi(v), o[d][1]);
+                    if (w1 != 0.f) o[d][2] = fmaf(w1, bf_lo(v), o[d][2]), o[d][3] = fmaf(w1, bf_hi(v), o[d][3]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int n = 0; n < T::NK / 16; ++n) {
+#pragma unroll
+                for (int d = 0; d < DP / 16; ++d) {
+                    uint32_t vf[4];
+                    const uint32_t key = wn * T::NK + n * 16 + lm_hi * 8 + lm_row;
+                    ldsm4_t(vf, vb + key * T::kRowBytes + (((d * 2 + lm_top) ^ (key & 7)) << 4));
+                    mma_bf16(o[2 * d], pf[2 * n][0], pf[2 * n][1], pf[2 * n + 1][0], pf[2 * n + 1][1], vf[0], vf[1]);
+                    mma_bf16(o[2 * d + 1], pf[2 * n][0], pf[2 * n][1], pf[2 * n + 1][0], pf[2 * n + 1][1], vf[2], vf[3]);
+                }
+            }
+        }
+        // ---- the unit or the share ends: join the warps and write
+        if (c.tile + 1 == c.r.key_tiles || i + 1 == n_tiles) {
+#pragma unroll
+            for (int hrow = 0; hrow < 2; ++hrow) {
+                l[hrow] += __shfl_xor_sync(0xffffffffu, l[hrow], 1);
+                l[hrow] += __shfl_xor_sync(0xffffffffu, l[hrow], 2);
+                m[hrow] = m[hrow] == -INFINITY ? -INFINITY : m[hrow] * c2;
+            }
+            if constexpr (WN > 1) {
+                // the warps that share rows, through the stage just consumed (the next copies into it are issued
+                // after the next step's barrier)
+                float *buf = reinterpret_cast<float *>(smem + i % kStages * T::kStage);   // [WN - 1][M][DP + 2]
+                __syncthreads();
+                if (wn > 0) {
+#pragma unroll
+                    for (int hrow = 0; hrow < 2; ++hrow) {
+                        float *r = buf + ((size_t)(wn - 1) * T::M + wm * 16 + g4 + hrow * 8) * (DP + 2);
+#pragma unroll
+                        for (int d = 0; d < DP / 8; ++d)
+                            *reinterpret_cast<float2 *>(r + d * 8 + t4 * 2) =
+                                make_float2(o[d][hrow * 2], o[d][hrow * 2 + 1]);
+                        if (t4 == 0) *reinterpret_cast<float2 *>(r + DP) = make_float2(m[hrow], l[hrow]);
+                    }
+                }
+                __syncthreads();
+                if (wn == 0) {
+#pragma unroll
+                    for (int w = 1; w < WN; ++w)
+#pragma unroll
+                        for (int hrow = 0; hrow < 2; ++hrow) {
+                            const float *r = buf + ((size_t)(w - 1) * T::M + wm * 16 + g4 + hrow * 8) * (DP + 2);
+                            const float2 ml = *reinterpret_cast<const float2 *>(r + DP);
+                            const float t = fmaxf(m[hrow], ml.x), b = t == -INFINITY ? 0.f : t;
+                            const float f = exp2_fast(m[hrow] - b), h = exp2_fast(ml.x - b);
+                            m[hrow] = t;
+                            l[hrow] = l[hrow] * f + ml.y * h;
+#pragma unroll
+                            for (int d = 0; d < DP / 8; ++d) {
+                                const float2 v = *reinterpret_cast<const float2 *>(r + d * 8 + t4 * 2);
+                                o[d][hrow * 2] = o[d][hrow * 2] * f + v.x * h;
+                                o[d][hrow * 2 + 1] = o[d][hrow * 2 + 1] * f + v.y * h;
+                            }
+                        }
+                }
+            }
+            const bool starts = seg_first == 0, ends = c.tile + 1 == c.r.key_tiles;
+            if (wn == 0) {
+#pragma unroll
+                for (int hrow = 0; hrow < 2; ++hrow) {
+                    const int r = wm * 16 + g4 + hrow * 8;
+                    const int row = c.row_tile * T::M + r, node = row / group;
+                    if (node >= c.r.nodes) continue;
+                    if (starts && ends) {
+                        const long long token = c.r.start + node;
+                        const int head = c.head * group + row % group;
+                        const float inv = l[hrow] > 0.f ? 1.f / l[hrow] : 0.f;
+                        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + token * a.o_token + head * a.o_head;
+                        // a row without keys is 0, whatever the (zero-filled) tiles held
+                        const bool none = m[hrow] == -INFINITY;
+#pragma unroll
+                        for (int d = 0; d < DP / 8; ++d)
+                            if (d * 8 < a.head_dim)
+                                *reinterpret_cast<uint32_t *>(out + d * 8 + t4 * 2) =
+                                    none ? 0u : pack_bf16(o[d][hrow * 2] * inv, o[d][hrow * 2 + 1] * inv);
+                        if (a.lse && t4 == 0)
+                            a.lse[token * a.n_heads + head] =
+                                none ? -INFINITY : m[hrow] * 0.6931471805599453f + logf(l[hrow]);
+                    } else {
+                        const long long slot = 2ll * blockIdx.x + (starts ? 1 : 0);
+                        float *part = plan.part + (slot * T::M + r) * DP;
+#pragma unroll
+                        for (int d = 0; d < DP / 8; ++d)
+                            *reinterpret_cast<float2 *>(part + d * 8 + t4 * 2) =
+                                make_float2(o[d][hrow * 2], o[d][hrow * 2 + 1]);
+                        if (t4 == 0) plan.stat[slot * T::M + r] = make_float2(m[hrow], l[hrow]);
+                    }
+                }
+            }
+            if (tid == 0 && starts && !ends) {
+                // the unit's last tile lies in the share of CTA floor((x + 1) used - 1) / total), x its index
+                const long long x = lo + i + (c.r.key_tiles - 1 - c.tile);
+                const int parts = (int)(((x + 1) * used - 1) / total) - (int)blockIdx.x + 1;
+                plan.seg[blockIdx.x] = make_int4(c.b, c.row_tile, c.head, parts);
+            }
+            fresh = true;
+        }
+        if (i + kStages < n_tiles) store_off(i + kStages, pending);
+        next_tile(a, c, T::M);
+    }
+}
+
+// Join the parts of the unit that goes on past CTA blockIdx.x's share. A warp
+// takes a row, or, where there are many parts, the block takes one row after
+// another and a warp every eighth part of it.
+template <int DP, int M>
+__global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan) {
+    constexpr int kVec = DP / 32, kMany = 24;
+    __shared__ float so[8][DP];
+    __shared__ float2 sm[8];
+    grid_dependency_wait();
+    const int4 seg = plan.seg[blockIdx.x];
+    if (seg.w == 0) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = a.n_heads / a.n_kv;
+    const int start = node_start(a, seg.x), rows = (node_start(a, seg.x + 1) - start) * group - seg.y * M;
+    const bool many = seg.w > kMany;
+    for (int i = 0; i < (many ? 8 : 1); ++i) {
+        const int r = blockIdx.y * 8 + (many ? i : warp);
+        if (r >= rows) break;                            // rows of a block are alike in `many`: no barrier is missed
+        float o[kVec], m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) o[e] = 0.f;
+        auto add = [&](float2 ml, const float *v) {
+            const float t = fmaxf(m, ml.x), b = t == -INFINITY ? 0.f : t;
+            const float f = exp2_fast(m - b), h = exp2_fast(ml.x - b);
+            m = t;
+            l = l * f + ml.y * h;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) o[e] = o[e] * f + v[e] * h;
+        };
+        constexpr int kAhead = 4;                        // parts whose loads are in flight together
+        const int step = many ? 8 : 1;
+        for (int p = many ? warp : 0; p < seg.w; p += kAhead * step) {
+            float v[kAhead][kVec];
+            float2 ml[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int part = p + u * step;
+                ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) v[u][e] = 0.f;
+                if (part < seg.w) {
+                    const long long slot = part == 0 ? 2ll * blockIdx.x + 1 : 2ll * (blockIdx.x + part);
+                    ml[u] = plan.stat[slot * M + r];
+                    const float *src = plan.part + (slot * M + r) * DP + lane * kVec;
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) v[u][e] = src[e];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) add(ml[u], v[u]);
+        }
+        if (many) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) so[warp][lane * kVec + e] = o[e];
+            if (lane == 0) sm[warp] = make_float2(m, l);
+            __syncthreads();
+            if (warp != i) continue;
+            m = -INFINITY;
+            l = 0.f;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) o[e] = 0.f;
+            for (int w = 0; w < 8; ++w) add(sm[w], &so[w][lane * kVec]);
+        }
+        const int row = seg.y * M + r, head = seg.z * group + row % group;
+        const long long token = start + row / group;
+        const bool none = m == -INFINITY;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + token * a.o_token + head * a.o_head + lane * kVec;
+        if (lane * kVec < a.head_dim)
+#pragma unroll
+            for (int e = 0; e < kVec; e += 2)
+                *reinterpret_cast<uint32_t *>(out + e) = none ? 0u : pack_bf16(o[e] * inv, o[e + 1] * inv);
+        if (a.lse && lane == 0) a.lse[token * a.n_heads + head] = none ? -INFINITY : m * 0.6931471805599453f + logf(l);
+    }
+}
+
+constexpr int kMaxRows = 64;
+constexpr int kMaxCtas = 2 * 160;
+
+// The row tile by the average rows (nodes times query heads of a key/value head) of a request.
+int rows_of_tile(int n_requests, int n_tokens, int group) {
+    const double rows = (double)n_tokens * group / n_requests;
+    return rows <= 16.0 ? 16 : rows <= 32.0 ? 32 : 64;
+}
+
+size_t plan_bytes(int ctas) {
+    return (size_t)ctas * sizeof(int4) + 2 * (size_t)ctas * kMaxRows * (128 * sizeof(float) + sizeof(float2));
+}
+
+template <int DP, int WM>
+cudaError_t launch_tiles(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
+    using T = Tile<DP, WM, 4 / WM>;
+    auto kernel = tree_tiles_kernel<DP, WM, 4 / WM>;
+    static std::atomic<uint64_t> ready{0};
+    if (!device_bit(ready)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+        if (e != cudaSuccess) return e;
+        set_device_bit(ready);
+    }
+    kernel<<<plan.ctas, T::kThreads, T::kSmem, st>>>(a, plan);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_pdl(tree_join_kernel<DP, T::M>, dim3(plan.ctas, T::M / 8), dim3(256), 0, st, a, plan);
+}
+
+template <int DP>
+cudaError_t launch_rows_of(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
+    switch (rows_of_tile(a.n_requests, a.n_tokens, a.n_heads / a.n_kv)) {
+        case 16: return launch_tiles<DP, 1>(a, plan, st);
+        case 32: return launch_tiles<DP, 2>(a, plan, st);
+        default: return launch_tiles<DP, 4>(a, plan, st);
+    }
+}
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return n;
+}
+
 bool shape_ok(int n_requests, int n_tokens, int n_heads, int n_kv, int head_dim, int dtype) {
     return known_dtype(dtype) && n_requests >= 0 && n_tokens >= 0 && n_heads >= 1 && n_heads <= 65535 && n_kv >= 1 &&
            n_heads % n_kv == 0 && head_dim >= 8 && head_dim <= 128 && head_dim % 8 == 0;
@@ -130,7 +734,8 @@ using namespace lora::step;
 extern "C" size_t lora_tree_attention_workspace_bytes(int n_requests, int n_tokens, int n_heads, int n_kv_heads,
                                                       int head_dim, int dtype) {
     if (!shape_ok(n_requests, n_tokens, n_heads, n_kv_heads, head_dim, dtype)) return 0;
-    return 256;
+    // the largest grid of any GPU this library is built for: the size does not depend on the device
+    return dtype == LORA_DTYPE_BF16 ? plan_bytes(kMaxCtas) : 256;
 }
 
 extern "C" int lora_tree_attention(const lora_tree_attention_desc *d, void *stream) {
@@ -143,6 +748,9 @@ extern "C" int lora_tree_attention(const lora_tree_attention_desc *d, void *stre
     if (d->page_size < 1 || d->table_pages < 0 || d->n_pages < 0 || d->mask_words < 0)
         return fail(LORA_ERR_ARG, "tree_attention: page_size %d, table_pages %d, n_pages %lld, mask_words %d",
                     d->page_size, d->table_pages, (long long)d->n_pages, d->mask_words);
+    if ((long long)d->n_tokens * d->n_heads > (1 << 30))
+        return fail(LORA_ERR_ARG, "tree_attention: n_tokens %d times n_heads %d is above 2^30", d->n_tokens,
+                    d->n_heads);
     if (!std::isfinite(d->scale)) return fail(LORA_ERR_ARG, "tree_attention: scale is not finite");
     if (d->n_tokens == 0 || d->n_requests == 0) return LORA_OK;
     if (!d->q || !d->out || !d->ctx_lens || !d->node_starts || (d->table_pages > 0 && !d->page_table) ||
@@ -154,8 +762,10 @@ extern "C" int lora_tree_attention(const lora_tree_attention_desc *d, void *stre
                                  (long long)d->cache_slot, (long long)d->cache_head, (long long)d->out_token,
                                  (long long)d->out_head};
     bool ok = aligned16(d->q) && aligned16(d->out) && aligned16(d->k_cache) && aligned16(d->v_cache);
-    for (long long s : strides) ok = ok && s * eb % 16 == 0;
-    if (!ok) return fail(LORA_ERR_ARG, "tree_attention: q, out and cache pointers and strides must be multiples of 16 bytes");
+    for (long long s : strides) ok = ok && s >= 0 && s * eb % 16 == 0;
+    if (!ok)
+        return fail(LORA_ERR_ARG, "tree_attention: q, out and cache pointers and strides must be multiples of 16 bytes, "
+                                  "no stride negative");
     const size_t need = lora_tree_attention_workspace_bytes(d->n_requests, d->n_tokens, d->n_heads, d->n_kv_heads,
                                                             d->head_dim, d->dtype);
     if (!d->workspace || d->workspace_bytes < need || reinterpret_cast<uintptr_t>(d->workspace) % 256)
@@ -165,10 +775,18 @@ extern "C" int lora_tree_attention(const lora_tree_attention_desc *d, void *stre
                d->out_token, d->out_head, d->table_stride, d->n_pages, d->scale,   d->page_size,  d->table_pages,
                d->mask_words, d->n_requests, d->n_tokens, d->n_heads, d->n_kv_heads, d->head_dim};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    dim3 grid(d->n_tokens, d->n_heads);
-    if (d->dtype == LORA_DTYPE_BF16)
-        tree_rows_kernel<__nv_bfloat16><<<grid, 128, 0, st>>>(a);
-    else
-        tree_rows_kernel<float><<<grid, 128, 0, st>>>(a);
+    if (d->dtype == LORA_DTYPE_BF16) {
+        const int sms = sm_count();
+        if (sms < 1) return fail(LORA_ERR_CUDA, "tree_attention: no CUDA device");
+        Plan plan;
+        plan.ctas = std::min(2 * sms, kMaxCtas);
+        char *ws = static_cast<char *>(d->workspace);
+        plan.part = reinterpret_cast<float *>(ws);
+        plan.stat = reinterpret_cast<float2 *>(plan.part + 2 * (size_t)plan.ctas * kMaxRows * 128);
+        plan.seg = reinterpret_cast<int4 *>(plan.stat + 2 * (size_t)plan.ctas * kMaxRows);
+        return launched("tree_attention",
+                        d->head_dim <= 64 ? launch_rows_of<64>(a, plan, st) : launch_rows_of<128>(a, plan, st));
+    }
+    tree_rows_kernel<float><<<dim3(d->n_tokens, d->n_heads), 128, 0, st>>>(a);
     return launched("tree_attention", cudaGetLastError());
 }

@@ -407,6 +407,40 @@ def test_tree_attention_score_range(ops, spread, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim,nodes", [(64, 2), (128, 3), (72, 9), (128, 20)])
+def test_tree_attention_poison_in_skipped_keys(ops, dim, nodes, dtype):
+    """Infinities and NaN in tree keys reach the rows that see those keys and no other row: two forks of the root, a
+    poisoned value in one of them, a poisoned key in the other, and both in a node that nobody sees."""
+    import torch
+    c = _tree_case([70], [nodes + 2], 8, 2, dim, 16, dtype, seed=13)
+    n = nodes + 2
+    mask = np.zeros((n, 64), bool)
+    mask[:, 0] = True
+    for i in range(1, n):
+        mask[i, i] = True
+    mask[n - 1, n - 1] = False
+    c["mask"], c["bits"] = mask, _dev(np.packbits(mask, axis=1, bitorder="little").view(np.int64).reshape(n, 1))
+    want = _run_tree(ops, c)
+    _check_tree(c, *want)
+
+    def at(node):
+        return int(c["table"][0, (70 + node) // 16]), (70 + node) % 16
+    c["vc"][at(1)[0], at(1)[1], 0, 5] = float("inf")
+    c["kc"][at(2)[0], at(2)[1], 1, 3] = float("nan")
+    c["kc"][at(n - 1)[0], at(n - 1)[1]] = float("-inf")
+    c["vc"][at(n - 1)[0], at(n - 1)[1]] = float("nan")
+    out, lse = _run_tree(ops, c)
+    assert torch.isinf(out[1, :4, 5]).all() and (out[1, :4, 5] > 0).all()
+    assert torch.isnan(lse[2, 4:]).all() and torch.isnan(out[2, 4:]).all()
+    keep = torch.ones_like(out, dtype=torch.bool)
+    keep[1, :4, 5] = False
+    keep[2, 4:] = False
+    tol = 2.0 ** -6 if dtype == "bf16" else 2.0 ** -18      # both within their tolerance of the same values
+    assert ((out - want[0]).abs()[keep] <= tol * (1 + want[0].abs()[keep])).all()
+    assert torch.equal(lse[[0, 1] + list(range(3, n))], want[1][[0, 1] + list(range(3, n))])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_tree_attention_long_context(ops, dtype):
     """A context long enough to be split over many blocks, beside short ones."""
     c = _tree_case([9000, 3, 400], [3, 5, 2], 4, 1, 64, 64, dtype, seed=10)
