@@ -602,10 +602,11 @@ typedef struct {
     const uint8_t *qweight;   /* [d_out][d_in / 2], 16-byte aligned: byte j of a row holds n of
                                  column 2j in its low and of column 2j + 1 in its high four bits */
     const void *scales;       /* [d_out][d_in / group], type dtype */
-    const uint8_t *zeros;     /* [d_out][d_in / group], 0..255 (0..15 in practice); NULL: 8 everywhere */
+    const uint8_t *zeros;     /* [d_out][d_in / group], 0..128 (more counts as 128); NULL: 8 everywhere */
     void *y;                  /* [n_tokens][d_out], rows y_stride apart */
     int64_t y_stride;
-    int n_tokens, d_in, d_out;
+    int n_tokens;             /* 0..262144 */
+    int d_in, d_out;
     int group;                /* 32, 64 or 128; d_in is a multiple of it */
     int dtype;                /* of x, scales and y */
 } lora_base_linear_desc;

@@ -32,6 +32,15 @@ inline int launched(const char *what, cudaError_t e) {
     return fail(LORA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// SMs of the current device, 0 where there is none.
+inline int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return n;
+}
+
 inline bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 inline bool known_dtype(int dtype) { return dtype == LORA_DTYPE_F32 || dtype == LORA_DTYPE_BF16; }
 

@@ -712,14 +712,6 @@ cudaError_t launch_rows_of(const TreeArgs &a, const Plan &plan, cudaStream_t st)
     }
 }
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return n;
-}
-
 bool shape_ok(int n_requests, int n_tokens, int n_heads, int n_kv, int head_dim, int dtype) {
     return known_dtype(dtype) && n_requests >= 0 && n_tokens >= 0 && n_heads >= 1 && n_heads <= 65535 && n_kv >= 1 &&
            n_heads % n_kv == 0 && head_dim >= 8 && head_dim <= 128 && head_dim % 8 == 0;
