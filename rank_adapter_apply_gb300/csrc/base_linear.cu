@@ -61,29 +61,34 @@ __global__ void __launch_bounds__(256) linear_rows_kernel(LinearArgs a) {
     }
 }
 
+constexpr int kMaxCluster = 8;
+
 // ---- bf16: tensor-core tiles --------------------------------------------------------
 //
-// A CTA takes R rows of W and, as one of the CK CTAs of a cluster, a slice of
-// the columns, in chunks of KC columns staged by asynchronous copies. Its eight
-// warps are WR groups of 16 * MT rows times WK groups of the chunk's columns. A
-// product mma(W 16 x 16, x^T 16 x 8) has the rows of W as its rows and eight
-// tokens as its columns. The 4-bit values become bf16 integers in registers:
-// 0x4300 | n is 128 + n, and subtracting 128 + z leaves n - z exactly. So the
-// products within a group are exact in fp32, and the group's fp32 sum is scaled
-// once. A column order within eight columns that suits the unpacking (0 4, 1 5, 2
-// 6, 3 7: nibbles 16 bits apart) is used for W and x alike. At the end the warps'
-// and the cluster's parts are added in a fixed order through (distributed) shared
-// memory: no workspace, no atomics.
-template <int NT_, int MT_, int WR_, int KC_, int kStages_, int kCtas_>
+// A CTA takes 128 rows of W, 16 to a warp, and, as one of the CTAs of a cluster, a
+// range of the columns. Each warp streams its rows' 4-bit words from global memory
+// into registers, kAhead blocks of 128 columns ahead, and meets nobody on the way;
+// x of a slice of KS columns lies in shared memory for all eight warps. A product
+// mma(W 16 x 16, x^T 16 x 8) has the rows of W as its rows and eight tokens as its
+// columns. The 4-bit values become bf16 integers in registers: 0x4300 | n is 128 +
+// n, and subtracting 128 + z leaves n - z exactly. So the products within a group
+// are exact in fp32, and the group's fp32 sum is scaled once. At the end the
+// cluster's parts are added in a fixed order through distributed shared memory: no
+// workspace, no atomics.
+//
+// Order of the columns. A block of 128 columns is four units of two products. Lane
+// t of a quad loads 16 bytes of a row, columns 32 t .. 32 t + 31. With groups of 128
+// its word u is its part of unit u. With groups of 64 or 32 a unit has to stay
+// within a group, so the quad first exchanges words (exchange()). Within a word the
+// halves of a register are nibbles 16 bits apart: 0 4 | 1 5 | 2 6 | 3 7. x is put
+// into the same order when it is staged (x_place() and the byte permutes).
+template <int NT_, int KS_, int kAhead_, int kCtas_>
 struct LinearTile {
-    static constexpr int NT = NT_, MT = MT_, WR = WR_, KC = KC_, kStages = kStages_, kCtas = kCtas_;
-    static constexpr int WK = 8 / WR, R = WR * 16 * MT, T = 8 * NT, KW = KC / WK;
-    static constexpr int kWRow = KC / 2, kXRow = KC * 2;            // bytes of a staged row
-    static constexpr int kWStage = R * kWRow, kStage = kWStage + T * kXRow;
+    static constexpr int NT = NT_, KS = KS_, kAhead = kAhead_, kCtas = kCtas_;
+    static constexpr int R = 128, T = 8 * NT, kXRow = KS * 2;       // rows, tokens, bytes of a staged row of x
     static constexpr int kRedRow = R + 1;                           // floats of a token's row of the parts
-    static constexpr int kRed = WK * T * kRedRow * 4;
-    static constexpr int kSmem = kStages * kStage > kRed ? kStages * kStage : kRed;
-    static_assert(KW % 128 == 0 && kWRow % 128 == 0, "a warp's columns come in blocks of 128");
+    static constexpr int kSmem = T * kXRow > T * kRedRow * 4 ? T * kXRow : T * kRedRow * 4;
+    static_assert(KS % (128 * kAhead) == 0, "a slice is whole rounds of the register ring");
 };
 
 __device__ __forceinline__ uint32_t nibbles(uint32_t w, uint32_t zz) {
@@ -93,220 +98,236 @@ __device__ __forceinline__ uint32_t nibbles(uint32_t w, uint32_t zz) {
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
-template <class C, int GU>   // GU: groups are GU * 32 columns
+// The first product of a group: D = A * B.
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// W is read once: 16 bytes past the L1.
+__device__ __forceinline__ uint4 load_w(const uint8_t *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
+// Words of a quad's 16 bytes each into units: w[u] becomes this lane's word of unit u.
+template <int GU>
+__device__ __forceinline__ void exchange(uint32_t (&w)[4], int t4) {
+    if constexpr (GU <= 2) {
+        // lanes t and t ^ 2: the lower keeps its words 0, 1 and gives 2, 3
+        const bool up = t4 & 2;
+        const uint32_t a = __shfl_xor_sync(0xffffffffu, up ? w[0] : w[2], 2);
+        const uint32_t b = __shfl_xor_sync(0xffffffffu, up ? w[1] : w[3], 2);
+        if (up)
+            w[0] = a, w[1] = b;
+        else
+            w[2] = a, w[3] = b;
+    }
+    if constexpr (GU == 1) {
+        // now w[0..1] are of pieces 0, 1 and w[2..3] of pieces 2, 3: lanes t and t ^ 1
+        const bool up = t4 & 1;
+        const uint32_t a = __shfl_xor_sync(0xffffffffu, up ? w[0] : w[1], 1);
+        const uint32_t b = __shfl_xor_sync(0xffffffffu, up ? w[2] : w[3], 1);
+        if (up)
+            w[0] = a, w[2] = b;
+        else
+            w[1] = a, w[3] = b;
+    }
+}
+
+// Where eight columns of x (piece q of a block's 16) go: 4 * unit + lane of the quad.
+template <int GU>
+__device__ __forceinline__ int x_place(int q) {
+    if constexpr (GU == 4) return (q & 3) * 4 + (q >> 2);
+    // lane t has, of each half block, words 2 (t >> 1) and the next of piece t & 1
+    if constexpr (GU == 2) return ((q >> 3) * 2 + (q & 1)) * 4 + (q >> 2 & 1) + (q >> 1 & 1) * 2;
+    return q;                                                       // a full transpose: unit u is piece u
+}
+
+template <class C, int GU, bool kZeros>   // GU: groups are GU * 32 columns
 __global__ void __launch_bounds__(256, C::kCtas) linear_tiles_kernel(LinearArgs a, int cluster, int x_vec) {
     extern __shared__ __align__(128) unsigned char smem[];
+    constexpr int kGroups = 4 / GU, kSliceBlocks = C::KS / 128, kAhead = C::kAhead;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t4 = lane & 3;
-    const int wr = warp % C::WR, wk = warp / C::WR;
     const int rank = blockIdx.x % cluster, row0 = blockIdx.x / cluster * C::R, tok0 = blockIdx.y * C::T;
     const int nt = min(C::T, a.n_tokens - tok0);
-    const int groups = a.d_in / a.group, chunks = (a.d_in + C::KC - 1) / C::KC;
-    const int c_lo = (int)((long long)chunks * rank / cluster), c_hi = (int)((long long)chunks * (rank + 1) / cluster);
+    const int groups = a.d_in / (GU * 32), blocks = (a.d_in + 127) / 128;
+    const int b_lo = (int)((long long)blocks * rank / cluster), b_hi = (int)((long long)blocks * (rank + 1) / cluster);
     const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.x) + (size_t)tok0 * a.x_stride;
-    const __nv_bfloat16 *scales = static_cast<const __nv_bfloat16 *>(a.scales);
 
-    // rows of x past the tokens are zero in every stage and never copied to
-    for (int i = tid; i < C::kStages * (C::T - nt) * (C::kXRow / 16); i += 256) {
-        const int st = i / ((C::T - nt) * (C::kXRow / 16)), at = i % ((C::T - nt) * (C::kXRow / 16));
-        *reinterpret_cast<uint4 *>(smem + st * C::kStage + C::kWStage + nt * C::kXRow + at * 16) = make_uint4(0, 0, 0, 0);
-    }
-    auto issue = [&](int chunk, int st) {
-        unsigned char *base = smem + st * C::kStage;
-        const int k0 = chunk * C::KC;
-        constexpr int kWPieces = C::kWRow / 16, kXPieces = C::kXRow / 16;
+    // ---- this lane's rows: words, scales and zeros of a block. A row past d_out reads the last row (nobody stores
+    // what comes of it), and columns past d_in meet an x of zero.
+    const int r_in = warp * 16 + g4;                                // and r_in + 8
+    const uint8_t *wsrc[2];
+    const uint16_t *ssrc[2];
+    const uint8_t *zsrc[2];
 #pragma unroll
-        for (int i = 0; i < C::R * kWPieces / 256; ++i) {
-            const int n = tid + i * 256, r = n / kWPieces, p = n % kWPieces;
-            const bool ok = row0 + r < a.d_out && k0 + p * 32 < a.d_in;
-            const uint8_t *src = a.qweight + (ok ? (size_t)(row0 + r) * (a.d_in / 2) + k0 / 2 + p * 16 : 0);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             smem_u32(base + r * C::kWRow + ((p ^ (r & 7)) << 4))),
-                         "l"(src), "r"(ok ? 16 : 0)
-                         : "memory");
-        }
-        for (int n = tid; n < nt * kXPieces; n += 256) {
-            const int t = n / kXPieces, p = n % kXPieces;
-            unsigned char *dst = base + C::kWStage + t * C::kXRow + ((p ^ ((t & 1) << 2)) << 4);
-            const bool ok = k0 + p * 8 < a.d_in;                    // d_in is a multiple of 32
-            const __nv_bfloat16 *src = x + (ok ? (size_t)t * a.x_stride + k0 + p * 8 : 0);
-            if (x_vec) {
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
-                             "r"(ok ? 16 : 0)
-                             : "memory");
-            } else {
-                *reinterpret_cast<uint4 *>(dst) = ok ? load8_bf16(reinterpret_cast<const uint16_t *>(src), 0, 8, true, 0)
-                                                     : make_uint4(0, 0, 0, 0);
-            }
+    for (int h = 0; h < 2; ++h) {
+        const size_t row = min(row0 + r_in + h * 8, a.d_out - 1);
+        wsrc[h] = a.qweight + row * (a.d_in / 2) + (size_t)b_lo * 64 + t4 * 16;
+        ssrc[h] = static_cast<const uint16_t *>(a.scales) + row * groups + b_lo * kGroups + t4 % kGroups;
+        zsrc[h] = kZeros ? a.zeros + row * groups + b_lo * kGroups + t4 % kGroups : nullptr;
+    }
+    uint4 w[kAhead][2];
+    uint32_t sc[kAhead][2], zr[kAhead][2];
+    // block i of the round whose first block is b (the pointers are at b)
+    auto fetch = [&](int i, int b, int slot) {
+        if (b + i >= b_hi) return;
+        const bool in = GU == 4 || (b + i) * 128 + t4 * 32 < a.d_in;
+        const bool gin = GU == 4 || (b + i) * kGroups + t4 % kGroups < groups;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            w[slot][h] = in ? load_w(wsrc[h] + i * 64) : make_uint4(0, 0, 0, 0);
+            sc[slot][h] = gin ? __ldg(ssrc[h] + i * kGroups) : 0;
+            if (kZeros) zr[slot][h] = gin ? __ldg(zsrc[h] + i * kGroups) : 0;
         }
     };
-    // Scales and zeros of one block of 128 columns: lane t4 of a quad has the block's group t4 / GU..., of both rows
-    struct Groups {
-        float s[C::MT][2];
-        uint32_t z[C::MT][2];
-    };
-    auto read_groups = [&](int chunk, int block) {
-        Groups g;
-        const int k = chunk * C::KC + wk * C::KW + block * 128 + t4 / GU * GU * 32, gi = k / (GU * 32);
 #pragma unroll
-        for (int mt = 0; mt < C::MT; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = row0 + (wr * C::MT + mt) * 16 + g4 + h * 8;
-                const bool ok = row < a.d_out && chunk < c_hi && gi < groups;
-                const size_t at = ok ? (size_t)row * groups + gi : 0;
-                g.s[mt][h] = ok ? __bfloat162float(scales[at]) : 0.f;
-                // 128 + z as a bf16 pair: exact up to 256
-                const uint32_t z = a.zeros && ok ? min((int)a.zeros[at], 128) : 8;
-                const uint32_t b = __float_as_uint(128.f + (float)z) >> 16;
-                g.z[mt][h] = b | b << 16;
-            }
-        return g;
-    };
+    for (int i = 0; i < kAhead; ++i) fetch(i, b_lo, i);
 
-    float acc[C::MT][C::NT][4];
+    float acc[C::NT][4];
 #pragma unroll
-    for (int mt = 0; mt < C::MT; ++mt)
-#pragma unroll
-        for (int n = 0; n < C::NT; ++n) acc[mt][n][0] = acc[mt][n][1] = acc[mt][n][2] = acc[mt][n][3] = 0.f;
+    for (int n = 0; n < C::NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 
-    for (int s = 0; s < C::kStages - 1; ++s) {
-        if (c_lo + s < c_hi) issue(c_lo + s, s);
-        cp_async_commit();
-    }
-    constexpr int kBlocks = C::KW / 128;
-    Groups now = read_groups(c_lo, 0);
-    for (int c = c_lo, st = 0; c < c_hi; ++c, st = st + 1 == C::kStages ? 0 : st + 1) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
-        // this thread's pieces of x into the order of the unpacked weights: 0 4 | 1 5 | 2 6 | 3 7
-        for (int n = tid; n < nt * (C::kXRow / 16); n += 256) {
-            uint4 *v = reinterpret_cast<uint4 *>(smem + st * C::kStage + C::kWStage + n * 16);
-            const uint4 o = *v;
-            *v = make_uint4(__byte_perm(o.x, o.z, 0x5410), __byte_perm(o.x, o.z, 0x7632), __byte_perm(o.y, o.w, 0x5410),
-                            __byte_perm(o.y, o.w, 0x7632));
+    for (int s_lo = b_lo; s_lo < b_hi; s_lo += kSliceBlocks) {
+        // ---- x of the slice: rows past the tokens and columns past d_in are zero
+        const int n_blocks = min(kSliceBlocks, b_hi - s_lo);
+        if (s_lo != b_lo) __syncthreads();
+        for (int i = tid; i < C::T * n_blocks * 16; i += 256) {
+            const int t = i / (n_blocks * 16), p = i % (n_blocks * 16), k = s_lo * 128 + p * 8;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (t < nt && k < a.d_in)
+                v = load8_bf16(reinterpret_cast<const uint16_t *>(x + (size_t)t * a.x_stride + k), 0, 8, true, x_vec);
+            const int place = (p & ~15) + x_place<GU>(p & 15);
+            *reinterpret_cast<uint4 *>(smem + t * C::kXRow + ((place ^ ((t & 1) << 2)) << 4)) =
+                make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                           __byte_perm(v.y, v.w, 0x7632));
         }
         __syncthreads();
-        if (c + C::kStages - 1 < c_hi) issue(c + C::kStages - 1, st == 0 ? C::kStages - 1 : st - 1);
-        cp_async_commit();
-        const unsigned char *wbase = smem + st * C::kStage, *xbase = wbase + C::kWStage;
+        // lane t4's piece of unit u: place 4 u + t4, odd tokens with the halves of eight places swapped
+        const unsigned char *xbase = smem + g4 * C::kXRow + ((t4 ^ ((g4 & 1) << 2)) << 4);
+        const int x_odd = (g4 & 1) ? -64 : 64;
+        for (int r0 = 0; r0 < n_blocks; r0 += kAhead, xbase += kAhead * 256) {
 #pragma unroll
-        for (int blk = 0; blk < kBlocks; ++blk) {
-            const Groups next = blk + 1 < kBlocks ? read_groups(c, blk + 1) : read_groups(c + 1, 0);
-            float part[C::MT][C::NT][4];
+            for (int i = 0; i < kAhead; ++i) {
+                if (r0 + i >= n_blocks) break;
+                uint32_t wd[2][4], z[2];
+                float sf[2];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {                           // units of 32 columns
-                if (u % GU == 0) {
-#pragma unroll
-                    for (int mt = 0; mt < C::MT; ++mt)
-#pragma unroll
-                        for (int n = 0; n < C::NT; ++n)
-                            part[mt][n][0] = part[mt][n][1] = part[mt][n][2] = part[mt][n][3] = 0.f;
-                }
-                const int piece = (wk * C::KW + blk * 128) / 32 + u;
-                uint32_t w[C::MT][2], zz[C::MT][2];
-#pragma unroll
-                for (int mt = 0; mt < C::MT; ++mt)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int r = (wr * C::MT + mt) * 16 + g4 + h * 8;
-                        w[mt][h] = *reinterpret_cast<const uint32_t *>(wbase + r * C::kWRow + ((piece ^ (r & 7)) << 4) + t4 * 4);
-                        zz[mt][h] = __shfl_sync(0xffffffffu, now.z[mt][h], u, 4);
+                for (int h = 0; h < 2; ++h) {
+                    wd[h][0] = w[i][h].x, wd[h][1] = w[i][h].y, wd[h][2] = w[i][h].z, wd[h][3] = w[i][h].w;
+                    exchange<GU>(wd[h], t4);
+                    sf[h] = __uint_as_float(sc[i][h] << 16);
+                    z[h] = 0x43084308u;                             // 128 + 8, twice
+                    if (kZeros) {                                   // 128 + z, twice: exact in bf16 up to 256
+                        const uint32_t zb = __float_as_uint(128.f + (float)min(zr[i][h], 128u)) >> 16;
+                        z[h] = zb | zb << 16;
                     }
-                uint32_t f[C::MT][2][4];
+                }
+                fetch(i + kAhead, s_lo + r0, i);
+                float part[C::NT][4];
 #pragma unroll
-                for (int mt = 0; mt < C::MT; ++mt)
+                for (int u = 0; u < 4; ++u) {
+                    uint32_t f[2][4];
+                    const uint32_t z0 = kZeros && kGroups > 1 ? __shfl_sync(0xffffffffu, z[0], u / GU, 4) : z[0];
+                    const uint32_t z1 = kZeros && kGroups > 1 ? __shfl_sync(0xffffffffu, z[1], u / GU, 4) : z[1];
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        f[mt][half][0] = nibbles(w[mt][0] >> (8 * half), zz[mt][0]);
-                        f[mt][half][1] = nibbles(w[mt][1] >> (8 * half), zz[mt][1]);
-                        f[mt][half][2] = nibbles(w[mt][0] >> (8 * half + 4), zz[mt][0]);
-                        f[mt][half][3] = nibbles(w[mt][1] >> (8 * half + 4), zz[mt][1]);
+                        f[half][0] = nibbles(wd[0][u] >> (8 * half), z0);
+                        f[half][1] = nibbles(wd[1][u] >> (8 * half), z1);
+                        f[half][2] = nibbles(wd[0][u] >> (8 * half + 4), z0);
+                        f[half][3] = nibbles(wd[1][u] >> (8 * half + 4), z1);
                     }
 #pragma unroll
-                for (int n = 0; n < C::NT; ++n) {
-                    const int t = n * 8 + g4;
-                    const uint4 b = *reinterpret_cast<const uint4 *>(xbase + t * C::kXRow +
-                                                                     (((piece * 4 + t4) ^ ((t & 1) << 2)) << 4));
-#pragma unroll
-                    for (int mt = 0; mt < C::MT; ++mt) {
-                        mma_bf16(part[mt][n], f[mt][0][0], f[mt][0][1], f[mt][0][2], f[mt][0][3], b.x, b.y);
-                        mma_bf16(part[mt][n], f[mt][1][0], f[mt][1][1], f[mt][1][2], f[mt][1][3], b.z, b.w);
+                    for (int n = 0; n < C::NT; ++n) {
+                        const uint4 b = *reinterpret_cast<const uint4 *>(
+                            xbase + n * 8 * C::kXRow + i * 256 + (u >> 1) * 128 + (u & 1) * x_odd);
+                        if (u % GU == 0)
+                            mma_bf16_first(part[n], f[0], b.x, b.y);
+                        else
+                            mma_bf16(part[n], f[0][0], f[0][1], f[0][2], f[0][3], b.x, b.y);
+                        mma_bf16(part[n], f[1][0], f[1][1], f[1][2], f[1][3], b.z, b.w);
                     }
-                }
-                if (u % GU == GU - 1) {
-#pragma unroll
-                    for (int mt = 0; mt < C::MT; ++mt) {
-                        const float s0 = __shfl_sync(0xffffffffu, now.s[mt][0], u, 4);
-                        const float s1 = __shfl_sync(0xffffffffu, now.s[mt][1], u, 4);
+                    if (u % GU == GU - 1) {
+                        const float s0 = kGroups > 1 ? __shfl_sync(0xffffffffu, sf[0], u / GU, 4) : sf[0];
+                        const float s1 = kGroups > 1 ? __shfl_sync(0xffffffffu, sf[1], u / GU, 4) : sf[1];
 #pragma unroll
                         for (int n = 0; n < C::NT; ++n) {
-                            acc[mt][n][0] = fmaf(s0, part[mt][n][0], acc[mt][n][0]);
-                            acc[mt][n][1] = fmaf(s0, part[mt][n][1], acc[mt][n][1]);
-                            acc[mt][n][2] = fmaf(s1, part[mt][n][2], acc[mt][n][2]);
-                            acc[mt][n][3] = fmaf(s1, part[mt][n][3], acc[mt][n][3]);
+                            acc[n][0] = fmaf(s0, part[n][0], acc[n][0]);
+                            acc[n][1] = fmaf(s0, part[n][1], acc[n][1]);
+                            acc[n][2] = fmaf(s1, part[n][2], acc[n][2]);
+                            acc[n][3] = fmaf(s1, part[n][3], acc[n][3]);
                         }
                     }
                 }
             }
-            now = next;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                wsrc[h] += kAhead * 64;
+                ssrc[h] += kAhead * kGroups;
+                if (kZeros) zsrc[h] += kAhead * kGroups;
+            }
         }
     }
-    // ---- parts of the warps and the cluster, added in a fixed order
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // ---- the cluster's parts, added in a fixed order
     __syncthreads();
-    float *red = reinterpret_cast<float *>(smem);                   // [WK][T][kRedRow]
+    float *red = reinterpret_cast<float *>(smem);                   // [T][kRedRow]
 #pragma unroll
-    for (int mt = 0; mt < C::MT; ++mt)
+    for (int n = 0; n < C::NT; ++n)
 #pragma unroll
-        for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = (wr * C::MT + mt) * 16 + g4 + (e >> 1) * 8, t = n * 8 + t4 * 2 + (e & 1);
-                red[(wk * C::T + t) * C::kRedRow + r] = acc[mt][n][e];
-            }
+        for (int e = 0; e < 4; ++e)
+            red[(n * 8 + t4 * 2 + (e & 1)) * C::kRedRow + r_in + (e >> 1) * 8] = acc[n][e];
     if (cluster > 1)
         cluster_sync_all();
     else
         __syncthreads();
-    const int slice = C::R / cluster, r_lo = rank * slice;
+    const int r_lo = C::R * rank / cluster, slice = C::R * (rank + 1) / cluster - r_lo;
     const uint32_t red_at = smem_u32(red);
     for (int i = tid; i < nt * slice; i += 256) {
-        const int t = i / slice, r = r_lo + i % slice;
+        const int t = i / slice, r = r_lo + i % slice, at = t * C::kRedRow + r;
         if (row0 + r >= a.d_out) continue;
-        float sum = 0.f;
-        for (int p = 0; p < cluster; ++p) {
-            const uint32_t peer = cluster > 1 ? map_peer(red_at, p) : red_at;
+        float sum = red[at];
+        if (cluster > 1) {
+            float v[kMaxCluster];
 #pragma unroll
-            for (int k = 0; k < C::WK; ++k) {
-                const uint32_t at = peer + ((k * C::T + t) * C::kRedRow + r) * 4;
-                float v;
-                if (cluster > 1)
-                    v = __uint_as_float(ld_peer_u32(at));
-                else
-                    v = red[(k * C::T + t) * C::kRedRow + r];
-                sum += v;
-            }
+            for (int p = 0; p < kMaxCluster; ++p)
+                v[p] = p < cluster ? __uint_as_float(ld_peer_u32(map_peer(red_at, p) + at * 4)) : 0.f;
+            sum = v[0];
+#pragma unroll
+            for (int p = 1; p < kMaxCluster; ++p) sum += v[p];
         }
         static_cast<__nv_bfloat16 *>(a.y)[(size_t)(tok0 + t) * a.y_stride + row0 + r] = __float2bfloat16_rn(sum);
     }
     if (cluster > 1) cluster_sync_all();                            // the peers have read this CTA's parts
 }
 
-template <class C, int GU>
+template <class C, int GU, bool kZeros>
 cudaError_t launch_tiles(const LinearArgs &a, int sms, cudaStream_t st) {
-    auto kernel = linear_tiles_kernel<C, GU>;
+    auto kernel = linear_tiles_kernel<C, GU, kZeros>;
     static std::atomic<uint64_t> ready{0};
     if (!device_bit(ready)) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (e != cudaSuccess) return e;
         set_device_bit(ready);
     }
-    const int row_blocks = (a.d_out + C::R - 1) / C::R, tok_blocks = (a.n_tokens + C::T - 1) / C::T;
-    const int chunks = (a.d_in + C::KC - 1) / C::KC;
+    const int tiles = (a.d_out + C::R - 1) / C::R * ((a.n_tokens + C::T - 1) / C::T);
+    const int blocks = (a.d_in + 127) / 128;
+    // CTAs of a cluster: the least work on the fullest SM, ceil(tiles * c / sms) / c; on a tie the larger c, whose
+    // CTAs have more loads in flight, as long as a range has kAhead blocks
     int cluster = 1;
-    while (cluster < 8 && 2 * cluster <= chunks && (long long)row_blocks * tok_blocks * cluster < sms) cluster *= 2;
+    double least = 1e30;
+    for (int c = 1; c <= kMaxCluster && (c == 1 || blocks / c >= C::kAhead); ++c) {
+        const double full = (double)(((long long)tiles * c + sms - 1) / sms) / c;
+        if (full <= least && (c == 1 || (long long)tiles * c <= (long long)C::kCtas * sms)) least = full, cluster = c;
+    }
     const int x_vec = aligned16(a.x) && a.x_stride % 8 == 0;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(row_blocks * cluster, tok_blocks);
+    cfg.gridDim = dim3((a.d_out + C::R - 1) / C::R * cluster, (a.n_tokens + C::T - 1) / C::T);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
@@ -320,22 +341,26 @@ cudaError_t launch_tiles(const LinearArgs &a, int sms, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kernel, a, cluster, x_vec);
 }
 
+template <class C, int GU>
+cudaError_t launch_zeros(const LinearArgs &a, int sms, cudaStream_t st) {
+    return a.zeros ? launch_tiles<C, GU, true>(a, sms, st) : launch_tiles<C, GU, false>(a, sms, st);
+}
+
 template <class C>
 cudaError_t launch_group(const LinearArgs &a, int sms, cudaStream_t st) {
     switch (a.group) {
-        case 32: return launch_tiles<C, 1>(a, sms, st);
-        case 64: return launch_tiles<C, 2>(a, sms, st);
-        default: return launch_tiles<C, 4>(a, sms, st);
+        case 32: return launch_zeros<C, 1>(a, sms, st);
+        case 64: return launch_zeros<C, 2>(a, sms, st);
+        default: return launch_zeros<C, 4>(a, sms, st);
     }
 }
 
-// Tokens of a CTA's tile and, with them, its rows: the more tokens, the more
-// rows share their copy of x.
+// The tokens' tile.
 cudaError_t launch_bf16(const LinearArgs &a, int sms, cudaStream_t st) {
-    if (a.n_tokens <= 8) return launch_group<LinearTile<1, 1, 2, 512, 4, 3>>(a, sms, st);
-    if (a.n_tokens <= 16) return launch_group<LinearTile<2, 1, 4, 512, 3, 2>>(a, sms, st);
-    if (a.n_tokens <= 32) return launch_group<LinearTile<4, 1, 8, 256, 3, 2>>(a, sms, st);
-    return launch_group<LinearTile<8, 1, 8, 256, 2, 2>>(a, sms, st);
+    if (a.n_tokens <= 8) return launch_group<LinearTile<1, 2048, 4, 2>>(a, sms, st);
+    if (a.n_tokens <= 16) return launch_group<LinearTile<2, 2048, 4, 2>>(a, sms, st);
+    if (a.n_tokens <= 32) return launch_group<LinearTile<4, 1024, 4, 2>>(a, sms, st);
+    return launch_group<LinearTile<8, 512, 2, 2>>(a, sms, st);
 }
 
 template <typename T>
