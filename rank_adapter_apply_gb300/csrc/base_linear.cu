@@ -198,15 +198,29 @@ __global__ void __launch_bounds__(256, C::kCtas) linear_tiles_kernel(LinearArgs 
         // ---- x of the slice: rows past the tokens and columns past d_in are zero
         const int n_blocks = min(kSliceBlocks, b_hi - s_lo);
         if (s_lo != b_lo) __syncthreads();
-        for (int i = tid; i < C::T * n_blocks * 16; i += 256) {
-            const int t = i / (n_blocks * 16), p = i % (n_blocks * 16), k = s_lo * 128 + p * 8;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (t < nt && k < a.d_in)
-                v = load8_bf16(reinterpret_cast<const uint16_t *>(x + (size_t)t * a.x_stride + k), 0, 8, true, x_vec);
-            const int place = (p & ~15) + x_place<GU>(p & 15);
-            *reinterpret_cast<uint4 *>(smem + t * C::kXRow + ((place ^ ((t & 1) << 2)) << 4)) =
-                make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                           __byte_perm(v.y, v.w, 0x7632));
+        // A warp takes a block's 16 pieces of two tokens at a time: piece and place of a lane are always the same.
+        constexpr int kBatch = C::NT == 1 ? 4 : 8;                  // pieces of a thread whose loads are in flight
+        const int q = lane & 15, odd = lane >> 4;                   // odd token of the pair
+        unsigned char *dst = smem + odd * C::kXRow + ((x_place<GU>(q) ^ (odd << 2)) << 4);
+        const int pairs = s_lo == b_lo ? C::T / 2 : (nt + 1) / 2;   // rows past the tokens are cleared once
+        for (int i0 = warp; i0 < pairs * kSliceBlocks; i0 += 8 * kBatch) {
+            uint4 v[kBatch];
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+                const int i = i0 + e * 8, t = i / kSliceBlocks * 2 + odd, blk = i % kSliceBlocks;
+                const int k = (s_lo + blk) * 128 + q * 8;
+                v[e] = make_uint4(0, 0, 0, 0);
+                if (t < nt && blk < n_blocks && k < a.d_in)
+                    v[e] = load8_bf16(reinterpret_cast<const uint16_t *>(x + (size_t)t * a.x_stride + k), 0, 8, true, x_vec);
+            }
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+                const int i = i0 + e * 8, t2 = i / kSliceBlocks * 2, blk = i % kSliceBlocks;
+                if (t2 >= C::T) break;
+                *reinterpret_cast<uint4 *>(dst + t2 * C::kXRow + blk * 256) =
+                    make_uint4(__byte_perm(v[e].x, v[e].z, 0x5410), __byte_perm(v[e].x, v[e].z, 0x7632),
+                               __byte_perm(v[e].y, v[e].w, 0x5410), __byte_perm(v[e].y, v[e].w, 0x7632));
+            }
         }
         __syncthreads();
         // lane t4's piece of unit u: place 4 u + t4, odd tokens with the halves of eight places swapped
