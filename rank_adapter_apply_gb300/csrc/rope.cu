@@ -69,55 +69,202 @@ struct RopeArgs {
     int n_positions, page_size, n_tokens, n_heads, n_kv, head_dim, rot_dim, inverse;
 };
 
-// One warp per head row of one token; a lane takes pairs one by one.
+// Where head row r of token t (q heads, then k, then v) is read and written.
+template <typename T>
+struct Row {
+    const T *src;
+    T *dst;          // nullptr: the row is not written
+    bool turned;
+};
+
+template <typename T>
+__device__ __forceinline__ Row<T> row_of(const RopeArgs &a, long long t, int r, long long cache_at) {
+    Row<T> w{};
+    if (r < a.n_heads) {
+        w.src = static_cast<const T *>(a.q) + t * a.q_token + r * a.q_head;
+        w.dst = static_cast<T *>(a.q_out) + t * a.qo_token + r * a.qo_head;
+        w.turned = true;
+        return w;
+    }
+    r -= a.n_heads;
+    w.turned = r < a.n_kv;
+    const int h = w.turned ? r : r - a.n_kv;
+    w.src = w.turned ? static_cast<const T *>(a.k) + t * a.k_token + h * a.k_head
+                     : static_cast<const T *>(a.v) + t * a.v_token + h * a.v_head;
+    if (cache_at >= 0) w.dst = static_cast<T *>(w.turned ? a.k_cache : a.v_cache) + cache_at + h * a.c_head;
+    return w;
+}
+
+// Element offset of the token's place in the caches, -1: it has none.
+__device__ __forceinline__ long long cache_place(const RopeArgs &a, long long t) {
+    if (a.n_kv == 0) return -1;
+    const long long slot = a.slots[t];
+    if (slot < 0 || slot >= a.n_slots) return -1;
+    if ((slot >> 31) == 0) {                               // 32-bit division where it will do
+        const uint32_t page = (uint32_t)slot / (uint32_t)a.page_size;
+        return page * a.c_page + ((uint32_t)slot - page * (uint32_t)a.page_size) * a.c_slot;
+    }
+    return slot / a.page_size * a.c_page + slot % a.page_size * a.c_slot;
+}
+
+// Any layout: one warp per head row of one token, a lane takes pairs one by one.
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(256) rope_rows_kernel(RopeArgs a) {
     const int lane = threadIdx.x & 31;
     const int rows = a.n_heads + 2 * a.n_kv;
     const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (item >= (long long)a.n_tokens * rows) return;
-    const int t = (int)(item / rows), r = (int)(item % rows);
+    const long long t = item / rows;
     const int pos = a.positions[t];
     if (pos < 0 || pos >= a.n_positions) return;
-    const T *src;
-    T *dst;
-    if (r < a.n_heads) {
-        src = static_cast<const T *>(a.q) + t * a.q_token + r * a.q_head;
-        dst = static_cast<T *>(a.q_out) + t * a.qo_token + r * a.qo_head;
-    } else {
-        const long long slot = a.slots[t];
-        if (slot < 0 || slot >= a.n_slots) return;
-        const bool is_v = r >= a.n_heads + a.n_kv;
-        const int h = r - a.n_heads - (is_v ? a.n_kv : 0);
-        const long long at = slot / a.page_size * a.c_page + slot % a.page_size * a.c_slot + h * a.c_head;
-        src = is_v ? static_cast<const T *>(a.v) + t * a.v_token + h * a.v_head
-                   : static_cast<const T *>(a.k) + t * a.k_token + h * a.k_head;
-        dst = static_cast<T *>(is_v ? a.v_cache : a.k_cache) + at;
-        if (is_v) {
-            for (int i = lane; i < a.head_dim; i += 32) dst[i] = src[i];
-            return;
-        }
-    }
+    const Row<T> w = row_of<T>(a, t, (int)(item % rows), cache_place(a, t));
+    if (!w.dst) return;
     const int half = a.rot_dim / 2;
     const float *row = a.table + (size_t)pos * a.rot_dim;
-    for (int j = lane; j < half; j += 32) {
-        const float c = row[j], s = a.inverse ? -row[half + j] : row[half + j];
-        const int i0 = kInterleaved ? 2 * j : j, i1 = kInterleaved ? 2 * j + 1 : j + half;
-        const float x0 = to_f32(src[i0]), x1 = to_f32(src[i1]);
-        dst[i0] = from_f32<T>(x0 * c - x1 * s);
-        dst[i1] = from_f32<T>(x0 * s + x1 * c);
+    if (w.turned) {
+        for (int j = lane; j < half; j += 32) {
+            const float c = row[j], s = a.inverse ? -row[half + j] : row[half + j];
+            const int i0 = kInterleaved ? 2 * j : j, i1 = kInterleaved ? 2 * j + 1 : j + half;
+            const float x0 = to_f32(w.src[i0]), x1 = to_f32(w.src[i1]);
+            w.dst[i0] = from_f32<T>(x0 * c - x1 * s);
+            w.dst[i1] = from_f32<T>(x0 * s + x1 * c);
+        }
     }
-    for (int i = a.rot_dim + lane; i < a.head_dim; i += 32) dst[i] = src[i];
+    for (int i = (w.turned ? a.rot_dim : 0) + lane; i < a.head_dim; i += 32) w.dst[i] = w.src[i];
 }
 
+// Rows in 16-byte vectors. A unit is two vectors of a row that are turned
+// together: halves: vectors u and u + rot_dim / 2 elements; interleaved: vectors 2u
+// and 2u + 1; past rot_dim (and in v): two neighbours to copy. A block has `units`
+// lanes for a row (unit = threadIdx.x) times blockDim.y rows; a thread takes its
+// unit of kRows rows of one token, whose cosines and sines it reads once, with all
+// loads in flight before the first is used.
 template <typename T>
-cudaError_t launch_rope(const RopeArgs &a, int interleaved, cudaStream_t st) {
-    const long long items = (long long)a.n_tokens * (a.n_heads + 2 * a.n_kv);
-    const unsigned grid = (unsigned)((items + 7) / 8);
-    if (interleaved)
-        rope_rows_kernel<T, true><<<grid, 256, 0, st>>>(a);
-    else
-        rope_rows_kernel<T, false><<<grid, 256, 0, st>>>(a);
+__device__ __forceinline__ void unpack(const uint4 &v, float (&f)[16 / sizeof(T)]);
+template <>
+__device__ __forceinline__ void unpack<float>(const uint4 &v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+}
+template <>
+__device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4 &v, float (&f)[8]) {
+    f[0] = bf_lo(v.x), f[1] = bf_hi(v.x), f[2] = bf_lo(v.y), f[3] = bf_hi(v.y);
+    f[4] = bf_lo(v.z), f[5] = bf_hi(v.z), f[6] = bf_lo(v.w), f[7] = bf_hi(v.w);
+}
+__device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+}
+
+template <typename T, bool kInterleaved, int kRows>
+__global__ void __launch_bounds__(512) rope_vectors_kernel(RopeArgs a) {
+    constexpr int N = 16 / sizeof(T);
+    const long long t = blockIdx.x;
+    const int u = threadIdx.x, rows = a.n_heads + 2 * a.n_kv, r0 = (blockIdx.y * blockDim.y + threadIdx.y) * kRows;
+    const int vectors = a.head_dim / N, rot_vectors = a.rot_dim / N, half = a.rot_dim / 2;
+    const int pos = a.positions[t];
+    const long long at = cache_place(a, t);
+    if (pos < 0 || pos >= a.n_positions) return;
+    // this unit's vectors in a row that is turned, and in one that is copied
+    const bool turns = kInterleaved ? 2 * u < rot_vectors : u < rot_vectors / 2;
+    const int v0 = kInterleaved || !turns ? 2 * u : u, v1 = kInterleaved || !turns ? 2 * u + 1 : u + rot_vectors / 2;
+    Row<T> w[kRows];
+    uint4 x0[kRows], x1[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        w[i].dst = nullptr;
+        if (r0 + i < rows) w[i] = row_of<T>(a, t, r0 + i, at);
+        if (!w[i].dst) continue;
+        const int e0 = w[i].turned ? v0 : 2 * u, e1 = w[i].turned ? v1 : 2 * u + 1;
+        x0[i] = *reinterpret_cast<const uint4 *>(w[i].src + e0 * N);
+        if (e1 < vectors) x1[i] = *reinterpret_cast<const uint4 *>(w[i].src + e1 * N);
+    }
+    // N angles: of elements 2u N .. (interleaved: of N pairs) or u N ..
+    float c[N], s[N];
+    if (turns) {
+        const float *row = a.table + (size_t)pos * a.rot_dim + u * N;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            c[j] = row[j];
+            s[j] = a.inverse ? -row[half + j] : row[half + j];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        if (!w[i].dst) continue;
+        int e0 = 2 * u, e1 = 2 * u + 1;
+        if (w[i].turned) {
+            e0 = v0, e1 = v1;
+            if (turns) {
+                float f0[N], f1[N], g0[N], g1[N];
+                unpack<T>(x0[i], f0);
+                unpack<T>(x1[i], f1);
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    if (kInterleaved) {                    // pairs (2j, 2j + 1) of the two vectors in a row
+                        const int p = j % (N / 2) * 2;
+                        float(&f)[N] = j < N / 2 ? f0 : f1;
+                        float(&g)[N] = j < N / 2 ? g0 : g1;
+                        g[p] = f[p] * c[j] - f[p + 1] * s[j];
+                        g[p + 1] = f[p] * s[j] + f[p + 1] * c[j];
+                    } else {
+                        g0[j] = f0[j] * c[j] - f1[j] * s[j];
+                        g1[j] = f0[j] * s[j] + f1[j] * c[j];
+                    }
+                }
+                x0[i] = pack(g0);
+                x1[i] = pack(g1);
+            }
+        }
+        *reinterpret_cast<uint4 *>(w[i].dst + e0 * N) = x0[i];
+        if (e1 < vectors) *reinterpret_cast<uint4 *>(w[i].dst + e1 * N) = x1[i];
+    }
+}
+
+// Whether every row is whole 16-byte vectors at 16-byte addresses and the pairs
+// fall into units.
+template <typename T>
+bool by_vectors(const RopeArgs &a, bool interleaved) {
+    constexpr int N = 16 / sizeof(T);
+    bool ok = a.head_dim % N == 0 && a.rot_dim % (interleaved ? N : 2 * N) == 0 && (a.head_dim / N + 1) / 2 <= 128;
+    // an interleaved unit may not be half turned and half copied
+    ok = ok && (a.rot_dim / N % 2 == 0);
+    const long long q[] = {a.q_token, a.q_head, a.qo_token, a.qo_head};
+    const long long kv[] = {a.k_token, a.k_head, a.v_token, a.v_head, a.c_page, a.c_slot, a.c_head};
+    if (a.n_heads > 0) {
+        ok = ok && aligned16(a.q) && aligned16(a.q_out);
+        for (long long s : q) ok = ok && s % N == 0;
+    }
+    if (a.n_kv > 0) {
+        ok = ok && aligned16(a.k) && aligned16(a.v) && aligned16(a.k_cache) && aligned16(a.v_cache);
+        for (long long s : kv) ok = ok && s % N == 0;
+    }
+    return ok;
+}
+
+template <typename T, bool kInterleaved, int kRows>
+void launch_vectors(const RopeArgs &a, cudaStream_t st) {
+    constexpr int N = 16 / sizeof(T);
+    const int rows = a.n_heads + 2 * a.n_kv, units = (a.head_dim / N + 1) / 2;
+    const int need = (rows + kRows - 1) / kRows;             // rows of threads
+    const int fit = 256 / units > 0 ? 256 / units : 1;
+    const int blocks = (need + fit - 1) / fit, each = (need + blocks - 1) / blocks;
+    rope_vectors_kernel<T, kInterleaved, kRows><<<dim3(a.n_tokens, blocks), dim3(units, each), 0, st>>>(a);
+}
+
+template <typename T, bool kInterleaved>
+cudaError_t launch_rope(const RopeArgs &a, int sms, cudaStream_t st) {
+    const long long rows = (long long)a.n_tokens * (a.n_heads + 2 * a.n_kv);
+    if (by_vectors<T>(a, kInterleaved)) {
+        // rows of a thread: one where few rows leave SMs idle anyway
+        if (rows <= 64ll * sms)
+            launch_vectors<T, kInterleaved, 1>(a, st);
+        else
+            launch_vectors<T, kInterleaved, 4>(a, st);
+    } else {
+        rope_rows_kernel<T, kInterleaved><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a);
+    }
     return cudaGetLastError();
 }
 
@@ -181,7 +328,12 @@ extern "C" int lora_rope(const lora_rope_desc *d, void *stream) {
                d->n_positions, append ? d->page_size : 1, d->n_tokens, d->n_heads, d->n_kv_heads, d->head_dim,
                d->rot_dim, d->inverse};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = d->dtype == LORA_DTYPE_BF16 ? launch_rope<__nv_bfloat16>(a, d->interleaved, st)
-                                                      : launch_rope<float>(a, d->interleaved, st);
+    const int sms = sm_count();
+    if (sms < 1) return fail(LORA_ERR_CUDA, "rope: no CUDA device");
+    cudaError_t e;
+    if (d->dtype == LORA_DTYPE_BF16)
+        e = d->interleaved ? launch_rope<__nv_bfloat16, true>(a, sms, st) : launch_rope<__nv_bfloat16, false>(a, sms, st);
+    else
+        e = d->interleaved ? launch_rope<float, true>(a, sms, st) : launch_rope<float, false>(a, sms, st);
     return launched("rope", e);
 }
