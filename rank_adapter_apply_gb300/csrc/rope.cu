@@ -139,17 +139,6 @@ __global__ void __launch_bounds__(256) rope_rows_kernel(RopeArgs a) {
 // lanes for a row (unit = threadIdx.x) times blockDim.y rows; a thread takes its
 // unit of kRows rows of one token, whose cosines and sines it reads once, with all
 // loads in flight before the first is used.
-template <typename T>
-__device__ __forceinline__ void unpack(const uint4 &v, float (&f)[16 / sizeof(T)]);
-template <>
-__device__ __forceinline__ void unpack<float>(const uint4 &v, float (&f)[4]) {
-    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
-}
-template <>
-__device__ __forceinline__ void unpack<__nv_bfloat16>(const uint4 &v, float (&f)[8]) {
-    f[0] = bf_lo(v.x), f[1] = bf_hi(v.x), f[2] = bf_lo(v.y), f[3] = bf_hi(v.y);
-    f[4] = bf_lo(v.z), f[5] = bf_hi(v.z), f[6] = bf_lo(v.w), f[7] = bf_hi(v.w);
-}
 __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
