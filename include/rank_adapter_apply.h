@@ -719,6 +719,11 @@ size_t lora_tree_attention_workspace_bytes(int n_requests, int n_tokens, int n_h
 
 int lora_tree_attention(const lora_tree_attention_desc *desc, void *stream);
 
+/* *count = thread blocks of lora_tree_attention on the current device whose
+ * bounded device-side waits gave up so far; their rows are wrong (never
+ * expected). Synchronises the device. */
+int lora_step_wait_timeouts(uint64_t *count);
+
 /*
  * Verify drafted trees against the target's probabilities, from given random
  * numbers. Request b owns the nodes node_starts[b] .. node_starts[b + 1); node

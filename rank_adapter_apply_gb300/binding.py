@@ -39,7 +39,7 @@ EXPORTED = [
     "lora_selftest_wait_timeout", "lora_assign_tokens", "lora_sync_host", "lora_abort_load",
     "lora_register_host_adapters", "lora_set_warm_set", "lora_serve_step",
     "lora_base_linear", "lora_rope_table", "lora_rope", "lora_tree_attention_workspace_bytes",
-    "lora_tree_attention", "lora_verify_drafts",
+    "lora_tree_attention", "lora_step_wait_timeouts", "lora_verify_drafts",
 ]
 
 
@@ -164,6 +164,7 @@ def load(path: str = LIB_PATH):
         "lora_rope": (i32, [P(LoraRopeDesc), vp]),
         "lora_tree_attention_workspace_bytes": (sz, [i32] * 6),
         "lora_tree_attention": (i32, [P(LoraTreeAttentionDesc), vp]),
+        "lora_step_wait_timeouts": (i32, [P(u64)]),
         "lora_verify_drafts": (i32, [P(LoraVerifyDesc), vp]),
     }
     for name, (res, args) in sig.items():
@@ -480,6 +481,12 @@ def lora_tree_attention_workspace_bytes(n_requests, n_tokens, n_heads, n_kv_head
 
 def lora_tree_attention(desc, stream):
     return check(load().lora_tree_attention(desc, stream))
+
+
+def lora_step_wait_timeouts():
+    n = ctypes.c_uint64(0)
+    check(load().lora_step_wait_timeouts(ctypes.byref(n)))
+    return n.value
 
 
 def lora_verify_drafts(desc, stream):

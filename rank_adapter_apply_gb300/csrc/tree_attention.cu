@@ -1,5 +1,5 @@
 // lora_tree_attention: attention of drafted trees over a paged cache.
-#include "step_util.cuh"
+#include "tree_common.cuh"
 
 #include <algorithm>
 #include <atomic>
@@ -9,21 +9,7 @@ namespace lora {
 namespace {
 
 using namespace step;
-
-struct TreeArgs {
-    const void *q, *k_cache, *v_cache;
-    void *out;
-    float *lse;
-    const int32_t *page_table, *ctx_lens, *node_starts;
-    const uint64_t *tree_mask;
-    long long q_token, q_head, c_page, c_slot, c_head, o_token, o_head, table_stride, n_pages;
-    float scale;
-    int page_size, table_pages, mask_words, n_requests, n_tokens, n_heads, n_kv, head_dim;
-};
-
-__device__ __forceinline__ int node_start(const TreeArgs &a, int b) {
-    return min(max(a.node_starts[b], 0), a.n_tokens);
-}
+using namespace tree;
 
 // Request that owns node `t`: the last b with node_starts[b] <= t, or -1.
 __device__ int request_of(const TreeArgs &a, int t) {
@@ -111,27 +97,9 @@ __global__ void __launch_bounds__(128) tree_rows_kernel(TreeArgs a) {
     if (a.lse && lane == 0) a.lse[(size_t)t * a.n_heads + h] = top == -INFINITY ? -INFINITY : top + logf(sum);
 }
 
-// ---- bf16: tensor-core tiles over the paged cache --------------------------------
-//
-// A unit is (request, row tile, key/value head): the query rows of one tile (a
-// node's query heads that share the key/value head lie side by side) against all
-// keys of the request in tiles of 64. The key tiles of all units, in a row, are
-// dealt to the CTAs in equal shares: a share is a run of tiles that may start and
-// end inside a unit, so ragged lengths cost nothing, and a unit is split over
-// many CTAs where there are few. A CTA that covers a whole unit writes its result;
-// the others write (O, m, l) to the workspace, and join_kernel joins them.
-constexpr int kTileKeys = 64;
-constexpr int kStages = 3;
+// ---- bf16, up to 32 rows a tile: mma.sync over the paged cache -------------------
 
-struct Plan {                 // workspace regions
-    float *part;              // [2 * ctas][M][DP] unnormalised O
-    float2 *stat;             // [2 * ctas][M] (m, l), m in powers of two
-    int4 *seg;                // [ctas] (request, row tile, head, parts) of the unit that starts in a CTA's share and
-                              // goes on past it; parts = 0: there is none
-    int ctas;
-};
-// Part slots: 2c + 1 holds the first part of the unit that goes on past CTA c's
-// share, 2c the part of the unit that began before it.
+constexpr int kStages = 3;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -141,70 +109,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-// 16 bytes to shared memory, zeros when !ok (the source is then not read).
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-struct Request {
-    int start, nodes, row_tiles, key_tiles, ctx, keys;
-};
-
-__device__ Request request(const TreeArgs &a, int b, int m_rows) {
-    Request r;
-    r.start = node_start(a, b);
-    r.nodes = max(node_start(a, b + 1) - r.start, 0);
-    // keys that fit the page table; the largest count is a multiple of the tile below 2^31
-    const long long room = min((long long)a.table_pages * a.page_size, 0x7fffffc0ll);
-    r.ctx = max(a.ctx_lens[b], 0);
-    r.keys = (int)min((long long)r.ctx + r.nodes, room);
-    r.row_tiles = (r.nodes * (a.n_heads / a.n_kv) + m_rows - 1) / m_rows;
-    r.key_tiles = max((r.keys + kTileKeys - 1) / kTileKeys, 1);   // one for rows without keys, too
-    return r;
-}
-
-// Where a CTA is in the run of tiles.
-struct Cursor {
-    Request r;
-    int b, row_tile, head, tile;
-};
-
-__device__ __forceinline__ void next_tile(const TreeArgs &a, Cursor &c, int m_rows) {
-    if (++c.tile < c.r.key_tiles) return;
-    c.tile = 0;
-    if (++c.head < a.n_kv) return;
-    c.head = 0;
-    if (++c.row_tile < c.r.row_tiles) return;
-    c.row_tile = 0;
-    do {
-        if (++c.b >= a.n_requests) return;
-        c.r = request(a, c.b, m_rows);
-    } while (c.r.row_tiles == 0);
-}
-
-// Bits 0..63: which of the tile's keys p0 .. p0 + 63 node i (row `token`) sees.
-__device__ uint64_t seen_keys(const TreeArgs &a, const Request &r, int i, int p0) {
-    const int in_ctx = r.ctx - p0;
-    uint64_t seen = in_ctx >= 64 ? ~0ull : in_ctx <= 0 ? 0ull : (1ull << in_ctx) - 1;
-    if (in_ctx >= 64) return seen;
-    const int j0 = -in_ctx;                             // the node that is the tile's first key
-    if (!a.tree_mask) {
-        const int n = in_ctx + i + 1;                   // keys up to the node itself
-        return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1;
-    }
-    const uint64_t *m = a.tree_mask + (size_t)(r.start + i) * a.mask_words;
-    if (j0 < 0) return seen | m[0] << (-j0);
-    const int w = j0 >> 6, sh = j0 & 63;
-    if (w < a.mask_words) seen = m[w] >> sh;
-    if (sh && w + 1 < a.mask_words) seen |= m[w + 1] << (64 - sh);
-    return seen;
-}
-
 template <int DP, int WM, int WN>
 struct Tile {
     static constexpr int M = 16 * WM, NK = kTileKeys / WN, kWarps = WM * WN, kThreads = 32 * kWarps;
@@ -223,79 +127,22 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
     extern __shared__ __align__(128) unsigned char smem[];
     long long *offs = reinterpret_cast<long long *>(smem + T::kOff);        // element offset of a key's row, -1: none
     uint32_t *valid = reinterpret_cast<uint32_t *>(smem + T::kValid);       // two words a tile
-    long long *first = reinterpret_cast<long long *>(smem + T::kStart);     // request, tiles before it, total, scratch
+    long long *scratch = reinterpret_cast<long long *>(smem + T::kStart);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int wm = warp % WM, wn = warp / WM, g4 = lane >> 2, t4 = lane & 3;
     const int group = a.n_heads / a.n_kv;
 
     grid_launch_dependents();                            // join_kernel waits for this grid's end itself
     if (tid == 0) plan.seg[blockIdx.x] = make_int4(0, 0, 0, 0);
-    // ---- this CTA's share: tiles [lo, hi) of the total
-    long long lo, hi, total = 0, used;
-    {
-        long long mine = 0;
-        for (int b = tid; b < a.n_requests; b += T::kThreads) {
-            const Request r = request(a, b, T::M);
-            mine += (long long)r.row_tiles * r.key_tiles * a.n_kv;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-        if (lane == 0) first[warp] = mine;
-        __syncthreads();
-        for (int w = 0; w < T::kWarps; ++w) total += first[w];
-        used = min((long long)gridDim.x, total);
-        if (blockIdx.x >= used) return;
-        lo = total * blockIdx.x / used;
-        hi = total * (blockIdx.x + 1) / used;
-        __syncthreads();
-    }
-    Cursor load;
-    {
-        long long before = 0;
-        for (int b0 = 0;; b0 += T::kThreads) {           // ends at the latest in the chunk that holds tile lo < total
-            const int b = b0 + tid;
-            long long n = 0;
-            if (b < a.n_requests) {
-                const Request r = request(a, b, T::M);
-                n = (long long)r.row_tiles * r.key_tiles * a.n_kv;
-            }
-            long long upto = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += v;
-            }
-            if (lane == 31) first[2 + warp] = upto;
-            if (tid == 0) first[0] = -1;
-            __syncthreads();
-            for (int w = 0; w < warp; ++w) upto += first[2 + w];
-            upto += before;
-            if (upto - n <= lo && lo < upto) first[0] = b, first[1] = upto - n;
-            for (int w = 0; w < T::kWarps; ++w) before += first[2 + w];
-            __syncthreads();
-            if (first[0] >= 0 || b0 + T::kThreads >= a.n_requests) break;
-            __syncthreads();
-        }
-        if (first[0] < 0) return;                        // not reached: lo < total
-        load.b = (int)first[0];
-        load.r = request(a, load.b, T::M);
-        long long at = lo - first[1];
-        load.tile = (int)(at % load.r.key_tiles);
-        at /= load.r.key_tiles;
-        load.head = (int)(at % a.n_kv);
-        load.row_tile = (int)(at / a.n_kv);
-    }
+    Share share;
+    if (!find_share<T::kThreads>(a, T::M, scratch, share)) return;
+    Cursor load = share.start;
     Cursor c = load;                                     // the tile being computed; `load` runs ahead of it
     Cursor look = load;                                  // the tile whose page ids are being read: one further ahead
-    const int n_tiles = (int)(hi - lo);
+    const int n_tiles = (int)(share.hi - share.lo);
 
     // Offsets of tile i's keys: read into a register by threads 0..63, stored to the ring at the end of the step.
-    auto read_off = [&](const Cursor &u) -> long long {
-        const int p = u.tile * kTileKeys + tid;
-        if (tid >= kTileKeys || p >= u.r.keys) return -1;
-        const int at = p / a.page_size, id = a.page_table[u.b * a.table_stride + at];
-        return id >= 0 && id < a.n_pages ? id * a.c_page + (p - at * a.page_size) * a.c_slot : -1;
-    };
+    auto read_off = [&](const Cursor &u) -> long long { return tid < kTileKeys ? key_offset(a, u, tid) : -1; };
     auto store_off = [&](int i, long long off) {
         if (tid >= kTileKeys) return;
         offs[i % T::kRing * kTileKeys + tid] = off;
@@ -586,10 +433,7 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
                 }
             }
             if (tid == 0 && starts && !ends) {
-                // the unit's last tile lies in the share of CTA floor((x + 1) used - 1) / total), x its index
-                const long long x = lo + i + (c.r.key_tiles - 1 - c.tile);
-                const int parts = (int)(((x + 1) * used - 1) / total) - (int)blockIdx.x + 1;
-                plan.seg[blockIdx.x] = make_int4(c.b, c.row_tile, c.head, parts);
+                plan.seg[blockIdx.x] = make_int4(c.b, c.row_tile, c.head, parts_of(share, c, i));
             }
             fresh = true;
         }
@@ -602,7 +446,7 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
 // takes a row, or, where there are many parts, the block takes one row after
 // another and a warp every eighth part of it.
 template <int DP, int M>
-__global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan) {
+__global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan, int m_rows) {
     constexpr int kVec = DP / 32, kMany = 24;
     __shared__ float so[8][DP];
     __shared__ float2 sm[8];
@@ -610,7 +454,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan) {
     const int4 seg = plan.seg[blockIdx.x];
     if (seg.w == 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = a.n_heads / a.n_kv;
-    const int start = node_start(a, seg.x), rows = (node_start(a, seg.x + 1) - start) * group - seg.y * M;
+    const int start = node_start(a, seg.x), rows = min((node_start(a, seg.x + 1) - start) * group - seg.y * m_rows, m_rows);
     const bool many = seg.w > kMany;
     for (int i = 0; i < (many ? 8 : 1); ++i) {
         const int r = blockIdx.y * 8 + (many ? i : warp);
@@ -661,7 +505,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan) {
             for (int e = 0; e < kVec; ++e) o[e] = 0.f;
             for (int w = 0; w < 8; ++w) add(sm[w], &so[w][lane * kVec]);
         }
-        const int row = seg.y * M + r, head = seg.z * group + row % group;
+        const int row = seg.y * m_rows + r, head = seg.z * group + row % group;
         const long long token = start + row / group;
         const bool none = m == -INFINITY;
         const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -674,13 +518,13 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan) {
     }
 }
 
-constexpr int kMaxRows = 64;
+constexpr int kMaxRows = 128;
 constexpr int kMaxCtas = 2 * 160;
 
 // The row tile by the average rows (nodes times query heads of a key/value head) of a request.
-int rows_of_tile(int n_requests, int n_tokens, int group) {
-    const double rows = (double)n_tokens * group / n_requests;
-    return rows <= 16.0 ? 16 : rows <= 32.0 ? 32 : 64;
+int rows_of_tile(const TreeArgs &a) {
+    const double rows = (double)a.n_tokens * (a.n_heads / a.n_kv) / a.n_requests;
+    return rows <= 16.0 ? 16 : rows <= 32.0 || !tc_takes(a) ? 32 : 128;
 }
 
 size_t plan_bytes(int ctas) {
@@ -698,18 +542,29 @@ cudaError_t launch_tiles(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
         set_device_bit(ready);
     }
     kernel<<<plan.ctas, T::kThreads, T::kSmem, st>>>(a, plan);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    return launch_pdl(tree_join_kernel<DP, T::M>, dim3(plan.ctas, T::M / 8), dim3(256), 0, st, a, plan);
+    return cudaGetLastError();
+}
+
+template <int DP, int M>
+cudaError_t launch_join(const TreeArgs &a, const Plan &plan, int m_rows, cudaStream_t st) {
+    return launch_pdl(tree_join_kernel<DP, M>, dim3(plan.ctas, M / 8), dim3(256), 0, st, a, plan, m_rows);
 }
 
 template <int DP>
-cudaError_t launch_rows_of(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
-    switch (rows_of_tile(a.n_requests, a.n_tokens, a.n_heads / a.n_kv)) {
-        case 16: return launch_tiles<DP, 1>(a, plan, st);
-        case 32: return launch_tiles<DP, 2>(a, plan, st);
-        default: return launch_tiles<DP, 4>(a, plan, st);
+cudaError_t launch_bf16(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
+    const int rows = rows_of_tile(a);
+    cudaError_t e = cudaErrorNotSupported;
+    if (rows == 128) {
+        e = launch_tc(a, plan, st);
+        if (e == cudaSuccess) return launch_join<DP, 128>(a, plan, tc_rows(a), st);
     }
+    if (rows == 16) {
+        e = launch_tiles<DP, 1>(a, plan, st);
+        return e != cudaSuccess ? e : launch_join<DP, 16>(a, plan, 16, st);
+    }
+    if (e != cudaErrorNotSupported) return e;
+    e = launch_tiles<DP, 2>(a, plan, st);
+    return e != cudaSuccess ? e : launch_join<DP, 32>(a, plan, 32, st);
 }
 
 bool shape_ok(int n_requests, int n_tokens, int n_heads, int n_kv, int head_dim, int dtype) {
@@ -777,8 +632,17 @@ extern "C" int lora_tree_attention(const lora_tree_attention_desc *d, void *stre
         plan.stat = reinterpret_cast<float2 *>(plan.part + 2 * (size_t)plan.ctas * kMaxRows * 128);
         plan.seg = reinterpret_cast<int4 *>(plan.stat + 2 * (size_t)plan.ctas * kMaxRows);
         return launched("tree_attention",
-                        d->head_dim <= 64 ? launch_rows_of<64>(a, plan, st) : launch_rows_of<128>(a, plan, st));
+                        d->head_dim <= 64 ? launch_bf16<64>(a, plan, st) : launch_bf16<128>(a, plan, st));
     }
     tree_rows_kernel<float><<<dim3(d->n_tokens, d->n_heads), 128, 0, st>>>(a);
     return launched("tree_attention", cudaGetLastError());
+}
+
+extern "C" int lora_step_wait_timeouts(uint64_t *count) {
+    if (!count) return fail(LORA_ERR_ARG, "step_wait_timeouts: NULL pointer argument");
+    unsigned n = 0;
+    const cudaError_t e = read_timeouts(&n);
+    if (e != cudaSuccess) return launched("step_wait_timeouts", e);
+    *count = n;
+    return LORA_OK;
 }

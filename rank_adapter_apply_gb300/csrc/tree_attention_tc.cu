@@ -1,0 +1,543 @@
+// lora_tree_attention, row tiles of 128 on the 5th-generation tensor cores.
+//
+// Scores S = Q K^T (128 rows x 64 keys) and O += P V are tcgen05 products with
+// their accumulators in tensor memory; P goes back into S's columns in bf16 and is
+// the A operand of the second product from there. 192 threads:
+//   warps 0-3  softmax: thread = row = tensor-memory lane, so the running maximum
+//              and sum need no exchange; at a unit's end they write its result;
+//   warp 4     loads: TMA boxes of up to 64 cache rows of a page into a ring of
+//              16 KB items (K and V alternate), Q at a unit's start;
+//   warp 5     one thread issues the products.
+// S is double-buffered: the scores of tile i + 1 are formed while the softmax of
+// tile i runs. Two CTAs fit an SM (256 tensor-memory columns and 113 KB each).
+//
+// The maximum is a reference that moves only when a row's scores pass it by 2^8:
+// P and l share it, so the quotient does not depend on it, P stays below 2^8 (bf16
+// has the range) and O in tensor memory is rescaled a few times in a unit at most.
+//
+// A weight of zero times an infinity or NaN is NaN, so a V row that is not finite
+// may not meet a row that skips it. Only tree keys, and what lies past the last
+// key, can be skipped: in tiles with such keys the softmax warps look through V,
+// clear the rows that are not finite, and the rows that see one of them add it in
+// fp32 at the end of the unit.
+#include "tree_common.cuh"
+
+#include "tc_util.cuh"
+
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
+namespace lora {
+namespace tree {
+namespace {
+
+constexpr int kRows = 128;                     // lanes of an accumulator; rows of a tile: whole nodes, at most this
+constexpr int kThreads = 192;
+constexpr int kItems = 5;                      // ring of K and V items
+constexpr int kMeta = 4;                       // ring of the tiles' masks
+constexpr uint32_t kWaitLimit = 1u << 22;
+
+template <int DP>
+struct Tc {
+    static constexpr int kHalves = DP / 64;    // columns in blocks of 64: rows of 128 bytes, 128-byte swizzle
+    static constexpr int kItem = kTileKeys * DP * 2, kQ = kRows * DP * 2;
+    static constexpr int kSmem = kQ + kItems * kItem;
+};
+
+struct Meta {
+    uint32_t valid[2];                         // keys that are there
+    uint32_t first;                            // first tile of a unit in this share
+};
+
+struct TcArgs {
+    CUtensorMap q, k, v;                       // boxes of 64 columns: q {group heads, whole nodes}, k, v {box rows}
+    TreeArgs a;
+    Plan plan;
+    int box;                                   // cache rows of a box: a power of two, 8..64
+    int slot_first;                            // order of the cache maps' dimensions: columns, place, head, page (else
+                                               // columns, head, place, page)
+};
+
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
+                                       uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)) : "memory");
+}
+
+// CTAs whose bounded waits gave up (lora_step_wait_timeouts).
+__device__ unsigned g_gave_up = 0;
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+          "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
+          "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// B operand with its rows (N) contiguous: 64 of them in the 128 bytes of a k, eight
+// ks 1024 bytes further, the next 64 rows one block of the tile further.
+__device__ __forceinline__ uint64_t desc_n_major(uint32_t addr, uint32_t block_bytes) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)((block_bytes >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)((1024u >> 4) & 0x3FFFu) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)tc::kSwz128 << 61;
+    return d;
+}
+
+// Whether a 16-byte piece of bf16 holds an infinity or NaN.
+__device__ __forceinline__ bool odd_piece(const uint4 &v) {
+    return ((((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
+             ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u)) & 0x80008000u) != 0;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_constant__ TcArgs args) {
+    using C = Tc<DP>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ uint64_t full[kItems], empty[kItems], meta_full[kMeta], s_full[2], p_ready[2], pv_done[2], q_full, drained;
+    __shared__ int poison_at[2];                       // 1 + the last tile (even, odd) whose V had a row that is not finite
+    __shared__ Meta meta[kMeta];
+    __shared__ long long scratch[kThreads / 32 + 2];
+    __shared__ uint32_t tmem_base;
+    __shared__ int error;
+    volatile int *err = &error;
+
+    const TreeArgs &a = args.a;
+    const Plan &plan = args.plan;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = a.n_heads / a.n_kv;
+    const int rows = kRows / group * group;            // of a tile
+    grid_launch_dependents();                          // the join kernel waits for this grid's end itself
+    if (tid == 0) plan.seg[blockIdx.x] = make_int4(0, 0, 0, 0);
+    Share share;
+    if (!find_share<kThreads>(a, rows, scratch, share)) return;
+    const int n_tiles = (int)(share.hi - share.lo);
+    if (tid == 0) {
+        for (int i = 0; i < kItems; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+        for (int i = 0; i < kMeta; ++i) mbar_init(&meta_full[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 128), mbar_init(&pv_done[i], 1);
+        mbar_init(&q_full, 1);
+        mbar_init(&drained, 1);
+        error = 0;
+        poison_at[0] = poison_at[1] = 0;
+        fence_mbar_init();
+        tc::prefetch_tensormap(&args.q);
+        tc::prefetch_tensormap(&args.k);
+        tc::prefetch_tensormap(&args.v);
+    }
+    if (warp == 5) {
+        tc::tmem_alloc(&tmem_base, 256);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_base, tmem_o = tmem + 128;   // S of the two buffers at columns 0 and 64, O at 128
+    const uint32_t q_at = smem_u32(smem), ring = q_at + C::kQ;
+    auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
+        if (*err) return false;
+        if (mbar_wait_bounded(bar, phase & 1u, kWaitLimit)) return true;
+        *err = 1;
+        return false;
+    };
+    // item j of the ring (K of tile i is 2i, V is 2i + 1); its round is j / kItems
+    auto wait_full = [&](int j) { return wait(&full[j % kItems], (uint32_t)(j / kItems)); };
+    auto wait_empty = [&](int j) { return wait(&empty[j % kItems], (uint32_t)(j / kItems)); };
+
+    if (warp == 4) {
+        // ---------------- loads: lane b < 64 / box has box b of a tile ----------------
+        const int boxes = kTileKeys / args.box;
+        Cursor u = share.start, look = u;
+        // the lane's page (n_pages, outside the cache, reads zeros) and its rows that hold keys
+        auto read_page = [&](const Cursor &t, int &page, int &held) {
+            const int p = t.tile * kTileKeys + lane * args.box;
+            held = lane < boxes ? min(max(t.r.keys - p, 0), args.box) : 0;
+            page = held > 0 ? a.page_table[t.b * a.table_stride + p / a.page_size] : -1;
+        };
+        int page, held;
+        read_page(look, page, held);
+        int i = 0, issued = 0, units = 0;
+        for (; i < n_tiles; ++i) {
+            if (page < 0 || page >= a.n_pages) page = (int)a.n_pages, held = 0;
+            const int at = page, n = held, place = (u.tile * kTileKeys + lane * args.box) % a.page_size;
+            const bool first = i == 0 || u.tile == 0;
+            if (i + 1 < n_tiles) {                     // the next tile's page ids, one tile ahead
+                next_tile(a, look, rows);
+                read_page(look, page, held);
+            }
+            const uint64_t bits = n == 64 ? ~0ull : ((1ull << n) - 1) << (lane * args.box & 63);
+            const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)bits);
+            const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(bits >> 32));
+            if (first) {
+                // the last scores of the unit before have been formed: Q may be overwritten
+                if (i > 0 && !__all_sync(0xffffffffu, wait_empty(2 * (i - 1)))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&q_full, rows * DP * 2);
+                    for (int h = 0; h < C::kHalves; ++h)
+                        tma_3d(q_at + h * (kRows * 128), &args.q, h * 64, u.head * group,
+                               u.r.start + u.row_tile * (rows / group), &q_full);
+                }
+                ++units;
+            }
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const int j = 2 * i + kv;
+                if (j >= kItems && !__all_sync(0xffffffffu, wait_empty(j - kItems))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&full[j % kItems], C::kItem);
+                    if (kv == 0) {
+                        meta[i % kMeta].valid[0] = lo;
+                        meta[i % kMeta].valid[1] = hi;
+                        meta[i % kMeta].first = first;
+                        tc::mbar_arrive(&meta_full[i % kMeta]);
+                    }
+                }
+                __syncwarp();
+                const uint32_t dst = ring + j % kItems * C::kItem + lane * args.box * 128;
+                if (lane < boxes)
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+                        tma_4d(dst + h * (C::kItem / C::kHalves), kv == 0 ? &args.k : &args.v, h * 64,
+                               args.slot_first ? place : u.head, args.slot_first ? u.head : place, at, &full[j % kItems]);
+                issued = j + 1;
+            }
+            if (issued != 2 * i + 2) break;
+            next_tile(a, u, rows);
+        }
+        // no copy is in flight when the CTA ends
+        for (int j = max(issued - kItems, 0); j < issued; ++j)
+            mbar_wait_bounded(&full[j % kItems], (uint32_t)(j / kItems) & 1u, kWaitLimit);
+        if (units > 0) mbar_wait_bounded(&q_full, (uint32_t)(units - 1) & 1u, kWaitLimit);
+    } else if (warp == 5) {
+        if (lane == 0) {
+            // ---------------- products ----------------
+            constexpr uint32_t idesc_s = tc::idesc_bf16(kRows, kTileKeys);
+            constexpr uint32_t idesc_o = tc::idesc_bf16(kRows, DP) | (1u << 16);    // B (V) with N contiguous
+            auto pv = [&](int i) -> bool {
+                if (!wait(&p_ready[i & 1], (uint32_t)(i >> 1)) || !wait_full(2 * i + 1)) return false;
+                tc::fence_after_sync();
+                const bool first = meta[i % kMeta].first != 0;
+                const uint32_t vb = ring + (2 * i + 1) % kItems * C::kItem;
+#pragma unroll
+                for (int k = 0; k < kTileKeys / 16; ++k)
+                    tc::mma_bf16_tmem_a(tmem_o, tmem + (i & 1) * 64 + k * 8, desc_n_major(vb + k * 2048, C::kItem / C::kHalves),
+                                        idesc_o, !first || k > 0);
+                tc::mma_commit(&empty[(2 * i + 1) % kItems]);
+                tc::mma_commit(&pv_done[i & 1]);
+                return true;
+            };
+            int i = 0, units = 0;
+            for (; i < n_tiles; ++i) {
+                if (!wait_full(2 * i) || !wait(&meta_full[i % kMeta], (uint32_t)(i / kMeta))) break;
+                if (meta[i % kMeta].first && !wait(&q_full, (uint32_t)units++)) break;
+                if (i >= 2 && !wait(&pv_done[i & 1], (uint32_t)((i - 2) >> 1))) break;     // P of tile i - 2 was read
+                tc::fence_after_sync();
+                const uint32_t kb = ring + 2 * i % kItems * C::kItem;
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+                    tc::mma_bf16(tmem + (i & 1) * 64,
+                                 tc::smem_desc(q_at + (k >> 2) * (kRows * 128) + (k & 3) * 32, 128, tc::kSwz128),
+                                 tc::smem_desc(kb + (k >> 2) * (C::kItem / 2) + (k & 3) * 32, 128, tc::kSwz128), idesc_s,
+                                 k > 0);
+                tc::mma_commit(&empty[2 * i % kItems]);
+                tc::mma_commit(&s_full[i & 1]);
+                if (i > 0 && !pv(i - 1)) break;
+            }
+            if (i == n_tiles) pv(n_tiles - 1);
+            // every product is done before tensor memory is freed
+            tc::mma_commit(&drained);
+            mbar_wait_bounded(&drained, 0, kWaitLimit);
+        }
+    } else {
+        // ---------------- softmax: thread = row ----------------
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const float c2 = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * 1.4426950408889634f;   // scores in powers of two
+        Cursor c = share.start;
+        float m = -INFINITY, l = 0.f;                  // m: the reference, in powers of two
+        int seg_first = c.tile;
+        bool poison = false;
+        for (int i = 0; i < n_tiles; ++i) {
+            const bool first = i == 0 || c.tile == 0;
+            if (first) m = -INFINITY, l = 0.f, seg_first = c.tile, poison = false;
+            bool ok = wait(&meta_full[i % kMeta], (uint32_t)(i / kMeta)) && wait(&s_full[i & 1], (uint32_t)(i >> 1));
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc::fence_after_sync();
+            const uint64_t there = meta[i % kMeta].valid[0] | (uint64_t)meta[i % kMeta].valid[1] << 32;
+            uint32_t raw[64];
+            tc::tmem_ld64_sync(tmem + lanes + (i & 1) * 64, raw);
+            float(&s)[64] = reinterpret_cast<float(&)[64]>(raw);
+            if (a.scale <= 0.f) {
+#pragma unroll
+                for (int k = 0; k < 64; ++k) s[k] = a.scale < 0.f ? -s[k] : 0.f;
+            }
+            const int p0 = c.tile * kTileKeys, row = c.row_tile * rows + tid;
+            const int node = tid < rows ? row / group : c.r.nodes;
+            if (there != ~0ull || p0 + kTileKeys > c.r.ctx) {
+                const uint64_t seen = node < c.r.nodes ? seen_keys(a, c.r, node, p0) & there : 0;
+                const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    if (!(lo >> k & 1)) s[k] = -INFINITY;
+                    if (!(hi >> k & 1)) s[k + 32] = -INFINITY;
+                }
+            }
+            float top = s[0], top2 = s[1];
+#pragma unroll
+            for (int k = 2; k < 64; k += 2) top = fmaxf(top, s[k]), top2 = fmaxf(top2, s[k + 1]);
+            top = fmaxf(top, top2) * c2;
+            const bool move = top > m + 8.f;
+            if (__any_sync(0xffffffffu, move)) {
+                const float f = move ? exp2_fast(m - top) : 1.f;
+                if (move) m = top;
+                l *= f;
+                if (!first) {                          // O of the tiles before, once it is complete
+                    ok = wait(&pv_done[(i - 1) & 1], (uint32_t)((i - 1) >> 1));
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int d = 0; d < DP; d += 32) {
+                        uint32_t o[32];
+                        tc::tmem_ld32_sync(tmem_o + lanes + d, o);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tmem_st32(tmem_o + lanes + d, o);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.f : m;
+            uint32_t p[32];
+            float l2 = 0.f;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                const float e0 = exp2_fast(fmaf(s[2 * k], c2, -base)), e1 = exp2_fast(fmaf(s[2 * k + 1], c2, -base));
+                l += e0;
+                l2 += e1;
+                // weights to bf16 for the second product: 2^-9 relative, below the output's own rounding; their sum
+                // l stays in fp32 and unrounded
+                p[k] = pack_bf16(e0, e1);
+            }
+            l += l2;
+            tmem_st32(tmem + lanes + (i & 1) * 64, p);
+            tc::tmem_st_wait();
+            if (p0 + kTileKeys > min(c.r.ctx, c.r.keys)) {
+                // some row may skip a key of this tile: no V row with an infinity or NaN in it may stay
+                ok = wait_full(2 * i + 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                // two threads for a row
+                constexpr int kPieces = DP / 16;
+                unsigned char *v = smem + C::kQ + (2 * i + 1) % kItems * C::kItem + (tid >> 1) * 128 +
+                                   (tid & 1) * (C::kHalves == 2 ? C::kItem / 2 : 64);
+                bool bad = false;
+#pragma unroll
+                for (int k = 0; k < kPieces; ++k) bad = bad || odd_piece(*reinterpret_cast<const uint4 *>(v + k * 16));
+                bad = __shfl_xor_sync(0xffffffffu, (int)bad, 1) || bad;
+                if (bad) {
+#pragma unroll
+                    for (int k = 0; k < kPieces; ++k) *reinterpret_cast<uint4 *>(v + k * 16) = make_uint4(0, 0, 0, 0);
+                    if (there >> (tid >> 1) & 1) poison_at[i & 1] = i + 1;
+                }
+                tc::fence_proxy_async_smem();
+                tc::named_bar(1, 128);
+                poison = poison || *reinterpret_cast<volatile int *>(&poison_at[i & 1]) == i + 1;
+            }
+            tc::fence_before_sync();
+            tc::mbar_arrive(&p_ready[i & 1]);
+
+            if (c.tile + 1 == c.r.key_tiles || i + 1 == n_tiles) {
+                // ---- the unit or the share ends: write
+                const bool starts = seg_first == 0, ends = c.tile + 1 == c.r.key_tiles;
+                ok = wait(&pv_done[i & 1], (uint32_t)(i >> 1));
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc::fence_after_sync();
+                const bool mine = node < c.r.nodes, none = m == -INFINITY, done = starts && ends;
+                const long long token = c.r.start + node, slot = 2ll * blockIdx.x + (starts ? 1 : 0);
+                const int head = c.head * group + row % group;
+                const float inv = !done ? 1.f : l > 0.f ? 1.f / l : 0.f;
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + token * a.o_token + head * a.o_head;
+                float *part = plan.part + (slot * kRows + tid) * DP;
+#pragma unroll 1
+                for (int d = 0; d < DP; d += 32) {
+                    uint32_t o[32];
+                    tc::tmem_ld32_sync(tmem_o + lanes + d, o);
+                    if (poison && mine) {
+                        // tree keys of this part whose V row is not finite
+                        for (int t = max(seg_first, c.r.ctx / kTileKeys); t <= c.tile; ++t) {
+                            const uint64_t seen = seen_keys(a, c.r, node, t * kTileKeys);
+                            for (int k = 0; k < kTileKeys; ++k) {
+                                Cursor at = c;
+                                at.tile = t;
+                                const long long off = t * kTileKeys + k < c.r.ctx || !(seen >> k & 1) ? -1 : key_offset(a, at, k);
+                                if (off < 0) continue;
+                                const long long kv = off + (long long)c.head * a.c_head;
+                                const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(a.k_cache) + kv;
+                                const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.v_cache) + kv;
+                                const __nv_bfloat16 *qp =
+                                    static_cast<const __nv_bfloat16 *>(a.q) + token * a.q_token + (long long)head * a.q_head;
+                                bool bad = false;
+                                float dot = 0.f;
+                                for (int e = 0; e < a.head_dim; ++e) {
+                                    bad = bad || !isfinite(to_f32(vp[e]));
+                                    dot = fmaf(to_f32(qp[e]), to_f32(kp[e]), dot);
+                                }
+                                const float x = a.scale < 0.f ? -dot : a.scale == 0.f ? 0.f : dot;
+                                const float weight = exp2_fast(fmaf(x, c2, -base));
+                                if (!bad || weight == 0.f) continue;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (d + e < a.head_dim)
+                                        o[e] = __float_as_uint(fmaf(weight, to_f32(vp[d + e]), __uint_as_float(o[e])));
+                            }
+                        }
+                    }
+                    if (mine && done) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 8) {
+                            if (d + k >= a.head_dim) break;
+                            float v[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] = none ? 0.f : __uint_as_float(o[k + e]) * inv;
+                            *reinterpret_cast<uint4 *>(out + d + k) =
+                                make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                           pack_bf16(v[6], v[7]));
+                        }
+                    } else if (mine) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<uint4 *>(part + d + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (mine && done && a.lse)
+                    a.lse[token * a.n_heads + head] = none ? -INFINITY : m * 0.6931471805599453f + logf(l);
+                if (mine && !done) plan.stat[slot * kRows + tid] = make_float2(m, l);
+                if (tid == 0 && starts && !ends)
+                    plan.seg[blockIdx.x] = make_int4(c.b, c.row_tile, c.head, parts_of(share, c, i));
+                tc::fence_before_sync();
+            }
+            __syncwarp();
+            next_tile(a, c, rows);
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (tid == 0 && error) atomicAdd(&g_gave_up, 1u);
+    if (warp == 5) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 256);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 fn = known.load(std::memory_order_acquire);
+    if (fn) return fn;
+    cudaDriverEntryPointQueryResult q;
+    void *p = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !p)
+        return nullptr;
+    fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    known.store(fn, std::memory_order_release);
+    return fn;
+}
+
+// A bf16 map of `rank` dimensions, boxes of 64 columns, 128-byte swizzle. The
+// stride of a dimension of one element is never used: any legal one stands in.
+bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims, const long long *strides,
+            const cuuint32_t *box) {
+    cuuint64_t bytes[3];
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    for (int i = 0; i + 1 < rank; ++i) bytes[i] = dims[i + 1] == 1 ? 16 : (cuuint64_t)strides[i] * 2;
+    const auto fn = encoder();
+    return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, bytes, box, ones,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Cache rows of a box: what divides a page and the tile.
+int box_of(int page_size) {
+    int box = kTileKeys;
+    while (page_size % box) box /= 2;
+    return box;
+}
+
+template <int DP>
+cudaError_t launch(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
+    static std::atomic<uint64_t> ready{0};
+    if (!device_bit(ready)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(tree_tc_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<DP>::kSmem);
+        if (e != cudaSuccess) return e;
+        set_device_bit(ready);
+    }
+    const int group = a.n_heads / a.n_kv;
+    TcArgs args;
+    args.a = a;
+    args.plan = plan;
+    args.box = box_of(a.page_size);
+    const cuuint64_t q_dims[] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.n_heads, (cuuint64_t)a.n_tokens};
+    const long long q_strides[] = {a.q_head, a.q_token};
+    const cuuint32_t q_box[] = {64, (cuuint32_t)group, (cuuint32_t)(kRows / group)};
+    args.slot_first = a.c_slot < a.c_head;
+    const cuuint64_t heads = a.n_kv, places = a.page_size;
+    const cuuint32_t box = args.box;
+    const bool sf = args.slot_first;
+    const cuuint64_t c_dims[] = {(cuuint64_t)a.head_dim, sf ? places : heads, sf ? heads : places, (cuuint64_t)a.n_pages};
+    const long long c_strides[] = {sf ? a.c_slot : a.c_head, sf ? a.c_head : a.c_slot, a.c_page};
+    const cuuint32_t c_box[] = {64, sf ? box : 1, sf ? 1 : box, 1};
+    if (!encode(&args.q, a.q, 3, q_dims, q_strides, q_box) || !encode(&args.k, a.k_cache, 4, c_dims, c_strides, c_box) ||
+        !encode(&args.v, a.v_cache, 4, c_dims, c_strides, c_box))
+        return cudaErrorNotSupported;
+    tree_tc_kernel<DP><<<plan.ctas, kThreads, Tc<DP>::kSmem, st>>>(args);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t read_timeouts(unsigned *count) { return cudaMemcpyFromSymbol(count, g_gave_up, sizeof *count); }
+
+// Whether strides s of dimensions of n elements, innermost first, rise and are
+// those of a tensor map: 0 < s < 2^40 bytes.
+static bool rising(const long long *s, const long long *n, int count) {
+    long long last = 0;
+    for (int i = 0; i < count; ++i) {
+        if (n[i] == 1) continue;
+        if (s[i] <= last || s[i] >= 1ll << 39) return false;
+        last = s[i];
+    }
+    return true;
+}
+
+// Pages in boxes of eight rows or more (the swizzle's period), whole nodes in a
+// tile, a query's heads within its token, pages outermost in the cache.
+bool tc_takes(const TreeArgs &a) {
+    const int group = a.n_heads / a.n_kv;
+    if (box_of(a.page_size) < 8 || group > kRows || a.n_pages < 1 || a.n_pages >= INT32_MAX) return false;
+    const long long q[] = {a.q_head, a.q_token}, qn[] = {a.n_heads, a.n_tokens};
+    const bool sf = a.c_slot < a.c_head;
+    const long long c[] = {sf ? a.c_slot : a.c_head, sf ? a.c_head : a.c_slot, a.c_page};
+    const long long cn[] = {sf ? a.page_size : a.n_kv, sf ? a.n_kv : a.page_size, a.n_pages};
+    return rising(q, qn, 2) && rising(c, cn, 3);
+}
+
+int tc_rows(const TreeArgs &a) { return kRows / (a.n_heads / a.n_kv) * (a.n_heads / a.n_kv); }
+
+cudaError_t launch_tc(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
+    return a.head_dim <= 64 ? launch<64>(a, plan, st) : launch<128>(a, plan, st);
+}
+
+}  // namespace tree
+}  // namespace lora

@@ -319,6 +319,11 @@ TREES = [
     ([0, 17, 200], [4, 0, 9], 14, 2, 96, 16), ([130], [16], 32, 8, 128, 64), ([257, 1, 40], [7, 33, 2], 16, 2, 72, 48),
     ([700], [64], 4, 1, 128, 32), ([31, 500, 3, 77, 0], [5, 6, 20, 1, 12], 24, 3, 64, 128), ([1500], [2], 16, 8, 128, 16),
     ([0, 0], [64, 1], 6, 6, 40, 16), ([90] * 20, [3] * 20, 4, 4, 128, 16), ([2100, 33], [17, 40], 8, 1, 128, 64),
+    # more than 32 rows a head: whole nodes in a tile (groups of 7, 3 and 48), pages of 8, 24 and 128 places, pages that
+    # no box of eight rows fits, many short units, a unit over many blocks
+    ([150, 3], [40, 64], 14, 2, 128, 8), ([64, 65, 0, 1], [33, 20, 64, 64], 9, 3, 72, 24), ([500], [3], 48, 1, 96, 128),
+    ([77, 200], [30, 21], 8, 2, 64, 12), ([1, 2, 3, 4, 5, 6, 7, 8], [11] * 8, 32, 8, 128, 32), ([6000], [64], 16, 1, 128, 64),
+    ([40, 900, 0], [64, 1, 30], 64, 8, 128, 16), ([127, 128, 129], [48, 64, 49], 130, 1, 64, 16),
 ]
 
 
@@ -381,33 +386,43 @@ def test_tree_attention_bad_entries(ops, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_tree_attention_layouts(ops, dtype):
+@pytest.mark.parametrize("nodes", [[5, 12], [25, 60]])
+def test_tree_attention_layouts(ops, nodes, dtype):
     """q inside a fused projection's rows, a cache with heads before places, keys and values interleaved, an output
     with padded heads: the same as from contiguous tensors."""
     import torch
-    c = _tree_case([100, 33], [5, 12], 8, 2, 64, 16, dtype, seed=8)
+    c = _tree_case([100, 33], nodes, 8, 2, 64, 16, dtype, seed=8)
     want = _run_tree(ops, c)
     _check_tree(c, *want)
-    q = torch.full((17, 3, 8, 64), float("nan"), dtype=c["q"].dtype, device="cuda")
+    total = sum(nodes)
+    q = torch.full((total, 3, 8, 64), float("nan"), dtype=c["q"].dtype, device="cuda")
     q[:, 1] = c["q"]
     both = torch.stack([c["kc"].permute(0, 2, 1, 3), c["vc"].permute(0, 2, 1, 3)], 1).contiguous()
     d = dict(c, q=q[:, 1], kc=both[:, 0].permute(0, 2, 1, 3), vc=both[:, 1].permute(0, 2, 1, 3))
-    out = torch.full((17, 8, 80), 4.0, dtype=c["q"].dtype, device="cuda")
+    out = torch.full((total, 8, 80), 4.0, dtype=c["q"].dtype, device="cuda")
     got = _run_tree(ops, d, out=out[:, :, :64])
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert (out[:, :, 64:] == 4.0).all()
+    # queries with tokens inside heads, and a cache with places outermost
+    e = dict(c, q=c["q"].permute(1, 0, 2).contiguous().permute(1, 0, 2),
+             kc=c["kc"].permute(1, 0, 2, 3).contiguous().permute(1, 0, 2, 3),
+             vc=c["vc"].permute(1, 0, 2, 3).contiguous().permute(1, 0, 2, 3))
+    _check_tree(e, *_run_tree(ops, e))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("spread", [40.0, 1e-3])
-def test_tree_attention_score_range(ops, spread, dtype):
-    """Scores of hundreds (one key takes all the weight) and of nothing; another scale."""
-    c = _tree_case([300, 64], [6, 3], 8, 2, 128, 16, dtype, seed=9, spread=spread)
-    _check_tree(c, *_run_tree(ops, c, scale=0.5), scale=0.5)
+@pytest.mark.parametrize("nodes", [[6, 3], [60, 33]])
+@pytest.mark.parametrize("scale", [0.5, -0.3, 0.0])
+def test_tree_attention_score_range(ops, scale, nodes, spread, dtype):
+    """Scores of hundreds (one key takes all the weight, and the running maximum moves often) and of nothing; other
+    scales, negative and zero."""
+    c = _tree_case([300, 64], nodes, 8, 2, 128, 16, dtype, seed=9, spread=spread)
+    _check_tree(c, *_run_tree(ops, c, scale=scale), scale=scale)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("dim,nodes", [(64, 2), (128, 3), (72, 9), (128, 20)])
+@pytest.mark.parametrize("dim,nodes", [(64, 2), (128, 3), (72, 9), (128, 20), (64, 60)])
 def test_tree_attention_poison_in_skipped_keys(ops, dim, nodes, dtype):
     """Infinities and NaN in tree keys reach the rows that see those keys and no other row: two forks of the root, a
     poisoned value in one of them, a poisoned key in the other, and both in a node that nobody sees."""
@@ -443,32 +458,37 @@ def test_tree_attention_poison_in_skipped_keys(ops, dim, nodes, dtype):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_tree_attention_long_context(ops, dtype):
     """A context long enough to be split over many blocks, beside short ones."""
-    c = _tree_case([9000, 3, 400], [3, 5, 2], 4, 1, 64, 64, dtype, seed=10)
-    _check_tree(c, *_run_tree(ops, c))
+    for nodes in ([3, 5, 2], [20, 33, 14]):
+        c = _tree_case([9000, 3, 400], nodes, 4, 1, 64, 64, dtype, seed=10)
+        _check_tree(c, *_run_tree(ops, c))
 
 
 def test_tree_attention_offsets_past_32_bits(ops):
     """Pages more than 2^31 elements into the cache."""
     import torch
     page, kv, dim = 64, 8, 128
-    c = _tree_case([100], [4], 16, kv, dim, page, "bf16", seed=11)
     far = (1 << 31) // (page * kv * dim) + 1
-    kc = torch.empty((far + c["kc"].shape[0], page, kv, dim), dtype=torch.bfloat16, device="cuda")
+    kc = torch.empty((far + 5, page, kv, dim), dtype=torch.bfloat16, device="cuda")
     vc = torch.empty_like(kc)
-    kc[far:], vc[far:] = c["kc"], c["vc"]
-    want = _run_tree(ops, c)
-    d = dict(c, kc=kc, vc=vc, table=c["table"] + far)
-    got = _run_tree(ops, d)
-    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for nodes in (4, 30):
+        c = _tree_case([100], [nodes], 16, kv, dim, page, "bf16", seed=11)
+        kc[far:far + c["kc"].shape[0]], vc[far:far + c["kc"].shape[0]] = c["kc"], c["vc"]
+        want = _run_tree(ops, c)
+        d = dict(c, kc=kc, vc=vc, table=c["table"] + far)
+        got = _run_tree(ops, d)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_tree_attention_repeats_bit_for_bit(ops):
     import torch
-    c = _tree_case([1000, 77], [9, 3], 16, 4, 128, 16, "bf16", seed=12)
-    first = _run_tree(ops, c)
-    for _ in range(4):
-        again = _run_tree(ops, c)
-        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    from rank_adapter_apply_gb300 import binding as B
+    for nodes in ([9, 3], [60, 14]):
+        c = _tree_case([1000, 77], nodes, 16, 4, 128, 16, "bf16", seed=12)
+        first = _run_tree(ops, c)
+        for _ in range(4):
+            again = _run_tree(ops, c)
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    assert B.lora_step_wait_timeouts() == 0
 
 
 # ---- verification ---------------------------------------------------------------------------
