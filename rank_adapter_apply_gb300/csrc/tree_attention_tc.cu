@@ -98,6 +98,26 @@ __device__ __forceinline__ uint64_t desc_n_major(uint32_t addr, uint32_t block_b
     return d;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // Whether a 16-byte piece of bf16 holds an infinity or NaN.
 __device__ __forceinline__ bool odd_piece(const uint4 &v) {
     return ((((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
@@ -148,42 +168,78 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
     const uint32_t tmem = tmem_base, tmem_o = tmem + 128;   // S of the two buffers at columns 0 and 64, O at 128
     const uint32_t q_at = smem_u32(smem), ring = q_at + C::kQ;
     auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
+        if (mbar_try_wait(bar, phase & 1u)) return true;
         if (*err) return false;
         if (mbar_wait_bounded(bar, phase & 1u, kWaitLimit)) return true;
         *err = 1;
         return false;
     };
-    // item j of the ring (K of tile i is 2i, V is 2i + 1); its round is j / kItems
+    // Items are loaded in the order in which the products take them: K0 K1 V0 K2 V1 .. Item j lies in place
+    // j % kItems of the ring, in round j / kItems.
+    auto item_k = [&](int i) { return i == 0 ? 0 : 2 * i - 1; };
+    auto item_v = [&](int i) { return i + 1 < n_tiles ? 2 * i + 2 : 2 * i + 1; };
     auto wait_full = [&](int j) { return wait(&full[j % kItems], (uint32_t)(j / kItems)); };
     auto wait_empty = [&](int j) { return wait(&empty[j % kItems], (uint32_t)(j / kItems)); };
 
     if (warp == 4) {
-        // ---------------- loads: lane b < 64 / box has box b of a tile ----------------
+        // ---------------- loads: lane b < 64 / box loads box b of a tile ----------------
+        // The lanes hold the pages of 32 boxes of the request in a row (a tile's boxes lie in one such run): the run
+        // in use, the one after it, whose reads are in flight meanwhile, and the first, where the next head begins.
         const int boxes = kTileKeys / args.box;
-        Cursor u = share.start, look = u;
-        // the lane's page (n_pages, outside the cache, reads zeros) and its rows that hold keys
-        auto read_page = [&](const Cursor &t, int &page, int &held) {
-            const int p = t.tile * kTileKeys + lane * args.box;
-            held = lane < boxes ? min(max(t.r.keys - p, 0), args.box) : 0;
-            page = held > 0 ? a.page_table[t.b * a.table_stride + p / a.page_size] : -1;
+        Cursor u = share.start;
+        struct Run {
+            int page, place;                           // page -1: no such box
         };
-        int page, held;
-        read_page(look, page, held);
-        int i = 0, issued = 0, units = 0;
-        for (; i < n_tiles; ++i) {
-            if (page < 0 || page >= a.n_pages) page = (int)a.n_pages, held = 0;
-            const int at = page, n = held, place = (u.tile * kTileKeys + lane * args.box) % a.page_size;
-            const bool first = i == 0 || u.tile == 0;
-            if (i + 1 < n_tiles) {                     // the next tile's page ids, one tile ahead
-                next_tile(a, look, rows);
-                read_page(look, page, held);
+        auto read_run = [&](int run) -> Run {
+            const int p = (run * 32 + lane) * args.box, at = p / a.page_size;
+            return {p < u.r.keys ? a.page_table[u.b * a.table_stride + at] : -1, p - at * a.page_size};
+        };
+        int run_b = -1, run_at = 0;                    // request, and number of the run in use
+        Run now{}, ahead{}, head_run{};
+        int issued = 0, units = 0;
+        struct Box {
+            int page, place, head;
+        } last{};                                      // of the tile whose V is still to be loaded
+        auto load = [&](int j, const CUtensorMap *map, const Box &b) -> bool {
+            if (j >= kItems && !__all_sync(0xffffffffu, wait_empty(j - kItems))) return false;
+            if (lane == 0) mbar_arrive_expect_tx(&full[j % kItems], C::kItem);
+            __syncwarp();
+            const uint32_t dst = ring + j % kItems * C::kItem + lane * args.box * 128;
+            if (lane < boxes)
+#pragma unroll
+                for (int h = 0; h < C::kHalves; ++h)
+                    tma_4d(dst + h * (C::kItem / C::kHalves), map, h * 64, args.slot_first ? b.place : b.head,
+                           args.slot_first ? b.head : b.place, b.page, &full[j % kItems]);
+            issued = j + 1;
+            return true;
+        };
+        for (int i = 0; i < n_tiles; ++i) {
+            const int box0 = u.tile * boxes, run = box0 >> 5;
+            if (run_b != u.b) {
+                run_b = u.b;
+                head_run = read_run(0);
+                run_at = run;
+                now = run == 0 ? head_run : read_run(run);
+                ahead = read_run(run + 1);
+            } else if (run != run_at) {
+                now = run == 0 ? head_run : run == run_at + 1 ? ahead : read_run(run);
+                run_at = run;
+                ahead = read_run(run + 1);
             }
+            const int from = (box0 & 31) + lane;       // lanes past the tile's boxes read a lane that nobody uses
+            int page = __shfl_sync(0xffffffffu, now.page, from & 31);
+            const int place = __shfl_sync(0xffffffffu, now.place, from & 31);
+            // rows of the box that hold keys; a page outside the cache reads zeros
+            int n = lane < boxes ? min(max(u.r.keys - (box0 + lane) * args.box, 0), args.box) : 0;
+            if (n == 0 || page < 0 || page >= a.n_pages) page = (int)a.n_pages, n = 0;
+            const Box here{page, place, u.head};
+            const bool first = i == 0 || u.tile == 0;
             const uint64_t bits = n == 64 ? ~0ull : ((1ull << n) - 1) << (lane * args.box & 63);
             const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)bits);
             const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(bits >> 32));
             if (first) {
                 // the last scores of the unit before have been formed: Q may be overwritten
-                if (i > 0 && !__all_sync(0xffffffffu, wait_empty(2 * (i - 1)))) break;
+                if (i > 0 && !__all_sync(0xffffffffu, wait_empty(item_k(i - 1)))) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&q_full, rows * DP * 2);
                     for (int h = 0; h < C::kHalves; ++h)
@@ -192,29 +248,16 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
                 }
                 ++units;
             }
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                const int j = 2 * i + kv;
-                if (j >= kItems && !__all_sync(0xffffffffu, wait_empty(j - kItems))) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&full[j % kItems], C::kItem);
-                    if (kv == 0) {
-                        meta[i % kMeta].valid[0] = lo;
-                        meta[i % kMeta].valid[1] = hi;
-                        meta[i % kMeta].first = first;
-                        tc::mbar_arrive(&meta_full[i % kMeta]);
-                    }
-                }
-                __syncwarp();
-                const uint32_t dst = ring + j % kItems * C::kItem + lane * args.box * 128;
-                if (lane < boxes)
-#pragma unroll
-                    for (int h = 0; h < C::kHalves; ++h)
-                        tma_4d(dst + h * (C::kItem / C::kHalves), kv == 0 ? &args.k : &args.v, h * 64,
-                               args.slot_first ? place : u.head, args.slot_first ? u.head : place, at, &full[j % kItems]);
-                issued = j + 1;
+            if (!load(item_k(i), &args.k, here)) break;
+            if (lane == 0) {
+                meta[i % kMeta].valid[0] = lo;
+                meta[i % kMeta].valid[1] = hi;
+                meta[i % kMeta].first = first;
+                tc::mbar_arrive(&meta_full[i % kMeta]);
             }
-            if (issued != 2 * i + 2) break;
+            if (i > 0 && !load(item_v(i - 1), &args.v, last)) break;
+            if (i + 1 == n_tiles && !load(item_v(i), &args.v, here)) break;
+            last = here;
             next_tile(a, u, rows);
         }
         // no copy is in flight when the CTA ends
@@ -227,32 +270,32 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
             constexpr uint32_t idesc_s = tc::idesc_bf16(kRows, kTileKeys);
             constexpr uint32_t idesc_o = tc::idesc_bf16(kRows, DP) | (1u << 16);    // B (V) with N contiguous
             auto pv = [&](int i) -> bool {
-                if (!wait(&p_ready[i & 1], (uint32_t)(i >> 1)) || !wait_full(2 * i + 1)) return false;
+                if (!wait(&p_ready[i & 1], (uint32_t)(i >> 1)) || !wait_full(item_v(i))) return false;
                 tc::fence_after_sync();
                 const bool first = meta[i % kMeta].first != 0;
-                const uint32_t vb = ring + (2 * i + 1) % kItems * C::kItem;
+                const uint32_t vb = ring + item_v(i) % kItems * C::kItem;
 #pragma unroll
                 for (int k = 0; k < kTileKeys / 16; ++k)
                     tc::mma_bf16_tmem_a(tmem_o, tmem + (i & 1) * 64 + k * 8, desc_n_major(vb + k * 2048, C::kItem / C::kHalves),
                                         idesc_o, !first || k > 0);
-                tc::mma_commit(&empty[(2 * i + 1) % kItems]);
+                tc::mma_commit(&empty[item_v(i) % kItems]);
                 tc::mma_commit(&pv_done[i & 1]);
                 return true;
             };
             int i = 0, units = 0;
             for (; i < n_tiles; ++i) {
-                if (!wait_full(2 * i) || !wait(&meta_full[i % kMeta], (uint32_t)(i / kMeta))) break;
+                if (!wait_full(item_k(i)) || !wait(&meta_full[i % kMeta], (uint32_t)(i / kMeta))) break;
                 if (meta[i % kMeta].first && !wait(&q_full, (uint32_t)units++)) break;
                 if (i >= 2 && !wait(&pv_done[i & 1], (uint32_t)((i - 2) >> 1))) break;     // P of tile i - 2 was read
                 tc::fence_after_sync();
-                const uint32_t kb = ring + 2 * i % kItems * C::kItem;
+                const uint32_t kb = ring + item_k(i) % kItems * C::kItem;
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
                     tc::mma_bf16(tmem + (i & 1) * 64,
                                  tc::smem_desc(q_at + (k >> 2) * (kRows * 128) + (k & 3) * 32, 128, tc::kSwz128),
                                  tc::smem_desc(kb + (k >> 2) * (C::kItem / 2) + (k & 3) * 32, 128, tc::kSwz128), idesc_s,
                                  k > 0);
-                tc::mma_commit(&empty[2 * i % kItems]);
+                tc::mma_commit(&empty[item_k(i) % kItems]);
                 tc::mma_commit(&s_full[i & 1]);
                 if (i > 0 && !pv(i - 1)) break;
             }
@@ -267,78 +310,90 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
         const float c2 = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * 1.4426950408889634f;   // scores in powers of two
         Cursor c = share.start;
         float m = -INFINITY, l = 0.f;                  // m: the reference, in powers of two
-        int seg_first = c.tile;
-        bool poison = false;
+        int seg_first = c.tile, node = 0, head = 0;
+        bool poison = false, idle = false;             // idle: no row of this warp exists
         for (int i = 0; i < n_tiles; ++i) {
             const bool first = i == 0 || c.tile == 0;
-            if (first) m = -INFINITY, l = 0.f, seg_first = c.tile, poison = false;
+            if (first) {
+                m = -INFINITY, l = 0.f, seg_first = c.tile, poison = false;
+                const int row = c.row_tile * rows + tid;
+                node = tid < rows ? row / group : c.r.nodes;
+                head = c.head * group + row % group;
+                idle = __all_sync(0xffffffffu, node >= c.r.nodes);
+            }
             bool ok = wait(&meta_full[i % kMeta], (uint32_t)(i / kMeta)) && wait(&s_full[i & 1], (uint32_t)(i >> 1));
             if (!__all_sync(0xffffffffu, ok)) break;
             tc::fence_after_sync();
             const uint64_t there = meta[i % kMeta].valid[0] | (uint64_t)meta[i % kMeta].valid[1] << 32;
-            uint32_t raw[64];
-            tc::tmem_ld64_sync(tmem + lanes + (i & 1) * 64, raw);
-            float(&s)[64] = reinterpret_cast<float(&)[64]>(raw);
-            if (a.scale <= 0.f) {
+            const int p0 = c.tile * kTileKeys;
+            if (!idle) {
+                uint32_t raw[64];
+                tc::tmem_ld64_sync(tmem + lanes + (i & 1) * 64, raw);
+                float(&s)[64] = reinterpret_cast<float(&)[64]>(raw);
+                if (a.scale <= 0.f) {
 #pragma unroll
-                for (int k = 0; k < 64; ++k) s[k] = a.scale < 0.f ? -s[k] : 0.f;
-            }
-            const int p0 = c.tile * kTileKeys, row = c.row_tile * rows + tid;
-            const int node = tid < rows ? row / group : c.r.nodes;
-            if (there != ~0ull || p0 + kTileKeys > c.r.ctx) {
-                const uint64_t seen = node < c.r.nodes ? seen_keys(a, c.r, node, p0) & there : 0;
-                const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    if (!(lo >> k & 1)) s[k] = -INFINITY;
-                    if (!(hi >> k & 1)) s[k + 32] = -INFINITY;
+                    for (int k = 0; k < 64; ++k) s[k] = a.scale < 0.f ? -s[k] : 0.f;
                 }
-            }
-            float top = s[0], top2 = s[1];
+                if (there != ~0ull || p0 + kTileKeys > c.r.ctx) {
+                    const uint64_t seen = node < c.r.nodes ? seen_keys(a, c.r, node, p0) & there : 0;
+                    const uint32_t lo = (uint32_t)seen, hi = (uint32_t)(seen >> 32);
 #pragma unroll
-            for (int k = 2; k < 64; k += 2) top = fmaxf(top, s[k]), top2 = fmaxf(top2, s[k + 1]);
-            top = fmaxf(top, top2) * c2;
-            const bool move = top > m + 8.f;
-            if (__any_sync(0xffffffffu, move)) {
-                const float f = move ? exp2_fast(m - top) : 1.f;
-                if (move) m = top;
-                l *= f;
-                if (!first) {                          // O of the tiles before, once it is complete
-                    ok = wait(&pv_done[(i - 1) & 1], (uint32_t)((i - 1) >> 1));
-                    if (!__all_sync(0xffffffffu, ok)) break;
-                    tc::fence_after_sync();
-#pragma unroll 1
-                    for (int d = 0; d < DP; d += 32) {
-                        uint32_t o[32];
-                        tc::tmem_ld32_sync(tmem_o + lanes + d, o);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                        tmem_st32(tmem_o + lanes + d, o);
+                    for (int k = 0; k < 32; ++k) {
+                        if (!(lo >> k & 1)) s[k] = -INFINITY;
+                        if (!(hi >> k & 1)) s[k + 32] = -INFINITY;
                     }
                 }
-            }
-            const float base = m == -INFINITY ? 0.f : m;
-            uint32_t p[32];
-            float l2 = 0.f;
+                float top = s[0], top2 = s[1];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-                const float e0 = exp2_fast(fmaf(s[2 * k], c2, -base)), e1 = exp2_fast(fmaf(s[2 * k + 1], c2, -base));
-                l += e0;
-                l2 += e1;
-                // weights to bf16 for the second product: 2^-9 relative, below the output's own rounding; their sum
-                // l stays in fp32 and unrounded
-                p[k] = pack_bf16(e0, e1);
+                for (int k = 2; k < 64; k += 2) top = fmaxf(top, s[k]), top2 = fmaxf(top2, s[k + 1]);
+                top = fmaxf(top, top2) * c2;
+                const bool move = top > m + 8.f;
+                if (__any_sync(0xffffffffu, move)) {
+                    const float f = move ? exp2_fast(m - top) : 1.f;
+                    if (move) m = top;
+                    l *= f;
+                    if (!first) {                          // O of the tiles before, once it is complete
+                        ok = wait(&pv_done[(i - 1) & 1], (uint32_t)((i - 1) >> 1));
+                        if (!__all_sync(0xffffffffu, ok)) break;
+                        tc::fence_after_sync();
+#pragma unroll 1
+                        for (int d = 0; d < DP; d += 32) {
+                            uint32_t o[32];
+                            tc::tmem_ld32_sync(tmem_o + lanes + d, o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st32(tmem_o + lanes + d, o);
+                        }
+                    }
+                }
+                const float minus = m == -INFINITY ? 0.f : -m;
+                const uint64_t cc = pair(c2, c2), mm = pair(minus, minus);
+                uint32_t p[32];
+                uint64_t sums[2] = {pair(l, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    float e0, e1;
+                    unpair(fma2(pair(s[2 * k], s[2 * k + 1]), cc, mm), e0, e1);
+                    e0 = exp2_fast(e0);
+                    e1 = exp2_fast(e1);
+                    sums[k & 1] = add2(sums[k & 1], pair(e0, e1));
+                    // weights to bf16 for the second product: 2^-9 relative, below the output's own rounding; their sum
+                    // l stays in fp32 and unrounded
+                    p[k] = pack_bf16(e0, e1);
+                }
+                float l0, l1;
+                unpair(add2(sums[0], sums[1]), l0, l1);
+                l = l0 + l1;
+                tmem_st32(tmem + lanes + (i & 1) * 64, p);
+                tc::tmem_st_wait();
             }
-            l += l2;
-            tmem_st32(tmem + lanes + (i & 1) * 64, p);
-            tc::tmem_st_wait();
             if (p0 + kTileKeys > min(c.r.ctx, c.r.keys)) {
                 // some row may skip a key of this tile: no V row with an infinity or NaN in it may stay
-                ok = wait_full(2 * i + 1);
+                ok = wait_full(item_v(i));
                 if (!__all_sync(0xffffffffu, ok)) break;
                 // two threads for a row
                 constexpr int kPieces = DP / 16;
-                unsigned char *v = smem + C::kQ + (2 * i + 1) % kItems * C::kItem + (tid >> 1) * 128 +
+                unsigned char *v = smem + C::kQ + item_v(i) % kItems * C::kItem + (tid >> 1) * 128 +
                                    (tid & 1) * (C::kHalves == 2 ? C::kItem / 2 : 64);
                 bool bad = false;
 #pragma unroll
@@ -364,7 +419,6 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
                 tc::fence_after_sync();
                 const bool mine = node < c.r.nodes, none = m == -INFINITY, done = starts && ends;
                 const long long token = c.r.start + node, slot = 2ll * blockIdx.x + (starts ? 1 : 0);
-                const int head = c.head * group + row % group;
                 const float inv = !done ? 1.f : l > 0.f ? 1.f / l : 0.f;
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + token * a.o_token + head * a.o_head;
                 float *part = plan.part + (slot * kRows + tid) * DP;
@@ -373,13 +427,13 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
                     uint32_t o[32];
                     tc::tmem_ld32_sync(tmem_o + lanes + d, o);
                     if (poison && mine) {
-                        // tree keys of this part whose V row is not finite
-                        for (int t = max(seg_first, c.r.ctx / kTileKeys); t <= c.tile; ++t) {
+                        // keys of this part's looked-through tiles whose V row is not finite
+                        for (int t = max(seg_first, min(c.r.ctx, c.r.keys) / kTileKeys); t <= c.tile; ++t) {
                             const uint64_t seen = seen_keys(a, c.r, node, t * kTileKeys);
                             for (int k = 0; k < kTileKeys; ++k) {
                                 Cursor at = c;
                                 at.tile = t;
-                                const long long off = t * kTileKeys + k < c.r.ctx || !(seen >> k & 1) ? -1 : key_offset(a, at, k);
+                                const long long off = seen >> k & 1 ? key_offset(a, at, k) : -1;
                                 if (off < 0) continue;
                                 const long long kv = off + (long long)c.head * a.c_head;
                                 const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(a.k_cache) + kv;
@@ -393,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
                                     dot = fmaf(to_f32(qp[e]), to_f32(kp[e]), dot);
                                 }
                                 const float x = a.scale < 0.f ? -dot : a.scale == 0.f ? 0.f : dot;
-                                const float weight = exp2_fast(fmaf(x, c2, -base));
+                                const float weight = exp2_fast(fmaf(x, c2, m == -INFINITY ? 0.f : -m));
                                 if (!bad || weight == 0.f) continue;
 #pragma unroll
                                 for (int e = 0; e < 32; ++e)

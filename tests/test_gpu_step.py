@@ -456,6 +456,25 @@ def test_tree_attention_poison_in_skipped_keys(ops, dim, nodes, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nodes", [3, 7, 40])
+@pytest.mark.parametrize("at", [10, 66])
+def test_tree_attention_poison_in_context(ops, at, nodes, dtype):
+    """An infinity in a context key's value reaches every row of its head, and no other head, whether the key lies in a
+    tile of context keys alone or beside tree keys."""
+    import torch
+    c = _tree_case([70], [nodes], 8, 2, 128, 16, dtype, seed=14)
+    want = _run_tree(ops, c)
+    c["vc"][int(c["table"][0, at // 16]), at % 16, 0, 5] = float("-inf")
+    out, lse = _run_tree(ops, c)
+    assert torch.isinf(out[:, :4, 5]).all() and (out[:, :4, 5] < 0).all()
+    keep = torch.ones_like(out, dtype=torch.bool)
+    keep[:, :4, 5] = False
+    tol = 2.0 ** -6 if dtype == "bf16" else 2.0 ** -18
+    assert ((out - want[0]).abs()[keep] <= tol * (1 + want[0].abs()[keep])).all()
+    assert torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_tree_attention_long_context(ops, dtype):
     """A context long enough to be split over many blocks, beside short ones."""
     for nodes in ([3, 5, 2], [20, 33, 14]):
