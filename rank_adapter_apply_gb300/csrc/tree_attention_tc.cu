@@ -71,6 +71,41 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int
         "[%6];" ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)) : "memory");
 }
 
+__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *err) {
+    if (*err) return false;
+    if (mbar_wait_bounded(bar, parity, kWaitLimit)) return true;
+    *err = 1;
+    return false;
+}
+
+// o[0..31] += the weight times V of every key of tiles first .. c.tile that row
+// `node` sees and whose V row is not finite (columns d .. d + 31).
+__device__ __noinline__ void add_poison(const TreeArgs &a, const Cursor &c, int first, int node, int head, int d, float c2,
+                                        float m, float *o) {
+    const __nv_bfloat16 *q =
+        static_cast<const __nv_bfloat16 *>(a.q) + (c.r.start + node) * a.q_token + (long long)head * a.q_head;
+    Cursor at = c;
+    for (at.tile = first; at.tile <= c.tile; ++at.tile) {
+        const uint64_t seen = seen_keys(a, c.r, node, at.tile * kTileKeys);
+        for (int k = 0; k < kTileKeys; ++k) {
+            const long long off = seen >> k & 1 ? key_offset(a, at, k) : -1;
+            if (off < 0) continue;
+            const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(a.k_cache) + off + (long long)c.head * a.c_head;
+            const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.v_cache) + off + (long long)c.head * a.c_head;
+            bool bad = false;
+            float dot = 0.f;
+            for (int e = 0; e < a.head_dim; ++e) {
+                bad = bad || !isfinite(to_f32(vp[e]));
+                dot = fmaf(to_f32(q[e]), to_f32(kp[e]), dot);
+            }
+            const float x = a.scale < 0.f ? -dot : a.scale == 0.f ? 0.f : dot;
+            const float weight = exp2_fast(fmaf(x, c2, m == -INFINITY ? 0.f : -m));
+            if (!bad || weight == 0.f) continue;
+            for (int e = 0; e < 32 && d + e < a.head_dim; ++e) o[e] = fmaf(weight, to_f32(vp[d + e]), o[e]);
+        }
+    }
+}
+
 // CTAs whose bounded waits gave up (lora_step_wait_timeouts).
 __device__ unsigned g_gave_up = 0;
 
@@ -148,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
     if (tid == 0) {
         for (int i = 0; i < kItems; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         for (int i = 0; i < kMeta; ++i) mbar_init(&meta_full[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 128), mbar_init(&pv_done[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 4), mbar_init(&pv_done[i], 1);
         mbar_init(&q_full, 1);
         mbar_init(&drained, 1);
         error = 0;
@@ -168,18 +203,15 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
     const uint32_t tmem = tmem_base, tmem_o = tmem + 128;   // S of the two buffers at columns 0 and 64, O at 128
     const uint32_t q_at = smem_u32(smem), ring = q_at + C::kQ;
     auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
-        if (mbar_try_wait(bar, phase & 1u)) return true;
-        if (*err) return false;
-        if (mbar_wait_bounded(bar, phase & 1u, kWaitLimit)) return true;
-        *err = 1;
-        return false;
+        return mbar_try_wait(bar, phase & 1u) || wait_long(bar, phase & 1u, err);
     };
-    // Items are loaded in the order in which the products take them: K0 K1 V0 K2 V1 .. Item j lies in place
-    // j % kItems of the ring, in round j / kItems.
-    auto item_k = [&](int i) { return i == 0 ? 0 : 2 * i - 1; };
-    auto item_v = [&](int i) { return i + 1 < n_tiles ? 2 * i + 2 : 2 * i + 1; };
-    auto wait_full = [&](int j) { return wait(&full[j % kItems], (uint32_t)(j / kItems)); };
-    auto wait_empty = [&](int j) { return wait(&empty[j % kItems], (uint32_t)(j / kItems)); };
+    // Items are loaded in the order in which the products take them, K0 K1 V0 K2 V1 .., round and round the ring; a
+    // role steps through them with a place and the parity of its round.
+    auto step = [](int &place, uint32_t &round) {
+        if (++place == kItems) place = 0, round ^= 1u;
+    };
+    auto place_v = [&](int i) { return (i + 1 < n_tiles ? 2 * i + 2 : 2 * i + 1) % kItems; };
+    auto round_v = [&](int i) { return (uint32_t)((i + 1 < n_tiles ? 2 * i + 2 : 2 * i + 1) / kItems); };
 
     if (warp == 4) {
         // ---------------- loads: lane b < 64 / box loads box b of a tile ----------------
@@ -196,50 +228,54 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
         };
         int run_b = -1, run_at = 0;                    // request, and number of the run in use
         Run now{}, ahead{}, head_run{};
-        int issued = 0, units = 0;
+        int at = 0, units = 0, issued = 0, k_at = 0;   // the ring's next place, and that of the last K
+        uint32_t round = 0, k_round = 0;
         struct Box {
-            int page, place, head;
+            int page, c1, c2;                          // the cache maps' outer coordinates
         } last{};                                      // of the tile whose V is still to be loaded
-        auto load = [&](int j, const CUtensorMap *map, const Box &b) -> bool {
-            if (j >= kItems && !__all_sync(0xffffffffu, wait_empty(j - kItems))) return false;
-            if (lane == 0) mbar_arrive_expect_tx(&full[j % kItems], C::kItem);
+        auto load = [&](const CUtensorMap *map, const Box &b) -> bool {
+            if (!__all_sync(0xffffffffu, wait(&empty[at], round ^ 1u))) return false;   // at once in the first round
+            if (lane == 0) mbar_arrive_expect_tx(&full[at], C::kItem);
             __syncwarp();
-            const uint32_t dst = ring + j % kItems * C::kItem + lane * args.box * 128;
-            if (lane < boxes)
+            if (lane < boxes) {
+                const uint32_t dst = ring + at * C::kItem + lane * args.box * 128;
 #pragma unroll
                 for (int h = 0; h < C::kHalves; ++h)
-                    tma_4d(dst + h * (C::kItem / C::kHalves), map, h * 64, args.slot_first ? b.place : b.head,
-                           args.slot_first ? b.head : b.place, b.page, &full[j % kItems]);
-            issued = j + 1;
+                    tma_4d(dst + h * (C::kItem / C::kHalves), map, h * 64, b.c1, b.c2, b.page, &full[at]);
+            }
+            step(at, round);
+            ++issued;
             return true;
         };
-        for (int i = 0; i < n_tiles; ++i) {
+        int i = 0;
+        for (; i < n_tiles; ++i) {
             const int box0 = u.tile * boxes, run = box0 >> 5;
-            if (run_b != u.b) {
+            if (run_b != u.b || run != run_at) {
+                if (run_b != u.b) head_run = read_run(0);
+                now = run == 0 ? head_run : run_b == u.b && run == run_at + 1 ? ahead : read_run(run);
                 run_b = u.b;
-                head_run = read_run(0);
-                run_at = run;
-                now = run == 0 ? head_run : read_run(run);
-                ahead = read_run(run + 1);
-            } else if (run != run_at) {
-                now = run == 0 ? head_run : run == run_at + 1 ? ahead : read_run(run);
                 run_at = run;
                 ahead = read_run(run + 1);
             }
             const int from = (box0 & 31) + lane;       // lanes past the tile's boxes read a lane that nobody uses
             int page = __shfl_sync(0xffffffffu, now.page, from & 31);
             const int place = __shfl_sync(0xffffffffu, now.place, from & 31);
-            // rows of the box that hold keys; a page outside the cache reads zeros
-            int n = lane < boxes ? min(max(u.r.keys - (box0 + lane) * args.box, 0), args.box) : 0;
-            if (n == 0 || page < 0 || page >= a.n_pages) page = (int)a.n_pages, n = 0;
-            const Box here{page, place, u.head};
+            uint32_t lo = ~0u, hi = ~0u;               // the tile's keys that are there
+            const bool whole = lane >= boxes ||
+                               (page >= 0 && page < (int)a.n_pages && (box0 + lane + 1) * args.box <= u.r.keys);
+            if (!__all_sync(0xffffffffu, whole)) {
+                // rows of the box that hold keys; a page outside the cache reads zeros
+                int n = lane < boxes ? min(max(u.r.keys - (box0 + lane) * args.box, 0), args.box) : 0;
+                if (n == 0 || page < 0 || page >= a.n_pages) page = (int)a.n_pages, n = 0;
+                const uint64_t bits = n == 64 ? ~0ull : ((1ull << n) - 1) << (lane * args.box & 63);
+                lo = __reduce_or_sync(0xffffffffu, (uint32_t)bits);
+                hi = __reduce_or_sync(0xffffffffu, (uint32_t)(bits >> 32));
+            }
+            const Box here{page, args.slot_first ? place : u.head, args.slot_first ? u.head : place};
             const bool first = i == 0 || u.tile == 0;
-            const uint64_t bits = n == 64 ? ~0ull : ((1ull << n) - 1) << (lane * args.box & 63);
-            const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)bits);
-            const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(bits >> 32));
             if (first) {
                 // the last scores of the unit before have been formed: Q may be overwritten
-                if (i > 0 && !__all_sync(0xffffffffu, wait_empty(item_k(i - 1)))) break;
+                if (i > 0 && !__all_sync(0xffffffffu, wait(&empty[k_at], k_round))) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&q_full, rows * DP * 2);
                     for (int h = 0; h < C::kHalves; ++h)
@@ -248,18 +284,20 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
                 }
                 ++units;
             }
-            if (!load(item_k(i), &args.k, here)) break;
+            k_at = at, k_round = round;
+            if (!load(&args.k, here)) break;
             if (lane == 0) {
-                meta[i % kMeta].valid[0] = lo;
-                meta[i % kMeta].valid[1] = hi;
-                meta[i % kMeta].first = first;
+                Meta &m = meta[i % kMeta];
+                m.valid[0] = lo;
+                m.valid[1] = hi;
+                m.first = first;
                 tc::mbar_arrive(&meta_full[i % kMeta]);
             }
-            if (i > 0 && !load(item_v(i - 1), &args.v, last)) break;
-            if (i + 1 == n_tiles && !load(item_v(i), &args.v, here)) break;
+            if (i > 0 && !load(&args.v, last)) break;
             last = here;
             next_tile(a, u, rows);
         }
+        if (i == n_tiles) load(&args.v, last);
         // no copy is in flight when the CTA ends
         for (int j = max(issued - kItems, 0); j < issued; ++j)
             mbar_wait_bounded(&full[j % kItems], (uint32_t)(j / kItems) & 1u, kWaitLimit);
@@ -269,37 +307,43 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
             // ---------------- products ----------------
             constexpr uint32_t idesc_s = tc::idesc_bf16(kRows, kTileKeys);
             constexpr uint32_t idesc_o = tc::idesc_bf16(kRows, DP) | (1u << 16);    // B (V) with N contiguous
-            auto pv = [&](int i) -> bool {
-                if (!wait(&p_ready[i & 1], (uint32_t)(i >> 1)) || !wait_full(item_v(i))) return false;
-                tc::fence_after_sync();
-                const bool first = meta[i % kMeta].first != 0;
-                const uint32_t vb = ring + item_v(i) % kItems * C::kItem;
+            // descriptors of the operands' first slices; slices and places differ in the address field alone
+            const uint64_t q_desc = tc::smem_desc(q_at, 128, tc::kSwz128), k_desc = tc::smem_desc(ring, 128, tc::kSwz128);
+            const uint64_t v_desc = desc_n_major(ring, C::kItem / C::kHalves);
+            int at = 0, units = 0;
+            uint32_t round = 0;
+            bool ok = true;
+            for (int i = 0; ok && i <= n_tiles; ++i) {
+                if (i < n_tiles) {
+                    ok = wait(&full[at], round) && wait(&meta_full[i % kMeta], (uint32_t)(i / kMeta)) &&
+                         (!meta[i % kMeta].first || wait(&q_full, (uint32_t)units++)) &&
+                         (i < 2 || wait(&pv_done[i & 1], (uint32_t)((i - 2) >> 1)));      // P of tile i - 2 was read
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    const uint64_t kd = k_desc + (uint64_t)(at * (C::kItem >> 4));
 #pragma unroll
-                for (int k = 0; k < kTileKeys / 16; ++k)
-                    tc::mma_bf16_tmem_a(tmem_o, tmem + (i & 1) * 64 + k * 8, desc_n_major(vb + k * 2048, C::kItem / C::kHalves),
-                                        idesc_o, !first || k > 0);
-                tc::mma_commit(&empty[item_v(i) % kItems]);
-                tc::mma_commit(&pv_done[i & 1]);
-                return true;
-            };
-            int i = 0, units = 0;
-            for (; i < n_tiles; ++i) {
-                if (!wait_full(item_k(i)) || !wait(&meta_full[i % kMeta], (uint32_t)(i / kMeta))) break;
-                if (meta[i % kMeta].first && !wait(&q_full, (uint32_t)units++)) break;
-                if (i >= 2 && !wait(&pv_done[i & 1], (uint32_t)((i - 2) >> 1))) break;     // P of tile i - 2 was read
-                tc::fence_after_sync();
-                const uint32_t kb = ring + item_k(i) % kItems * C::kItem;
+                    for (int k = 0; k < DP / 16; ++k)
+                        tc::mma_bf16(tmem + (i & 1) * 64, q_desc + (k >> 2) * (kRows * 128 >> 4) + (k & 3) * 2,
+                                     kd + (k >> 2) * (C::kItem / 2 >> 4) + (k & 3) * 2, idesc_s, k > 0);
+                    tc::mma_commit(&empty[at]);
+                    tc::mma_commit(&s_full[i & 1]);
+                    step(at, round);
+                }
+                if (i > 0) {
+                    const int t = i - 1;
+                    ok = wait(&p_ready[t & 1], (uint32_t)(t >> 1)) && wait(&full[at], round);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    const uint32_t more = meta[t % kMeta].first == 0;
+                    const uint64_t vd = v_desc + (uint64_t)(at * (C::kItem >> 4));
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
-                    tc::mma_bf16(tmem + (i & 1) * 64,
-                                 tc::smem_desc(q_at + (k >> 2) * (kRows * 128) + (k & 3) * 32, 128, tc::kSwz128),
-                                 tc::smem_desc(kb + (k >> 2) * (C::kItem / 2) + (k & 3) * 32, 128, tc::kSwz128), idesc_s,
-                                 k > 0);
-                tc::mma_commit(&empty[item_k(i) % kItems]);
-                tc::mma_commit(&s_full[i & 1]);
-                if (i > 0 && !pv(i - 1)) break;
+                    for (int k = 0; k < kTileKeys / 16; ++k)
+                        tc::mma_bf16_tmem_a(tmem_o, tmem + (t & 1) * 64 + k * 8, vd + k * (2048 >> 4), idesc_o, more | (k > 0));
+                    tc::mma_commit(&empty[at]);
+                    tc::mma_commit(&pv_done[t & 1]);
+                    step(at, round);
+                }
             }
-            if (i == n_tiles) pv(n_tiles - 1);
             // every product is done before tensor memory is freed
             tc::mma_commit(&drained);
             mbar_wait_bounded(&drained, 0, kWaitLimit);
@@ -389,11 +433,12 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
             }
             if (p0 + kTileKeys > min(c.r.ctx, c.r.keys)) {
                 // some row may skip a key of this tile: no V row with an infinity or NaN in it may stay
-                ok = wait_full(item_v(i));
+                const int vp = place_v(i);
+                ok = wait(&full[vp], round_v(i));
                 if (!__all_sync(0xffffffffu, ok)) break;
                 // two threads for a row
                 constexpr int kPieces = DP / 16;
-                unsigned char *v = smem + C::kQ + item_v(i) % kItems * C::kItem + (tid >> 1) * 128 +
+                unsigned char *v = smem + C::kQ + vp * C::kItem + (tid >> 1) * 128 +
                                    (tid & 1) * (C::kHalves == 2 ? C::kItem / 2 : 64);
                 bool bad = false;
 #pragma unroll
@@ -409,7 +454,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
                 poison = poison || *reinterpret_cast<volatile int *>(&poison_at[i & 1]) == i + 1;
             }
             tc::fence_before_sync();
-            tc::mbar_arrive(&p_ready[i & 1]);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&p_ready[i & 1]);       // one of a warp: arrivals at one address queue up
 
             if (c.tile + 1 == c.r.key_tiles || i + 1 == n_tiles) {
                 // ---- the unit or the share ends: write
@@ -427,34 +473,12 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
                     uint32_t o[32];
                     tc::tmem_ld32_sync(tmem_o + lanes + d, o);
                     if (poison && mine) {
-                        // keys of this part's looked-through tiles whose V row is not finite
-                        for (int t = max(seg_first, min(c.r.ctx, c.r.keys) / kTileKeys); t <= c.tile; ++t) {
-                            const uint64_t seen = seen_keys(a, c.r, node, t * kTileKeys);
-                            for (int k = 0; k < kTileKeys; ++k) {
-                                Cursor at = c;
-                                at.tile = t;
-                                const long long off = seen >> k & 1 ? key_offset(a, at, k) : -1;
-                                if (off < 0) continue;
-                                const long long kv = off + (long long)c.head * a.c_head;
-                                const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(a.k_cache) + kv;
-                                const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.v_cache) + kv;
-                                const __nv_bfloat16 *qp =
-                                    static_cast<const __nv_bfloat16 *>(a.q) + token * a.q_token + (long long)head * a.q_head;
-                                bool bad = false;
-                                float dot = 0.f;
-                                for (int e = 0; e < a.head_dim; ++e) {
-                                    bad = bad || !isfinite(to_f32(vp[e]));
-                                    dot = fmaf(to_f32(qp[e]), to_f32(kp[e]), dot);
-                                }
-                                const float x = a.scale < 0.f ? -dot : a.scale == 0.f ? 0.f : dot;
-                                const float weight = exp2_fast(fmaf(x, c2, m == -INFINITY ? 0.f : -m));
-                                if (!bad || weight == 0.f) continue;
+                        float t[32];
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (d + e < a.head_dim)
-                                        o[e] = __float_as_uint(fmaf(weight, to_f32(vp[d + e]), __uint_as_float(o[e])));
-                            }
-                        }
+                        for (int k = 0; k < 32; ++k) t[k] = __uint_as_float(o[k]);
+                        add_poison(a, c, max(seg_first, min(c.r.ctx, c.r.keys) / kTileKeys), node, head, d, c2, m, t);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(t[k]);
                     }
                     if (mine && done) {
 #pragma unroll

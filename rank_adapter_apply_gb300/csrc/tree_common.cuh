@@ -58,7 +58,9 @@ struct Request {
     int start, nodes, row_tiles, key_tiles, ctx, keys;
 };
 
-__device__ inline Request request(const TreeArgs &a, int b, int m_rows) {
+// Not inlined, like everything that a tile in the middle of a unit does not need: a warp of a role runs alone on its
+// scheduler, and straight code that does not fit the instruction cache would be its pace.
+__device__ __noinline__ inline Request request(const TreeArgs &a, int b, int m_rows) {
     Request r;
     r.start = node_start(a, b);
     r.nodes = max(node_start(a, b + 1) - r.start, 0);
@@ -77,8 +79,7 @@ struct Cursor {
     int b, row_tile, head, tile;
 };
 
-__device__ __forceinline__ void next_tile(const TreeArgs &a, Cursor &c, int m_rows) {
-    if (++c.tile < c.r.key_tiles) return;
+__device__ __noinline__ inline void next_unit(const TreeArgs &a, Cursor &c, int m_rows) {
     c.tile = 0;
     if (++c.head < a.n_kv) return;
     c.head = 0;
@@ -90,8 +91,15 @@ __device__ __forceinline__ void next_tile(const TreeArgs &a, Cursor &c, int m_ro
     } while (c.r.row_tiles == 0);
 }
 
+__device__ __forceinline__ void next_tile(const TreeArgs &a, Cursor &c, int m_rows) {
+    if (++c.tile < c.r.key_tiles) return;
+    Cursor next = c;                                     // c itself stays in registers
+    next_unit(a, next, m_rows);
+    c = next;
+}
+
 // Bits 0..63: which of the tile's keys p0 .. p0 + 63 node i (row `token`) sees.
-__device__ inline uint64_t seen_keys(const TreeArgs &a, const Request &r, int i, int p0) {
+__device__ __noinline__ inline uint64_t seen_keys(const TreeArgs &a, const Request &r, int i, int p0) {
     const int in_ctx = r.ctx - p0;
     uint64_t seen = in_ctx >= 64 ? ~0ull : in_ctx <= 0 ? 0ull : (1ull << in_ctx) - 1;
     if (in_ctx >= 64) return seen;
