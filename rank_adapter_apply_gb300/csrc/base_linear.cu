@@ -18,53 +18,8 @@ struct LinearArgs {
     int n_tokens, d_in, d_out, group;
 };
 
-// One warp per output row and TT tokens: a lane takes eight columns (one
-// 32-bit word of the row) at a time, in fp32.
-template <typename T, int TT>
-__global__ void __launch_bounds__(256) linear_rows_kernel(LinearArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int t0 = blockIdx.y * TT;
-    if (row >= a.d_out) return;
-    const int nt = min(TT, a.n_tokens - t0);
-    const int words = a.d_in / 8, groups = a.d_in / a.group;
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(a.qweight + (size_t)row * (a.d_in / 2));
-    const T *sc = static_cast<const T *>(a.scales) + (size_t)row * groups;
-    const uint8_t *zr = a.zeros ? a.zeros + (size_t)row * groups : nullptr;
-    const T *x = static_cast<const T *>(a.x) + (size_t)t0 * a.x_stride;
-    float acc[TT];
-#pragma unroll
-    for (int t = 0; t < TT; ++t) acc[t] = 0.f;
-    for (int i = lane; i < words; i += 32) {
-        const uint32_t q = w[i];
-        const int g = i * 8 / a.group;
-        const float s = to_f32(sc[g]);
-        const float z = zr ? fminf((float)zr[g], 128.f) : 8.f;
-        float n[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) n[j] = (float)((q >> (4 * j)) & 15u) - z;
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            if (t < nt) {
-                const T *xt = x + (size_t)t * a.x_stride + i * 8;
-                float p = 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) p = fmaf(n[j], to_f32(xt[j]), p);
-                acc[t] = fmaf(s, p, acc[t]);
-            }
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-        const float v = warp_sum(acc[t]);
-        if (lane == 0 && t < nt) static_cast<T *>(a.y)[(size_t)(t0 + t) * a.y_stride + row] = from_f32<T>(v);
-    }
-}
-
 constexpr int kMaxCluster = 8;
 
-// ---- bf16: tensor-core tiles --------------------------------------------------------
-//
 // A CTA takes 128 rows of W, 16 to a warp, and, as one of the CTAs of a cluster, a
 // range of the columns. Each warp streams its rows' 4-bit words from global memory
 // into registers, kAhead blocks of 128 columns ahead, and meets nobody on the way;
@@ -72,7 +27,9 @@ constexpr int kMaxCluster = 8;
 // mma(W 16 x 16, x^T 16 x 8) has the rows of W as its rows and eight tokens as its
 // columns. The 4-bit values become bf16 integers in registers: 0x4300 | n is 128 +
 // n, and subtracting 128 + z leaves n - z exactly. So the products within a group
-// are exact in fp32, and the group's fp32 sum is scaled once. At the end the
+// are exact in fp32, and the group's fp32 sum is scaled once. An x in fp32 is cut
+// into three bf16 parts of eight bits each that sum to it exactly, so the same
+// products serve it with three times the multiplications. At the end the
 // cluster's parts are added in a fixed order through distributed shared memory: no
 // workspace, no atomics.
 //
@@ -82,12 +39,15 @@ constexpr int kMaxCluster = 8;
 // within a group, so the quad first exchanges words (exchange()). Within a word the
 // halves of a register are nibbles 16 bits apart: 0 4 | 1 5 | 2 6 | 3 7. x is put
 // into the same order when it is staged (x_place() and the byte permutes).
-template <int NT_, int KS_, int kAhead_, int kCtas_>
+template <typename X_, int NT_, int KS_, int kAhead_, int kCtas_>
 struct LinearTile {
+    using X = X_;                                                   // type of x, scales and y
     static constexpr int NT = NT_, KS = KS_, kAhead = kAhead_, kCtas = kCtas_;
-    static constexpr int R = 128, T = 8 * NT, kXRow = KS * 2;       // rows, tokens, bytes of a staged row of x
+    static constexpr int kParts = sizeof(X) == 4 ? 3 : 1;           // bf16 parts of x
+    static constexpr int R = 128, T = 8 * NT;                       // rows, tokens
+    static constexpr int kXRow = KS * 2, kPlane = T * kXRow;        // bytes of a staged row, of a part, of x
     static constexpr int kRedRow = R + 1;                           // floats of a token's row of the parts
-    static constexpr int kSmem = T * kXRow > T * kRedRow * 4 ? T * kXRow : T * kRedRow * 4;
+    static constexpr int kSmem = kParts * kPlane > T * kRedRow * 4 ? kParts * kPlane : T * kRedRow * 4;
     static_assert(KS % (128 * kAhead) == 0, "a slice is whole rounds of the register ring");
 };
 
@@ -106,6 +66,50 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
+
+// Eight columns of a token, as one bf16 part or three.
+template <typename X>
+struct Piece;
+template <>
+struct Piece<__nv_bfloat16> {
+    uint4 raw;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool ok, int vec) {
+        raw = load8_bf16(reinterpret_cast<const uint16_t *>(p), 0, 8, ok, vec);
+    }
+    __device__ __forceinline__ uint4 take() const { return raw; }
+};
+template <>
+struct Piece<float> {
+    float v[8];
+    __device__ __forceinline__ void load(const float *p, bool ok, int vec) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        if (!ok) return;
+        if (vec) {
+            *reinterpret_cast<float4 *>(v) = __ldg(reinterpret_cast<const float4 *>(p));
+            *reinterpret_cast<float4 *>(v + 4) = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = p[i];
+        }
+    }
+    // The next part: the upper eight significand bits (cut, not rounded, so that it stays in range); what is left
+    // is exact. An infinity or NaN is the first part alone.
+    __device__ __forceinline__ uint4 take() {
+        uint32_t h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            h[i] = __float_as_uint(v[i]) & 0xffff0000u;
+            if ((h[i] & 0x7f800000u) == 0x7f800000u) {
+                if (v[i] != v[i]) h[i] |= 0x00400000u;              // a NaN whose upper half reads as an infinity
+                v[i] = 0.f;
+            } else {
+                v[i] -= __uint_as_float(h[i]);
+            }
+        }
+        return make_uint4(h[0] >> 16 | h[1], h[2] >> 16 | h[3], h[4] >> 16 | h[5], h[6] >> 16 | h[7]);
+    }
+};
 
 // W is read once: 16 bytes past the L1.
 __device__ __forceinline__ uint4 load_w(const uint8_t *p) {
@@ -158,23 +162,25 @@ __global__ void __launch_bounds__(256, C::kCtas) linear_tiles_kernel(LinearArgs 
     const int nt = min(C::T, a.n_tokens - tok0);
     const int groups = a.d_in / (GU * 32), blocks = (a.d_in + 127) / 128;
     const int b_lo = (int)((long long)blocks * rank / cluster), b_hi = (int)((long long)blocks * (rank + 1) / cluster);
-    const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.x) + (size_t)tok0 * a.x_stride;
+    using X = typename C::X;
+    const X *x = static_cast<const X *>(a.x) + (size_t)tok0 * a.x_stride;
 
     // ---- this lane's rows: words, scales and zeros of a block. A row past d_out reads the last row (nobody stores
     // what comes of it), and columns past d_in meet an x of zero.
     const int r_in = warp * 16 + g4;                                // and r_in + 8
     const uint8_t *wsrc[2];
-    const uint16_t *ssrc[2];
+    const X *ssrc[2];
     const uint8_t *zsrc[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const size_t row = min(row0 + r_in + h * 8, a.d_out - 1);
         wsrc[h] = a.qweight + row * (a.d_in / 2) + (size_t)b_lo * 64 + t4 * 16;
-        ssrc[h] = static_cast<const uint16_t *>(a.scales) + row * groups + b_lo * kGroups + t4 % kGroups;
+        ssrc[h] = static_cast<const X *>(a.scales) + row * groups + b_lo * kGroups + t4 % kGroups;
         zsrc[h] = kZeros ? a.zeros + row * groups + b_lo * kGroups + t4 % kGroups : nullptr;
     }
     uint4 w[kAhead][2];
-    uint32_t sc[kAhead][2], zr[kAhead][2];
+    X sc[kAhead][2];
+    uint32_t zr[kAhead][2];
     // block i of the round whose first block is b (the pointers are at b)
     auto fetch = [&](int i, int b, int slot) {
         if (b + i >= b_hi) return;
@@ -183,7 +189,7 @@ __global__ void __launch_bounds__(256, C::kCtas) linear_tiles_kernel(LinearArgs 
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             w[slot][h] = in ? load_w(wsrc[h] + i * 64) : make_uint4(0, 0, 0, 0);
-            sc[slot][h] = gin ? __ldg(ssrc[h] + i * kGroups) : 0;
+            sc[slot][h] = gin ? __ldg(ssrc[h] + i * kGroups) : from_f32<X>(0.f);
             if (kZeros) zr[slot][h] = gin ? __ldg(zsrc[h] + i * kGroups) : 0;
         }
     };
@@ -199,27 +205,29 @@ __global__ void __launch_bounds__(256, C::kCtas) linear_tiles_kernel(LinearArgs 
         const int n_blocks = min(kSliceBlocks, b_hi - s_lo);
         if (s_lo != b_lo) __syncthreads();
         // A warp takes a block's 16 pieces of two tokens at a time: piece and place of a lane are always the same.
-        constexpr int kBatch = C::NT == 1 ? 4 : 8;                  // pieces of a thread whose loads are in flight
+        constexpr int kBatch = C::NT == 1 || C::kParts == 3 ? 4 : 8;    // pieces of a thread whose loads are in flight
         const int q = lane & 15, odd = lane >> 4;                   // odd token of the pair
         unsigned char *dst = smem + odd * C::kXRow + ((x_place<GU>(q) ^ (odd << 2)) << 4);
         const int pairs = s_lo == b_lo ? C::T / 2 : (nt + 1) / 2;   // rows past the tokens are cleared once
         for (int i0 = warp; i0 < pairs * kSliceBlocks; i0 += 8 * kBatch) {
-            uint4 v[kBatch];
+            Piece<X> v[kBatch];
 #pragma unroll
             for (int e = 0; e < kBatch; ++e) {
                 const int i = i0 + e * 8, t = i / kSliceBlocks * 2 + odd, blk = i % kSliceBlocks;
                 const int k = (s_lo + blk) * 128 + q * 8;
-                v[e] = make_uint4(0, 0, 0, 0);
-                if (t < nt && blk < n_blocks && k < a.d_in)
-                    v[e] = load8_bf16(reinterpret_cast<const uint16_t *>(x + (size_t)t * a.x_stride + k), 0, 8, true, x_vec);
+                v[e].load(x + (size_t)t * a.x_stride + k, t < nt && blk < n_blocks && k < a.d_in, x_vec);
             }
 #pragma unroll
             for (int e = 0; e < kBatch; ++e) {
                 const int i = i0 + e * 8, t2 = i / kSliceBlocks * 2, blk = i % kSliceBlocks;
                 if (t2 >= C::T) break;
-                *reinterpret_cast<uint4 *>(dst + t2 * C::kXRow + blk * 256) =
-                    make_uint4(__byte_perm(v[e].x, v[e].z, 0x5410), __byte_perm(v[e].x, v[e].z, 0x7632),
-                               __byte_perm(v[e].y, v[e].w, 0x5410), __byte_perm(v[e].y, v[e].w, 0x7632));
+#pragma unroll
+                for (int part = 0; part < C::kParts; ++part) {
+                    const uint4 o = v[e].take();
+                    *reinterpret_cast<uint4 *>(dst + part * C::kPlane + t2 * C::kXRow + blk * 256) =
+                        make_uint4(__byte_perm(o.x, o.z, 0x5410), __byte_perm(o.x, o.z, 0x7632),
+                                   __byte_perm(o.y, o.w, 0x5410), __byte_perm(o.y, o.w, 0x7632));
+                }
             }
         }
         __syncthreads();
@@ -236,7 +244,7 @@ __global__ void __launch_bounds__(256, C::kCtas) linear_tiles_kernel(LinearArgs 
                 for (int h = 0; h < 2; ++h) {
                     wd[h][0] = w[i][h].x, wd[h][1] = w[i][h].y, wd[h][2] = w[i][h].z, wd[h][3] = w[i][h].w;
                     exchange<GU>(wd[h], t4);
-                    sf[h] = __uint_as_float(sc[i][h] << 16);
+                    sf[h] = to_f32(sc[i][h]);
                     z[h] = 0x43084308u;                             // 128 + 8, twice
                     if (kZeros) {                                   // 128 + z, twice: exact in bf16 up to 256
                         const uint32_t zb = __float_as_uint(128.f + (float)min(zr[i][h], 128u)) >> 16;
@@ -259,13 +267,16 @@ __global__ void __launch_bounds__(256, C::kCtas) linear_tiles_kernel(LinearArgs 
                     }
 #pragma unroll
                     for (int n = 0; n < C::NT; ++n) {
-                        const uint4 b = *reinterpret_cast<const uint4 *>(
-                            xbase + n * 8 * C::kXRow + i * 256 + (u >> 1) * 128 + (u & 1) * x_odd);
-                        if (u % GU == 0)
-                            mma_bf16_first(part[n], f[0], b.x, b.y);
-                        else
-                            mma_bf16(part[n], f[0][0], f[0][1], f[0][2], f[0][3], b.x, b.y);
-                        mma_bf16(part[n], f[1][0], f[1][1], f[1][2], f[1][3], b.z, b.w);
+#pragma unroll
+                        for (int e = 0; e < C::kParts; ++e) {
+                            const uint4 b = *reinterpret_cast<const uint4 *>(xbase + e * C::kPlane + n * 8 * C::kXRow + i * 256 +
+                                                                             (u >> 1) * 128 + (u & 1) * x_odd);
+                            if (u % GU == 0 && e == 0)
+                                mma_bf16_first(part[n], f[0], b.x, b.y);
+                            else
+                                mma_bf16(part[n], f[0][0], f[0][1], f[0][2], f[0][3], b.x, b.y);
+                            mma_bf16(part[n], f[1][0], f[1][1], f[1][2], f[1][3], b.z, b.w);
+                        }
                     }
                     if (u % GU == GU - 1) {
                         const float s0 = kGroups > 1 ? __shfl_sync(0xffffffffu, sf[0], u / GU, 4) : sf[0];
@@ -315,7 +326,7 @@ __global__ void __launch_bounds__(256, C::kCtas) linear_tiles_kernel(LinearArgs 
 #pragma unroll
             for (int p = 1; p < kMaxCluster; ++p) sum += v[p];
         }
-        static_cast<__nv_bfloat16 *>(a.y)[(size_t)(tok0 + t) * a.y_stride + row0 + r] = __float2bfloat16_rn(sum);
+        static_cast<X *>(a.y)[(size_t)(tok0 + t) * a.y_stride + row0 + r] = from_f32<X>(sum);
     }
     if (cluster > 1) cluster_sync_all();                            // the peers have read this CTA's parts
 }
@@ -339,7 +350,7 @@ cudaError_t launch_tiles(const LinearArgs &a, int sms, cudaStream_t st) {
         const double full = (double)(((long long)tiles * c + sms - 1) / sms) / c;
         if (full <= least && (c == 1 || (long long)tiles * c <= (long long)C::kCtas * sms)) least = full, cluster = c;
     }
-    const int x_vec = aligned16(a.x) && a.x_stride % 8 == 0;
+    const int x_vec = aligned16(a.x) && a.x_stride * sizeof(typename C::X) % 16 == 0;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((a.d_out + C::R - 1) / C::R * cluster, (a.n_tokens + C::T - 1) / C::T);
     cfg.blockDim = dim3(256);
@@ -370,19 +381,13 @@ cudaError_t launch_group(const LinearArgs &a, int sms, cudaStream_t st) {
 }
 
 // The tokens' tile.
-cudaError_t launch_bf16(const LinearArgs &a, int sms, cudaStream_t st) {
-    if (a.n_tokens <= 8) return launch_group<LinearTile<1, 2048, 4, 2>>(a, sms, st);
-    if (a.n_tokens <= 16) return launch_group<LinearTile<2, 2048, 4, 2>>(a, sms, st);
-    if (a.n_tokens <= 32) return launch_group<LinearTile<4, 1024, 4, 2>>(a, sms, st);
-    return launch_group<LinearTile<8, 512, 2, 2>>(a, sms, st);
-}
-
-template <typename T>
-cudaError_t launch_rows(const LinearArgs &a, cudaStream_t st) {
-    constexpr int TT = 8;
-    dim3 grid((a.d_out + 7) / 8, (a.n_tokens + TT - 1) / TT);
-    linear_rows_kernel<T, TT><<<grid, 256, 0, st>>>(a);
-    return cudaGetLastError();
+template <typename X>
+cudaError_t launch_linear(const LinearArgs &a, int sms, cudaStream_t st) {
+    constexpr int kCut = sizeof(X) == 4 ? 2 : 1;                    // shared memory holds fewer columns of three parts
+    if (a.n_tokens <= 8) return launch_group<LinearTile<X, 1, 2048 / kCut, 4, 2>>(a, sms, st);
+    if (a.n_tokens <= 16) return launch_group<LinearTile<X, 2, 2048 / kCut / kCut, 4, 2>>(a, sms, st);
+    if (a.n_tokens <= 32) return launch_group<LinearTile<X, 4, 1024 / kCut, 4, 2>>(a, sms, st);
+    return launch_group<LinearTile<X, 8, 512 / kCut, 2, 2>>(a, sms, st);
 }
 
 }  // namespace
@@ -409,8 +414,8 @@ extern "C" int lora_base_linear(const lora_base_linear_desc *d, void *stream) {
     LinearArgs a{d->x,        d->qweight,  d->scales, d->zeros, d->y,    (long long)d->x_stride,
                  (long long)d->y_stride, d->n_tokens, d->d_in,   d->d_out, d->group};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (d->dtype == LORA_DTYPE_F32) return launched("base_linear", launch_rows<float>(a, st));
     const int sms = sm_count();
     if (sms < 1) return fail(LORA_ERR_CUDA, "base_linear: no CUDA device");
-    return launched("base_linear", launch_bf16(a, sms, st));
+    return launched("base_linear", d->dtype == LORA_DTYPE_BF16 ? launch_linear<__nv_bfloat16>(a, sms, st)
+                                                               : launch_linear<float>(a, sms, st));
 }
