@@ -690,7 +690,7 @@ int lora_rope(const lora_rope_desc *desc, void *stream);
  * [0, n_tokens]. Rows that belong to no request are not written.
  * head_dim: a multiple of 8 up to 128. The q, out and cache pointers and
  * strides must be multiples of 16 bytes, no stride negative. n_tokens *
- * n_heads: at most 2^30. A bf16 call queues two kernels, an fp32 call one.
+ * n_heads: at most 2^30. A call queues two kernels.
  */
 typedef struct {
     const void *q;            /* [n_tokens][n_heads][head_dim] */

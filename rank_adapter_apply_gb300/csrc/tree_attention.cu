@@ -11,92 +11,6 @@ namespace {
 using namespace step;
 using namespace tree;
 
-// Request that owns node `t`: the last b with node_starts[b] <= t, or -1.
-__device__ int request_of(const TreeArgs &a, int t) {
-    int lo = 0, hi = a.n_requests;           // invariant: start(lo) <= t < start(hi), if any
-    if (node_start(a, 0) > t || node_start(a, a.n_requests) <= t) return -1;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (node_start(a, mid) <= t) lo = mid; else hi = mid;
-    }
-    return lo;
-}
-
-__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
-
-// One CTA of four warps for each query row; a warp takes every fourth key, a
-// lane four elements of the head; the running maximum and sum in fp32, the
-// four warps joined at the end.
-template <typename T>
-__global__ void __launch_bounds__(128) tree_rows_kernel(TreeArgs a) {
-    const int t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int b = request_of(a, t);
-    if (b < 0) return;
-    const int start = node_start(a, b), nodes = node_start(a, b + 1) - start, self = t - start;
-    const long long ctx = max(a.ctx_lens[b], 0);
-    long long keys = ctx + nodes;
-    const long long room = (long long)a.table_pages * a.page_size;
-    if (keys > room) keys = room;
-    const bool mine = lane * 4 < a.head_dim;
-    const float4 q = mine ? load4(static_cast<const T *>(a.q) + t * a.q_token + h * a.q_head + lane * 4)
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
-    const long long head_at = (long long)(h / (a.n_heads / a.n_kv)) * a.c_head + lane * 4;
-    const int32_t *pages = a.page_table + b * a.table_stride;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (long long p = warp; p < keys; p += 4) {
-        if (p >= ctx) {
-            const long long j = p - ctx;
-            bool sees = j <= self;
-            if (a.tree_mask)
-                sees = j < 64ll * a.mask_words && (a.tree_mask[(size_t)t * a.mask_words + j / 64] >> (j % 64) & 1);
-            if (!sees) continue;
-        }
-        const int page = pages[p / a.page_size];
-        if (page < 0 || page >= a.n_pages) continue;
-        const long long at = page * a.c_page + p % a.page_size * a.c_slot + head_at;
-        float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-        if (mine) {
-            k = load4(static_cast<const T *>(a.k_cache) + at);
-            v = load4(static_cast<const T *>(a.v_cache) + at);
-        }
-        const float s = warp_sum(q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w) * a.scale;
-        const float m2 = fmaxf(m, s);
-        if (m2 == -INFINITY) continue;
-        const float keep = expf(m - m2), w = expf(s - m2);
-        m = m2;
-        l = l * keep + w;
-        o.x = o.x * keep + w * v.x;
-        o.y = o.y * keep + w * v.y;
-        o.z = o.z * keep + w * v.z;
-        o.w = o.w * keep + w * v.w;
-    }
-    __shared__ float sm[4], sl[4];
-    __shared__ float4 so[4][32];
-    if (lane == 0) sm[warp] = m, sl[warp] = l;
-    so[warp][lane] = o;
-    __syncthreads();
-    if (warp != 0) return;
-    const float top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    float sum = 0.f;
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (top != -INFINITY) {
-        for (int w = 0; w < 4; ++w) {
-            const float f = expf(sm[w] - top);
-            sum += f * sl[w];
-            o.x += f * so[w][lane].x;
-            o.y += f * so[w][lane].y;
-            o.z += f * so[w][lane].z;
-            o.w += f * so[w][lane].w;
-        }
-        const float r = 1.f / sum;
-        o = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
-    }
-    if (mine) store4(static_cast<T *>(a.out) + t * a.o_token + h * a.o_head + lane * 4, o);
-    if (a.lse && lane == 0) a.lse[(size_t)t * a.n_heads + h] = top == -INFINITY ? -INFINITY : top + logf(sum);
-}
-
 // ---- bf16, up to 32 rows a tile: mma.sync over the paged cache -------------------
 
 constexpr int kStages = 3;
@@ -445,7 +359,7 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
 // Join the parts of the unit that goes on past CTA blockIdx.x's share. A warp
 // takes a row, or, where there are many parts, the block takes one row after
 // another and a warp every eighth part of it.
-template <int DP, int M>
+template <typename T, int DP, int M>
 __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan, int m_rows) {
     constexpr int kVec = DP / 32, kMany = 24;
     __shared__ float so[8][DP];
@@ -509,11 +423,17 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan, i
         const long long token = start + row / group;
         const bool none = m == -INFINITY;
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + token * a.o_token + head * a.o_head + lane * kVec;
-        if (lane * kVec < a.head_dim)
+        T *out = static_cast<T *>(a.out) + token * a.o_token + (long long)head * a.o_head + lane * kVec;
+        if (lane * kVec < a.head_dim) {
 #pragma unroll
-            for (int e = 0; e < kVec; e += 2)
-                *reinterpret_cast<uint32_t *>(out + e) = none ? 0u : pack_bf16(o[e] * inv, o[e + 1] * inv);
+            for (int e = 0; e < kVec; e += 2) {
+                const float x = none ? 0.f : o[e] * inv, y = none ? 0.f : o[e + 1] * inv;
+                if constexpr (sizeof(T) == 2)
+                    *reinterpret_cast<uint32_t *>(out + e) = pack_bf16(x, y);
+                else
+                    *reinterpret_cast<float2 *>(out + e) = make_float2(x, y);
+            }
+        }
         if (a.lse && lane == 0) a.lse[token * a.n_heads + head] = none ? -INFINITY : m * 0.6931471805599453f + logf(l);
     }
 }
@@ -545,9 +465,9 @@ cudaError_t launch_tiles(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <int DP, int M>
+template <typename T, int DP, int M>
 cudaError_t launch_join(const TreeArgs &a, const Plan &plan, int m_rows, cudaStream_t st) {
-    return launch_pdl(tree_join_kernel<DP, M>, dim3(plan.ctas, M / 8), dim3(256), 0, st, a, plan, m_rows);
+    return launch_pdl(tree_join_kernel<T, DP, M>, dim3(plan.ctas, M / 8), dim3(256), 0, st, a, plan, m_rows);
 }
 
 template <int DP>
@@ -556,15 +476,24 @@ cudaError_t launch_bf16(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
     cudaError_t e = cudaErrorNotSupported;
     if (rows == 128) {
         e = launch_tc(a, plan, st);
-        if (e == cudaSuccess) return launch_join<DP, 128>(a, plan, tc_rows(a), st);
+        if (e == cudaSuccess) return launch_join<__nv_bfloat16, DP, 128>(a, plan, tc_rows(a), st);
     }
     if (rows == 16) {
         e = launch_tiles<DP, 1>(a, plan, st);
-        return e != cudaSuccess ? e : launch_join<DP, 16>(a, plan, 16, st);
+        return e != cudaSuccess ? e : launch_join<__nv_bfloat16, DP, 16>(a, plan, 16, st);
     }
     if (e != cudaErrorNotSupported) return e;
     e = launch_tiles<DP, 2>(a, plan, st);
-    return e != cudaSuccess ? e : launch_join<DP, 32>(a, plan, 32, st);
+    return e != cudaSuccess ? e : launch_join<__nv_bfloat16, DP, 32>(a, plan, 32, st);
+}
+
+template <int DP>
+cudaError_t launch_fp32(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
+    // rows beyond a request's cost their FMAs all the same: 16 up to an average of 16, as below
+    const int rows = (double)a.n_tokens * (a.n_heads / a.n_kv) / a.n_requests <= 16.0 ? 16 : 64;
+    const cudaError_t e = launch_f32(a, plan, rows, st);
+    if (e != cudaSuccess) return e;
+    return rows == 16 ? launch_join<float, DP, 16>(a, plan, 16, st) : launch_join<float, DP, 64>(a, plan, 64, st);
 }
 
 bool shape_ok(int n_requests, int n_tokens, int n_heads, int n_kv, int head_dim, int dtype) {
@@ -582,7 +511,7 @@ extern "C" size_t lora_tree_attention_workspace_bytes(int n_requests, int n_toke
                                                       int head_dim, int dtype) {
     if (!shape_ok(n_requests, n_tokens, n_heads, n_kv_heads, head_dim, dtype)) return 0;
     // the largest grid of any GPU this library is built for: the size does not depend on the device
-    return dtype == LORA_DTYPE_BF16 ? plan_bytes(kMaxCtas) : 256;
+    return plan_bytes(kMaxCtas);
 }
 
 extern "C" int lora_tree_attention(const lora_tree_attention_desc *d, void *stream) {
@@ -622,20 +551,19 @@ extern "C" int lora_tree_attention(const lora_tree_attention_desc *d, void *stre
                d->out_token, d->out_head, d->table_stride, d->n_pages, d->scale,   d->page_size,  d->table_pages,
                d->mask_words, d->n_requests, d->n_tokens, d->n_heads, d->n_kv_heads, d->head_dim};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (d->dtype == LORA_DTYPE_BF16) {
-        const int sms = sm_count();
-        if (sms < 1) return fail(LORA_ERR_CUDA, "tree_attention: no CUDA device");
-        Plan plan;
-        plan.ctas = std::min(2 * sms, kMaxCtas);
-        char *ws = static_cast<char *>(d->workspace);
-        plan.part = reinterpret_cast<float *>(ws);
-        plan.stat = reinterpret_cast<float2 *>(plan.part + 2 * (size_t)plan.ctas * kMaxRows * 128);
-        plan.seg = reinterpret_cast<int4 *>(plan.stat + 2 * (size_t)plan.ctas * kMaxRows);
-        return launched("tree_attention",
-                        d->head_dim <= 64 ? launch_bf16<64>(a, plan, st) : launch_bf16<128>(a, plan, st));
-    }
-    tree_rows_kernel<float><<<dim3(d->n_tokens, d->n_heads), 128, 0, st>>>(a);
-    return launched("tree_attention", cudaGetLastError());
+    const int sms = sm_count();
+    if (sms < 1) return fail(LORA_ERR_CUDA, "tree_attention: no CUDA device");
+    Plan plan;
+    plan.ctas = std::min(2 * sms, kMaxCtas);
+    plan.part = static_cast<float *>(d->workspace);
+    plan.stat = reinterpret_cast<float2 *>(plan.part + 2 * (size_t)plan.ctas * kMaxRows * 128);
+    plan.seg = reinterpret_cast<int4 *>(plan.stat + 2 * (size_t)plan.ctas * kMaxRows);
+    cudaError_t e;
+    if (d->dtype == LORA_DTYPE_BF16)
+        e = d->head_dim <= 64 ? launch_bf16<64>(a, plan, st) : launch_bf16<128>(a, plan, st);
+    else
+        e = d->head_dim <= 64 ? launch_fp32<64>(a, plan, st) : launch_fp32<128>(a, plan, st);
+    return launched("tree_attention", e);
 }
 
 extern "C" int lora_step_wait_timeouts(uint64_t *count) {

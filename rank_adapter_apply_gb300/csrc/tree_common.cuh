@@ -200,8 +200,11 @@ __device__ __forceinline__ long long key_offset(const TreeArgs &a, const Cursor 
 bool tc_takes(const TreeArgs &a);
 int tc_rows(const TreeArgs &a);
 cudaError_t launch_tc(const TreeArgs &a, const Plan &plan, cudaStream_t st);
-// CTAs of it on the current device whose bounded waits gave up so far.
+// CTAs of its kernel on the current device whose bounded waits gave up so far.
 cudaError_t read_timeouts(unsigned *count);
+
+// tree_attention_f32.cu: row tiles of 16 or 64 in fp32.
+cudaError_t launch_f32(const TreeArgs &a, const Plan &plan, int m_rows, cudaStream_t st);
 
 }  // namespace tree
 }  // namespace lora
