@@ -31,7 +31,7 @@ struct Tile {
     // written while the tile one stage-count before it may still be read), then the search's scratch
     static constexpr int kRing = kStages + 1;
     static constexpr int kOff = kStages * kStage, kValid = kOff + kRing * kTileKeys * 8;
-    static constexpr int kStart = kValid + kRing * 8, kSmem = kStart + 64;
+    static constexpr int kStart = kValid + kRing * 8, kSmem = kStart + 96;
 };
 
 template <int DP, int WM, int WN>
@@ -357,85 +357,126 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
 }
 
 // Join the parts of the unit that goes on past CTA blockIdx.x's share. A warp
-// takes a row, or, where there are many parts, the block takes one row after
-// another and a warp every eighth part of it.
-template <typename T, int DP, int M>
+// takes kR rows, with kAhead parts of each in flight; with kR = 1, for few units cut
+// into many parts, the block may take one row after another, a warp every eighth
+// part of it. (Most units have two or three parts and most blocks little to do: as
+// many blocks as rows / 8 cost 8 us more than rows / 32 with 128 rows to a tile.)
+template <int DP>
+struct Joined {
+    static constexpr int V = DP / 32;                    // columns of a lane
+    float o[V], m = -INFINITY, l = 0.f;
+    __device__ __forceinline__ void add(float2 ml, const float (&v)[V]) {
+        const float t = fmaxf(m, ml.x), b = t == -INFINITY ? 0.f : t;
+        const float f = exp2_fast(m - b), h = exp2_fast(ml.x - b);
+        m = t;
+        l = l * f + ml.y * h;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = o[e] * f + v[e] * h;
+    }
+};
+
+template <typename T, int DP>
+__device__ __forceinline__ void store_joined(const TreeArgs &a, const int4 &seg, int start, int row, const Joined<DP> &j) {
+    constexpr int V = Joined<DP>::V;
+    const int lane = threadIdx.x & 31, group = a.n_heads / a.n_kv, head = seg.z * group + row % group;
+    const long long token = start + row / group;
+    const bool none = j.m == -INFINITY;
+    const float inv = j.l > 0.f ? 1.f / j.l : j.l;       // a NaN stays one
+    T *out = static_cast<T *>(a.out) + token * a.o_token + (long long)head * a.o_head + lane * V;
+    if (lane * V < a.head_dim) {
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+            const float x = none ? 0.f : j.o[e] * inv, y = none ? 0.f : j.o[e + 1] * inv;
+            if constexpr (sizeof(T) == 2)
+                *reinterpret_cast<uint32_t *>(out + e) = pack_bf16(x, y);
+            else
+                *reinterpret_cast<float2 *>(out + e) = make_float2(x, y);
+        }
+    }
+    if (a.lse && lane == 0) a.lse[token * a.n_heads + head] = none ? -INFINITY : j.m * 0.6931471805599453f + logf(j.l);
+}
+
+template <typename T, int DP, int M, int kR>
 __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan, int m_rows) {
-    constexpr int kVec = DP / 32, kMany = 24;
+    constexpr int V = Joined<DP>::V, kAhead = kR == 1 ? 4 : 2, kMany = 24;
     __shared__ float so[8][DP];
     __shared__ float2 sm[8];
     grid_dependency_wait();
     const int4 seg = plan.seg[blockIdx.x];
     if (seg.w == 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = a.n_heads / a.n_kv;
-    const int start = node_start(a, seg.x), rows = min((node_start(a, seg.x + 1) - start) * group - seg.y * m_rows, m_rows);
-    const bool many = seg.w > kMany;
-    for (int i = 0; i < (many ? 8 : 1); ++i) {
-        const int r = blockIdx.y * 8 + (many ? i : warp);
-        if (r >= rows) break;                            // rows of a block are alike in `many`: no barrier is missed
-        float o[kVec], m = -INFINITY, l = 0.f;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) o[e] = 0.f;
-        auto add = [&](float2 ml, const float *v) {
-            const float t = fmaxf(m, ml.x), b = t == -INFINITY ? 0.f : t;
-            const float f = exp2_fast(m - b), h = exp2_fast(ml.x - b);
-            m = t;
-            l = l * f + ml.y * h;
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) o[e] = o[e] * f + v[e] * h;
-        };
-        constexpr int kAhead = 4;                        // parts whose loads are in flight together
-        const int step = many ? 8 : 1;
-        for (int p = many ? warp : 0; p < seg.w; p += kAhead * step) {
-            float v[kAhead][kVec];
-            float2 ml[kAhead];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int part = p + u * step;
-                ml[u] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) v[u][e] = 0.f;
-                if (part < seg.w) {
-                    const long long slot = part == 0 ? 2ll * blockIdx.x + 1 : 2ll * (blockIdx.x + part);
-                    ml[u] = plan.stat[slot * M + r];
-                    const float *src = plan.part + (slot * M + r) * DP + lane * kVec;
-#pragma unroll
-                    for (int e = 0; e < kVec; ++e) v[u][e] = src[e];
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) add(ml[u], v[u]);
+    const int start = node_start(a, seg.x);
+    const int rows = min((node_start(a, seg.x + 1) - start) * group - seg.y * m_rows, m_rows);
+    auto read = [&](int part, int r, float2 &ml, float (&v)[V]) {
+        const long long slot = part == 0 ? 2ll * blockIdx.x + 1 : 2ll * (blockIdx.x + part);
+        ml = plan.stat[slot * M + r];
+        const float *src = plan.part + (slot * M + r) * DP + lane * V;
+        if constexpr (V == 4) {
+            *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(src);
+        } else {
+            *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(src);
         }
-        if (many) {
+    };
+    if (kR == 1 && seg.w > kMany) {
+        for (int i = 0; i < 8; ++i) {
+            const int r = blockIdx.y * 8 + i;
+            if (r >= rows) break;
+            Joined<DP> j;
+#pragma unroll
+            for (int e = 0; e < V; ++e) j.o[e] = 0.f;
+            for (int p = warp; p < seg.w; p += kAhead * 8) {
+                float v[kAhead][V];
+                float2 ml[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+                    if (p + u * 8 < seg.w) read(p + u * 8, r, ml[u], v[u]);
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+                    if (p + u * 8 < seg.w) j.add(ml[u], v[u]);
+            }
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) so[warp][lane * kVec + e] = o[e];
-            if (lane == 0) sm[warp] = make_float2(m, l);
+            for (int e = 0; e < V; ++e) so[warp][lane * V + e] = j.o[e];
+            if (lane == 0) sm[warp] = make_float2(j.m, j.l);
             __syncthreads();
             if (warp != i) continue;
-            m = -INFINITY;
-            l = 0.f;
+            Joined<DP> all;
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) o[e] = 0.f;
-            for (int w = 0; w < 8; ++w) add(sm[w], &so[w][lane * kVec]);
-        }
-        const int row = seg.y * m_rows + r, head = seg.z * group + row % group;
-        const long long token = start + row / group;
-        const bool none = m == -INFINITY;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        T *out = static_cast<T *>(a.out) + token * a.o_token + (long long)head * a.o_head + lane * kVec;
-        if (lane * kVec < a.head_dim) {
+            for (int e = 0; e < V; ++e) all.o[e] = 0.f;
+            for (int w = 0; w < 8; ++w) {
+                float v[V];
 #pragma unroll
-            for (int e = 0; e < kVec; e += 2) {
-                const float x = none ? 0.f : o[e] * inv, y = none ? 0.f : o[e + 1] * inv;
-                if constexpr (sizeof(T) == 2)
-                    *reinterpret_cast<uint32_t *>(out + e) = pack_bf16(x, y);
-                else
-                    *reinterpret_cast<float2 *>(out + e) = make_float2(x, y);
+                for (int e = 0; e < V; ++e) v[e] = so[w][lane * V + e];
+                all.add(sm[w], v);
             }
+            store_joined<T, DP>(a, seg, start, seg.y * m_rows + r, all);
         }
-        if (a.lse && lane == 0) a.lse[token * a.n_heads + head] = none ? -INFINITY : m * 0.6931471805599453f + logf(l);
+        return;
     }
+    const int r0 = (blockIdx.y * 8 + warp) * kR;
+    if (r0 >= rows) return;
+    Joined<DP> j[kR];
+#pragma unroll
+    for (int k = 0; k < kR; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e) j[k].o[e] = 0.f;
+    for (int p = 0; p < seg.w; p += kAhead) {
+        float v[kAhead][kR][V];
+        float2 ml[kAhead][kR];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int k = 0; k < kR; ++k)
+                if (p + u < seg.w && r0 + k < rows) read(p + u, r0 + k, ml[u][k], v[u][k]);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+            for (int k = 0; k < kR; ++k)
+                if (p + u < seg.w && r0 + k < rows) j[k].add(ml[u][k], v[u][k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kR; ++k)
+        if (r0 + k < rows) store_joined<T, DP>(a, seg, start, seg.y * m_rows + r0 + k, j[k]);
 }
 
 constexpr int kMaxRows = 128;
@@ -467,7 +508,13 @@ cudaError_t launch_tiles(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
 
 template <typename T, int DP, int M>
 cudaError_t launch_join(const TreeArgs &a, const Plan &plan, int m_rows, cudaStream_t st) {
-    return launch_pdl(tree_join_kernel<T, DP, M>, dim3(plan.ctas, M / 8), dim3(256), 0, st, a, plan, m_rows);
+    // few units: each is cut into many parts, and the rows need the blocks
+    const double units = (double)a.n_requests * a.n_kv *
+                         std::max(1.0, (double)a.n_tokens * (a.n_heads / a.n_kv) / a.n_requests / m_rows);
+    if (units * 8 < plan.ctas)
+        return launch_pdl(tree_join_kernel<T, DP, M, 1>, dim3(plan.ctas, M / 8), dim3(256), 0, st, a, plan, m_rows);
+    constexpr int kR = M >= 32 ? 4 : 2;
+    return launch_pdl(tree_join_kernel<T, DP, M, kR>, dim3(plan.ctas, M / 8 / kR), dim3(256), 0, st, a, plan, m_rows);
 }
 
 template <int DP>

@@ -117,65 +117,83 @@ __device__ __noinline__ inline uint64_t seen_keys(const TreeArgs &a, const Reque
 }
 
 // A CTA's share of the tiles: [lo, hi) of total, dealt to `used` CTAs, and where it
-// starts. false: it has none. scratch: kWarps + 2 words. Every thread calls it.
+// starts. false: it has none. scratch: 2 kWarps + 2 words. Every thread calls it.
 struct Share {
     long long lo, hi, total, used;
     Cursor start;
 };
 
+// x * y / z, in 32 bits where they will do.
+__device__ __forceinline__ long long scaled(long long x, long long y, long long z) {
+    const long long p = x * y;
+    return p >> 32 == 0 ? (long long)((uint32_t)p / (uint32_t)z) : p / z;
+}
+
 template <int kThreads>
 __device__ inline bool find_share(const TreeArgs &a, int m_rows, long long *scratch, Share &s) {
     constexpr int kWarps = kThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long mine = 0;
+    // tiles of the requests tid, tid + kThreads, ..; of the first of them and its prefix sum, which is all in most calls
+    Request mine{};
+    long long n0 = 0, sum = 0;
     for (int b = tid; b < a.n_requests; b += kThreads) {
         const Request r = request(a, b, m_rows);
-        mine += (long long)r.row_tiles * r.key_tiles * a.n_kv;
+        const long long n = (long long)r.row_tiles * r.key_tiles * a.n_kv;
+        if (b == tid) mine = r, n0 = n;
+        sum += n;
     }
+    long long upto = n0, all = sum;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) scratch[warp] = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (a.n_requests > kThreads) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    if (lane == 31) scratch[2 + warp] = upto, scratch[2 + kWarps + warp] = a.n_requests > kThreads ? all : upto;
+    if (tid == 0) scratch[0] = -1;
     __syncthreads();
     s.total = 0;
-    for (int w = 0; w < kWarps; ++w) s.total += scratch[w];
+    long long before = 0;
+    for (int w = 0; w < kWarps; ++w) s.total += scratch[2 + kWarps + w];
     s.used = min((long long)gridDim.x, s.total);
     if (blockIdx.x >= s.used) return false;
-    s.lo = s.total * blockIdx.x / s.used;
-    s.hi = s.total * (blockIdx.x + 1) / s.used;
-    __syncthreads();
-    long long before = 0;
+    s.lo = scaled(s.total, blockIdx.x, s.used);
+    s.hi = scaled(s.total, blockIdx.x + 1, s.used);
     for (int b0 = 0; b0 < a.n_requests; b0 += kThreads) {    // ends in the chunk that holds tile lo < total
         const int b = b0 + tid;
-        long long n = 0;
-        if (b < a.n_requests) {
-            const Request r = request(a, b, m_rows);
-            n = (long long)r.row_tiles * r.key_tiles * a.n_kv;
-        }
-        long long upto = n;
+        if (b0 > 0) {
+            n0 = 0;
+            if (b < a.n_requests) {
+                mine = request(a, b, m_rows);
+                n0 = (long long)mine.row_tiles * mine.key_tiles * a.n_kv;
+            }
+            upto = n0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            __syncthreads();
+            if (lane == 31) scratch[2 + warp] = upto;
+            __syncthreads();
         }
-        if (lane == 31) scratch[2 + warp] = upto;
-        if (tid == 0) scratch[0] = -1;
-        __syncthreads();
         for (int w = 0; w < warp; ++w) upto += scratch[2 + w];
         upto += before;
-        if (upto - n <= s.lo && s.lo < upto) scratch[0] = b, scratch[1] = upto - n;
+        if (upto - n0 <= s.lo && s.lo < upto) scratch[0] = b, scratch[1] = upto - n0;
         for (int w = 0; w < kWarps; ++w) before += scratch[2 + w];
         __syncthreads();
         if (scratch[0] >= 0) break;
-        __syncthreads();
     }
     if (scratch[0] < 0) return false;                        // not reached
     s.start.b = (int)scratch[0];
     s.start.r = request(a, s.start.b, m_rows);
-    long long at = s.lo - scratch[1];
-    s.start.tile = (int)(at % s.start.r.key_tiles);
-    at /= s.start.r.key_tiles;
-    s.start.head = (int)(at % a.n_kv);
-    s.start.row_tile = (int)(at / a.n_kv);
+    const long long at = s.lo - scratch[1], unit = scaled(at, 1, s.start.r.key_tiles);
+    s.start.tile = (int)(at - unit * s.start.r.key_tiles);
+    s.start.row_tile = (int)scaled(unit, 1, a.n_kv);
+    s.start.head = (int)(unit - (long long)s.start.row_tile * a.n_kv);
     return true;
 }
 
@@ -183,7 +201,8 @@ __device__ inline bool find_share(const TreeArgs &a, int m_rows, long long *scra
 // the share: CTA floor(((x + 1) used - 1) / total) has tile x.
 __device__ __forceinline__ int parts_of(const Share &s, const Cursor &c, int i) {
     const long long x = s.lo + i + (c.r.key_tiles - 1 - c.tile);
-    return (int)(((x + 1) * s.used - 1) / s.total) - (int)blockIdx.x + 1;
+    const long long p = (x + 1) * s.used - 1;
+    return (int)scaled(p, 1, s.total) - (int)blockIdx.x + 1;
 }
 
 // Element offset of key `key` of the cursor's tile in the caches, -1: nobody sees it.
