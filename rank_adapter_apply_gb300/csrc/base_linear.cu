@@ -165,6 +165,8 @@ __global__ void __launch_bounds__(256, C::kCtas) linear_tiles_kernel(LinearArgs 
     using X = typename C::X;
     const X *x = static_cast<const X *>(a.x) + (size_t)tok0 * a.x_stride;
 
+    grid_dependency_wait();
+    grid_launch_dependents();
     // ---- this lane's rows: words, scales and zeros of a block. A row past d_out reads the last row (nobody stores
     // what comes of it), and columns past d_in meet an x of zero.
     const int r_in = warp * 16 + g4;                                // and r_in + 8
@@ -351,19 +353,8 @@ cudaError_t launch_tiles(const LinearArgs &a, int sms, cudaStream_t st) {
         if (full <= least && (c == 1 || (long long)tiles * c <= (long long)C::kCtas * sms)) least = full, cluster = c;
     }
     const int x_vec = aligned16(a.x) && a.x_stride * sizeof(typename C::X) % 16 == 0;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((a.d_out + C::R - 1) / C::R * cluster, (a.n_tokens + C::T - 1) / C::T);
-    cfg.blockDim = dim3(256);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a, cluster, x_vec);
+    const dim3 grid((a.d_out + C::R - 1) / C::R * cluster, (a.n_tokens + C::T - 1) / C::T);
+    return launch_step(kernel, grid, dim3(256), C::kSmem, cluster, st, a, cluster, x_vec);
 }
 
 template <class C, int GU>

@@ -110,6 +110,8 @@ __device__ __forceinline__ long long cache_place(const RopeArgs &a, long long t)
 // Any layout: one warp per head row of one token, a lane takes pairs one by one.
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(256) rope_rows_kernel(RopeArgs a) {
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int rows = a.n_heads + 2 * a.n_kv;
     const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -149,6 +151,8 @@ __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
 template <typename T, bool kInterleaved, int kRows>
 __global__ void __launch_bounds__(512) rope_vectors_kernel(RopeArgs a) {
     constexpr int N = 16 / sizeof(T);
+    grid_dependency_wait();
+    grid_launch_dependents();
     const long long t = blockIdx.x;
     const int u = threadIdx.x, rows = a.n_heads + 2 * a.n_kv, r0 = (blockIdx.y * blockDim.y + threadIdx.y) * kRows;
     const int vectors = a.head_dim / N, rot_vectors = a.rot_dim / N, half = a.rot_dim / 2;
@@ -233,28 +237,22 @@ bool by_vectors(const RopeArgs &a, bool interleaved) {
 }
 
 template <typename T, bool kInterleaved, int kRows>
-void launch_vectors(const RopeArgs &a, cudaStream_t st) {
+cudaError_t launch_vectors(const RopeArgs &a, cudaStream_t st) {
     constexpr int N = 16 / sizeof(T);
     const int rows = a.n_heads + 2 * a.n_kv, units = (a.head_dim / N + 1) / 2;
     const int need = (rows + kRows - 1) / kRows;             // rows of threads
     const int fit = 256 / units > 0 ? 256 / units : 1;
     const int blocks = (need + fit - 1) / fit, each = (need + blocks - 1) / blocks;
-    rope_vectors_kernel<T, kInterleaved, kRows><<<dim3(a.n_tokens, blocks), dim3(units, each), 0, st>>>(a);
+    return launch_step(rope_vectors_kernel<T, kInterleaved, kRows>, dim3(a.n_tokens, blocks), dim3(units, each), 0, 1, st, a);
 }
 
 template <typename T, bool kInterleaved>
 cudaError_t launch_rope(const RopeArgs &a, int sms, cudaStream_t st) {
     const long long rows = (long long)a.n_tokens * (a.n_heads + 2 * a.n_kv);
-    if (by_vectors<T>(a, kInterleaved)) {
+    if (by_vectors<T>(a, kInterleaved))
         // rows of a thread: one where few rows leave SMs idle anyway
-        if (rows <= 64ll * sms)
-            launch_vectors<T, kInterleaved, 1>(a, st);
-        else
-            launch_vectors<T, kInterleaved, 4>(a, st);
-    } else {
-        rope_rows_kernel<T, kInterleaved><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(a);
-    }
-    return cudaGetLastError();
+        return rows <= 64ll * sms ? launch_vectors<T, kInterleaved, 1>(a, st) : launch_vectors<T, kInterleaved, 4>(a, st);
+    return launch_step(rope_rows_kernel<T, kInterleaved>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, 1, st, a);
 }
 
 }  // namespace

@@ -41,6 +41,29 @@ inline int sm_count() {
     return n;
 }
 
+// Launch in clusters of `cluster` CTAs (1: none) with programmatic stream
+// serialization: the kernel calls grid_dependency_wait() before it touches
+// memory, so its launch alone overlaps the end of the kernel before it.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_step(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t st,
+                               const Args &...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 inline bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 inline bool known_dtype(int dtype) { return dtype == LORA_DTYPE_F32 || dtype == LORA_DTYPE_BF16; }
 

@@ -46,7 +46,8 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
     const int wm = warp % WM, wn = warp / WM, g4 = lane >> 2, t4 = lane & 3;
     const int group = a.n_heads / a.n_kv;
 
-    grid_launch_dependents();                            // join_kernel waits for this grid's end itself
+    grid_dependency_wait();
+    grid_launch_dependents();                            // the join kernel waits for this grid's end itself
     if (tid == 0) plan.seg[blockIdx.x] = make_int4(0, 0, 0, 0);
     Share share;
     if (!find_share<T::kThreads>(a, T::M, scratch, share)) return;
@@ -402,6 +403,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan, i
     __shared__ float so[8][DP];
     __shared__ float2 sm[8];
     grid_dependency_wait();
+    grid_launch_dependents();
     const int4 seg = plan.seg[blockIdx.x];
     if (seg.w == 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = a.n_heads / a.n_kv;
@@ -502,8 +504,7 @@ cudaError_t launch_tiles(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         set_device_bit(ready);
     }
-    kernel<<<plan.ctas, T::kThreads, T::kSmem, st>>>(a, plan);
-    return cudaGetLastError();
+    return launch_step(kernel, dim3(plan.ctas), dim3(T::kThreads), T::kSmem, 1, st, a, plan);
 }
 
 template <typename T, int DP, int M>
@@ -512,9 +513,9 @@ cudaError_t launch_join(const TreeArgs &a, const Plan &plan, int m_rows, cudaStr
     const double units = (double)a.n_requests * a.n_kv *
                          std::max(1.0, (double)a.n_tokens * (a.n_heads / a.n_kv) / a.n_requests / m_rows);
     if (units * 8 < plan.ctas)
-        return launch_pdl(tree_join_kernel<T, DP, M, 1>, dim3(plan.ctas, M / 8), dim3(256), 0, st, a, plan, m_rows);
+        return launch_step(tree_join_kernel<T, DP, M, 1>, dim3(plan.ctas, M / 8), dim3(256), 0, 1, st, a, plan, m_rows);
     constexpr int kR = M >= 32 ? 4 : 2;
-    return launch_pdl(tree_join_kernel<T, DP, M, kR>, dim3(plan.ctas, M / 8 / kR), dim3(256), 0, st, a, plan, m_rows);
+    return launch_step(tree_join_kernel<T, DP, M, kR>, dim3(plan.ctas, M / 8 / kR), dim3(256), 0, 1, st, a, plan, m_rows);
 }
 
 template <int DP>

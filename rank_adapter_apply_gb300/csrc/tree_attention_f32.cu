@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(TreeArgs a, Plan 
     __shared__ uint32_t valid[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = tid >> 4, l16 = tid & 15;
     const int group = a.n_heads / a.n_kv, row0 = half * R;     // this half-warp's rows of the tile
+    grid_dependency_wait();
     grid_launch_dependents();                                  // the join kernel waits for this grid's end itself
     if (tid == 0) plan.seg[blockIdx.x] = make_int4(0, 0, 0, 0);
     Share share;
@@ -231,8 +232,7 @@ cudaError_t launch(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         set_device_bit(ready);
     }
-    kernel<<<plan.ctas, kThreads, F32<DP, M>::kSmem, st>>>(a, plan);
-    return cudaGetLastError();
+    return launch_step(kernel, dim3(plan.ctas), dim3(kThreads), F32<DP, M>::kSmem, 1, st, a, plan);
 }
 
 }  // namespace

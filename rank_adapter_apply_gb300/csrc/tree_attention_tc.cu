@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
     const Plan &plan = args.plan;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = a.n_heads / a.n_kv;
     const int rows = kRows / group * group;            // of a tile
+    grid_dependency_wait();
     grid_launch_dependents();                          // the join kernel waits for this grid's end itself
     if (tid == 0) plan.seg[blockIdx.x] = make_int4(0, 0, 0, 0);
     Share share;
@@ -579,8 +580,7 @@ cudaError_t launch(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
     if (!encode(&args.q, a.q, 3, q_dims, q_strides, q_box) || !encode(&args.k, a.k_cache, 4, c_dims, c_strides, c_box) ||
         !encode(&args.v, a.v_cache, 4, c_dims, c_strides, c_box))
         return cudaErrorNotSupported;
-    tree_tc_kernel<DP><<<plan.ctas, kThreads, Tc<DP>::kSmem, st>>>(args);
-    return cudaGetLastError();
+    return launch_step(tree_tc_kernel<DP>, dim3(plan.ctas), dim3(kThreads), Tc<DP>::kSmem, 1, st, args);
 }
 
 }  // namespace

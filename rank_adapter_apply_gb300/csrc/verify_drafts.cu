@@ -104,6 +104,8 @@ template <typename T, bool kDraft, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(VerifyArgs a, int cluster) {
     __shared__ Shared<kThreads> sh;
     const int b = blockIdx.x / cluster, rank = blockIdx.x % cluster, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int start = min(max(a.node_starts[b], 0), a.n_nodes);
     const int nodes = min(max(min(a.node_starts[b + 1], a.n_nodes) - start, 0), kMaxNodes);
     const T *target = static_cast<const T *>(a.target), *draft = static_cast<const T *>(a.draft);
@@ -245,18 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(Verif
 
 template <typename T, bool kDraft, int kThreads>
 cudaError_t launch_threads(const VerifyArgs &a, int cluster, cudaStream_t st) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)a.n_requests * cluster);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, verify_kernel<T, kDraft, kThreads>, a, cluster);
+    return launch_step(verify_kernel<T, kDraft, kThreads>, dim3((unsigned)a.n_requests * cluster), dim3(kThreads), 0, cluster,
+                       st, a, cluster);
 }
 
 // CTAs for a request: 1024 threads of them fit an SM, and few requests are cut
