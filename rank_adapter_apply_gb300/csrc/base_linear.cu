@@ -1,6 +1,7 @@
 // lora_base_linear: y = W x for a few tokens, W in 4 bits with group scales.
 #include "step_util.cuh"
 
+#include <algorithm>
 #include <atomic>
 
 namespace lora {
@@ -20,10 +21,11 @@ struct LinearArgs {
 
 constexpr int kMaxCluster = 8;
 
-// A CTA takes 128 rows of W, 16 to a warp, and, as one of the CTAs of a cluster, a
-// range of the columns. Each warp streams its rows' 4-bit words from global memory
+// A CTA of up to eight warps takes 16 rows of W to a warp and, as one of the CTAs
+// of a cluster, a range of the columns; warps and cluster are chosen so that the
+// CTAs fill the SMs evenly (launch_tiles). Each warp streams its rows' 4-bit words from global memory
 // into registers, kAhead blocks of 128 columns ahead, and meets nobody on the way;
-// x of a slice of KS columns lies in shared memory for all eight warps. A product
+// x of a slice of KS columns lies in shared memory for all of them. A product
 // mma(W 16 x 16, x^T 16 x 8) has the rows of W as its rows and eight tokens as its
 // columns. The 4-bit values become bf16 integers in registers: 0x4300 | n is 128 +
 // n, and subtracting 128 + z leaves n - z exactly. So the products within a group
@@ -44,10 +46,10 @@ struct LinearTile {
     using X = X_;                                                   // type of x, scales and y
     static constexpr int NT = NT_, KS = KS_, kAhead = kAhead_, kCtas = kCtas_;
     static constexpr int kParts = sizeof(X) == 4 ? 3 : 1;           // bf16 parts of x
-    static constexpr int R = 128, T = 8 * NT;                       // rows, tokens
+    static constexpr int kMaxWarps = 8, T = 8 * NT;                 // tokens
     static constexpr int kXRow = KS * 2, kPlane = T * kXRow;        // bytes of a staged row, of a part, of x
-    static constexpr int kRedRow = R + 1;                           // floats of a token's row of the parts
-    static constexpr int kSmem = kParts * kPlane > T * kRedRow * 4 ? kParts * kPlane : T * kRedRow * 4;
+    static constexpr int kParted = T * (16 * kMaxWarps + 1) * 4;    // bytes of the parts of the sums, at most
+    static constexpr int kSmem = kParts * kPlane > kParted ? kParts * kPlane : kParted;
     static_assert(KS % (128 * kAhead) == 0, "a slice is whole rounds of the register ring");
 };
 
@@ -158,7 +160,8 @@ __global__ void __launch_bounds__(256, C::kCtas) linear_tiles_kernel(LinearArgs 
     extern __shared__ __align__(128) unsigned char smem[];
     constexpr int kGroups = 4 / GU, kSliceBlocks = C::KS / 128, kAhead = C::kAhead;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t4 = lane & 3;
-    const int rank = blockIdx.x % cluster, row0 = blockIdx.x / cluster * C::R, tok0 = blockIdx.y * C::T;
+    const int warps = blockDim.x >> 5, rows = 16 * warps;
+    const int rank = blockIdx.x % cluster, row0 = blockIdx.x / cluster * rows, tok0 = blockIdx.y * C::T;
     const int nt = min(C::T, a.n_tokens - tok0);
     const int groups = a.d_in / (GU * 32), blocks = (a.d_in + 127) / 128;
     const int b_lo = (int)((long long)blocks * rank / cluster), b_hi = (int)((long long)blocks * (rank + 1) / cluster);
@@ -211,17 +214,17 @@ __global__ void __launch_bounds__(256, C::kCtas) linear_tiles_kernel(LinearArgs 
         const int q = lane & 15, odd = lane >> 4;                   // odd token of the pair
         unsigned char *dst = smem + odd * C::kXRow + ((x_place<GU>(q) ^ (odd << 2)) << 4);
         const int pairs = s_lo == b_lo ? C::T / 2 : (nt + 1) / 2;   // rows past the tokens are cleared once
-        for (int i0 = warp; i0 < pairs * kSliceBlocks; i0 += 8 * kBatch) {
+        for (int i0 = warp; i0 < pairs * kSliceBlocks; i0 += warps * kBatch) {
             Piece<X> v[kBatch];
 #pragma unroll
             for (int e = 0; e < kBatch; ++e) {
-                const int i = i0 + e * 8, t = i / kSliceBlocks * 2 + odd, blk = i % kSliceBlocks;
+                const int i = i0 + e * warps, t = i / kSliceBlocks * 2 + odd, blk = i % kSliceBlocks;
                 const int k = (s_lo + blk) * 128 + q * 8;
                 v[e].load(x + (size_t)t * a.x_stride + k, t < nt && blk < n_blocks && k < a.d_in, x_vec);
             }
 #pragma unroll
             for (int e = 0; e < kBatch; ++e) {
-                const int i = i0 + e * 8, t2 = i / kSliceBlocks * 2, blk = i % kSliceBlocks;
+                const int i = i0 + e * warps, t2 = i / kSliceBlocks * 2, blk = i % kSliceBlocks;
                 if (t2 >= C::T) break;
 #pragma unroll
                 for (int part = 0; part < C::kParts; ++part) {
@@ -303,20 +306,21 @@ __global__ void __launch_bounds__(256, C::kCtas) linear_tiles_kernel(LinearArgs 
     }
     // ---- the cluster's parts, added in a fixed order
     __syncthreads();
-    float *red = reinterpret_cast<float *>(smem);                   // [T][kRedRow]
+    float *red = reinterpret_cast<float *>(smem);                   // [T][red_row]
+    const int red_row = rows + 1;
 #pragma unroll
     for (int n = 0; n < C::NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            red[(n * 8 + t4 * 2 + (e & 1)) * C::kRedRow + r_in + (e >> 1) * 8] = acc[n][e];
+            red[(n * 8 + t4 * 2 + (e & 1)) * red_row + r_in + (e >> 1) * 8] = acc[n][e];
     if (cluster > 1)
         cluster_sync_all();
     else
         __syncthreads();
-    const int r_lo = C::R * rank / cluster, slice = C::R * (rank + 1) / cluster - r_lo;
+    const int r_lo = rows * rank / cluster, slice = rows * (rank + 1) / cluster - r_lo;
     const uint32_t red_at = smem_u32(red);
-    for (int i = tid; i < nt * slice; i += 256) {
-        const int t = i / slice, r = r_lo + i % slice, at = t * C::kRedRow + r;
+    for (int i = tid; i < nt * slice; i += 32 * warps) {
+        const int t = i / slice, r = r_lo + i % slice, at = t * red_row + r;
         if (row0 + r >= a.d_out) continue;
         float sum = red[at];
         if (cluster > 1) {
@@ -333,6 +337,41 @@ __global__ void __launch_bounds__(256, C::kCtas) linear_tiles_kernel(LinearArgs 
     if (cluster > 1) cluster_sync_all();                            // the peers have read this CTA's parts
 }
 
+// Clusters of c CTAs of w warps that the current device holds at once; asked of the runtime once.
+template <class C, int GU, bool kZeros>
+int active_clusters(int w, int c) {
+    static std::atomic<int> known[9][kMaxCluster + 1];       // 1 + the answer
+    static std::atomic<int> device{-1};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const bool same = device.load(std::memory_order_acquire) == dev;
+    int n = same ? known[w][c].load(std::memory_order_relaxed) : 0;
+    if (n > 0) return n - 1;
+    if (!same) {
+        for (auto &row : known)
+            for (auto &k : row) k.store(0, std::memory_order_relaxed);
+        device.store(dev, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(32 * w);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, linear_tiles_kernel<C, GU, kZeros>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    known[w][c].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
 template <class C, int GU, bool kZeros>
 cudaError_t launch_tiles(const LinearArgs &a, int sms, cudaStream_t st) {
     auto kernel = linear_tiles_kernel<C, GU, kZeros>;
@@ -342,19 +381,30 @@ cudaError_t launch_tiles(const LinearArgs &a, int sms, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         set_device_bit(ready);
     }
-    const int tiles = (a.d_out + C::R - 1) / C::R * ((a.n_tokens + C::T - 1) / C::T);
-    const int blocks = (a.d_in + 127) / 128;
-    // CTAs of a cluster: the least work on the fullest SM, ceil(tiles * c / sms) / c; on a tie the larger c, whose
-    // CTAs have more loads in flight, as long as a range has kAhead blocks
-    int cluster = 1;
-    double least = 1e30;
-    for (int c = 1; c <= kMaxCluster && (c == 1 || blocks / c >= C::kAhead); ++c) {
-        const double full = (double)(((long long)tiles * c + sms - 1) / sms) / c;
-        if (full <= least && (c == 1 || (long long)tiles * c <= (long long)C::kCtas * sms)) least = full, cluster = c;
-    }
+    // Warps of a CTA and CTAs of a cluster: the least of an estimate in clocks. A round of CTAs costs about 5000 (launch,
+    // first loads, the cluster's sums) and for each block of columns the latency of a warp's chain, 900, and the issue
+    // slots or tensor time of every warp of the SM's four schedulers, with the staging of x. A round is what the device
+    // holds at once: clusters fill whole places of a GPC. It comes within 10 % of what was measured: 1x4096x4096 8 warps,
+    // clusters of 8: 5.7 us; 7 and 4: 7.1; 7 and 8, in two rounds: 8.9. 1x14336x4096: 8, 8: 13.0; 7, 4: 20.7.
+    // 1x4096x14336: 6, 2: 10.5; 8, 2: 12.0; 4, 5, in two rounds: 15.4.
+    const int tok_tiles = (a.n_tokens + C::T - 1) / C::T, blocks = (a.d_in + 127) / 128;
+    constexpr int kProducts = C::NT * C::kParts, kIssue = (150 + 28 * kProducts) / 4, kTensor = 16 * kProducts;
+    int warps = C::kMaxWarps, cluster = 1;
+    long long least = INT64_MAX;
+    for (int w = C::kMaxWarps; w >= 4; --w)
+        for (int c = 1; c <= kMaxCluster && (c == 1 || c <= blocks); ++c) {
+            const long long clusters = (long long)((a.d_out + 16 * w - 1) / (16 * w)) * tok_tiles;
+            const int at_once = active_clusters<C, GU, kZeros>(w, c);
+            if (at_once < 1) continue;
+            const long long rounds = (clusters + at_once - 1) / at_once;
+            const long long on_sm = (std::min<long long>(clusters, at_once) * c + sms - 1) / sms;
+            const long long cost = rounds * (5000 + (long long)((blocks + c - 1) / c) *
+                                                        (900 + on_sm * (w * std::max(kIssue, kTensor) + 2 * C::T)));
+            if (cost < least) least = cost, warps = w, cluster = c;
+        }
     const int x_vec = aligned16(a.x) && a.x_stride * sizeof(typename C::X) % 16 == 0;
-    const dim3 grid((a.d_out + C::R - 1) / C::R * cluster, (a.n_tokens + C::T - 1) / C::T);
-    return launch_step(kernel, grid, dim3(256), C::kSmem, cluster, st, a, cluster, x_vec);
+    const dim3 grid((a.d_out + 16 * warps - 1) / (16 * warps) * cluster, tok_tiles);
+    return launch_step(kernel, grid, dim3(32 * warps), C::kSmem, cluster, st, a, cluster, x_vec);
 }
 
 template <class C, int GU>
@@ -377,8 +427,10 @@ cudaError_t launch_linear(const LinearArgs &a, int sms, cudaStream_t st) {
     constexpr int kCut = sizeof(X) == 4 ? 2 : 1;                    // shared memory holds fewer columns of three parts
     if (a.n_tokens <= 8) return launch_group<LinearTile<X, 1, 2048 / kCut, 4, 2>>(a, sms, st);
     if (a.n_tokens <= 16) return launch_group<LinearTile<X, 2, 2048 / kCut / kCut, 4, 2>>(a, sms, st);
-    if (a.n_tokens <= 32) return launch_group<LinearTile<X, 4, 1024 / kCut, 4, 2>>(a, sms, st);
-    return launch_group<LinearTile<X, 8, 512 / kCut, 2, 2>>(a, sms, st);
+    if (a.n_tokens <= 24) return launch_group<LinearTile<X, 3, 1024 / kCut, 2, 2>>(a, sms, st);
+    if (a.n_tokens <= 32) return launch_group<LinearTile<X, 4, 1024 / kCut, 2, 2>>(a, sms, st);
+    if (a.n_tokens <= 48) return launch_group<LinearTile<X, 6, 512 / kCut, 2, 2>>(a, sms, st);
+    return launch_group<LinearTile<X, 8, 512 / kCut, 1, 2>>(a, sms, st);
 }
 
 }  // namespace
