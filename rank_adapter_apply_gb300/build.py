@@ -25,9 +25,10 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "librank_adapter_apply.so")
 SOURCES = ["lora_abi.cu", "group.cu", "decode.cu", "decode_cluster.cu", "static_scratch.cu",
-           "prefill_tc.cu", "upload.cu", "base_linear.cu", "rope.cu", "tree_attention.cu",
+           "prefill_tc.cu", "upload.cu", "base_linear.cu", "base_linear_tc.cu", "rope.cu", "tree_attention.cu",
            "tree_attention_tc.cu", "tree_attention_f32.cu", "verify_drafts.cu", "slot_table.cpp"]
-HEADERS = ["kernels.cuh", "slot_table.h", "device_util.cuh", "tc_util.cuh", "step_util.cuh", "tree_common.cuh"]
+HEADERS = ["kernels.cuh", "slot_table.h", "device_util.cuh", "tc_util.cuh", "step_util.cuh", "tree_common.cuh",
+           "base_linear.cuh", "tensor_map.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          f"-I{os.path.join(ROOT, 'include')}"]

@@ -1,25 +1,13 @@
 // lora_base_linear: y = W x for a few tokens, W in 4 bits with group scales.
-#include "step_util.cuh"
+#include "base_linear.cuh"
 
 #include <algorithm>
-#include <atomic>
 
 namespace lora {
+namespace linear {
 namespace {
 
 using namespace step;
-
-struct LinearArgs {
-    const void *x;
-    const uint8_t *qweight;
-    const void *scales;
-    const uint8_t *zeros;
-    void *y;
-    long long x_stride, y_stride;
-    int n_tokens, d_in, d_out, group;
-};
-
-constexpr int kMaxCluster = 8;
 
 // A CTA of up to eight warps takes 16 rows of W to a warp and, as one of the CTAs
 // of a cluster, a range of the columns; warps and cluster are chosen so that the
@@ -337,41 +325,6 @@ __global__ void __launch_bounds__(32 * C::kMaxWarps, C::kCtas) linear_tiles_kern
     if (cluster > 1) cluster_sync_all();                            // the peers have read this CTA's parts
 }
 
-// Clusters of c CTAs of w warps that the current device holds at once; asked of the runtime once.
-template <class C, int GU, bool kZeros>
-int active_clusters(int w, int c) {
-    static std::atomic<int> known[C::kMaxWarps + 1][kMaxCluster + 1];       // 1 + the answer
-    static std::atomic<int> device{-1};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    const bool same = device.load(std::memory_order_acquire) == dev;
-    int n = same ? known[w][c].load(std::memory_order_relaxed) : 0;
-    if (n > 0) return n - 1;
-    if (!same) {
-        for (auto &row : known)
-            for (auto &k : row) k.store(0, std::memory_order_relaxed);
-        device.store(dev, std::memory_order_release);
-    }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(c);
-    cfg.blockDim = dim3(32 * w);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = c;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, linear_tiles_kernel<C, GU, kZeros>, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        n = 0;
-    }
-    known[w][c].store(n + 1, std::memory_order_relaxed);
-    return n;
-}
-
 template <class C, int GU, bool kZeros>
 cudaError_t launch_tiles(const LinearArgs &a, int sms, cudaStream_t st) {
     auto kernel = linear_tiles_kernel<C, GU, kZeros>;
@@ -389,12 +342,13 @@ cudaError_t launch_tiles(const LinearArgs &a, int sms, cudaStream_t st) {
     // 1x4096x14336: 6, 2: 10.5; 8, 2: 12.0; 4, 5, in two rounds: 15.4.
     const int tok_tiles = (a.n_tokens + C::T - 1) / C::T, blocks = (a.d_in + 127) / 128;
     constexpr int kProducts = C::NT * C::kParts, kIssue = (150 + 28 * kProducts) / 4, kTensor = 16 * kProducts;
+    static ActiveClusters known[C::kMaxWarps + 1];
     int warps = C::kMaxWarps, cluster = 1;
     long long least = INT64_MAX;
     for (int w = C::kMaxWarps; w >= 4; --w)
         for (int c = 1; c <= kMaxCluster && (c == 1 || c <= blocks); ++c) {
             const long long clusters = (long long)((a.d_out + 16 * w - 1) / (16 * w)) * tok_tiles;
-            const int at_once = active_clusters<C, GU, kZeros>(w, c);
+            const int at_once = active_clusters(kernel, 32 * w, C::kSmem, c, known[w]);
             if (at_once < 1) continue;
             const long long rounds = (clusters + at_once - 1) / at_once;
             const long long on_sm = (std::min<long long>(clusters, at_once) * c + sms - 1) / sms;
@@ -421,17 +375,19 @@ cudaError_t launch_group(const LinearArgs &a, int sms, cudaStream_t st) {
     }
 }
 
-// The tokens' tile. Up to 16 tokens: two CTAs of eight warps to an SM. Above, the accumulators want the registers
-// of twelve warps to an SM, in one CTA, whose copy of x then serves more rows (48 tokens: 12.5 / 33 / 23.4 / 26.2 us for
-// 4096x4096, 14336x4096, 5120x8192, 4096x14336, against 14.1 / 37.6 / 25.5 / 32.1 with two CTAs of eight).
+// The kernel and its tokens' tile. bf16 above 8 tokens goes to the 5th-generation tensor cores where TMA can load x (16-byte
+// aligned rows), measured for 4096x4096, 5120x8192 and 4096x14336 (d_in x d_out): 1 token 5.3 / 9.0 / 10.4 us here and
+// 5.9 / 9.3 / 11.2 there, 8 tokens 6.0 / 10.0 / 11.7 and 6.0 / 9.4 / 11.3, 16 tokens 8.3 / 12.7 / 14.9 and 6.3 / 9.5 / 11.5,
+// 64 tokens 15.1 / 29.9 / 32.3 and 7.8 / 12.7 / 13.6. Up to 16 tokens: two CTAs of eight warps to an SM. Above, the
+// accumulators want the registers of twelve warps to an SM (16 with the three parts of fp32), in one CTA, whose copy of x
+// then serves more rows (48 tokens in bf16: 12.5 / 23.4 / 26.2 us, against 14.1 / 25.5 / 32.1 with two CTAs of eight).
 cudaError_t launch_linear(const LinearArgs &a, int dtype, int sms, cudaStream_t st) {
     if (dtype == LORA_DTYPE_BF16) {
         using X = __nv_bfloat16;
         if (a.n_tokens <= 8) return launch_group<LinearTile<X, 1, 2048, 4, 2, 8>>(a, sms, st);
+        if (tc_takes(a)) return launch_tc(a, sms, st);
         if (a.n_tokens <= 16) return launch_group<LinearTile<X, 2, 2048, 4, 2, 8>>(a, sms, st);
-        if (a.n_tokens <= 24) return launch_group<LinearTile<X, 3, 1024, 4, 1, 12>>(a, sms, st);
         if (a.n_tokens <= 32) return launch_group<LinearTile<X, 4, 1024, 4, 1, 12>>(a, sms, st);
-        if (a.n_tokens <= 48) return launch_group<LinearTile<X, 6, 1024, 2, 1, 12>>(a, sms, st);
         return launch_group<LinearTile<X, 8, 1024, 1, 1, 12>>(a, sms, st);
     }
     if (a.n_tokens <= 8) return launch_group<LinearTile<float, 1, 1024, 4, 2, 8>>(a, sms, st);
@@ -443,9 +399,11 @@ cudaError_t launch_linear(const LinearArgs &a, int dtype, int sms, cudaStream_t 
 }
 
 }  // namespace
+}  // namespace linear
 }  // namespace lora
 
 using namespace lora;
+using namespace lora::linear;
 using namespace lora::step;
 
 extern "C" int lora_base_linear(const lora_base_linear_desc *d, void *stream) {

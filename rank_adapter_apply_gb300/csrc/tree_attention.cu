@@ -1,4 +1,5 @@
 // lora_tree_attention: attention of drafted trees over a paged cache.
+#include "base_linear.cuh"
 #include "tree_common.cuh"
 
 #include <algorithm>
@@ -616,9 +617,10 @@ extern "C" int lora_tree_attention(const lora_tree_attention_desc *d, void *stre
 
 extern "C" int lora_step_wait_timeouts(uint64_t *count) {
     if (!count) return fail(LORA_ERR_ARG, "step_wait_timeouts: NULL pointer argument");
-    unsigned n = 0;
-    const cudaError_t e = read_timeouts(&n);
+    unsigned n = 0, of_linear = 0;
+    cudaError_t e = read_timeouts(&n);
+    if (e == cudaSuccess) e = linear::read_timeouts(&of_linear);
     if (e != cudaSuccess) return launched("step_wait_timeouts", e);
-    *count = n;
+    *count = (uint64_t)n + of_linear;
     return LORA_OK;
 }

@@ -21,10 +21,8 @@
 // clear the rows that are not finite, and the rows that see one of them add it in
 // fp32 at the end of the unit.
 #include "tree_common.cuh"
-
 #include "tc_util.cuh"
-
-#include <cudaTypedefs.h>
+#include "tensor_map.cuh"
 
 #include <atomic>
 
@@ -173,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
 
     const TreeArgs &a = args.a;
     const Plan &plan = args.plan;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = a.n_heads / a.n_kv;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), group = a.n_heads / a.n_kv;
     const int rows = kRows / group * group;            // of a tile
     grid_dependency_wait();
     grid_launch_dependents();                          // the join kernel waits for this grid's end itself
@@ -304,51 +302,54 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
             mbar_wait_bounded(&full[j % kItems], (uint32_t)(j / kItems) & 1u, kWaitLimit);
         if (units > 0) mbar_wait_bounded(&q_full, (uint32_t)(units - 1) & 1u, kWaitLimit);
     } else if (warp == 5) {
-        if (lane == 0) {
-            // ---------------- products ----------------
-            constexpr uint32_t idesc_s = tc::idesc_bf16(kRows, kTileKeys);
-            constexpr uint32_t idesc_o = tc::idesc_bf16(kRows, DP) | (1u << 16);    // B (V) with N contiguous
-            // descriptors of the operands' first slices; slices and places differ in the address field alone
-            const uint64_t q_desc = tc::smem_desc(q_at, 128, tc::kSwz128), k_desc = tc::smem_desc(ring, 128, tc::kSwz128);
-            const uint64_t v_desc = desc_n_major(ring, C::kItem / C::kHalves);
-            int at = 0, units = 0;
-            uint32_t round = 0;
-            bool ok = true;
-            for (int i = 0; ok && i <= n_tiles; ++i) {
-                if (i < n_tiles) {
-                    ok = wait(&full[at], round) && wait(&meta_full[i % kMeta], (uint32_t)(i / kMeta)) &&
-                         (!meta[i % kMeta].first || wait(&q_full, (uint32_t)units++)) &&
-                         (i < 2 || wait(&pv_done[i & 1], (uint32_t)((i - 2) >> 1)));      // P of tile i - 2 was read
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    const uint64_t kd = k_desc + (uint64_t)(at * (C::kItem >> 4));
+        // ---------------- products ----------------
+        // The whole warp runs the loop, so that addresses and descriptors stay in uniform registers (a product issued
+        // by one lane of a divergent branch costs its thread 60 clocks); one lane's instructions count.
+        const uint32_t lead = tc::elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0), tm_o = tm + 128;
+        constexpr uint32_t idesc_s = tc::idesc_bf16(kRows, kTileKeys);
+        constexpr uint32_t idesc_o = tc::idesc_bf16(kRows, DP) | (1u << 16);    // B (V) with N contiguous
+        // descriptors of the operands' first slices; slices and places differ in the address field alone
+        const uint64_t q_desc = tc::smem_desc(q_at, 128, tc::kSwz128), k_desc = tc::smem_desc(ring, 128, tc::kSwz128);
+        const uint64_t v_desc = desc_n_major(ring, C::kItem / C::kHalves);
+        const int n = __shfl_sync(0xffffffffu, n_tiles, 0);
+        int at = 0, units = 0;
+        uint32_t round = 0;
+        bool ok = true;
+        for (int i = 0; i <= n; ++i) {
+            if (i < n) {
+                ok = wait(&full[at], round) && wait(&meta_full[i % kMeta], (uint32_t)(i / kMeta)) &&
+                     (!meta[i % kMeta].first || wait(&q_full, (uint32_t)units++)) &&
+                     (i < 2 || wait(&pv_done[i & 1], (uint32_t)((i - 2) >> 1)));      // P of tile i - 2 was read
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc::fence_after_sync();
+                const uint64_t kd = k_desc + (uint64_t)(at * (C::kItem >> 4));
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k)
-                        tc::mma_bf16(tmem + (i & 1) * 64, q_desc + (k >> 2) * (kRows * 128 >> 4) + (k & 3) * 2,
-                                     kd + (k >> 2) * (C::kItem / 2 >> 4) + (k & 3) * 2, idesc_s, k > 0);
-                    tc::mma_commit(&empty[at]);
-                    tc::mma_commit(&s_full[i & 1]);
-                    step(at, round);
-                }
-                if (i > 0) {
-                    const int t = i - 1;
-                    ok = wait(&p_ready[t & 1], (uint32_t)(t >> 1)) && wait(&full[at], round);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    const uint32_t more = meta[t % kMeta].first == 0;
-                    const uint64_t vd = v_desc + (uint64_t)(at * (C::kItem >> 4));
-#pragma unroll
-                    for (int k = 0; k < kTileKeys / 16; ++k)
-                        tc::mma_bf16_tmem_a(tmem_o, tmem + (t & 1) * 64 + k * 8, vd + k * (2048 >> 4), idesc_o, more | (k > 0));
-                    tc::mma_commit(&empty[at]);
-                    tc::mma_commit(&pv_done[t & 1]);
-                    step(at, round);
-                }
+                for (int k = 0; k < DP / 16; ++k)
+                    tc::mma_bf16_lead(tm + (i & 1) * 64, q_desc + (k >> 2) * (kRows * 128 >> 4) + (k & 3) * 2,
+                                 kd + (k >> 2) * (C::kItem / 2 >> 4) + (k & 3) * 2, idesc_s, k > 0, lead);
+                tc::mma_commit_lead(&empty[at], lead);
+                tc::mma_commit_lead(&s_full[i & 1], lead);
+                step(at, round);
             }
-            // every product is done before tensor memory is freed
-            tc::mma_commit(&drained);
-            mbar_wait_bounded(&drained, 0, kWaitLimit);
+            if (i > 0) {
+                const int t = i - 1;
+                ok = wait(&p_ready[t & 1], (uint32_t)(t >> 1)) && wait(&full[at], round);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc::fence_after_sync();
+                const uint32_t more = meta[t % kMeta].first == 0;
+                const uint64_t vd = v_desc + (uint64_t)(at * (C::kItem >> 4));
+#pragma unroll
+                for (int k = 0; k < kTileKeys / 16; ++k)
+                    tc::mma_bf16_tmem_a_lead(tm_o, tm + (t & 1) * 64 + k * 8, vd + k * (2048 >> 4), idesc_o, more | (k > 0),
+                                                 lead);
+                tc::mma_commit_lead(&empty[at], lead);
+                tc::mma_commit_lead(&pv_done[t & 1], lead);
+                step(at, round);
+            }
         }
+        // every product is done before tensor memory is freed
+        tc::mma_commit_lead(&drained, lead);
+        mbar_wait_bounded(&drained, 0, kWaitLimit);
     } else {
         // ---------------- softmax: thread = row ----------------
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
@@ -519,20 +520,6 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
-    PFN_cuTensorMapEncodeTiled_v12000 fn = known.load(std::memory_order_acquire);
-    if (fn) return fn;
-    cudaDriverEntryPointQueryResult q;
-    void *p = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || !p)
-        return nullptr;
-    fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    known.store(fn, std::memory_order_release);
-    return fn;
-}
-
 // A bf16 map of `rank` dimensions, boxes of 64 columns, 128-byte swizzle. The
 // stride of a dimension of one element is never used: any legal one stands in.
 bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims, const long long *strides,
@@ -540,7 +527,7 @@ bool encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims
     cuuint64_t bytes[3];
     const cuuint32_t ones[4] = {1, 1, 1, 1};
     for (int i = 0; i + 1 < rank; ++i) bytes[i] = dims[i + 1] == 1 ? 16 : (cuuint64_t)strides[i] * 2;
-    const auto fn = encoder();
+    const auto fn = map_encoder();
     return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, bytes, box, ones,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
