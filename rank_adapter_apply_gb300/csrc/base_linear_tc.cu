@@ -40,7 +40,7 @@ struct TcTile {
 struct TcArgs {
     CUtensorMap w, x;                                               // boxes: 128 bytes x 128 rows, 64 columns x N tokens
     LinearArgs a;
-    int cluster, y_vec;
+    int cluster, y_vec, group_vec;                                  // group_vec: a unit's scales, zeros in one load
 };
 
 __device__ unsigned g_gave_up = 0;
@@ -189,20 +189,43 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
         const int swz = row & 7;
 #pragma unroll
         for (int n = 0; n < N / 2; ++n) acc[n] = 0;
-        float sc[kGroups];                                          // of the unit whose products run
-        uint32_t z[kGroups];                                        // of the unit to be converted
+        uint32_t sc[(kGroups + 1) / 2] = {};                        // of the unit whose products run, two to a word
+        uint32_t z = 0;                                             // of the unit to be converted, a byte to a group
         auto load_zeros = [&](int u) {
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                const int at = (u_lo + u) * kGroups + g;
-                z[g] = u < n_units && at < groups ? zeros[at] : 0;
+            const int of = (u_lo + u) * kGroups;
+            if (kGroups > 1 && args.group_vec) {
+                if (u < n_units)
+                    z = kGroups == 4 ? *reinterpret_cast<const uint32_t *>(zeros + of) : *reinterpret_cast<const uint16_t *>(zeros + of);
+                return;
             }
+            z = 0;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+                if (u < n_units && of + g < groups) z |= (uint32_t)zeros[of + g] << (8 * g);
+        };
+        // two scales to a word
+        auto load_scales = [&](int u, uint32_t (&v)[(kGroups + 1) / 2]) {
+            const int of = (u_lo + u) * kGroups;
+            if (kGroups > 1 && args.group_vec) {
+                if (kGroups == 4) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(scales + of);
+                    v[0] = w.x, v[(kGroups + 1) / 2 - 1] = w.y;
+                } else {
+                    v[0] = *reinterpret_cast<const uint32_t *>(scales + of);
+                }
+                return;
+            }
+            const uint16_t *s16 = reinterpret_cast<const uint16_t *>(scales);
+#pragma unroll
+            for (int g = 0; g < kGroups; g += 2)
+                v[g / 2] = (of + g < groups ? s16[of + g] : 0u) | (g + 1 < kGroups && of + g + 1 < groups ? s16[of + g + 1] : 0u) << 16;
         };
         if (kZeros) load_zeros(set);
         auto drain = [&]() {
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
-                const uint64_t ss = pair(__float_as_uint(sc[g]), __float_as_uint(sc[g]));
+                const uint32_t f = __float_as_uint(g & 1 ? bf_hi(sc[g / 2]) : bf_lo(sc[g / 2]));
+                const uint64_t ss = pair(f, f);
 #pragma unroll
                 for (int n = 0; n < N; n += 16) {
                     uint32_t d[16];
@@ -216,15 +239,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
         int it = 0;
         for (int u = set; u < n_units; u += S, ++it) {
             const int i = u / kUnits, st = i % C::kStages;
-            __nv_bfloat16 sc_next[kGroups];
+            uint32_t sc_next[(kGroups + 1) / 2];
+            load_scales(u, sc_next);
             uint32_t zz[kGroups];                                   // -z / 64, twice
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
-                const int of = (u_lo + u) * kGroups + g;
-                sc_next[g] = of < groups ? scales[of] : from_f32<__nv_bfloat16>(0.f);
                 zz[g] = 0xbe00be00u;                                // z = 8
                 if (kZeros) {
-                    const uint32_t zb = __float_as_uint((float)min(z[g], 128u) * -0.015625f) >> 16;
+                    const uint32_t zb = __float_as_uint((float)min(z >> (8 * g) & 255u, 128u) * -0.015625f) >> 16;
                     zz[g] = zb | zb << 16;
                 }
             }
@@ -261,7 +283,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&a_ready[set]);
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) sc[g] = to_f32(sc_next[g]);
+            for (int g = 0; g < kGroups; g += 2) sc[g / 2] = sc_next[g / 2];
         }
         if (ok && it > 0) {
             ok = wait(&done[set], (uint32_t)(it - 1));
@@ -363,6 +385,9 @@ cudaError_t launch(const LinearArgs &a, int sms, cudaStream_t st) {
     args.a = a;
     args.cluster = cluster;
     args.y_vec = reinterpret_cast<uintptr_t>(a.y) % 8 == 0 && a.y_stride % 4 == 0;
+    constexpr int kGroups = Unit<C::N, C::S, GU>::kPieces / GU;
+    args.group_vec = a.d_in / (GU * 32) % kGroups == 0 && reinterpret_cast<uintptr_t>(a.scales) % (2 * kGroups) == 0 &&
+                     reinterpret_cast<uintptr_t>(a.zeros) % kGroups == 0;
     if (!encode(&args.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, a.qweight, a.d_in / 2, a.d_out, a.d_in / 2,
                 128, kRows) ||
         !encode(&args.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.x, a.d_in, a.n_tokens,
@@ -372,12 +397,17 @@ cudaError_t launch(const LinearArgs &a, int sms, cudaStream_t st) {
     return launch_step(kernel, grid, dim3(C::kThreads), C::kSmem, cluster, st, args);
 }
 
-template <class C>
+// Sets of warps, measured with two / three: 17x14336x4096 with groups of 32 and zeros 15.7 / 17.1 us (two sets have room
+// for the four D of 128 columns, three for those of 64), 64 tokens of it 20.5 / 19.7, 64x5120x8192 with groups of 64 12.5 /
+// 14.4, 16x5120x8192 9.4 / 9.4, 17x4096x14336 with groups of 128 12.1 / 11.7.
+template <int N>
 cudaError_t launch_group(const LinearArgs &a, int sms, cudaStream_t st) {
+    using Narrow = TcTile<N, N == 32 ? 2 : 3>;
+    using Wide = TcTile<N, N == 64 ? 2 : 3>;
     switch (a.group) {
-        case 32: return a.zeros ? launch<C, 1, true>(a, sms, st) : launch<C, 1, false>(a, sms, st);
-        case 64: return a.zeros ? launch<C, 2, true>(a, sms, st) : launch<C, 2, false>(a, sms, st);
-        default: return a.zeros ? launch<C, 4, true>(a, sms, st) : launch<C, 4, false>(a, sms, st);
+        case 32: return a.zeros ? launch<Narrow, 1, true>(a, sms, st) : launch<Narrow, 1, false>(a, sms, st);
+        case 64: return a.zeros ? launch<Wide, 2, true>(a, sms, st) : launch<Wide, 2, false>(a, sms, st);
+        default: return a.zeros ? launch<Wide, 4, true>(a, sms, st) : launch<Wide, 4, false>(a, sms, st);
     }
 }
 
@@ -390,9 +420,9 @@ bool tc_takes(const LinearArgs &a) {
 }
 
 cudaError_t launch_tc(const LinearArgs &a, int sms, cudaStream_t st) {
-    if (a.n_tokens <= 16) return launch_group<TcTile<16, 3>>(a, sms, st);
-    if (a.n_tokens <= 32) return launch_group<TcTile<32, 3>>(a, sms, st);
-    return launch_group<TcTile<64, 2>>(a, sms, st);
+    if (a.n_tokens <= 16) return launch_group<16>(a, sms, st);
+    if (a.n_tokens <= 32) return launch_group<32>(a, sms, st);
+    return launch_group<64>(a, sms, st);
 }
 
 }  // namespace linear
