@@ -32,7 +32,7 @@ struct Tile {
     // written while the tile one stage-count before it may still be read), then the search's scratch
     static constexpr int kRing = kStages + 1;
     static constexpr int kOff = kStages * kStage, kValid = kOff + kRing * kTileKeys * 8;
-    static constexpr int kStart = kValid + kRing * 8, kSmem = kStart + 96;
+    static constexpr int kStart = kValid + kRing * 8, kSmem = kStart + (kScratch + kThreads / 32) * 8;
 };
 
 template <int DP, int WM, int WN>
@@ -603,7 +603,7 @@ extern "C" int lora_tree_attention(const lora_tree_attention_desc *d, void *stre
     const int sms = sm_count();
     if (sms < 1) return fail(LORA_ERR_CUDA, "tree_attention: no CUDA device");
     Plan plan;
-    plan.ctas = std::min(2 * sms, kMaxCtas);
+    plan.ctas = std::min(std::max(2 * sms, 64), kMaxCtas);          // 64: a group of every class fits
     plan.part = static_cast<float *>(d->workspace);
     plan.stat = reinterpret_cast<float2 *>(plan.part + 2 * (size_t)plan.ctas * kMaxRows * 128);
     plan.seg = reinterpret_cast<int4 *>(plan.stat + 2 * (size_t)plan.ctas * kMaxRows);

@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(TreeArgs a, Plan 
     constexpr int R = T::R, C = T::C, kPieces = DP / 4;
     extern __shared__ __align__(128) unsigned char smem[];
     float *qs = reinterpret_cast<float *>(smem), *ks = qs + M * T::kRow, *vs = ks + T::kKeys;
-    __shared__ long long scratch[kThreads / 32 * 2 + 2], offs[kTileKeys];
+    __shared__ long long scratch[kScratch + kThreads / 32], offs[kTileKeys];
     __shared__ uint32_t valid[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = tid >> 4, l16 = tid & 15;
     const int group = a.n_heads / a.n_kv, row0 = half * R;     // this half-warp's rows of the tile

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
     __shared__ uint64_t full[kItems], empty[kItems], meta_full[kMeta], s_full[2], p_ready[2], pv_done[2], q_full, drained;
     __shared__ int poison_at[2];                       // 1 + the last tile (even, odd) whose V had a row that is not finite
     __shared__ Meta meta[kMeta];
-    __shared__ long long scratch[kThreads / 32 * 2 + 2];
+    __shared__ long long scratch[kScratch + kThreads / 32];
     __shared__ uint32_t tmem_base;
     __shared__ int error;
     volatile int *err = &error;

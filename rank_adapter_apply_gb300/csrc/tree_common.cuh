@@ -24,14 +24,18 @@ __device__ __forceinline__ int node_start(const TreeArgs &a, int b) {
     return min(max(a.node_starts[b], 0), a.n_tokens);
 }
 
-// The work of the tensor-core kernels. A unit is (request, row tile, key/value
-// head): the query rows of one tile (a node's query heads that share the key/value
-// head lie side by side) against all keys of the request in tiles of 64. The key
-// tiles of all units, in a row, are dealt to the CTAs in equal shares: a share is a
-// run of tiles that may start and end inside a unit, so ragged lengths cost
-// nothing, and a unit is split over many CTAs where there are few. A CTA that
-// covers a whole unit writes its result; the others write (O, m, l) to the
-// workspace, and the join kernel joins them.
+// The work of the kernels. A unit is (request, row tile, key/value head): the query
+// rows of one tile (a node's query heads that share the key/value head lie side by
+// side) against all keys of the request in tiles of 64. Row tiles of one request
+// read the same keys, so they are put side by side in blocks of up to eight, and the
+// blocks of k row tiles are class k. The key tiles of a class's blocks, in a row,
+// are its columns; they are dealt in equal shares to groups of k CTAs, of which each
+// takes one row tile of the block. So the CTAs of a group read the same keys at the
+// same time, and memory gives them once (4 requests of up to 64 nodes, 64 heads over
+// 8, 32768 keys: 1.5 GB a call when the row tiles went one after another). A share
+// may start and end inside a unit, so ragged lengths cost nothing, and a unit is
+// split over many CTAs where there are few. A CTA that covers a whole unit writes its
+// result; the others write (O, m, l) to the workspace, and the join kernel joins them.
 constexpr int kTileKeys = 64;
 
 struct Plan {                 // workspace regions
@@ -73,22 +77,29 @@ __device__ __noinline__ inline Request request(const TreeArgs &a, int b, int m_r
     return r;
 }
 
-// Where a CTA is in the run of tiles.
+constexpr int kMaxClass = 8;
+
+// Blocks of class k among a request's row tiles; the last, of less than eight, comes after the others.
+__device__ __forceinline__ int blocks_of(int row_tiles, int k) {
+    return k == kMaxClass ? row_tiles / kMaxClass : row_tiles % kMaxClass == k;
+}
+
+// Where a CTA is in the columns of its class `k`, of whose blocks it takes row tile `row`.
 struct Cursor {
     Request r;
-    int b, row_tile, head, tile;
+    int b, row_tile, head, tile, k, row;
 };
 
 __device__ __noinline__ inline void next_unit(const TreeArgs &a, Cursor &c, int m_rows) {
     c.tile = 0;
     if (++c.head < a.n_kv) return;
     c.head = 0;
-    if (++c.row_tile < c.r.row_tiles) return;
-    c.row_tile = 0;
+    if (c.k == kMaxClass && (c.row_tile += kMaxClass) / kMaxClass < c.r.row_tiles / kMaxClass) return;
     do {
         if (++c.b >= a.n_requests) return;
         c.r = request(a, c.b, m_rows);
-    } while (c.r.row_tiles == 0);
+    } while (blocks_of(c.r.row_tiles, c.k) == 0);
+    c.row_tile = (c.k == kMaxClass ? 0 : c.r.row_tiles - c.k) + c.row;
 }
 
 __device__ __forceinline__ void next_tile(const TreeArgs &a, Cursor &c, int m_rows) {
@@ -116,93 +127,162 @@ __device__ __noinline__ inline uint64_t seen_keys(const TreeArgs &a, const Reque
     return seen;
 }
 
-// A CTA's share of the tiles: [lo, hi) of total, dealt to `used` CTAs, and where it
-// starts. false: it has none. scratch: 2 kWarps + 2 words. Every thread calls it.
+// A CTA's share of its class's columns: [lo, hi) of total, dealt to `used` groups of which its is number `group`, and
+// where it starts. false: it has none. scratch: kScratch words and one for each warp. Every thread calls it.
+constexpr int kScratch = 2 + kMaxClass;
 struct Share {
     long long lo, hi, total, used;
+    int group;
     Cursor start;
 };
 
 // x * y / z, in 32 bits where they will do.
 __device__ __forceinline__ long long scaled(long long x, long long y, long long z) {
     const long long p = x * y;
-    return p >> 32 == 0 ? (long long)((uint32_t)p / (uint32_t)z) : p / z;
+    return (p | z) >> 32 == 0 ? (long long)((uint32_t)p / (uint32_t)z) : p / z;
 }
 
 template <int kThreads>
 __device__ inline bool find_share(const TreeArgs &a, int m_rows, long long *scratch, Share &s) {
     constexpr int kWarps = kThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // tiles of the requests tid, tid + kThreads, ..; of the first of them and its prefix sum, which is all in most calls
-    Request mine{};
-    long long n0 = 0, sum = 0;
-    for (int b = tid; b < a.n_requests; b += kThreads) {
-        const Request r = request(a, b, m_rows);
-        const long long n = (long long)r.row_tiles * r.key_tiles * a.n_kv;
-        if (b == tid) mine = r, n0 = n;
-        sum += n;
-    }
-    long long upto = n0, all = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += v;
-    }
-    if (a.n_requests > kThreads) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    }
-    if (lane == 31) scratch[2 + warp] = upto, scratch[2 + kWarps + warp] = a.n_requests > kThreads ? all : upto;
-    if (tid == 0) scratch[0] = -1;
-    __syncthreads();
-    s.total = 0;
-    long long before = 0;
-    for (int w = 0; w < kWarps; ++w) s.total += scratch[2 + kWarps + w];
-    s.used = min((long long)gridDim.x, s.total);
-    if (blockIdx.x >= s.used) return false;
-    s.lo = scaled(s.total, blockIdx.x, s.used);
-    s.hi = scaled(s.total, blockIdx.x + 1, s.used);
-    for (int b0 = 0; b0 < a.n_requests; b0 += kThreads) {    // ends in the chunk that holds tile lo < total
-        const int b = b0 + tid;
-        if (b0 > 0) {
-            n0 = 0;
-            if (b < a.n_requests) {
-                mine = request(a, b, m_rows);
-                n0 = (long long)mine.row_tiles * mine.key_tiles * a.n_kv;
-            }
-            upto = n0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += v;
-            }
-            __syncthreads();
-            if (lane == 31) scratch[2 + warp] = upto;
-            __syncthreads();
-        }
-        for (int w = 0; w < warp; ++w) upto += scratch[2 + w];
-        upto += before;
-        if (upto - n0 <= s.lo && s.lo < upto) scratch[0] = b, scratch[1] = upto - n0;
-        for (int w = 0; w < kWarps; ++w) before += scratch[2 + w];
+    long long *columns = scratch + 2, *sums = scratch + kScratch;    // of class k at k - 1; of the warps' requests
+    // Up to 32 requests: every warp finds it all for itself, a lane to a request. What the warps write to shared memory
+    // is the same, and none waits for another.
+    const bool few = a.n_requests <= 32;
+    const int each = few ? 32 : kThreads, me = few ? lane : tid;
+    if (!few) {
+        if (tid < kScratch) scratch[tid] = tid == 0 ? -1 : 0;
         __syncthreads();
-        if (scratch[0] >= 0) break;
     }
-    if (scratch[0] < 0) return false;                        // not reached
-    s.start.b = (int)scratch[0];
-    s.start.r = request(a, s.start.b, m_rows);
-    const long long at = s.lo - scratch[1], unit = scaled(at, 1, s.start.r.key_tiles);
+    Request mine{};                                          // request `me`: the only ones in most calls
+    long long my_columns = 0;                                // few: of class lane + 1
+    for (int b0 = 0; b0 < a.n_requests; b0 += each) {
+        const int b = b0 + me;
+        Request r{};
+        if (b < a.n_requests) r = request(a, b, m_rows);
+        if (b0 == 0) mine = r;
+        const uint32_t some = __reduce_or_sync(0xffffffffu, (r.row_tiles % kMaxClass ? 1u << r.row_tiles % kMaxClass : 0u) |
+                                                                (r.row_tiles >= kMaxClass ? 1u << kMaxClass : 0u));
+        for (uint32_t left = some; left; left &= left - 1) {
+            const int k = __ffs(left) - 1;
+            const long long n = (long long)blocks_of(r.row_tiles, k) * r.key_tiles * a.n_kv;
+            const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)n & 0xffffffu);
+            const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(n >> 24));
+            const unsigned long long sum = lo + ((unsigned long long)hi << 24);
+            if (few)
+                my_columns = lane == k - 1 ? (long long)sum : my_columns;
+            else if (lane == 0)
+                atomicAdd(reinterpret_cast<unsigned long long *>(columns) + k - 1, sum);
+        }
+    }
+    if (few) {
+        if (lane < kMaxClass) columns[lane] = my_columns;
+        __syncwarp();
+    } else {
+        __syncthreads();
+    }
+    const int grid = gridDim.x;
+    long long all = 0;
+    uint32_t present = 0;                                    // classes with columns
+#pragma unroll
+    for (int k = 1; k <= kMaxClass; ++k) {
+        const long long n = columns[k - 1];
+        all += k * n;
+        present |= n > 0 ? 1u << k : 0u;
+    }
+    if (all == 0) return false;
+    // The longest share t: the least of 32 from what equal shares would be, 0.65 % apart, with which the groups, of
+    // whole numbers, fit the grid. They do by 1.14 times that: rounding up costs 1 + 2 + .. + 8 CTAs at most. CTAs that
+    // are left go to the widest class that takes them; to one class alone all go.
+    long long t = 0;
+    int spare = grid;
+    if (present & (present - 1)) {
+        for (long long even = scaled(all + grid - 1, 1, grid);; even *= 2) {     // a grid of 216 CTAs or more never doubles
+            t = even + scaled(even * lane + 154, 1, 155);
+            long long ctas = 0;
+            for (uint32_t left = present; left; left &= left - 1) {
+                const int k = __ffs(left) - 1;
+                ctas += k * scaled(columns[k - 1] + t - 1, 1, t);
+            }
+            const uint32_t fits = __ballot_sync(0xffffffffu, ctas <= grid);
+            if (fits == 0) continue;
+            t = __shfl_sync(0xffffffffu, t, __ffs(fits) - 1);
+            spare = grid - (int)__shfl_sync(0xffffffffu, ctas, __ffs(fits) - 1);
+            break;
+        }
+    } else {
+        spare = grid - (__ffs(present) - 1);                 // a group of the one class
+    }
+    int k = 0, at_cta = blockIdx.x;
+    for (uint32_t left = present; left;) {
+        k = 31 - __clz(left);
+        left ^= 1u << k;
+        const long long need = present & (present - 1) ? scaled(columns[k - 1] + t - 1, 1, t) : 1;
+        s.used = min(need + spare / k, columns[k - 1]);
+        spare -= (int)(s.used - need) * k;
+        if (at_cta < k * s.used) break;
+        at_cta -= k * (int)s.used;
+        k = 0;
+    }
+    if (k == 0) return false;
+    s.total = columns[k - 1];
+    s.start.k = k;
+    s.start.row = (int)scaled(at_cta, 1, s.used);
+    s.group = at_cta - s.start.row * (int)s.used;
+    s.lo = scaled(s.total, s.group, s.used);
+    s.hi = scaled(s.total, s.group + 1, s.used);
+    auto scan = [&](long long n) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, n, o);
+            if (lane >= o) n += v;
+        }
+        return n;
+    };
+    long long before = 0;                                    // columns of the requests before the share's first
+    if (few) {
+        const long long n = (long long)blocks_of(mine.row_tiles, k) * mine.key_tiles * a.n_kv, upto = scan(n);
+        const int b = __ffs(__ballot_sync(0xffffffffu, upto - n <= s.lo && s.lo < upto)) - 1;
+        before = __shfl_sync(0xffffffffu, upto - n, b);
+        s.start.b = b;
+        s.start.r = {__shfl_sync(0xffffffffu, mine.start, b),     __shfl_sync(0xffffffffu, mine.nodes, b),
+                     __shfl_sync(0xffffffffu, mine.row_tiles, b), __shfl_sync(0xffffffffu, mine.key_tiles, b),
+                     __shfl_sync(0xffffffffu, mine.ctx, b),       __shfl_sync(0xffffffffu, mine.keys, b)};
+    } else {
+        for (int b0 = 0; b0 < a.n_requests; b0 += kThreads) {    // ends in the chunk that holds column lo < total
+            const int b = b0 + tid;
+            if (b0 > 0 && b < a.n_requests) mine = request(a, b, m_rows);
+            const long long n = b < a.n_requests ? (long long)blocks_of(mine.row_tiles, k) * mine.key_tiles * a.n_kv : 0;
+            long long upto = scan(n);
+            if (lane == 31) sums[warp] = upto;
+            __syncthreads();
+            for (int w = 0; w < warp; ++w) upto += sums[w];
+            upto += before;
+            if (upto - n <= s.lo && s.lo < upto) scratch[0] = b, scratch[1] = upto - n;
+            for (int w = 0; w < kWarps; ++w) before += sums[w];
+            __syncthreads();
+            if (scratch[0] >= 0) break;
+        }
+        if (scratch[0] < 0) return false;                    // not reached
+        before = scratch[1];
+        s.start.b = (int)scratch[0];
+        s.start.r = request(a, s.start.b, m_rows);
+    }
+    const long long at = s.lo - before, unit = scaled(at, 1, s.start.r.key_tiles), block = scaled(unit, 1, a.n_kv);
     s.start.tile = (int)(at - unit * s.start.r.key_tiles);
-    s.start.row_tile = (int)scaled(unit, 1, a.n_kv);
-    s.start.head = (int)(unit - (long long)s.start.row_tile * a.n_kv);
+    s.start.head = (int)(unit - block * a.n_kv);
+    s.start.row_tile = (k == kMaxClass ? (int)block * kMaxClass : s.start.r.row_tiles - k) + s.start.row;
     return true;
 }
 
 // Parts of the unit at cursor c whose tile is the share's tile i and the last of
-// the share: CTA floor(((x + 1) used - 1) / total) has tile x.
+// the share: group floor(((x + 1) used - 1) / total) has column x. The CTAs of
+// neighbouring groups with the same row are neighbours.
 __device__ __forceinline__ int parts_of(const Share &s, const Cursor &c, int i) {
     const long long x = s.lo + i + (c.r.key_tiles - 1 - c.tile);
     const long long p = (x + 1) * s.used - 1;
-    return (int)scaled(p, 1, s.total) - (int)blockIdx.x + 1;
+    return (int)scaled(p, 1, s.total) - s.group + 1;
 }
 
 // Element offset of key `key` of the cursor's tile in the caches, -1: nobody sees it.

@@ -361,6 +361,14 @@ def test_tree_attention_chain(ops, ctx, nodes, heads, kv, dim, page, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nodes", [[1, 300, 9], [40, 130, 64, 700, 3], [513] * 2])
+def test_tree_attention_many_row_tiles(ops, nodes, dtype):
+    """Chains of one to dozens of row tiles in one call, over contexts that end anywhere in a tile of keys."""
+    c = _tree_case([(137 * i) % 700 for i in range(len(nodes))], nodes, 8, 2, 64, 32, dtype, seed=len(nodes))
+    _check_tree(c, *_run_tree(ops, c, mask=False), mask=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_tree_attention_wide_masks(ops, dtype):
     """Two and three mask words; nodes past the words are seen by nobody."""
     c = _tree_case([20, 5], [100, 30], 4, 2, 64, 16, dtype, words=2, seed=3)
