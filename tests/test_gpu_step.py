@@ -369,6 +369,15 @@ def test_tree_attention_many_row_tiles(ops, nodes, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("requests", [33, 400])
+def test_tree_attention_many_requests(ops, requests, dtype):
+    """More requests than a warp or a block has threads, some without nodes, with one to three row tiles."""
+    nodes = [(7 * i) % 41 for i in range(requests)]
+    c = _tree_case([(11 * i) % 90 for i in range(requests)], nodes, 8, 2, 64, 16, dtype, seed=requests)
+    _check_tree(c, *_run_tree(ops, c))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_tree_attention_wide_masks(ops, dtype):
     """Two and three mask words; nodes past the words are seen by nobody."""
     c = _tree_case([20, 5], [100, 30], 4, 2, 64, 16, dtype, words=2, seed=3)
