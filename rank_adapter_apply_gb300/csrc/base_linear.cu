@@ -9,7 +9,7 @@ namespace {
 
 using namespace step;
 
-// A CTA of up to eight warps takes 16 rows of W to a warp and, as one of the CTAs
+// A CTA of up to 16 warps takes 16 rows of W to a warp and, as one of the CTAs
 // of a cluster, a range of the columns; warps and cluster are chosen so that the
 // CTAs fill the SMs evenly (launch_tiles). Each warp streams its rows' 4-bit words from global memory
 // into registers, kAhead blocks of 128 columns ahead, and meets nobody on the way;
@@ -22,6 +22,12 @@ using namespace step;
 // products serve it with three times the multiplications. At the end the
 // cluster's parts are added in a fixed order through distributed shared memory: no
 // workspace, no atomics.
+//
+// What bounds it: for one token the words of W ought to, and a third to a half of their
+// rate is reached (1x4096x4096 5.4 us, 1.6 TB/s; 1x4096x14336 10.4 us, 3.0 TB/s): the
+// launch, the first loads and the cluster's end take 3 us of a call. In fp32, and in bf16
+// where x is not aligned, the products take over with the tokens (64x5120x8192: 71 us in
+// fp32, three products for each).
 //
 // Order of the columns. A block of 128 columns is four units of two products. Lane
 // t of a quad loads 16 bytes of a row, columns 32 t .. 32 t + 31. With groups of 128

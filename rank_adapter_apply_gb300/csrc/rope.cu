@@ -12,7 +12,7 @@ using namespace step;
 // ---- the table -----------------------------------------------------------------
 // Angles are formed in double (position * f has to be exact to ~1e-8 at
 // positions of 1e6 and more, where a product in fp32 is off by 0.06 rad) and
-// cos and sin rounded once.
+// cos and sin rounded once. Bound by the double precision units; built once.
 struct TableArgs {
     float *table;
     int n_positions, half, scaling;
@@ -107,7 +107,8 @@ __device__ __forceinline__ long long cache_place(const RopeArgs &a, long long t)
     return slot / a.page_size * a.c_page + slot % a.page_size * a.c_slot;
 }
 
-// Any layout: one warp per head row of one token, a lane takes pairs one by one.
+// Any layout: one warp per head row of one token, a lane takes pairs one by one. Bound by
+// its issue slots; for rows that are not whole 16-byte vectors.
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(256) rope_rows_kernel(RopeArgs a) {
     grid_dependency_wait();
@@ -140,7 +141,9 @@ __global__ void __launch_bounds__(256) rope_rows_kernel(RopeArgs a) {
 // and 2u + 1; past rot_dim (and in v): two neighbours to copy. A block has `units`
 // lanes for a row (unit = threadIdx.x) times blockDim.y rows; a thread takes its
 // unit of kRows rows of one token, whose cosines and sines it reads once, with all
-// loads in flight before the first is used.
+// loads in flight before the first is used. Bound by memory: 16384 tokens of 32 + 8 heads
+// of 128, with the append, 109 us, 6.2 TB/s; 1021 tokens in fp32 5.7 us, 4.1 TB/s (the
+// launch is 1.5 of them); 8 tokens 1.8 us, a launch and one round of reads.
 __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
@@ -250,7 +253,8 @@ template <typename T, bool kInterleaved>
 cudaError_t launch_rope(const RopeArgs &a, int sms, cudaStream_t st) {
     const long long rows = (long long)a.n_tokens * (a.n_heads + 2 * a.n_kv);
     if (by_vectors<T>(a, kInterleaved))
-        // rows of a thread: one where few rows leave SMs idle anyway
+        // rows of a thread, one / four: 8 tokens of 48 rows 1.9 / 2.8 us, 128 2.4 / 2.9, 256 3.1 / 3.2, 512 4.8 / 4.1, 1024
+        // 8.1 / 7.5
         return rows <= 64ll * sms ? launch_vectors<T, kInterleaved, 1>(a, st) : launch_vectors<T, kInterleaved, 4>(a, st);
     return launch_step(rope_rows_kernel<T, kInterleaved>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, 1, st, a);
 }

@@ -123,7 +123,9 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
 }
 
 // The same, run by a whole converged warp of which the lane with `lead` set issues:
-// operands that are the same in all lanes stay in uniform registers.
+// operands that are the same in all lanes stay in uniform registers. Issued from a
+// divergent branch each product also moves its operands there (64x4096x14336 of
+// base_linear, eight products to a unit: 22.8 us so, 14.6 us converged).
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t lead;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(lead));

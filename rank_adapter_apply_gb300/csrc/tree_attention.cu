@@ -13,6 +13,11 @@ using namespace step;
 using namespace tree;
 
 // ---- bf16, up to 32 rows a tile: mma.sync over the paged cache -------------------
+// Four warps share a tile of 16 or 32 rows and 64 keys, by rows and by keys; K and V
+// come by cp.async through the page table into a ring, a softmax with a running maximum
+// and sum goes over the tiles, and O stays in registers. For long contexts it is bound by
+// memory (16 requests of 7 nodes, ctx 8192, 32 heads over 8: 90 us, 4.7 TB/s); for few
+// keys by the latency of two launches and a tile or two (1x8 ctx 777: 12.7 us).
 
 constexpr int kStages = 3;
 
@@ -360,9 +365,11 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
 
 // Join the parts of the unit that goes on past CTA blockIdx.x's share. A warp
 // takes kR rows, with kAhead parts of each in flight; with kR = 1, for few units cut
-// into many parts, the block may take one row after another, a warp every eighth
-// part of it. (Most units have two or three parts and most blocks little to do: as
-// many blocks as rows / 8 cost 8 us more than rows / 32 with 128 rows to a tile.)
+// into many parts, above 24 parts the warps of a block share the parts of its eight
+// rows instead. It is latency: a launch, one read of the segment and one or more
+// rounds of reads, 4 of the 13 us of 1x8 ctx 777. (One row to a warp and four: 1x8 ctx
+// 777 12.7 and 16.0 us, 32x16 ctx 4096 89.4 and 89.0. 38 parts, 1x6 ctx 3000: 24.5 us row
+// after row, 17.6 so.)
 template <int DP>
 struct Joined {
     static constexpr int V = DP / 32;                    // columns of a lane
@@ -400,9 +407,9 @@ __device__ __forceinline__ void store_joined(const TreeArgs &a, const int4 &seg,
 
 template <typename T, int DP, int M, int kR>
 __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan, int m_rows) {
-    constexpr int V = Joined<DP>::V, kAhead = kR == 1 ? 4 : 2, kMany = 24;
-    __shared__ float so[8][DP];
-    __shared__ float2 sm[8];
+    constexpr int V = Joined<DP>::V, kAhead = kR == 1 ? 4 : 2, kMany = 24, kShared = kR == 1 ? 8 : 1;
+    __shared__ float so[kShared][kShared][DP];               // of a warp's parts, of a row
+    __shared__ float2 sm[kShared][kShared];
     grid_dependency_wait();
     grid_launch_dependents();
     const int4 seg = plan.seg[blockIdx.x];
@@ -420,41 +427,45 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan, i
             *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(src);
         }
     };
-    if (kR == 1 && seg.w > kMany) {
-        for (int i = 0; i < 8; ++i) {
-            const int r = blockIdx.y * 8 + i;
-            if (r >= rows) break;
-            Joined<DP> j;
+    if constexpr (kR == 1) {
+        if (seg.w > kMany) {                                 // a warp adds every eighth part of the block's eight rows
+            const int r0 = blockIdx.y * 8;
+            if (r0 >= rows) return;
+            Joined<DP> j[8];
 #pragma unroll
-            for (int e = 0; e < V; ++e) j.o[e] = 0.f;
-            for (int p = warp; p < seg.w; p += kAhead * 8) {
-                float v[kAhead][V];
-                float2 ml[kAhead];
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u)
-                    if (p + u * 8 < seg.w) read(p + u * 8, r, ml[u], v[u]);
+                for (int e = 0; e < V; ++e) j[i].o[e] = 0.f;
+            for (int p = warp; p < seg.w; p += 8) {
+                float v[8][V];
+                float2 ml[8];
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u)
-                    if (p + u * 8 < seg.w) j.add(ml[u], v[u]);
+                for (int i = 0; i < 8; ++i)
+                    if (r0 + i < rows) read(p, r0 + i, ml[i], v[i]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (r0 + i < rows) j[i].add(ml[i], v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+#pragma unroll
+                for (int e = 0; e < V; ++e) so[warp][i][lane * V + e] = j[i].o[e];
+                if (lane == 0) sm[warp][i] = make_float2(j[i].m, j[i].l);
             }
             __syncthreads();
-#pragma unroll
-            for (int e = 0; e < V; ++e) so[warp][lane * V + e] = j.o[e];
-            if (lane == 0) sm[warp] = make_float2(j.m, j.l);
-            __syncthreads();
-            if (warp != i) continue;
+            if (r0 + warp >= rows) return;
             Joined<DP> all;
 #pragma unroll
             for (int e = 0; e < V; ++e) all.o[e] = 0.f;
             for (int w = 0; w < 8; ++w) {
                 float v[V];
 #pragma unroll
-                for (int e = 0; e < V; ++e) v[e] = so[w][lane * V + e];
-                all.add(sm[w], v);
+                for (int e = 0; e < V; ++e) v[e] = so[w][warp][lane * V + e];
+                all.add(sm[w][warp], v);
             }
-            store_joined<T, DP>(a, seg, start, seg.y * m_rows + r, all);
+            store_joined<T, DP>(a, seg, start, seg.y * m_rows + r0 + warp, all);
+            return;
         }
-        return;
     }
     const int r0 = (blockIdx.y * 8 + warp) * kR;
     if (r0 >= rows) return;
@@ -485,7 +496,10 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan, i
 constexpr int kMaxRows = 128;
 constexpr int kMaxCtas = 2 * 160;
 
-// The row tile by the average rows (nodes times query heads of a key/value head) of a request.
+// The row tile by the average rows (nodes times query heads of a key/value head) of a request. 8 requests, ctx 4096, 32
+// heads over 8, tiles of 16 / 32 / 128 rows: 8 rows 34.6 / 35.4 / 35.6 us, 16 rows 36.0 / 36.3 / 35.5, 24 rows 45.1 / 38.0 /
+// 36.8, 32 rows 45.5 / 38.2 / 37.4, 48 rows 58.9 / 50.9 / 38.9, 128 rows 119 / 80 / 47. For few keys 32 beats 128 up to 32
+// rows: 1x8 ctx 777 12.7 and 14.8, 4x8 ctx 500 13.6 and 17.7.
 int rows_of_tile(const TreeArgs &a) {
     const double rows = (double)a.n_tokens * (a.n_heads / a.n_kv) / a.n_requests;
     return rows <= 16.0 ? 16 : rows <= 32.0 || !tc_takes(a) ? 32 : 128;
@@ -538,7 +552,8 @@ cudaError_t launch_bf16(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
 
 template <int DP>
 cudaError_t launch_fp32(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
-    // rows beyond a request's cost their FMAs all the same: 16 up to an average of 16, as below
+    // rows beyond a request's cost their FMAs all the same: 8 requests, ctx 4096, tiles of 16 / 64 rows: 16 rows 117 / 182
+    // us, 24 rows 211 / 183
     const int rows = (double)a.n_tokens * (a.n_heads / a.n_kv) / a.n_requests <= 16.0 ? 16 : 64;
     const cudaError_t e = launch_f32(a, plan, rows, st);
     if (e != cudaSuccess) return e;

@@ -39,6 +39,11 @@ struct Shared {
 // distributed shared memory in a fixed order. A first child needs no pass: S_0 is 1.
 // So a request reads one row of p, q and noise, and p and q once more for each
 // rejection that is followed by another sibling.
+//
+// What bounds it: for large batches memory (256 requests of 8 nodes, vocabulary 131072, two
+// fp32 rows and the noise: 79 us, 5.1 TB/s of what one pass reads, and a rejection reads
+// more); for few the chain of passes, each a round of reads and two cluster barriers (32x13
+// of 100003 17.3 us, 1x5 of 32000 5.7 us).
 // Visit a CTA's part of a row: f(v, p[v], q[v], noise[v]) for every index v, in
 // rising order within a thread. Whole 16-byte vectors of p, at whatever element
 // the row's first one starts, are dealt to the cluster; the elements before and
@@ -253,6 +258,9 @@ cudaError_t launch_threads(const VerifyArgs &a, int cluster, cudaStream_t st) {
 
 // CTAs for a request: 1024 threads of them fit an SM, and few requests are cut
 // further, over at most eight CTAs; where even those leave room, they are larger.
+// Trees of 13 nodes over 100003 tokens in bf16, clusters until 2 / 6 / 12 CTAs to an SM:
+// 256 requests 73 / 65 / 75 us, 512 151 / 121 / 114, 32 and fewer alike. CTAs of 256 / 512
+// threads: 1 request 12.0 / 11.0 us, 32 17.6 / 17.3, 64 25.1 / 33.8, 256 65 / 77.
 template <typename T, bool kDraft>
 cudaError_t launch_verify(const VerifyArgs &a, int sms, cudaStream_t st) {
     int cluster = 1;
