@@ -15,9 +15,9 @@ using namespace step;
 // into registers, kAhead blocks of 128 columns ahead, and meets nobody on the way;
 // x of a slice of KS columns lies in shared memory for all of them. A product
 // mma(W 16 x 16, x^T 16 x 8) has the rows of W as its rows and eight tokens as its
-// columns. The 4-bit values become bf16 integers in registers: 0x4300 | n is 128 +
-// n, and subtracting 128 + z leaves n - z exactly. So the products within a group
-// are exact in fp32, and the group's fp32 sum is scaled once. An x in fp32 is cut
+// columns. The 4-bit values become (n - z) / 64 in registers, exact in bf16
+// (nibbles()). So the products within a group are exact, and the group's fp32 sum is
+// scaled once. An x in fp32 is cut
 // into three bf16 parts of eight bits each that sum to it exactly, so the same
 // products serve it with three times the multiplications. At the end the
 // cluster's parts are added in a fixed order through distributed shared memory: no
@@ -47,11 +47,14 @@ struct LinearTile {
     static_assert(KS % (128 * kAhead) == 0, "a slice is whole rounds of the register ring");
 };
 
-__device__ __forceinline__ uint32_t nibbles(uint32_t w, uint32_t zz) {
+// Nibbles 0 and 4 (kHigh: 1 and 5) of w, less the zero, over 64. Bits v < 256 of a bf16 are the number v 2^-133,
+// subnormal or not: n 2^-133 2^127 or 16 n 2^-133 2^123, and minus_z = -z / 64, twice, added in the same exact operation.
+template <bool kHigh>
+__device__ __forceinline__ uint32_t nibbles(uint32_t w, uint32_t minus_z) {
     uint32_t v;
-    asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xea;" : "=r"(v) : "r"(w));     // (w & mask) | magic
-    __nv_bfloat162 h = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&v), *reinterpret_cast<__nv_bfloat162 *>(&zz));
-    return *reinterpret_cast<uint32_t *>(&h);
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+        : "=r"(v) : "r"(w & (kHigh ? 0x00f000f0u : 0x000f000fu)), "r"(kHigh ? 0x7d007d00u : 0x7f007f00u), "r"(minus_z));
+    return v;
 }
 
 // The first product of a group: D = A * B.
@@ -244,9 +247,9 @@ __global__ void __launch_bounds__(32 * C::kMaxWarps, C::kCtas) linear_tiles_kern
                     wd[h][0] = w[i][h].x, wd[h][1] = w[i][h].y, wd[h][2] = w[i][h].z, wd[h][3] = w[i][h].w;
                     exchange<GU>(wd[h], t4);
                     sf[h] = to_f32(sc[i][h]);
-                    z[h] = 0x43084308u;                             // 128 + 8, twice
-                    if (kZeros) {                                   // 128 + z, twice: exact in bf16 up to 256
-                        const uint32_t zb = __float_as_uint(128.f + (float)min(zr[i][h], 128u)) >> 16;
+                    z[h] = 0xbe00be00u;                             // -8 / 64, twice
+                    if (kZeros) {
+                        const uint32_t zb = __float_as_uint((float)min(zr[i][h], 128u) * -0.015625f) >> 16;
                         z[h] = zb | zb << 16;
                     }
                 }
@@ -259,10 +262,10 @@ __global__ void __launch_bounds__(32 * C::kMaxWarps, C::kCtas) linear_tiles_kern
                     const uint32_t z1 = kZeros && kGroups > 1 ? __shfl_sync(0xffffffffu, z[1], u / GU, 4) : z[1];
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        f[half][0] = nibbles(wd[0][u] >> (8 * half), z0);
-                        f[half][1] = nibbles(wd[1][u] >> (8 * half), z1);
-                        f[half][2] = nibbles(wd[0][u] >> (8 * half + 4), z0);
-                        f[half][3] = nibbles(wd[1][u] >> (8 * half + 4), z1);
+                        f[half][0] = nibbles<false>(wd[0][u] >> (8 * half), z0);
+                        f[half][1] = nibbles<false>(wd[1][u] >> (8 * half), z1);
+                        f[half][2] = nibbles<true>(wd[0][u] >> (8 * half), z0);
+                        f[half][3] = nibbles<true>(wd[1][u] >> (8 * half), z1);
                     }
 #pragma unroll
                     for (int n = 0; n < C::NT; ++n) {
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(32 * C::kMaxWarps, C::kCtas) linear_tiles_kern
 #pragma unroll
             for (int p = 1; p < kMaxCluster; ++p) sum += v[p];
         }
-        static_cast<X *>(a.y)[(size_t)(tok0 + t) * a.y_stride + row0 + r] = from_f32<X>(sum);
+        static_cast<X *>(a.y)[(size_t)(tok0 + t) * a.y_stride + row0 + r] = from_f32<X>(sum * 64.f);       // nibbles() gives 64ths
     }
     if (cluster > 1) cluster_sync_all();                            // the peers have read this CTA's parts
 }
@@ -381,17 +384,18 @@ cudaError_t launch_group(const LinearArgs &a, int sms, cudaStream_t st) {
     }
 }
 
-// The kernel and its tokens' tile. bf16 above 8 tokens goes to the 5th-generation tensor cores where TMA can load x (16-byte
-// aligned rows), measured for 4096x4096, 5120x8192 and 4096x14336 (d_in x d_out): 1 token 5.3 / 9.0 / 10.4 us here and
-// 5.9 / 9.3 / 11.2 there, 8 tokens 6.0 / 10.0 / 11.7 and 6.0 / 9.4 / 11.3, 16 tokens 8.3 / 12.7 / 14.9 and 6.3 / 9.5 / 11.5,
-// 64 tokens 15.1 / 29.9 / 32.3 and 7.8 / 12.7 / 13.6. Up to 16 tokens: two CTAs of eight warps to an SM. Above, the
-// accumulators want the registers of twelve warps to an SM (16 with the three parts of fp32), in one CTA, whose copy of x
-// then serves more rows (48 tokens in bf16: 12.5 / 23.4 / 26.2 us, against 14.1 / 25.5 / 32.1 with two CTAs of eight).
+// The kernel and its tokens' tile. bf16 from 4 tokens goes to the 5th-generation tensor cores where TMA can load x (16-byte
+// aligned rows), measured for 4096x4096, 5120x8192 and 4096x14336 (d_in x d_out), W from memory: 2 tokens 6.3 / 10.6 / 11.4
+// us here and 6.5 / 10.0 / 11.6 there, 4 tokens 6.5 / 10.4 / 12.0 and 6.5 / 10.0 / 11.6, 8 tokens 6.9 / 10.8 / 12.7 and 6.6 /
+// 10.0 / 11.6; from L2, 16 tokens 8.3 / 12.7 / 14.9 and 6.3 / 9.5 / 11.5, 64 tokens 15.1 / 29.9 / 32.3 and 8.0 / 12.5 /
+// 13.4. Up to 16 tokens: two CTAs of eight warps to an SM. Above, the accumulators want the registers of twelve warps to an
+// SM (16 with the three parts of fp32), in one CTA, whose copy of x then serves more rows (48 tokens in bf16: 12.5 / 23.4 /
+// 26.2 us, against 14.1 / 25.5 / 32.1 with two CTAs of eight).
 cudaError_t launch_linear(const LinearArgs &a, int dtype, int sms, cudaStream_t st) {
     if (dtype == LORA_DTYPE_BF16) {
         using X = __nv_bfloat16;
+        if (a.n_tokens >= 4 && tc_takes(a)) return launch_tc(a, sms, st);
         if (a.n_tokens <= 8) return launch_group<LinearTile<X, 1, 2048, 4, 2, 8>>(a, sms, st);
-        if (tc_takes(a)) return launch_tc(a, sms, st);
         if (a.n_tokens <= 16) return launch_group<LinearTile<X, 2, 2048, 4, 2, 8>>(a, sms, st);
         if (a.n_tokens <= 32) return launch_group<LinearTile<X, 4, 1024, 4, 1, 12>>(a, sms, st);
         return launch_group<LinearTile<X, 8, 1024, 1, 1, 12>>(a, sms, st);
