@@ -24,7 +24,7 @@ using namespace step;
 // workspace, no atomics.
 //
 // What bounds it: for one token the words of W ought to, and a third to a half of their
-// rate is reached (1x4096x4096 5.4 us, 1.6 TB/s; 1x4096x14336 10.4 us, 3.0 TB/s): the
+// rate is reached (W from memory: 1x4096x4096 6.1 us, 1.4 TB/s; 1x4096x14336 11.2 us, 2.7 TB/s): the
 // launch, the first loads and the cluster's end take 3 us of a call. In fp32, and in bf16
 // where x is not aligned, the products take over with the tokens (64x5120x8192: 71 us in
 // fp32, three products for each).

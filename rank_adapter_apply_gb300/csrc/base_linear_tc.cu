@@ -33,7 +33,7 @@ namespace {
 using namespace step;
 
 constexpr int kRows = 128;
-constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr uint32_t kWaitLimit = 1u << 18;       // polls, of some microseconds each: about a second
 
 template <int N_, int S_>
 struct TcTile {
@@ -380,13 +380,17 @@ cudaError_t launch(const LinearArgs &a, int sms, cudaStream_t st) {
     static ActiveClusters known;
     const int blocks = (a.d_in + 255) / 256, tok_tiles = (a.n_tokens + C::N - 1) / C::N;
     const long long tiles = (long long)((a.d_out + kRows - 1) / kRows) * tok_tiles;
+    // CTAs of a cluster: the least of an estimate in clocks, 5000 for a round of CTAs (launch, first loads, sums), 3000 for a
+    // cluster's sums, 900 for a block of columns. It came within 1 % of the fastest of 1..8 for each of 45 shapes of
+    // 512 to 14336 columns and rows and 16 to 64 tokens. 32 tokens with 1 / 2 / 3 / 4 / 8: 4096x4096 11.8 / 9.3 / 8.2 / 7.4 / 18.2 us (two
+    // rounds), 4096x14336 12.4 / 19.0 / 24.4 / 28.1 / 49.6, 4096x1024 11.4 / 9.0 / 7.7 / 6.7 / 6.1.
     int cluster = 1;
     long long least = INT64_MAX;
     for (int c = 1; c <= kMaxCluster && (c == 1 || c <= blocks); ++c) {
         const int at_once = active_clusters(kernel, C::kThreads, C::kSmem, c, known);
         if (at_once < 1) continue;
         const long long rounds = (tiles + at_once - 1) / at_once;
-        const long long cost = rounds * (5000 + (c > 1 ? 1500 : 0) + (long long)((blocks + c - 1) / c) * 900);
+        const long long cost = rounds * (5000 + (c > 1 ? 3000 : 0) + (long long)((blocks + c - 1) / c) * 900);
         if (cost < least) least = cost, cluster = c;
     }
     TcArgs args;

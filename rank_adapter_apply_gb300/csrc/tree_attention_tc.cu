@@ -41,7 +41,7 @@ constexpr int kRows = 128;                     // lanes of an accumulator; rows 
 constexpr int kThreads = 192;
 constexpr int kItems = 5;                      // ring of K and V items
 constexpr int kMeta = 4;                       // ring of the tiles' masks
-constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr uint32_t kWaitLimit = 1u << 18;       // polls, of some microseconds each: about a second
 
 template <int DP>
 struct Tc {

@@ -84,6 +84,11 @@ def test_refused(lib, name, make, change):
         getattr(B, name)(ctypes.byref(d), None)
 
 
+def test_wait_timeouts_needs_a_place(lib):
+    assert lib.lora_step_wait_timeouts(None) == B.LORA_ERR_ARG
+    assert b"step_wait_timeouts" in lib.lora_last_error()
+
+
 def test_null_descriptors(lib):
     for name, _, _ in REFUSED:
         assert getattr(lib, name)(None, None) == B.LORA_ERR_ARG
