@@ -9,7 +9,7 @@ namespace {
 
 using namespace step;
 
-// A CTA of up to 16 warps takes 16 rows of W to a warp and, as one of the CTAs
+// bf16 on mma.sync. A CTA of up to 12 warps takes 16 rows of W to a warp and, as one of the CTAs
 // of a cluster, a range of the columns; warps and cluster are chosen so that the
 // CTAs fill the SMs evenly (launch_tiles). Each warp streams its rows' 4-bit words from global memory
 // into registers, kAhead blocks of 128 columns ahead, and meets nobody on the way;
@@ -17,17 +17,14 @@ using namespace step;
 // mma(W 16 x 16, x^T 16 x 8) has the rows of W as its rows and eight tokens as its
 // columns. The 4-bit values become (n - z) / 64 in registers, exact in bf16
 // (nibbles()). So the products within a group are exact, and the group's fp32 sum is
-// scaled once. An x in fp32 is cut
-// into three bf16 parts of eight bits each that sum to it exactly, so the same
-// products serve it with three times the multiplications. At the end the
+// scaled once. At the end the
 // cluster's parts are added in a fixed order through distributed shared memory: no
 // workspace, no atomics.
 //
 // What bounds it: for one token the words of W ought to, and a third to a half of their
 // rate is reached (W from memory: 1x4096x4096 6.1 us, 1.4 TB/s; 1x4096x14336 11.2 us, 2.7 TB/s): the
-// launch, the first loads and the cluster's end take 3 us of a call. In fp32, and in bf16
-// where x is not aligned, the products take over with the tokens (64x5120x8192: 71 us in
-// fp32, three products for each).
+// launch, the first loads and the cluster's end take 3 us of a call. Where x is not aligned
+// it also serves many tokens, and the products take over (64x5120x8192 29.9 us).
 //
 // Order of the columns. A block of 128 columns is four units of two products. Lane
 // t of a quad loads 16 bytes of a row, columns 32 t .. 32 t + 31. With groups of 128
@@ -35,15 +32,13 @@ using namespace step;
 // within a group, so the quad first exchanges words (exchange()). Within a word the
 // halves of a register are nibbles 16 bits apart: 0 4 | 1 5 | 2 6 | 3 7. x is put
 // into the same order when it is staged (x_place() and the byte permutes).
-template <typename X_, int NT_, int KS_, int kAhead_, int kCtas_, int kMaxWarps_>
+template <int NT_, int KS_, int kAhead_, int kCtas_, int kMaxWarps_>
 struct LinearTile {
-    using X = X_;                                                   // type of x, scales and y
     static constexpr int NT = NT_, KS = KS_, kAhead = kAhead_, kCtas = kCtas_;
-    static constexpr int kParts = sizeof(X) == 4 ? 3 : 1;           // bf16 parts of x
     static constexpr int kMaxWarps = kMaxWarps_, T = 8 * NT;        // tokens
-    static constexpr int kXRow = KS * 2, kPlane = T * kXRow;        // bytes of a staged row, of a part, of x
+    static constexpr int kXRow = KS * 2, kPlane = T * kXRow;        // bytes of a staged row, of x
     static constexpr int kParted = T * (16 * kMaxWarps + 1) * 4;    // bytes of the parts of the sums, at most
-    static constexpr int kSmem = kParts * kPlane > kParted ? kParts * kPlane : kParted;
+    static constexpr int kSmem = kPlane > kParted ? kPlane : kParted;
     static_assert(KS % (128 * kAhead) == 0, "a slice is whole rounds of the register ring");
 };
 
@@ -65,50 +60,6 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
-
-// Eight columns of a token, as one bf16 part or three.
-template <typename X>
-struct Piece;
-template <>
-struct Piece<__nv_bfloat16> {
-    uint4 raw;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool ok, int vec) {
-        raw = load8_bf16(reinterpret_cast<const uint16_t *>(p), 0, 8, ok, vec);
-    }
-    __device__ __forceinline__ uint4 take() const { return raw; }
-};
-template <>
-struct Piece<float> {
-    float v[8];
-    __device__ __forceinline__ void load(const float *p, bool ok, int vec) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
-        if (!ok) return;
-        if (vec) {
-            *reinterpret_cast<float4 *>(v) = __ldg(reinterpret_cast<const float4 *>(p));
-            *reinterpret_cast<float4 *>(v + 4) = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = p[i];
-        }
-    }
-    // The next part: the upper eight significand bits (cut, not rounded, so that it stays in range); what is left
-    // is exact. An infinity or NaN is the first part alone.
-    __device__ __forceinline__ uint4 take() {
-        uint32_t h[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            h[i] = __float_as_uint(v[i]) & 0xffff0000u;
-            if ((h[i] & 0x7f800000u) == 0x7f800000u) {
-                if (v[i] != v[i]) h[i] |= 0x00400000u;              // a NaN whose upper half reads as an infinity
-                v[i] = 0.f;
-            } else {
-                v[i] -= __uint_as_float(h[i]);
-            }
-        }
-        return make_uint4(h[0] >> 16 | h[1], h[2] >> 16 | h[3], h[4] >> 16 | h[5], h[6] >> 16 | h[7]);
-    }
-};
 
 // W is read once: 16 bytes past the L1.
 __device__ __forceinline__ uint4 load_w(const uint8_t *p) {
@@ -162,7 +113,7 @@ __global__ void __launch_bounds__(32 * C::kMaxWarps, C::kCtas) linear_tiles_kern
     const int nt = min(C::T, a.n_tokens - tok0);
     const int groups = a.d_in / (GU * 32), blocks = (a.d_in + 127) / 128;
     const int b_lo = (int)((long long)blocks * rank / cluster), b_hi = (int)((long long)blocks * (rank + 1) / cluster);
-    using X = typename C::X;
+    using X = __nv_bfloat16;
     const X *x = static_cast<const X *>(a.x) + (size_t)tok0 * a.x_stride;
 
     grid_dependency_wait();
@@ -207,29 +158,27 @@ __global__ void __launch_bounds__(32 * C::kMaxWarps, C::kCtas) linear_tiles_kern
         const int n_blocks = min(kSliceBlocks, b_hi - s_lo);
         if (s_lo != b_lo) __syncthreads();
         // A warp takes a block's 16 pieces of two tokens at a time: piece and place of a lane are always the same.
-        constexpr int kBatch = C::NT == 1 || C::kParts == 3 ? 4 : 8;    // pieces of a thread whose loads are in flight
+        constexpr int kBatch = C::NT == 1 ? 4 : 8;    // pieces of a thread whose loads are in flight
         const int q = lane & 15, odd = lane >> 4;                   // odd token of the pair
         unsigned char *dst = smem + odd * C::kXRow + ((x_place<GU>(q) ^ (odd << 2)) << 4);
         const int pairs = s_lo == b_lo ? C::T / 2 : (nt + 1) / 2;   // rows past the tokens are cleared once
         for (int i0 = warp; i0 < pairs * kSliceBlocks; i0 += warps * kBatch) {
-            Piece<X> v[kBatch];
+            uint4 v[kBatch];
 #pragma unroll
             for (int e = 0; e < kBatch; ++e) {
                 const int i = i0 + e * warps, t = i / kSliceBlocks * 2 + odd, blk = i % kSliceBlocks;
                 const int k = (s_lo + blk) * 128 + q * 8;
-                v[e].load(x + (size_t)t * a.x_stride + k, t < nt && blk < n_blocks && k < a.d_in, x_vec);
+                v[e] = load8_bf16(reinterpret_cast<const uint16_t *>(x + (size_t)t * a.x_stride + k), 0, 8,
+                                  t < nt && blk < n_blocks && k < a.d_in, x_vec);
             }
 #pragma unroll
             for (int e = 0; e < kBatch; ++e) {
                 const int i = i0 + e * warps, t2 = i / kSliceBlocks * 2, blk = i % kSliceBlocks;
                 if (t2 >= C::T) break;
-#pragma unroll
-                for (int part = 0; part < C::kParts; ++part) {
-                    const uint4 o = v[e].take();
-                    *reinterpret_cast<uint4 *>(dst + part * C::kPlane + t2 * C::kXRow + blk * 256) =
-                        make_uint4(__byte_perm(o.x, o.z, 0x5410), __byte_perm(o.x, o.z, 0x7632),
-                                   __byte_perm(o.y, o.w, 0x5410), __byte_perm(o.y, o.w, 0x7632));
-                }
+                const uint4 &o = v[e];
+                *reinterpret_cast<uint4 *>(dst + t2 * C::kXRow + blk * 256) =
+                    make_uint4(__byte_perm(o.x, o.z, 0x5410), __byte_perm(o.x, o.z, 0x7632), __byte_perm(o.y, o.w, 0x5410),
+                               __byte_perm(o.y, o.w, 0x7632));
             }
         }
         __syncthreads();
@@ -269,16 +218,13 @@ __global__ void __launch_bounds__(32 * C::kMaxWarps, C::kCtas) linear_tiles_kern
                     }
 #pragma unroll
                     for (int n = 0; n < C::NT; ++n) {
-#pragma unroll
-                        for (int e = 0; e < C::kParts; ++e) {
-                            const uint4 b = *reinterpret_cast<const uint4 *>(xbase + e * C::kPlane + n * 8 * C::kXRow + i * 256 +
-                                                                             (u >> 1) * 128 + (u & 1) * x_odd);
-                            if (u % GU == 0 && e == 0)
-                                mma_bf16_first(part[n], f[0], b.x, b.y);
-                            else
-                                mma_bf16(part[n], f[0][0], f[0][1], f[0][2], f[0][3], b.x, b.y);
-                            mma_bf16(part[n], f[1][0], f[1][1], f[1][2], f[1][3], b.z, b.w);
-                        }
+                        const uint4 b =
+                            *reinterpret_cast<const uint4 *>(xbase + n * 8 * C::kXRow + i * 256 + (u >> 1) * 128 + (u & 1) * x_odd);
+                        if (u % GU == 0)
+                            mma_bf16_first(part[n], f[0], b.x, b.y);
+                        else
+                            mma_bf16(part[n], f[0][0], f[0][1], f[0][2], f[0][3], b.x, b.y);
+                        mma_bf16(part[n], f[1][0], f[1][1], f[1][2], f[1][3], b.z, b.w);
                     }
                     if (u % GU == GU - 1) {
                         const float s0 = kGroups > 1 ? __shfl_sync(0xffffffffu, sf[0], u / GU, 4) : sf[0];
@@ -350,7 +296,7 @@ cudaError_t launch_tiles(const LinearArgs &a, int sms, cudaStream_t st) {
     // clusters of 8: 5.7 us; 7 and 4: 7.1; 7 and 8, in two rounds: 8.9. 1x14336x4096: 8, 8: 13.0; 7, 4: 20.7.
     // 1x4096x14336: 6, 2: 10.5; 8, 2: 12.0; 4, 5, in two rounds: 15.4.
     const int tok_tiles = (a.n_tokens + C::T - 1) / C::T, blocks = (a.d_in + 127) / 128;
-    constexpr int kProducts = C::NT * C::kParts, kIssue = (150 + 28 * kProducts) / 4, kTensor = 16 * kProducts;
+    constexpr int kIssue = (150 + 28 * C::NT) / 4, kTensor = 16 * C::NT;
     static ActiveClusters known[C::kMaxWarps + 1];
     int warps = C::kMaxWarps, cluster = 1;
     long long least = INT64_MAX;
@@ -365,7 +311,7 @@ cudaError_t launch_tiles(const LinearArgs &a, int sms, cudaStream_t st) {
                                                         (900 + on_sm * (w * std::max(kIssue, kTensor) + 2 * C::T)));
             if (cost < least) least = cost, warps = w, cluster = c;
         }
-    const int x_vec = aligned16(a.x) && a.x_stride * sizeof(typename C::X) % 16 == 0;
+    const int x_vec = aligned16(a.x) && a.x_stride % 8 == 0;
     const dim3 grid((a.d_out + 16 * warps - 1) / (16 * warps) * cluster, tok_tiles);
     return launch_step(kernel, grid, dim3(32 * warps), C::kSmem, cluster, st, a, cluster, x_vec);
 }
@@ -388,24 +334,16 @@ cudaError_t launch_group(const LinearArgs &a, int sms, cudaStream_t st) {
 // aligned rows), measured for 4096x4096, 5120x8192 and 4096x14336 (d_in x d_out), W from memory: 2 tokens 6.3 / 10.6 / 11.4
 // us here and 6.5 / 10.0 / 11.6 there, 4 tokens 6.5 / 10.4 / 12.0 and 6.5 / 10.0 / 11.6, 8 tokens 6.9 / 10.8 / 12.7 and 6.6 /
 // 10.0 / 11.6; from L2, 16 tokens 8.3 / 12.7 / 14.9 and 6.3 / 9.5 / 11.5, 64 tokens 15.1 / 29.9 / 32.3 and 8.0 / 12.5 /
-// 13.4. Up to 16 tokens: two CTAs of eight warps to an SM. Above, the accumulators want the registers of twelve warps to an
-// SM (16 with the three parts of fp32), in one CTA, whose copy of x then serves more rows (48 tokens in bf16: 12.5 / 23.4 /
-// 26.2 us, against 14.1 / 25.5 / 32.1 with two CTAs of eight).
+// 13.4. fp32 always goes there (with three products for each here, 1 token 8.8 / 16.5 / 19.0 us against 7.7 / 13.3 / 16.9, 64
+// tokens 41 / 71 / 88 against 17.7 / 37.7 / 58.6). Here, up to 16 tokens: two CTAs of eight warps to an SM. Above, the
+// accumulators want the registers of twelve warps to an SM, in one CTA, whose copy of x then serves more rows (48 tokens:
+// 12.5 / 23.4 / 26.2 us, against 14.1 / 25.5 / 32.1 with two CTAs of eight).
 cudaError_t launch_linear(const LinearArgs &a, int dtype, int sms, cudaStream_t st) {
-    if (dtype == LORA_DTYPE_BF16) {
-        using X = __nv_bfloat16;
-        if (a.n_tokens >= 4 && tc_takes(a)) return launch_tc(a, sms, st);
-        if (a.n_tokens <= 8) return launch_group<LinearTile<X, 1, 2048, 4, 2, 8>>(a, sms, st);
-        if (a.n_tokens <= 16) return launch_group<LinearTile<X, 2, 2048, 4, 2, 8>>(a, sms, st);
-        if (a.n_tokens <= 32) return launch_group<LinearTile<X, 4, 1024, 4, 1, 12>>(a, sms, st);
-        return launch_group<LinearTile<X, 8, 1024, 1, 1, 12>>(a, sms, st);
-    }
-    if (a.n_tokens <= 8) return launch_group<LinearTile<float, 1, 1024, 4, 2, 8>>(a, sms, st);
-    if (a.n_tokens <= 16) return launch_group<LinearTile<float, 2, 1024, 4, 2, 8>>(a, sms, st);
-    if (a.n_tokens <= 24) return launch_group<LinearTile<float, 3, 1024, 4, 1, 12>>(a, sms, st);
-    if (a.n_tokens <= 32) return launch_group<LinearTile<float, 4, 1024, 4, 1, 12>>(a, sms, st);
-    if (a.n_tokens <= 48) return launch_group<LinearTile<float, 6, 512, 2, 1, 16>>(a, sms, st);
-    return launch_group<LinearTile<float, 8, 512, 1, 1, 16>>(a, sms, st);
+    if (dtype == LORA_DTYPE_F32 || (a.n_tokens >= 4 && tc_takes(a))) return launch_tc(a, dtype, sms, st);
+    if (a.n_tokens <= 8) return launch_group<LinearTile<1, 2048, 4, 2, 8>>(a, sms, st);
+    if (a.n_tokens <= 16) return launch_group<LinearTile<2, 2048, 4, 2, 8>>(a, sms, st);
+    if (a.n_tokens <= 32) return launch_group<LinearTile<4, 1024, 4, 1, 12>>(a, sms, st);
+    return launch_group<LinearTile<8, 1024, 1, 1, 12>>(a, sms, st);
 }
 
 }  // namespace

@@ -57,9 +57,10 @@ int active_clusters(Kernel kernel, int threads, size_t smem, int c, ActiveCluste
     return n;
 }
 
-// In bf16 on the 5th-generation tensor cores (base_linear_tc.cu): whether TMA can load x, and the launch.
+// On the 5th-generation tensor cores (base_linear_tc.cu): whether TMA can load x in bf16 (fp32 it takes as it is), and the
+// launch.
 bool tc_takes(const LinearArgs &a);
-cudaError_t launch_tc(const LinearArgs &a, int sms, cudaStream_t st);
+cudaError_t launch_tc(const LinearArgs &a, int dtype, int sms, cudaStream_t st);
 // CTAs whose bounded waits gave up.
 cudaError_t read_timeouts(unsigned *count);
 

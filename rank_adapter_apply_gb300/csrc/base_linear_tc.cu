@@ -1,4 +1,4 @@
-// lora_base_linear in bf16 on the 5th-generation tensor cores.
+// lora_base_linear on the 5th-generation tensor cores.
 //
 // A CTA takes 128 rows of W, up to N tokens and, as one of the CTAs of a cluster, a
 // range of the columns. Blocks of 256 columns of the 4-bit words and of x come by
@@ -7,6 +7,10 @@
 // tensor memory as the A operand. The products within one group are exact, their sum is
 // fp32; it comes back to the row's thread, which scales it into its fp32 accumulators. So
 // no weight is ever rounded.
+//
+// An x in fp32 is cut by eight more warps into three bf16 parts of eight bits each that
+// sum to it exactly; they lie side by side as three times the tokens in one product, and
+// their sums meet in the row's accumulators.
 //
 // S sets of four warps take units of up to 128 columns in turn, each with its own A and
 // D in tensor memory, so the reads, the conversion, the products and the sums of S units
@@ -19,7 +23,8 @@
 // products 23 % of 64x5120x8192. It is the chain of a unit, reading, ten instructions for
 // eight values, tensor memory, products, sums, that two or three sets do not hide, and a
 // third set has no room for its D. 128 rows to a CTA leave SMs idle (4096 rows: 128 CTAs
-// of 152), and the launch, the first loads and the cluster's end take 4 us of a call.
+// of 152), and the launch, the first loads and the cluster's end take 4 us of a call. In
+// fp32 64x5120x8192 takes 38 us: cutting x, for each 128 rows again, is its pace.
 #include "base_linear.cuh"
 #include "tc_util.cuh"
 #include "tensor_map.cuh"
@@ -35,19 +40,23 @@ using namespace step;
 constexpr int kRows = 128;
 constexpr uint32_t kWaitLimit = 1u << 18;       // polls, of some microseconds each: about a second
 
-template <int N_, int S_>
+template <typename X_, int N_, int S_>
 struct TcTile {
+    using X = X_;                                                   // type of x, scales and y
     static constexpr int N = N_, S = S_;                            // tokens, sets of warps
-    static constexpr int kWBytes = kRows * 128, kStage = kWBytes + N * 512;  // 256 columns of W and of x
+    static constexpr int kParts = sizeof(X) == 4 ? 3 : 1;           // bf16 parts of x
+    static constexpr int ND = kParts * N;                           // columns of D, rows of B: the parts side by side
+    static constexpr int kWBytes = kRows * 128, kStage = kWBytes + ND * 512;    // 256 columns of W, and of x
     static constexpr int kStages = 192 * 1024 / kStage, kSmem = kStages * kStage;
-    static constexpr int kThreads = (4 * S + 2) * 32;
+    static constexpr int kCutters = kParts == 3 ? 8 : 0;             // warps that cut x
+    static constexpr int kThreads = (4 * S + 2 + kCutters) * 32;
     static_assert(S * N * kRows * 4 <= kSmem, "the sets' sums take the ring's place");
 };
 
 struct TcArgs {
-    CUtensorMap w, x;                                               // boxes: 128 bytes x 128 rows, 64 columns x N tokens
+    CUtensorMap w, x;                                               // boxes: 128 bytes x 128 rows; bf16: 64 columns x N tokens
     LinearArgs a;
-    int cluster, y_vec, group_vec;                                  // group_vec: a unit's scales, zeros in one load
+    int cluster, x_vec, y_vec, group_vec;                                  // group_vec: a unit's scales, zeros in one load
 };
 
 __device__ unsigned g_gave_up = 0;
@@ -100,6 +109,25 @@ struct Unit {
     static constexpr int kPieces = k4 ? 4 : k2 ? 2 : GU;
 };
 
+// Eight fp32 values (zeros where !there) as three bf16 each that sum to them exactly: the upper eight significand bits,
+// cut, the eight after them, and the rest. An infinity or NaN is the first part alone.
+__device__ __forceinline__ void cut(const float (&v)[8], bool there, uint4 (&part)[3]) {
+    uint32_t h[3][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float x = there ? v[e] : 0.f;
+        h[0][e] = __float_as_uint(x) & 0xffff0000u;
+        const float rest = fabsf(x) < INFINITY ? x - __uint_as_float(h[0][e]) : 0.f;
+        if (x != x) h[0][e] |= 0x00400000u;                         // a NaN whose upper half reads as an infinity
+        h[1][e] = __float_as_uint(rest) & 0xffff0000u;
+        h[2][e] = __float_as_uint(rest - __uint_as_float(h[1][e]));
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+        part[p] = make_uint4(__byte_perm(h[p][0], h[p][1], 0x7632), __byte_perm(h[p][2], h[p][3], 0x7632),
+                             __byte_perm(h[p][4], h[p][5], 0x7632), __byte_perm(h[p][6], h[p][7], 0x7632));
+}
+
 template <class C, int GU, bool kZeros>   // GU: groups are GU * 32 columns
 __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_constant__ TcArgs args) {
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -107,10 +135,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
     __shared__ uint32_t tmem_base;
     __shared__ int error;
     volatile int *err = &error;
-    constexpr int N = C::N, S = C::S, U = Unit<N, S, GU>::kPieces, kUnits = 8 / U, kGroups = U / GU;   // units of a block, groups of a unit
-    constexpr int kSetColumns = U * 16 + kGroups * N;               // of tensor memory: A, the groups' D
+    constexpr int N = C::N, ND = C::ND, S = C::S, U = Unit<ND, S, GU>::kPieces, kUnits = 8 / U, kGroups = U / GU;   // units of a block, groups of a unit
+    constexpr int kSetColumns = U * 16 + kGroups * ND;               // of tensor memory: A, the groups' D
     constexpr uint32_t kColumns = S * kSetColumns <= 128 ? 128 : S * kSetColumns <= 256 ? 256 : 512;
     static_assert(S * kSetColumns <= 512, "tensor memory");
+    using X = typename C::X;
     const LinearArgs &a = args.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), cluster = args.cluster;
     const int rank = blockIdx.x % cluster, row0 = blockIdx.x / cluster * kRows, tok0 = blockIdx.y * N;
@@ -119,13 +148,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
     const int u_lo = b_lo * kUnits, n_units = min(b_hi * kUnits, (groups + kGroups - 1) / kGroups) - u_lo;
 
     if (tid == 0) {
-        for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 5 * kUnits);
+        for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1 + C::kCutters), mbar_init(&empty[i], 5 * kUnits);
         for (int i = 0; i < S; ++i) mbar_init(&a_ready[i], 4), mbar_init(&done[i], 1);
         mbar_init(&drained, 1);
         error = 0;
         fence_mbar_init();
         tc::prefetch_tensormap(&args.w);
-        tc::prefetch_tensormap(&args.x);
+        if (C::kParts == 1) tc::prefetch_tensormap(&args.x);
     }
     if (warp == 4 * S + 1) {
         tc::tmem_alloc(&tmem_base, kColumns);
@@ -151,10 +180,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
                 const int st = i % C::kStages, b = b_lo + i;
                 if (i >= C::kStages && !wait(&empty[st], (uint32_t)(i / C::kStages - 1))) break;
                 unsigned char *to = smem + st * C::kStage;
-                mbar_arrive_expect_tx(&full[st], C::kStage);
+                mbar_arrive_expect_tx(&full[st], C::kParts == 1 ? C::kStage : C::kWBytes);
                 tc::tma_load_2d(to, &args.w, b * 128, row0, &full[st]);
 #pragma unroll
-                for (int h = 0; h < 4; ++h)
+                for (int h = 0; h < 4 && C::kParts == 1; ++h)
                     tc::tma_load_2d(to + C::kWBytes + h * N * 128, &args.x, b * 256 + h * 64, tok0, &full[st]);
             }
             // no copy is in flight when the ring is taken over
@@ -164,7 +193,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
     } else if (warp == 4 * S + 1) {
         // ---------------- products ----------------
         // The whole warp runs the loop, so that addresses and descriptors are uniform; one lane's instructions count.
-        constexpr uint32_t idesc = tc::idesc_bf16(kRows, N);
+        constexpr uint32_t idesc = tc::idesc_bf16(kRows, ND);
         const uint32_t lead = tc::elect_one();
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t x_desc = tc::smem_desc(ring + C::kWBytes, 128, tc::kSwz128);
@@ -178,26 +207,72 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
 #pragma unroll
             for (int k = 0; k < U * 2; ++k) {
                 const int kk = (u % kUnits) * U * 2 + k;            // of the block's sixteen products
-                tc::mma_bf16_tmem_a_lead(at + U * 16 + k / (GU * 2) * N, at + k * 8,
-                                         xd + (kk >> 2) * (N * 128 >> 4) + (kk & 3) * 2, idesc, k % (GU * 2) > 0, lead);
+                tc::mma_bf16_tmem_a_lead(at + U * 16 + k / (GU * 2) * ND, at + k * 8,
+                                         xd + (kk >> 2) * (ND * 128 >> 4) + (kk & 3) * 2, idesc, k % (GU * 2) > 0, lead);
             }
             tc::mma_commit_lead(&done[set], lead);
             tc::mma_commit_lead(&empty[st], lead);
         }
         tc::mma_commit_lead(&drained, lead);
         mbar_wait_bounded(&drained, 0, kWaitLimit);
+    } else if (warp > 4 * S + 1) {
+        // ---------------- x in fp32: three bf16 parts in the layout that TMA gives bf16 ----------------
+        if constexpr (C::kParts == 3) {
+            const int first = warp - (4 * S + 2);
+            constexpr int kMine = N / 8;
+            const float *x = static_cast<const float *>(a.x);
+            float next[kMine][8];
+            // no branch around a load, so that all are in flight: what is not there reads the first columns, for nothing
+            auto fetch = [&](int i) {
+                const int k = (b_lo + i) * 256 + lane * 8;
+#pragma unroll
+                for (int r = 0; r < kMine; ++r) {
+                    const int t = tok0 + first + r * 8;
+                    const float *p = t < a.n_tokens && k < a.d_in ? x + (long long)t * a.x_stride + k : x;
+                    if (args.x_vec) {
+                        *reinterpret_cast<float4 *>(next[r]) = __ldg(reinterpret_cast<const float4 *>(p));
+                        *reinterpret_cast<float4 *>(next[r] + 4) = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) next[r][e] = __ldg(p + e);
+                    }
+                }
+            };
+            fetch(0);
+            for (int i = 0; i < b_hi - b_lo; ++i) {
+                const int st = i % C::kStages, k = (b_lo + i) * 256 + lane * 8;
+                uint4 part[kMine][3];
+#pragma unroll
+                for (int r = 0; r < kMine; ++r) cut(next[r], tok0 + first + r * 8 < a.n_tokens && k < a.d_in, part[r]);
+                if (i + 1 < b_hi - b_lo) fetch(i + 1);
+                const bool ok = i < C::kStages || wait(&empty[st], (uint32_t)(i / C::kStages - 1));
+                if (!__all_sync(0xffffffffu, ok)) break;
+                unsigned char *to = smem + st * C::kStage + C::kWBytes + (lane >> 3) * (ND * 128);
+#pragma unroll
+                for (int r = 0; r < kMine; ++r) {
+                    const int n = first + r * 8;
+#pragma unroll
+                    for (int e = 0; e < 3; ++e)
+                        *reinterpret_cast<uint4 *>(to + (e * N + n) * 128 + (((lane & 7) ^ (n & 7)) << 4)) = part[r][e];
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&full[st]);
+            }
+        }
     } else {
         // ---------------- conversion and sums: thread = row ----------------
         const int set = warp >> 2, row = tid & 127;
         const size_t wrow = min(row0 + row, a.d_out - 1);           // a row past d_out is not stored
-        const __nv_bfloat16 *scales = static_cast<const __nv_bfloat16 *>(a.scales) + wrow * groups;
+        const X *scales = static_cast<const X *>(a.scales) + wrow * groups;
         const uint8_t *zeros = kZeros ? a.zeros + wrow * groups : nullptr;
         const uint32_t at = tmem + set * kSetColumns + ((uint32_t)(warp & 3) << 21);
         const unsigned char *wsrc = smem + row * 128;
         const int swz = row & 7;
 #pragma unroll
         for (int n = 0; n < N / 2; ++n) acc[n] = 0;
-        uint32_t sc[(kGroups + 1) / 2] = {};                        // of the unit whose products run, two to a word
+        constexpr int kScaleWords = C::kParts == 3 ? kGroups : (kGroups + 1) / 2;
+        uint32_t sc[kScaleWords] = {};                              // of the unit whose products run; bf16: two to a word
         uint32_t z = 0;                                             // of the unit to be converted, a byte to a group
         auto load_zeros = [&](int u) {
             const int of = (u_lo + u) * kGroups;
@@ -211,35 +286,47 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
             for (int g = 0; g < kGroups; ++g)
                 if (u < n_units && of + g < groups) z |= (uint32_t)zeros[of + g] << (8 * g);
         };
-        // two scales to a word
-        auto load_scales = [&](int u, uint32_t (&v)[(kGroups + 1) / 2]) {
+        auto load_scales = [&](int u, uint32_t (&v)[kScaleWords]) {
             const int of = (u_lo + u) * kGroups;
             if (kGroups > 1 && args.group_vec) {
-                if (kGroups == 4) {
+                if constexpr (kScaleWords == 4) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(scales + of);
+                    v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+                } else if constexpr (kScaleWords == 2) {
                     const uint2 w = *reinterpret_cast<const uint2 *>(scales + of);
-                    v[0] = w.x, v[(kGroups + 1) / 2 - 1] = w.y;
+                    v[0] = w.x, v[1] = w.y;
                 } else {
                     v[0] = *reinterpret_cast<const uint32_t *>(scales + of);
                 }
                 return;
             }
-            const uint16_t *s16 = reinterpret_cast<const uint16_t *>(scales);
+            if constexpr (C::kParts == 3) {
 #pragma unroll
-            for (int g = 0; g < kGroups; g += 2)
-                v[g / 2] = (of + g < groups ? s16[of + g] : 0u) | (g + 1 < kGroups && of + g + 1 < groups ? s16[of + g + 1] : 0u) << 16;
+                for (int g = 0; g < kGroups; ++g) v[g] = of + g < groups ? reinterpret_cast<const uint32_t *>(scales)[of + g] : 0u;
+            } else {
+                const uint16_t *s16 = reinterpret_cast<const uint16_t *>(scales);
+#pragma unroll
+                for (int g = 0; g < kGroups; g += 2)
+                    v[g / 2] =
+                        (of + g < groups ? s16[of + g] : 0u) | (g + 1 < kGroups && of + g + 1 < groups ? s16[of + g + 1] : 0u) << 16;
+            }
+        };
+        auto scale_of = [&](int g) {
+            return C::kParts == 3 ? __uint_as_float(sc[g]) : g & 1 ? bf_hi(sc[g / 2]) : bf_lo(sc[g / 2]);
         };
         if (kZeros) load_zeros(set);
         auto drain = [&]() {
 #pragma unroll
             for (int g = 0; g < kGroups; ++g) {
-                const uint32_t f = __float_as_uint(g & 1 ? bf_hi(sc[g / 2]) : bf_lo(sc[g / 2]));
+                const uint32_t f = __float_as_uint(scale_of(g));
                 const uint64_t ss = pair(f, f);
 #pragma unroll
-                for (int n = 0; n < N; n += 16) {
+                for (int n = 0; n < ND; n += 16) {
                     uint32_t d[16];
-                    tc::tmem_ld16_sync(at + U * 16 + g * N + n, d);
+                    tc::tmem_ld16_sync(at + U * 16 + g * ND + n, d);
+                    const int to = n % N / 2;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) acc[n / 2 + k] = fma2(pair(d[2 * k], d[2 * k + 1]), ss, acc[n / 2 + k]);
+                    for (int k = 0; k < 8; ++k) acc[to + k] = fma2(pair(d[2 * k], d[2 * k + 1]), ss, acc[to + k]);
                 }
             }
         };
@@ -247,7 +334,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
         int it = 0;
         for (int u = set; u < n_units; u += S, ++it) {
             const int i = u / kUnits, st = i % C::kStages;
-            uint32_t sc_next[(kGroups + 1) / 2];
+            uint32_t sc_next[kScaleWords];
             load_scales(u, sc_next);
             uint32_t zz[kGroups];                                   // -z / 64, twice
 #pragma unroll
@@ -291,7 +378,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&a_ready[set]);
 #pragma unroll
-            for (int g = 0; g < kGroups; g += 2) sc[g / 2] = sc_next[g / 2];
+            for (int g = 0; g < kScaleWords; ++g) sc[g] = sc_next[g];
         }
         if (ok && it > 0) {
             ok = wait(&done[set], (uint32_t)(it - 1));
@@ -328,14 +415,17 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
     };
     auto store = [&](int i, const float4 &s) {
         const int r = row0 + (i & 31) * 4;
-        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y) + (size_t)(tok0 + (i >> 5)) * a.y_stride + r;
+        X *y = static_cast<X *>(a.y) + (size_t)(tok0 + (i >> 5)) * a.y_stride + r;
         if (args.y_vec && r + 4 <= a.d_out) {
-            *reinterpret_cast<uint2 *>(y) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+            if constexpr (C::kParts == 3)
+                *reinterpret_cast<float4 *>(y) = s;
+            else
+                *reinterpret_cast<uint2 *>(y) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
         } else {
             const float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (r + e < a.d_out) y[e] = from_f32<__nv_bfloat16>(v[e]);
+                if (r + e < a.d_out) y[e] = from_f32<X>(v[e]);
         }
     };
     if (cluster == 1) {
@@ -396,14 +486,16 @@ cudaError_t launch(const LinearArgs &a, int sms, cudaStream_t st) {
     TcArgs args;
     args.a = a;
     args.cluster = cluster;
-    args.y_vec = reinterpret_cast<uintptr_t>(a.y) % 8 == 0 && a.y_stride % 4 == 0;
-    constexpr int kGroups = Unit<C::N, C::S, GU>::kPieces / GU;
-    args.group_vec = a.d_in / (GU * 32) % kGroups == 0 && reinterpret_cast<uintptr_t>(a.scales) % (2 * kGroups) == 0 &&
+    args.x_vec = aligned16(a.x) && a.x_stride % 4 == 0;
+    args.y_vec = reinterpret_cast<uintptr_t>(a.y) % (4 * sizeof(typename C::X)) == 0 && a.y_stride % 4 == 0;
+    constexpr int kGroups = Unit<C::ND, C::S, GU>::kPieces / GU;
+    args.group_vec = a.d_in / (GU * 32) % kGroups == 0 && reinterpret_cast<uintptr_t>(a.scales) % (sizeof(typename C::X) * kGroups) == 0 &&
                      reinterpret_cast<uintptr_t>(a.zeros) % kGroups == 0;
     if (!encode(&args.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, a.qweight, a.d_in / 2, a.d_out, a.d_in / 2,
                 128, kRows) ||
-        !encode(&args.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.x, a.d_in, a.n_tokens,
-                a.x_stride * 2, 64, C::N))
+        (C::kParts == 1 &&
+         !encode(&args.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.x, a.d_in, a.n_tokens,
+                 a.x_stride * 2, 64, C::N)))
         return cudaErrorNotSupported;
     const dim3 grid((a.d_out + kRows - 1) / kRows * cluster, tok_tiles);
     return launch_step(kernel, grid, dim3(C::kThreads), C::kSmem, cluster, st, args);
@@ -412,10 +504,10 @@ cudaError_t launch(const LinearArgs &a, int sms, cudaStream_t st) {
 // Sets of warps, measured with two / three: 17x14336x4096 with groups of 32 and zeros 15.7 / 17.1 us (two sets have room
 // for the four D of 128 columns, three for those of 64), 64 tokens of it 20.5 / 19.7, 64x5120x8192 with groups of 64 12.5 /
 // 14.4, 16x5120x8192 9.4 / 9.4, 17x4096x14336 with groups of 128 12.1 / 11.7.
-template <int N>
+template <typename X, int N>
 cudaError_t launch_group(const LinearArgs &a, int sms, cudaStream_t st) {
-    using Narrow = TcTile<N, N == 32 ? 2 : 3>;
-    using Wide = TcTile<N, N == 64 ? 2 : 3>;
+    using Narrow = TcTile<X, N, sizeof(X) == 4 || N == 32 ? 2 : 3>;
+    using Wide = TcTile<X, N, sizeof(X) == 4 || N == 64 ? 2 : 3>;
     switch (a.group) {
         case 32: return a.zeros ? launch<Narrow, 1, true>(a, sms, st) : launch<Narrow, 1, false>(a, sms, st);
         case 64: return a.zeros ? launch<Wide, 2, true>(a, sms, st) : launch<Wide, 2, false>(a, sms, st);
@@ -431,10 +523,13 @@ bool tc_takes(const LinearArgs &a) {
     return aligned16(a.x) && (a.n_tokens == 1 || (a.x_stride % 8 == 0 && a.x_stride < 1ll << 38));
 }
 
-cudaError_t launch_tc(const LinearArgs &a, int sms, cudaStream_t st) {
-    if (a.n_tokens <= 16) return launch_group<16>(a, sms, st);
-    if (a.n_tokens <= 32) return launch_group<32>(a, sms, st);
-    return launch_group<64>(a, sms, st);
+cudaError_t launch_tc(const LinearArgs &a, int dtype, int sms, cudaStream_t st) {
+    // three parts of 64 tokens would leave a ring of one stage
+    if (dtype == LORA_DTYPE_F32) return a.n_tokens <= 16 ? launch_group<float, 16>(a, sms, st) : launch_group<float, 32>(a, sms, st);
+    using X = __nv_bfloat16;
+    if (a.n_tokens <= 16) return launch_group<X, 16>(a, sms, st);
+    if (a.n_tokens <= 32) return launch_group<X, 32>(a, sms, st);
+    return launch_group<X, 64>(a, sms, st);
 }
 
 }  // namespace linear

@@ -367,7 +367,8 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
 // takes kR rows, with kAhead parts of each in flight; with kR = 1, for few units cut
 // into many parts, above 24 parts the warps of a block share the parts of its eight
 // rows instead. It is latency: a launch, one read of the segment and one or more
-// rounds of reads, 4 of the 13 us of 1x8 ctx 777. (One row to a warp and four: 1x8 ctx
+// rounds of reads, 4 of the 12.6 us of 1x8 ctx 777 (2 / 4 / 8 / 16 parts ahead: 13.8 / 13.0 / 12.6 /
+// 13.8). (One row to a warp and four: 1x8 ctx
 // 777 12.7 and 16.0 us, 32x16 ctx 4096 89.4 and 89.0. 38 parts, 1x6 ctx 3000: 24.5 us row
 // after row, 17.6 so.)
 template <int DP>
@@ -407,7 +408,7 @@ __device__ __forceinline__ void store_joined(const TreeArgs &a, const int4 &seg,
 
 template <typename T, int DP, int M, int kR>
 __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan, int m_rows) {
-    constexpr int V = Joined<DP>::V, kAhead = kR == 1 ? 4 : 2, kMany = 24, kShared = kR == 1 ? 8 : 1;
+    constexpr int V = Joined<DP>::V, kAhead = kR == 1 ? 8 : 2, kMany = 24, kShared = kR == 1 ? 8 : 1;
     __shared__ float so[kShared][kShared][DP];               // of a warp's parts, of a row
     __shared__ float2 sm[kShared][kShared];
     grid_dependency_wait();

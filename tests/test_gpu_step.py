@@ -89,20 +89,21 @@ def test_base_linear_strided_rows(ops, tokens, dtype):
     assert torch.isnan(out[:, :5]).all() and torch.isnan(out[:, 82:]).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("group", [32, 64, 128])
-@pytest.mark.parametrize("tokens", [9, 16, 17, 32, 33, 64, 65, 200])
-def test_base_linear_more_tokens(ops, tokens, group):
+@pytest.mark.parametrize("tokens", [4, 9, 16, 17, 32, 33, 64, 65, 200])
+def test_base_linear_more_tokens(ops, tokens, group, dtype):
     """Every tile of tokens with each group: rows of W past a tile of 128, columns past a block of 256, rows of x and y
     inside wider ones that keep the 16-byte alignment, zeros over the whole range the call takes."""
     import torch
     for d_in, d_out in ((group, 1), (256 + group, 128), (2560 + group, 300)):
-        x, qw, sc, z = _linear_inputs(tokens, d_in, d_out, group, True, "bf16", seed=tokens + d_out)
+        x, qw, sc, z = _linear_inputs(tokens, d_in, d_out, group, True, dtype, seed=tokens + d_out)
         z = torch.randint(0, 129, z.shape, dtype=torch.uint8, device=z.device) if d_out == 300 else z
         wide = torch.full((tokens, d_in + 24), float("nan"), dtype=x.dtype, device=x.device)
         wide[:, 8:8 + d_in] = x
         out = torch.full((tokens, d_out + 16), float("nan"), dtype=x.dtype, device=x.device)
         y = ops.base_linear(wide[:, 8:8 + d_in], qw, sc, z, out=out[:, 8:8 + d_out])
-        _check_linear(y, x, qw, sc, z, group, "bf16")
+        _check_linear(y, x, qw, sc, z, group, dtype)
         assert torch.isnan(out[:, :8]).all() and torch.isnan(out[:, 8 + d_out:]).all()
 
 
