@@ -9,22 +9,22 @@ namespace {
 
 using namespace step;
 
-// bf16 on mma.sync. A CTA of up to 12 warps takes 16 rows of W to a warp and, as one of the CTAs
-// of a cluster, a range of the columns; warps and cluster are chosen so that the
-// CTAs fill the SMs evenly (launch_tiles). Each warp streams its rows' 4-bit words from global memory
-// into registers, kAhead blocks of 128 columns ahead, and meets nobody on the way;
-// x of a slice of KS columns lies in shared memory for all of them. A product
-// mma(W 16 x 16, x^T 16 x 8) has the rows of W as its rows and eight tokens as its
-// columns. The 4-bit values become (n - z) / 64 in registers, exact in bf16
-// (nibbles()). So the products within a group are exact, and the group's fp32 sum is
-// scaled once. At the end the
-// cluster's parts are added in a fixed order through distributed shared memory: no
-// workspace, no atomics.
+// bf16 on mma.sync. A CTA of up to 12 warps takes 16 rows of W to a warp and, as
+// one of the CTAs of a cluster, a range of the columns; warps and cluster are
+// chosen so that the CTAs fill the SMs evenly (launch_tiles). Each warp streams its
+// rows' 4-bit words from global memory into registers, kAhead blocks of 128 columns
+// ahead, and meets nobody on the way; x of a slice of KS columns lies in shared
+// memory for all of them. A product mma(W 16 x 16, x^T 16 x 8) has the rows of W as
+// its rows and eight tokens as its columns. The 4-bit values become (n - z) / 64 in
+// registers, exact in bf16 (nibbles()). So the products within a group are exact,
+// and the group's fp32 sum is scaled once. At the end the cluster's parts are added
+// in a fixed order through distributed shared memory: no workspace, no atomics.
 //
-// What bounds it: for one token the words of W ought to, and a third to a half of their
-// rate is reached (W from memory: 1x4096x4096 6.1 us, 1.4 TB/s; 1x4096x14336 11.2 us, 2.7 TB/s): the
-// launch, the first loads and the cluster's end take 3 us of a call. Where x is not aligned
-// it also serves many tokens, and the products take over (64x5120x8192 29.9 us).
+// What bounds it: for one token the words of W ought to, and a third to a half of
+// their rate is reached (W from memory: 1x4096x4096 6.1 us, 1.4 TB/s; 1x4096x14336
+// 11.2 us, 2.7 TB/s): the launch, the first loads and the cluster's end take 3 us
+// of a call. Where x is not aligned it also serves many tokens, and the products
+// take over (64x5120x8192 29.9 us).
 //
 // Order of the columns. A block of 128 columns is four units of two products. Lane
 // t of a quad loads 16 bytes of a row, columns 32 t .. 32 t + 31. With groups of 128

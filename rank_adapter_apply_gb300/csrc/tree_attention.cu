@@ -363,14 +363,14 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
     }
 }
 
-// Join the parts of the unit that goes on past CTA blockIdx.x's share. A warp
-// takes kR rows, with kAhead parts of each in flight; with kR = 1, for few units cut
-// into many parts, above 24 parts the warps of a block share the parts of its eight
-// rows instead. It is latency: a launch, one read of the segment and one or more
-// rounds of reads, 4 of the 12.6 us of 1x8 ctx 777 (2 / 4 / 8 / 16 parts ahead: 13.8 / 13.0 / 12.6 /
-// 13.8). (One row to a warp and four: 1x8 ctx
-// 777 12.7 and 16.0 us, 32x16 ctx 4096 89.4 and 89.0. 38 parts, 1x6 ctx 3000: 24.5 us row
-// after row, 17.6 so.)
+// Join the parts of the unit that goes on past CTA blockIdx.x's share. A warp takes
+// kR rows, with kAhead parts of each in flight; with kR = 1, for few units cut into
+// many parts, above 24 parts the warps of a block share the parts of its eight rows
+// instead. It is latency: a launch, one read of the segment and one or more rounds
+// of reads, 4 of the 12.6 us of 1x8 ctx 777 (2 / 4 / 8 / 16 parts ahead: 13.8 /
+// 13.0 / 12.6 / 13.8). (One row to a warp and four: 1x8 ctx 777 12.7 and 16.0 us,
+// 32x16 ctx 4096 89.4 and 89.0. 38 parts, 1x6 ctx 3000: 24.5 us row after row, 17.6
+// so.)
 template <int DP>
 struct Joined {
     static constexpr int V = DP / 32;                    // columns of a lane
