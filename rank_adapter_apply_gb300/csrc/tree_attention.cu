@@ -330,10 +330,11 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
                     if (starts && ends) {
                         const long long token = c.r.start + node;
                         const int head = c.head * group + row % group;
-                        const float inv = l[hrow] > 0.f ? 1.f / l[hrow] : 0.f;
+                        const float inv = l[hrow] > 0.f ? 1.f / l[hrow] : l[hrow];
                         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + token * a.o_token + head * a.o_head;
-                        // a row without keys is 0, whatever the (zero-filled) tiles held
-                        const bool none = m[hrow] == -INFINITY;
+                        // a row without keys is 0; one whose scores are all NaN also has m = -inf (fmaxf drops them),
+                        // but its l is NaN
+                        const bool none = l[hrow] == 0.f;
 #pragma unroll
                         for (int d = 0; d < DP / 8; ++d)
                             if (d * 8 < a.head_dim)
@@ -390,7 +391,7 @@ __device__ __forceinline__ void store_joined(const TreeArgs &a, const int4 &seg,
     constexpr int V = Joined<DP>::V;
     const int lane = threadIdx.x & 31, group = a.n_heads / a.n_kv, head = seg.z * group + row % group;
     const long long token = start + row / group;
-    const bool none = j.m == -INFINITY;
+    const bool none = j.l == 0.f;                        // m is -inf for a row of NaN scores, too
     const float inv = j.l > 0.f ? 1.f / j.l : j.l;       // a NaN stays one
     T *out = static_cast<T *>(a.out) + token * a.o_token + (long long)head * a.o_head + lane * V;
     if (lane * V < a.head_dim) {

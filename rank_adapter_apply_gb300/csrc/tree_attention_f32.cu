@@ -196,7 +196,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(TreeArgs a, Plan 
                 if (node >= c.r.nodes) continue;
                 const long long token = c.r.start + node;
                 const int head = c.head * group + row % group;
-                const bool none = m[r] == -INFINITY, done = starts && ends;
+                // a row without keys is 0; one whose scores are all NaN also has m = -inf, but its l is NaN
+                const bool none = l[r] == 0.f, done = starts && ends;
                 const float inv = !done ? 1.f : l[r] > 0.f ? 1.f / l[r] : l[r];
                 float *dst = done ? static_cast<float *>(a.out) + token * a.o_token + (long long)head * a.o_head
                                   : plan.part + (slot * M + row0 + r) * DP;

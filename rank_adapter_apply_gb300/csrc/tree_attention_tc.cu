@@ -472,9 +472,10 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
                 ok = wait(&pv_done[i & 1], (uint32_t)(i >> 1));
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tc::fence_after_sync();
-                const bool mine = node < c.r.nodes, none = m == -INFINITY, done = starts && ends;
+                // a row without keys is 0; one whose scores are all NaN also has m = -inf, but its l is NaN
+                const bool mine = node < c.r.nodes, none = l == 0.f, done = starts && ends;
                 const long long token = c.r.start + node, slot = 2ll * blockIdx.x + (starts ? 1 : 0);
-                const float inv = !done ? 1.f : l > 0.f ? 1.f / l : 0.f;
+                const float inv = !done ? 1.f : l > 0.f ? 1.f / l : l;
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + token * a.o_token + head * a.o_head;
                 float *part = plan.part + (slot * kRows + tid) * DP;
 #pragma unroll 1

@@ -1,0 +1,67 @@
+"""What the drafted-token step's calls make of values, tensors and streams out of the ordinary, on the GPU."""
+import numpy as np
+import pytest
+
+from tests.test_gpu_step import _check_tree, _dev, _run_tree, _tree_case, ops  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- tree_attention: rows that see keys, but no finite score -----------------------------------
+# Rows of a request (nodes times query heads of a key/value head) choose the kernel: up to 16, up to 32, more. A context of
+# 20 is one tile of keys, whose rows a block writes itself; 3000 are joined from parts.
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nodes", [3, 7, 40])
+@pytest.mark.parametrize("ctx", [0, 20, 3000])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_tree_attention_query_row_not_finite(ops, value, ctx, nodes, dtype):  # noqa: F811
+    """A NaN in a query row makes every score of the row NaN, an infinity makes some +inf or NaN: its output is NaN and
+    its lse not finite, and no other row's changes by more than their tolerance."""
+    import torch
+    c = _tree_case([ctx], [nodes], 8, 2, 64, 16, dtype, seed=3)
+    c["kc"][:, :, :, 5] = c["kc"][:, :, :, 5].abs() * (1.0 if value > 0 else -1.0)    # infinite scores are +inf
+    want = _run_tree(ops, c)
+    _check_tree(c, *want)
+    c["q"][1, 2, 5] = value
+    c["q"][nodes - 1, 7, 5] = value
+    out, lse = _run_tree(ops, c)
+    keep = torch.ones_like(lse, dtype=torch.bool)
+    keep[1, 2] = keep[nodes - 1, 7] = False
+    assert torch.isnan(out[~keep]).all() and not torch.isneginf(lse[~keep]).any() and not torch.isfinite(lse[~keep]).any()
+    tol = 2.0 ** -6 if dtype == "bf16" else 2.0 ** -18      # both within their tolerance of the same values
+    assert ((out - want[0]).abs()[keep] <= tol * (1 + want[0].abs()[keep])).all()
+    assert ((lse - want[1]).abs()[keep] <= 2.0 ** -16 * (1 + want[1].abs()[keep])).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nodes", [3, 7, 40, 64])
+def test_tree_attention_one_visible_key_nan(ops, nodes, dtype):  # noqa: F811
+    """Nodes that see themselves alone, without context: the one whose key is NaN is NaN, the others see one key and
+    are its value, and a node that sees nothing is 0 with lse = -inf."""
+    import torch
+    c = _tree_case([0], [nodes], 8, 2, 64, 16, dtype, seed=4)
+    mask = np.zeros((nodes, 64), bool)
+    mask[np.arange(nodes), np.arange(nodes)] = True
+    mask[2] = False
+    c["mask"], c["bits"] = mask, _dev(np.packbits(mask, axis=1, bitorder="little").view(np.int64).reshape(nodes, 1))
+    c["kc"][int(c["table"][0, 0]), 1, 1, 9] = float("nan")
+    out, lse = _run_tree(ops, c)
+    assert torch.isnan(out[1, 4:]).all() and torch.isnan(lse[1, 4:]).all()
+    assert torch.isfinite(out[1, :4]).all() and torch.isfinite(lse[1, :4]).all()
+    assert not out[2].any() and torch.isneginf(lse[2]).all()
+    for i in [i for i in range(nodes) if i not in (1, 2)]:
+        v = c["vc"][int(c["table"][0, i // 16]), i % 16]
+        assert torch.equal(out[i], v.repeat_interleave(4, 0)) and torch.isfinite(lse[i]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("heads", [2, 8])
+def test_tree_attention_first_key_nan(ops, heads, dtype):  # noqa: F811
+    """A chain of 700 nodes, cut into parts, whose first key is NaN in one head: every row of that head sees it, the
+    first row sees nothing else."""
+    import torch
+    c = _tree_case([0], [700], heads, 2, 64, 16, dtype, seed=5)
+    c["kc"][int(c["table"][0, 0]), 0, 1, 9] = float("nan")
+    out, lse = _run_tree(ops, c, mask=False)
+    assert torch.isnan(out[:, heads // 2:]).all() and torch.isnan(lse[:, heads // 2:]).all()
+    assert torch.isfinite(out[:, :heads // 2]).all() and torch.isfinite(lse[:, :heads // 2]).all()
