@@ -57,13 +57,16 @@ class DraftModel:
         self.gen = torch.Generator(device="cuda").manual_seed(seed)
         self.slots = LoraSlots(cfg.shapes() * cfg.layers, cfg.max_loras, cfg.max_lora_rank, cfg.max_tokens,
                                dtype=cfg.dtype, max_layers_per_call=3)
-        self.weights = [[self._quantised(i, o) for i, o in cfg.shapes()] for _ in range(cfg.layers)]
-        self.head = self._quantised(cfg.hidden, cfg.vocab)
-        self.embedding = self._normal(cfg.vocab, cfg.hidden)
-        self.table = ops.rope_table(cfg.positions, cfg.head_dim, base=cfg.rope_base)
-        shape = (cfg.layers, cfg.pages, cfg.page_size, cfg.kv_heads, cfg.head_dim)
-        self.k_cache = torch.zeros(shape, dtype=cfg.dtype, device="cuda")
-        self.v_cache = torch.zeros(shape, dtype=cfg.dtype, device="cuda")
+        # made on the stream that reads them; the caller's stream may read them, too
+        with torch.cuda.stream(self.slots.compute):
+            self.weights = [[self._quantised(i, o) for i, o in cfg.shapes()] for _ in range(cfg.layers)]
+            self.head = self._quantised(cfg.hidden, cfg.vocab)
+            self.embedding = self._normal(cfg.vocab, cfg.hidden)
+            self.table = ops.rope_table(cfg.positions, cfg.head_dim, base=cfg.rope_base)
+            shape = (cfg.layers, cfg.pages, cfg.page_size, cfg.kv_heads, cfg.head_dim)
+            self.k_cache = torch.zeros(shape, dtype=cfg.dtype, device="cuda")
+            self.v_cache = torch.zeros(shape, dtype=cfg.dtype, device="cuda")
+        torch.cuda.current_stream().wait_stream(self.slots.compute)
 
     def _normal(self, *shape):
         return torch.randn(shape, generator=self.gen, device="cuda", dtype=torch.float32).to(self.cfg.dtype)
@@ -102,7 +105,7 @@ class DraftModel:
 
     def probabilities(self, batch):
         """The target's probabilities after every node (fp32); the nodes' keys and values are appended to the cache.
-        Runs on the slots' compute stream."""
+        To be called with the slots' compute stream as the current one, after the batch is there (step() sees to both)."""
         cfg = self.cfg
         tokens = batch.tokens.shape[0]
         x = self.embedding[batch.tokens.long()]
@@ -178,12 +181,23 @@ class DraftBatch:
 
 def step(model: DraftModel, batch: DraftBatch, draft, uniforms, noise, max_path):
     """One step: probabilities, verification, cache rows of the accepted nodes. draft: the rows the children were drawn
-    from (fp32) or None. Returns (path, n_accepted, next_token, probabilities)."""
-    with torch.no_grad(), torch.cuda.stream(model.slots.compute):
+    from (fp32) or None. Returns (path, n_accepted, next_token, probabilities).
+
+    The work runs on the slots' compute stream, behind what the caller's current stream holds so far; the current stream
+    in turn waits for the results. Inputs may be dropped right after the call."""
+    caller, compute = torch.cuda.current_stream(), model.slots.compute
+    compute.wait_stream(caller)
+    for t in (*vars(batch).values(), draft, uniforms, noise):
+        if t is not None:
+            t.record_stream(compute)
+    with torch.no_grad(), torch.cuda.stream(compute):
         target = model.probabilities(batch)
         path, count, token = ops.verify_drafts(target, draft, batch.tokens, batch.parents, batch.node_starts, uniforms,
                                                noise, max_path)
         model.keep(batch, path, count)
+    caller.wait_stream(compute)
+    for t in (path, count, token, target):
+        t.record_stream(caller)
     return path, count, token, target
 
 
@@ -201,16 +215,14 @@ def main(argv=None):
     pages = [list(range(r * per, (r + 1) * per)) for r in range(a.requests)]
     ctx, last = [0] * a.requests, [1 + r for r in range(a.requests)]
     gen = torch.Generator(device="cuda").manual_seed(2)
-    stream = model.slots.compute
     total, began = 0, 0.0
     for s in range(a.steps + 1):
         # drafts: chains of the tokens that a flat draft row gives
         nodes = a.requests * a.nodes
-        with torch.cuda.stream(stream):
-            drafted = torch.randint(0, cfg.vocab, (a.requests, a.nodes), generator=gen, device="cuda")
-            draft = torch.full((1, cfg.vocab), 1.0 / cfg.vocab, device="cuda").expand(nodes, -1)
-            uniforms = torch.rand((nodes,), generator=gen, device="cuda")
-            noise = torch.empty((a.requests, cfg.vocab), device="cuda").exponential_(generator=gen)
+        drafted = torch.randint(0, cfg.vocab, (a.requests, a.nodes), generator=gen, device="cuda")
+        draft = torch.full((1, cfg.vocab), 1.0 / cfg.vocab, device="cuda").expand(nodes, -1)
+        uniforms = torch.rand((nodes,), generator=gen, device="cuda")
+        noise = torch.empty((a.requests, cfg.vocab), device="cuda").exponential_(generator=gen)
         trees = [([last[r]] + drafted[r, 1:].tolist(), [-1] + list(range(a.nodes - 1))) for r in range(a.requests)]
         batch = DraftBatch.make(trees, ctx, pages, [r % cfg.max_loras for r in range(a.requests)], cfg.page_size)
         torch.cuda.synchronize()
