@@ -40,6 +40,10 @@ class LoraSlots:
         self.ws_ptr, self.ws_bytes = self.ws.data_ptr() + off, nbytes
         self.compute = compute_stream or torch.cuda.Stream(device=self.device)
         self.upload = upload_stream or torch.cuda.Stream(device=self.device)
+        # the zeros above are written on the current stream, before an upload or an apply may touch the pools
+        current = torch.cuda.current_stream(self.device)
+        self.compute.wait_stream(current)
+        self.upload.wait_stream(current)
         self.ctx = B.lora_slots_init(
             max_loras, max_lora_rank, max_tokens, self.max_layers, self.cdtype,
             [(di, do, a.data_ptr(), b.data_ptr()) for (di, do), a, b in zip(self.layers, self.A, self.B)],
