@@ -371,7 +371,13 @@ decode_cluster_kernel(const __grid_constant__ FusedArgs fa) {
     }
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0 && sm.invalid)
         atomicAdd(fa.hdr + kHdrInvalid, sm.invalid);
-    if (tile >= ntiles) return;             // the whole cluster leaves together
+    if (tile >= ntiles) {                   // the whole cluster leaves together
+        // Without any tile (no token has an adapter) somebody has to wait all
+        // the same: the kernel after this one takes this grid's end for the
+        // end of every kernel before it.
+        if (fa.early && tile == 0) grid_dependency_wait();
+        return;
+    }
 
     // ---- this tile: slot, tokens -----------------------------------------
     Tile t;

@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from tests.test_gpu_step import _check_tree, _dev, _run_tree, _tree_case, ops  # noqa: F401
+from tests.test_gpu_step import _check_tree, _dev, _linear_inputs, _run_tree, _tree_case, ops  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,44 @@ def test_tree_attention_first_key_nan(ops, heads, dtype):  # noqa: F811
     out, lse = _run_tree(ops, c, mask=False)
     assert torch.isnan(out[:, heads // 2:]).all() and torch.isnan(lse[:, heads // 2:]).all()
     assert torch.isfinite(out[:, :heads // 2]).all() and torch.isfinite(lse[:, :heads // 2]).all()
+
+
+# ---- kernels that start early -----------------------------------------------------------------------
+@pytest.mark.parametrize("adapters", ["none", "few", "all"])
+def test_adapters_between_calls_with_inputs_ready(ops, adapters):  # noqa: F811
+    """base_linear, the adapters' delta on its output with the inputs declared ready, the rotation of the result: each
+    may start before the one before it has ended. The same as with a wait in between, whether or not a token of the
+    batch has an adapter."""
+    import torch
+    from rank_adapter_apply_gb300 import binding as B
+    from rank_adapter_apply_gb300.slots import LoraSlots
+    tokens, d_in, d_out = 64, 4096, 2048
+    x, qw, sc, z = _linear_inputs(tokens, d_in, d_out, 64, True, "bf16", seed=41)
+    slots = LoraSlots([(d_in, d_out)], 4, 16, tokens)
+    try:
+        gen = torch.Generator().manual_seed(5)
+        for s in range(4):
+            slots.load_slot(s, [(torch.randn((16, d_in), generator=gen) / 64).bfloat16().pin_memory()],
+                            [(torch.randn((d_out, 16), generator=gen) / 4).bfloat16().pin_memory()], 16, 16.0)
+        slots.sync_uploads()
+        every = {"none": tokens + 1, "few": 13, "all": 1}[adapters]
+        idx = torch.tensor([t % 4 if t % every == every - 1 else -1 for t in range(tokens)], dtype=torch.int32, device="cuda")
+        pos, table = torch.arange(tokens, dtype=torch.int32, device="cuda"), ops.rope_table(tokens, 128)
+        xs = [x * (1 + i / 8) for i in range(6)]
+        ys, turned = [torch.empty((tokens, d_out), dtype=x.dtype, device="cuda") for _ in xs], []
+        torch.cuda.synchronize()
+        with torch.cuda.stream(slots.compute):
+            for wait in (True, False, False):
+                B.lora_set_inputs_ready(slots.ctx, not wait)
+                for i, xi in enumerate(xs):
+                    for step in (lambda: ops.base_linear(xi, qw, sc, z, out=ys[i]), lambda: slots.apply(0, xi, ys[i], idx),
+                                 lambda: turned.append(ops.rope(ys[i].view(tokens, 16, 128), pos, table))):
+                        step()
+                        if wait:
+                            torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert slots.stats()["device_wait_timeouts"] == 0
+        for i in range(len(xs), len(turned)):
+            assert torch.equal(turned[i], turned[i % len(xs)]), i
+    finally:
+        slots.close()
