@@ -169,6 +169,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
     auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
         return mbar_try_wait(bar, phase & 1u) || wait_long(bar, phase & 1u, err);
     };
+    // A wait of a warp: where it gave up for one lane, all leave.
+    auto together = [](bool ok) -> bool { return __all_sync(0xffffffffu, ok); };
 
     float *red = reinterpret_cast<float *>(smem);                   // [S][N][kRows]
     uint64_t acc[N / 2];
@@ -199,8 +201,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
         const uint64_t x_desc = tc::smem_desc(ring + C::kWBytes, 128, tc::kSwz128);
         for (int u = 0; u < n_units; ++u) {
             const int i = u / kUnits, st = i % C::kStages, set = u % S;
-            const bool ok = wait(&full[st], (uint32_t)(i / C::kStages)) && wait(&a_ready[set], (uint32_t)(u / S));
-            if (!__all_sync(0xffffffffu, ok)) break;
+            if (!together(wait(&full[st], (uint32_t)(i / C::kStages)) && wait(&a_ready[set], (uint32_t)(u / S)))) break;
             tc::fence_after_sync();
             const uint32_t at = tm + set * kSetColumns;
             const uint64_t xd = x_desc + (uint64_t)(st * (C::kStage >> 4));
@@ -245,8 +246,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
 #pragma unroll
                 for (int r = 0; r < kMine; ++r) cut(next[r], tok0 + first + r * 8 < a.n_tokens && k < a.d_in, part[r]);
                 if (i + 1 < b_hi - b_lo) fetch(i + 1);
-                const bool ok = i < C::kStages || wait(&empty[st], (uint32_t)(i / C::kStages - 1));
-                if (!__all_sync(0xffffffffu, ok)) break;
+                if (!together(i < C::kStages || wait(&empty[st], (uint32_t)(i / C::kStages - 1)))) break;
                 unsigned char *to = smem + st * C::kStage + C::kWBytes + (lane >> 3) * (ND * 128);
 #pragma unroll
                 for (int r = 0; r < kMine; ++r) {
@@ -346,8 +346,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
                 }
             }
             if (kZeros) load_zeros(u + S);
-            ok = wait(&full[st], (uint32_t)(i / C::kStages));
-            if (!__all_sync(0xffffffffu, ok)) break;
+            ok = together(wait(&full[st], (uint32_t)(i / C::kStages)));
+            if (!ok) break;
             uint4 w[U];
 #pragma unroll
             for (int j = 0; j < U; ++j)
@@ -362,8 +362,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&empty[st]);
             if (it > 0) {
-                ok = wait(&done[set], (uint32_t)(it - 1));
-                if (!__all_sync(0xffffffffu, ok)) break;
+                ok = together(wait(&done[set], (uint32_t)(it - 1)));
+                if (!ok) break;
                 tc::fence_after_sync();
                 drain();
             }
@@ -380,12 +380,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
 #pragma unroll
             for (int g = 0; g < kScaleWords; ++g) sc[g] = sc_next[g];
         }
-        if (ok && it > 0) {
-            ok = wait(&done[set], (uint32_t)(it - 1));
-            if (__all_sync(0xffffffffu, ok)) {
-                tc::fence_after_sync();
-                drain();
-            }
+        if (ok && it > 0 && together(wait(&done[set], (uint32_t)(it - 1)))) {
+            tc::fence_after_sync();
+            drain();
         }
     }
     // ---- the sets' and the cluster's parts, added in a fixed order; the ring is done with

@@ -168,7 +168,7 @@ template <int DP>
 __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_constant__ TcArgs args) {
     using C = Tc<DP>;
     extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ uint64_t full[kItems], empty[kItems], meta_full[kMeta], s_full[2], p_ready[2], pv_done[2], q_full, drained;
+    __shared__ uint64_t full[kItems], empty[kItems], meta_full[kMeta], s_full[2], p_ready[2], pv_done[2], q_full, drained, looked;
     __shared__ int poison_at[2];                       // 1 + the last tile (even, odd) whose V had a row that is not finite
     __shared__ Meta meta[kMeta];
     __shared__ long long scratch[kScratch + kThreads / 32];
@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
         for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 4), mbar_init(&pv_done[i], 1);
         mbar_init(&q_full, 1);
         mbar_init(&drained, 1);
+        mbar_init(&looked, 4);
         error = 0;
         poison_at[0] = poison_at[1] = 0;
         fence_mbar_init();
@@ -211,6 +212,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
     auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
         return mbar_try_wait(bar, phase & 1u) || wait_long(bar, phase & 1u, err);
     };
+    // A wait of a warp: where it gave up for one lane, all leave.
+    auto together = [](bool ok) -> bool { return __all_sync(0xffffffffu, ok); };
     // Items are loaded in the order in which the products take them, K0 K1 V0 K2 V1 .., round and round the ring; a
     // role steps through them with a place and the parity of its round.
     auto step = [](int &place, uint32_t &round) {
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
             int page, c1, c2;                          // the cache maps' outer coordinates
         } last{};                                      // of the tile whose V is still to be loaded
         auto load = [&](const CUtensorMap *map, const Box &b) -> bool {
-            if (!__all_sync(0xffffffffu, wait(&empty[at], round ^ 1u))) return false;   // at once in the first round
+            if (!together(wait(&empty[at], round ^ 1u))) return false;   // at once in the first round
             if (lane == 0) mbar_arrive_expect_tx(&full[at], C::kItem);
             __syncwarp();
             if (lane < boxes) {
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
             const bool first = i == 0 || u.tile == 0;
             if (first) {
                 // the last scores of the unit before have been formed: Q may be overwritten
-                if (i > 0 && !__all_sync(0xffffffffu, wait(&empty[k_at], k_round))) break;
+                if (i > 0 && !together(wait(&empty[k_at], k_round))) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&q_full, rows * DP * 2);
                     for (int h = 0; h < C::kHalves; ++h)
@@ -321,13 +324,12 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
         const int n = __shfl_sync(0xffffffffu, n_tiles, 0);
         int at = 0, units = 0;
         uint32_t round = 0;
-        bool ok = true;
         for (int i = 0; i <= n; ++i) {
             if (i < n) {
-                ok = wait(&full[at], round) && wait(&meta_full[i % kMeta], (uint32_t)(i / kMeta)) &&
-                     (!meta[i % kMeta].first || wait(&q_full, (uint32_t)units++)) &&
-                     (i < 2 || wait(&pv_done[i & 1], (uint32_t)((i - 2) >> 1)));      // P of tile i - 2 was read
-                if (!__all_sync(0xffffffffu, ok)) break;
+                const bool ok = wait(&full[at], round) && wait(&meta_full[i % kMeta], (uint32_t)(i / kMeta)) &&
+                                (!meta[i % kMeta].first || wait(&q_full, (uint32_t)units++)) &&
+                                (i < 2 || wait(&pv_done[i & 1], (uint32_t)((i - 2) >> 1)));      // P of tile i - 2 was read
+                if (!together(ok)) break;
                 tc::fence_after_sync();
                 const uint64_t kd = k_desc + (uint64_t)(at * (C::kItem >> 4));
 #pragma unroll
@@ -340,8 +342,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
             }
             if (i > 0) {
                 const int t = i - 1;
-                ok = wait(&p_ready[t & 1], (uint32_t)(t >> 1)) && wait(&full[at], round);
-                if (!__all_sync(0xffffffffu, ok)) break;
+                if (!together(wait(&p_ready[t & 1], (uint32_t)(t >> 1)) && wait(&full[at], round))) break;
                 tc::fence_after_sync();
                 const uint32_t more = meta[t % kMeta].first == 0;
                 const uint64_t vd = v_desc + (uint64_t)(at * (C::kItem >> 4));
@@ -364,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
         Cursor c = share.start;
         float m = -INFINITY, l = 0.f;                  // m: the reference, in powers of two
         int seg_first = c.tile, node = 0, head = 0;
+        uint32_t looks = 0;                            // tiles whose V was looked through
         bool poison = false, idle = false;             // idle: no row of this warp exists
         for (int i = 0; i < n_tiles; ++i) {
             const bool first = i == 0 || c.tile == 0;
@@ -374,8 +376,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
                 head = c.head * group + row % group;
                 idle = __all_sync(0xffffffffu, node >= c.r.nodes);
             }
-            bool ok = wait(&meta_full[i % kMeta], (uint32_t)(i / kMeta)) && wait(&s_full[i & 1], (uint32_t)(i >> 1));
-            if (!__all_sync(0xffffffffu, ok)) break;
+            if (!together(wait(&meta_full[i % kMeta], (uint32_t)(i / kMeta)) && wait(&s_full[i & 1], (uint32_t)(i >> 1)))) break;
             tc::fence_after_sync();
             const uint64_t there = meta[i % kMeta].valid[0] | (uint64_t)meta[i % kMeta].valid[1] << 32;
             const int p0 = c.tile * kTileKeys;
@@ -406,8 +407,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
                     if (move) m = top;
                     l *= f;
                     if (!first) {                          // O of the tiles before, once it is complete
-                        ok = wait(&pv_done[(i - 1) & 1], (uint32_t)((i - 1) >> 1));
-                        if (!__all_sync(0xffffffffu, ok)) break;
+                        if (!together(wait(&pv_done[(i - 1) & 1], (uint32_t)((i - 1) >> 1)))) break;
                         tc::fence_after_sync();
 #pragma unroll 1
                         for (int d = 0; d < DP; d += 32) {
@@ -443,8 +443,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
             if (p0 + kTileKeys > min(c.r.ctx, c.r.keys)) {
                 // some row may skip a key of this tile: no V row with an infinity or NaN in it may stay
                 const int vp = place_v(i);
-                ok = wait(&full[vp], round_v(i));
-                if (!__all_sync(0xffffffffu, ok)) break;
+                if (!together(wait(&full[vp], round_v(i)))) break;
                 // two threads for a row
                 constexpr int kPieces = DP / 16;
                 unsigned char *v = smem + C::kQ + vp * C::kItem + (tid >> 1) * 128 +
@@ -459,7 +458,10 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
                     if (there >> (tid >> 1) & 1) poison_at[i & 1] = i + 1;
                 }
                 tc::fence_proxy_async_smem();
-                tc::named_bar(1, 128);
+                // the four warps meet at a barrier whose wait is bounded, too: one of them may have given up
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&looked);
+                if (!together(wait(&looked, looks++))) break;
                 poison = poison || *reinterpret_cast<volatile int *>(&poison_at[i & 1]) == i + 1;
             }
             tc::fence_before_sync();
@@ -469,8 +471,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
             if (c.tile + 1 == c.r.key_tiles || i + 1 == n_tiles) {
                 // ---- the unit or the share ends: write
                 const bool starts = seg_first == 0, ends = c.tile + 1 == c.r.key_tiles;
-                ok = wait(&pv_done[i & 1], (uint32_t)(i >> 1));
-                if (!__all_sync(0xffffffffu, ok)) break;
+                if (!together(wait(&pv_done[i & 1], (uint32_t)(i >> 1)))) break;
                 tc::fence_after_sync();
                 // a row without keys is 0; one whose scores are all NaN also has m = -inf, but its l is NaN
                 const bool mine = node < c.r.nodes, none = l == 0.f, done = starts && ends;
