@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
             const int first = warp - (4 * S + 2);
             constexpr int kMine = N / 8;
             const float *x = static_cast<const float *>(a.x);
-            float next[kMine][8];
+            alignas(16) float next[kMine][8];
             // no branch around a load, so that all are in flight: what is not there reads the first columns, for nothing
             auto fetch = [&](int i) {
                 const int k = (b_lo + i) * 256 + lane * 8;

@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan, i
 #pragma unroll
                 for (int e = 0; e < V; ++e) j[i].o[e] = 0.f;
             for (int p = warp; p < seg.w; p += 8) {
-                float v[8][V];
+                alignas(4 * V) float v[8][V];
                 float2 ml[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan, i
 #pragma unroll
         for (int e = 0; e < V; ++e) j[k].o[e] = 0.f;
     for (int p = 0; p < seg.w; p += kAhead) {
-        float v[kAhead][kR][V];
+        alignas(4 * V) float v[kAhead][kR][V];
         float2 ml[kAhead][kR];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)

@@ -64,7 +64,7 @@ __device__ __forceinline__ void visit(const T *p, const T *q, const float *noise
     const int lo = (int)((long long)vectors * rank / cluster), hi = (int)((long long)vectors * (rank + 1) / cluster);
     for (int i0 = lo + tid; i0 < hi; i0 += kThreads * kBatch) {
         uint4 pv[kBatch], qv[kBatch];
-        float nv[kBatch][N];
+        alignas(16) float nv[kBatch][N];
 #pragma unroll
         for (int e = 0; e < kBatch; ++e) {
             const int i = i0 + e * kThreads, v = head + i * N;
@@ -74,7 +74,7 @@ __device__ __forceinline__ void visit(const T *p, const T *q, const float *noise
                 if (q_vec) {
                     qv[e] = *reinterpret_cast<const uint4 *>(q + v);
                 } else {
-                    T t[N];
+                    alignas(16) T t[N];
 #pragma unroll
                     for (int j = 0; j < N; ++j) t[j] = q[v + j];
                     qv[e] = *reinterpret_cast<const uint4 *>(t);

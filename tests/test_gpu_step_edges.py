@@ -2,7 +2,8 @@
 import numpy as np
 import pytest
 
-from tests.test_gpu_step import _check_tree, _dev, _linear_inputs, _run_tree, _tree_case, ops  # noqa: F401
+from tests.test_gpu_step import (_check_tree, _check_verify, _dev, _linear_inputs, _run_tree, _run_verify,  # noqa: F401
+                                 _tree_case, _verify_case, ops)
 
 pytestmark = pytest.mark.gpu
 
@@ -106,3 +107,26 @@ def test_adapters_between_calls_with_inputs_ready(ops, adapters):  # noqa: F811
             assert torch.equal(turned[i], turned[i % len(xs)]), i
     finally:
         slots.close()
+
+
+# ---- verify_drafts: rows that start at different places within 16 bytes -----------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("requests,vocab", [(5, 301), (3, 40001), (400, 1003)])
+@pytest.mark.parametrize("at", [(3, 6, 1), (0, 1, 0), (5, 0, 2), (1, 1, 3)])
+def test_verify_rows_at_different_offsets(ops, at, requests, vocab, dtype):  # noqa: F811
+    """Target, draft and noise inside wider rows of different widths, starting at different elements, with enough
+    rejections that both the sums and the final pass read them; NaN lies around them."""
+    import torch
+    c = _verify_case(requests, 6, 3, vocab, dtype, True, seed=requests + vocab)
+    c["u"][::2] = 0.97
+    plain = _run_verify(ops, c, 6)
+    _check_verify(c, plain, 6)
+    assert (plain[1] == 0).any() and (plain[1] > 0).any()
+
+    def inside(t, first, width):
+        w = torch.full((t.shape[0], width), float("nan"), dtype=t.dtype, device="cuda")
+        w[:, first:first + vocab] = t
+        return w[:, first:first + vocab]
+    got = ops.verify_drafts(inside(c["target"], at[0], vocab + 11), inside(c["draft"], at[1], vocab + 22), _dev(c["tokens"]),
+                            _dev(c["parents"]), _dev(c["starts"]), _dev(c["u"]), inside(_dev(c["noise"]), at[2], vocab + 5), 6)
+    _check_verify(c, got, 6)
