@@ -69,6 +69,16 @@ __device__ __forceinline__ uint4 load_w(const uint8_t *p) {
     return v;
 }
 
+// Eight consecutive bf16 of x, zeros when !ok. Ordinary loads: the kernel before may still have been writing x when this
+// one started, and the read-only path asks for memory that nobody writes as long as the kernel runs. (The weights are.)
+__device__ __forceinline__ uint4 load_x(const __nv_bfloat16 *p, bool ok, bool vec) {
+    if (!ok) return make_uint4(0, 0, 0, 0);
+    if (vec) return *reinterpret_cast<const uint4 *>(p);
+    const uint16_t *e = reinterpret_cast<const uint16_t *>(p);
+    return make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16,
+                      e[6] | (uint32_t)e[7] << 16);
+}
+
 // Words of a quad's 16 bytes each into units: w[u] becomes this lane's word of unit u.
 template <int GU>
 __device__ __forceinline__ void exchange(uint32_t (&w)[4], int t4) {
@@ -168,8 +178,7 @@ __global__ void __launch_bounds__(32 * C::kMaxWarps, C::kCtas) linear_tiles_kern
             for (int e = 0; e < kBatch; ++e) {
                 const int i = i0 + e * warps, t = i / kSliceBlocks * 2 + odd, blk = i % kSliceBlocks;
                 const int k = (s_lo + blk) * 128 + q * 8;
-                v[e] = load8_bf16(reinterpret_cast<const uint16_t *>(x + (size_t)t * a.x_stride + k), 0, 8,
-                                  t < nt && blk < n_blocks && k < a.d_in, x_vec);
+                v[e] = load_x(x + (size_t)t * a.x_stride + k, t < nt && blk < n_blocks && k < a.d_in, x_vec);
             }
 #pragma unroll
             for (int e = 0; e < kBatch; ++e) {

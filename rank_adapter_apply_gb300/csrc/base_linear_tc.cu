@@ -223,7 +223,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
             constexpr int kMine = N / 8;
             const float *x = static_cast<const float *>(a.x);
             alignas(16) float next[kMine][8];
-            // no branch around a load, so that all are in flight: what is not there reads the first columns, for nothing
+            // No branch around a load, so that all are in flight: what is not there reads the first columns, for nothing.
+            // Ordinary loads, since x may have been written while this kernel was already running.
             auto fetch = [&](int i) {
                 const int k = (b_lo + i) * 256 + lane * 8;
 #pragma unroll
@@ -231,11 +232,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) linear_tc_kernel(const __grid_
                     const int t = tok0 + first + r * 8;
                     const float *p = t < a.n_tokens && k < a.d_in ? x + (long long)t * a.x_stride + k : x;
                     if (args.x_vec) {
-                        *reinterpret_cast<float4 *>(next[r]) = __ldg(reinterpret_cast<const float4 *>(p));
-                        *reinterpret_cast<float4 *>(next[r] + 4) = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+                        *reinterpret_cast<float4 *>(next[r]) = *reinterpret_cast<const float4 *>(p);
+                        *reinterpret_cast<float4 *>(next[r] + 4) = *(reinterpret_cast<const float4 *>(p) + 1);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) next[r][e] = __ldg(p + e);
+                        for (int e = 0; e < 8; ++e) next[r][e] = p[e];
                     }
                 }
             };
