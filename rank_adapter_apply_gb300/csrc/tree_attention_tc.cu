@@ -232,8 +232,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
             int page, place;                           // page -1: no such box
         };
         auto read_run = [&](int run) -> Run {
-            const int p = (run * 32 + lane) * args.box, at = p / a.page_size;
-            return {p < u.r.keys ? a.page_table[u.b * a.table_stride + at] : -1, p - at * a.page_size};
+            // unsigned: the run after the last may begin past 2^31
+            const uint32_t p = ((uint32_t)run * 32 + lane) * (uint32_t)args.box, at = p / (uint32_t)a.page_size;
+            return {p < (uint32_t)u.r.keys ? a.page_table[u.b * a.table_stride + at] : -1, (int)(p - at * (uint32_t)a.page_size)};
         };
         int run_b = -1, run_at = 0;                    // request, and number of the run in use
         Run now{}, ahead{}, head_run{};

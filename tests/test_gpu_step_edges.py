@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from tests.test_gpu_step import (_check_tree, _check_verify, _dev, _linear_inputs, _run_tree, _run_verify,  # noqa: F401
+from tests.test_gpu_step import (_check_tree, _check_verify, _dev, _dt, _linear_inputs, _run_tree, _run_verify,  # noqa: F401
                                  _tree_case, _verify_case, ops)
 
 pytestmark = pytest.mark.gpu
@@ -130,3 +130,26 @@ def test_verify_rows_at_different_offsets(ops, at, requests, vocab, dtype):  # n
     got = ops.verify_drafts(inside(c["target"], at[0], vocab + 11), inside(c["draft"], at[1], vocab + 22), _dev(c["tokens"]),
                             _dev(c["parents"]), _dev(c["starts"]), _dev(c["u"]), inside(_dev(c["noise"]), at[2], vocab + 5), 6)
     _check_verify(c, got, 6)
+
+
+# ---- tree_attention: as many keys as an int counts ----------------------------------------------------
+@pytest.mark.parametrize("heads,dtype", [(8, "bf16"), (64, "bf16"), (8, "f32")])
+def test_tree_attention_two_to_the_31_keys(ops, heads, dtype):  # noqa: F811
+    """A context of 2^31 - 1 over one large page that fills the page table's row: the keys that an int can count are
+    seen, and nothing outside the table is read. Each row of the page counts 32768 times, the last 64 one time less. A
+    query of zero weighs all alike and the values are 0 or 1, so the sums of a block's share (2^31 / 304) are exact."""
+    import torch
+    page, dim = 65536, 8
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    q = torch.zeros((1, heads, dim), device="cuda", dtype=_dt(dtype))
+    kc = torch.randn((1, page, 1, dim), generator=gen, device="cuda").to(_dt(dtype))
+    vc = torch.randint(0, 2, (1, page, 1, dim), generator=gen, device="cuda").to(_dt(dtype))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out, lse = ops.tree_attention(q, kc, vc, torch.zeros((1, (1 << 31) // page), **i32), torch.tensor([2**31 - 1], **i32),
+                                  torch.tensor([0, 1], **i32))
+    count = torch.full((page, 1), 32768.0, dtype=torch.float64, device="cuda")
+    count[-64:] -= 1
+    want = (vc[0, :, 0].double() * count).sum(0) / count.sum()
+    tol = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -18
+    assert ((out[0].double() - want).abs() <= tol * want).all()
+    assert ((lse[0].double() - count.sum().log()).abs() <= 2.0 ** -18).all()
