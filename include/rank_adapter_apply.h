@@ -720,9 +720,9 @@ size_t lora_tree_attention_workspace_bytes(int n_requests, int n_tokens, int n_h
 
 int lora_tree_attention(const lora_tree_attention_desc *desc, void *stream);
 
-/* *count = thread blocks of lora_tree_attention on the current device whose
- * bounded device-side waits gave up so far; their rows are wrong (never
- * expected). Synchronises the device. */
+/* *count = thread blocks of lora_base_linear and lora_tree_attention on the
+ * current device whose bounded device-side waits gave up so far; their rows are
+ * wrong (never expected). Synchronises the device, all streams. */
 int lora_step_wait_timeouts(uint64_t *count);
 
 /*

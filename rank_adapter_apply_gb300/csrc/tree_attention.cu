@@ -635,7 +635,9 @@ extern "C" int lora_tree_attention(const lora_tree_attention_desc *d, void *stre
 extern "C" int lora_step_wait_timeouts(uint64_t *count) {
     if (!count) return fail(LORA_ERR_ARG, "step_wait_timeouts: NULL pointer argument");
     unsigned n = 0, of_linear = 0;
-    cudaError_t e = read_timeouts(&n);
+    // the copies below wait for the default stream and those that it waits for, not for non-blocking streams
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = read_timeouts(&n);
     if (e == cudaSuccess) e = linear::read_timeouts(&of_linear);
     if (e != cudaSuccess) return launched("step_wait_timeouts", e);
     *count = (uint64_t)n + of_linear;

@@ -153,3 +153,16 @@ def test_tree_attention_two_to_the_31_keys(ops, heads, dtype):  # noqa: F811
     tol = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -18
     assert ((out[0].double() - want).abs() <= tol * want).all()
     assert ((lse[0].double() - count.sum().log()).abs() <= 2.0 ** -18).all()
+
+
+# ---- the count of waits that gave up --------------------------------------------------------------
+def test_wait_timeouts_waits_for_every_stream(ops):  # noqa: F811
+    """The count is read when the device is idle: work queued on a stream that no other waits for is done by then."""
+    import torch
+    from rank_adapter_apply_gb300 import binding as B
+    side = torch.cuda.Stream()
+    B.lora_step_wait_timeouts()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)
+    assert B.lora_step_wait_timeouts() == 0
+    assert side.query()
