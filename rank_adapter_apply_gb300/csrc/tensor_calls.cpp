@@ -65,6 +65,11 @@ void same(const Tensor &t, const Where &w, at::ScalarType type, const char *name
                       " requires a gradient, which these calls do not record: detach it or use torch.no_grad()");
 }
 
+// A call wrote `t` in place: autograd sees by its version that what it saved of it is gone. (Inference tensors have none.)
+void written(const Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // Last dimension contiguous (as far as it has more than one element).
 void unit(const Tensor &t, int64_t dims, const char *name) {
     TORCH_CHECK_VALUE(t.dim() == dims, name, " has ", t.dim(), " dimensions: ", dims, " are needed");
@@ -148,6 +153,7 @@ PyObject *base_linear(PyObject *, PyObject *const *v, Py_ssize_t n) {
     d.group = (int)(d_in / groups);
     d.dtype = w.dtype;
     if (!done(g_base_linear(&d, w.stream))) return nullptr;
+    if (out) written(y);
     return THPVariable_Wrap(std::move(y));
     END_HANDLE_TH_ERRORS
 }
@@ -190,10 +196,12 @@ PyObject *rope(PyObject *, PyObject *const *v, Py_ssize_t n) {
     const Tensor &positions = *tensor(v[1], "positions"), &table = *tensor(v[2], "table");
     const Where w = start(x, "x");
     lora_rope_desc d{};
-    Tensor y = rotated(x, positions, table, tensor(v[5], "out", true), w, d);
+    const Tensor *out = tensor(v[5], "out", true);
+    Tensor y = rotated(x, positions, table, out, w, d);
     d.interleaved = PyObject_IsTrue(v[3]);
     d.inverse = PyObject_IsTrue(v[4]);
     if (!done(g_rope(&d, w.stream))) return nullptr;
+    if (out) written(y);
     return THPVariable_Wrap(std::move(y));
     END_HANDLE_TH_ERRORS
 }
@@ -229,7 +237,8 @@ PyObject *rope_append(PyObject *, PyObject *const *v, Py_ssize_t n) {
     TORCH_CHECK_VALUE(slots.size(0) == q.size(0), "slots holds ", slots.size(0), " entries: one for each of ", q.size(0),
                       " tokens is needed");
     check_cache(kc, vc, w, type, k.size(1), k.size(2));
-    Tensor y = rotated(q, positions, table, tensor(v[9], "out", true), w, d);
+    const Tensor *out = tensor(v[9], "out", true);
+    Tensor y = rotated(q, positions, table, out, w, d);
     d.interleaved = PyObject_IsTrue(v[8]);
     d.k = k.const_data_ptr();
     d.k_token = k.stride(0);
@@ -247,6 +256,9 @@ PyObject *rope_append(PyObject *, PyObject *const *v, Py_ssize_t n) {
     d.page_size = count(kc.size(1), "page_size");
     d.n_kv_heads = count(k.size(1), "kv_heads");
     if (!done(g_rope(&d, w.stream))) return nullptr;
+    if (out) written(y);
+    written(kc);
+    written(vc);
     return THPVariable_Wrap(std::move(y));
     END_HANDLE_TH_ERRORS
 }
@@ -323,6 +335,7 @@ PyObject *tree_attention(PyObject *, PyObject *const *v, Py_ssize_t n) {
     d.workspace = ws.mutable_data_ptr();
     d.workspace_bytes = bytes;
     if (!done(g_tree(&d, w.stream))) return nullptr;
+    if (out) written(y);
     PyObject *a = THPVariable_Wrap(std::move(y)), *b = THPVariable_Wrap(std::move(lse));
     return a && b ? Py_BuildValue("(NN)", a, b) : nullptr;
     END_HANDLE_TH_ERRORS

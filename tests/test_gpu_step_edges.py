@@ -2,8 +2,8 @@
 import numpy as np
 import pytest
 
-from tests.test_gpu_step import (_check_tree, _check_verify, _dev, _dt, _linear_inputs, _run_tree, _run_verify,  # noqa: F401
-                                 _tree_case, _verify_case, ops)
+from tests.test_gpu_step import (_check_tree, _check_verify, _dev, _dt, _linear_inputs, _rope_inputs, _run_tree,  # noqa: F401
+                                 _run_verify, _tree_case, _verify_case, ops)
 
 pytestmark = pytest.mark.gpu
 
@@ -166,3 +166,50 @@ def test_wait_timeouts_waits_for_every_stream(ops):  # noqa: F811
         torch.cuda._sleep(400_000_000)
     assert B.lora_step_wait_timeouts() == 0
     assert side.query()
+
+
+# ---- what autograd has to know ------------------------------------------------------------------------
+def _in_place_calls(ops):  # noqa: F811
+    """(call, tensors that it writes in place) of each call that takes such tensors."""
+    import torch
+    x, qw, sc, z = _linear_inputs(3, 128, 20, 32, True, "bf16")
+    y = torch.empty((3, 20), dtype=x.dtype, device="cuda")
+    q, k, v, pos, kc, vc, slots = _rope_inputs(4, 4, 2, 64, 64, "bf16")
+    turned, again, table = torch.empty_like(q), q.clone(), ops.rope_table(500, 64)
+    c = _tree_case([5], [3], 4, 2, 64, 16, "bf16")
+    out = torch.empty_like(c["q"])
+    return [(lambda: ops.base_linear(x, qw, sc, z, out=y), [y]),
+            (lambda: ops.rope(q, pos, table, out=turned), [turned]),
+            (lambda: ops.rope(again, pos, table, out=again), [again]),
+            (lambda: ops.rope_append(q, k, v, pos, table, kc, vc, slots, out=turned), [turned, kc, vc]),
+            (lambda: _run_tree(ops, c, out=out), [out])]
+
+
+def test_tensors_written_in_place_change_version(ops):  # noqa: F811
+    """A tensor that a call writes (out, the caches) has a new version, by which autograd finds that a value saved for
+    a backward pass is gone; tensors that are only read keep theirs."""
+    import torch
+    for i, (call, written) in enumerate(_in_place_calls(ops)):
+        before = [t._version for t in written]
+        call()
+        assert all(t._version > b for t, b in zip(written, before)), i
+    x, qw, sc, z = _linear_inputs(3, 128, 20, 32, True, "f32")
+    y = torch.ones((3, 20), device="cuda", requires_grad=True)
+    saved = (y * 2).exp()                        # exp keeps its result for the backward pass
+    before = [t._version for t in (x, qw, sc, z)]
+    ops.base_linear(x, qw, sc, z, out=saved.detach())
+    assert [t._version for t in (x, qw, sc, z)] == before
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        saved.sum().backward()
+
+
+def test_inference_tensors_are_written_as_before(ops):  # noqa: F811
+    """Tensors of the inference mode have no version; they are taken inside the mode and outside."""
+    import torch
+    with torch.inference_mode():
+        x, qw, sc, z = _linear_inputs(3, 128, 20, 32, True, "bf16")
+        y = torch.zeros((3, 20), dtype=x.dtype, device="cuda")
+        want = ops.base_linear(x, qw, sc, z)
+        assert torch.equal(ops.base_linear(x, qw, sc, z, out=y), want)
+    y2 = ops.base_linear(x, qw, sc, z, out=y)
+    assert torch.equal(y2, want)
