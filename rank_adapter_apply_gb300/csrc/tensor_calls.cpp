@@ -14,6 +14,7 @@
 
 #include <ATen/core/TensorBody.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -63,6 +64,8 @@ void same(const Tensor &t, const Where &w, at::ScalarType type, const char *name
     TORCH_CHECK_VALUE(t.scalar_type() == type, name, " has dtype ", t.scalar_type(), ": ", type, " is needed");
     TORCH_CHECK_VALUE(!t.requires_grad() || !c10::GradMode::is_enabled(), name,
                       " requires a gradient, which these calls do not record: detach it or use torch.no_grad()");
+    TORCH_CHECK_VALUE(!c10::AutogradState::get_tls_state().get_fw_grad_mode() || !t._fw_grad(0).defined(), name,
+                      " has a forward-mode tangent, which these calls do not carry on: take its primal");
 }
 
 // A call wrote `t` in place: autograd sees by its version that what it saved of it is gone. (Inference tensors have none.)

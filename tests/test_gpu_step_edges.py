@@ -213,3 +213,20 @@ def test_inference_tensors_are_written_as_before(ops):  # noqa: F811
         assert torch.equal(ops.base_linear(x, qw, sc, z, out=y), want)
     y2 = ops.base_linear(x, qw, sc, z, out=y)
     assert torch.equal(y2, want)
+
+
+def test_forward_mode_tangents_are_refused(ops):  # noqa: F811
+    """A dual tensor's tangent would be dropped: refused, like one that requires a gradient, unless forward mode is off."""
+    import torch
+    import torch.autograd.forward_ad as fwAD
+    x, qw, sc, z = _linear_inputs(3, 128, 20, 32, True, "bf16")
+    q, _, _, pos, _, _, _ = _rope_inputs(4, 4, 2, 64, 64, "bf16")
+    table = ops.rope_table(500, 64)
+    want = ops.base_linear(x, qw, sc, z)
+    with fwAD.dual_level():
+        dual = fwAD.make_dual(x, torch.ones_like(x))
+        with pytest.raises(ValueError, match="tangent"):
+            ops.base_linear(dual, qw, sc, z)
+        with pytest.raises(ValueError, match="tangent"):
+            ops.rope(fwAD.make_dual(q.contiguous(), torch.ones_like(q)), pos, table)
+        assert torch.equal(ops.base_linear(fwAD.unpack_dual(dual).primal, qw, sc, z), want)
