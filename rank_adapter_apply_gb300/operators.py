@@ -73,10 +73,10 @@ def rope_table(n_positions, rot_dim, base=10000.0, scaling=None, factor=1.0, ori
     if device.type != "cuda" or (device.index is not None and device.index != torch.cuda.current_device()):
         raise ValueError(f"device {device}: the current CUDA device is needed")
     table = torch.empty((n_positions, rot_dim), dtype=torch.float32, device=device)
+    high = 32.0 if scaling == "yarn" else 4.0
     B.lora_rope_table(table.data_ptr() or None, n_positions, rot_dim, _SCALING[scaling], float(base), float(factor),
-                      float(original or 1.0), float(low_freq or 1.0),
-                      float(high_freq or (32.0 if scaling == "yarn" else 4.0)),
-                      torch.cuda.current_stream().cuda_stream)
+                      float(1.0 if original is None else original), float(1.0 if low_freq is None else low_freq),
+                      float(high if high_freq is None else high_freq), torch.cuda.current_stream().cuda_stream)
     return table
 
 

@@ -230,3 +230,13 @@ def test_forward_mode_tangents_are_refused(ops):  # noqa: F811
         with pytest.raises(ValueError, match="tangent"):
             ops.rope(fwAD.make_dual(q.contiguous(), torch.ones_like(q)), pos, table)
         assert torch.equal(ops.base_linear(fwAD.unpack_dual(dual).primal, qw, sc, z), want)
+
+
+# ---- arguments --------------------------------------------------------------------------------------
+def test_rope_table_zero_is_not_a_default(ops):  # noqa: F811
+    """A frequency bound, or an original length, of zero is refused by the library, not replaced."""
+    from rank_adapter_apply_gb300 import binding as B
+    for scaling in ("pieces", "yarn"):
+        for kw in (dict(low_freq=0), dict(low_freq=0.0, high_freq=4.0), dict(high_freq=0), dict(original=0)):
+            with pytest.raises(B.LoraError):
+                ops.rope_table(10, 64, scaling=scaling, factor=2.0, **{"original": 4096, **kw})
