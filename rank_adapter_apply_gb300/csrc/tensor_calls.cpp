@@ -111,6 +111,12 @@ bool done(int rc) {
     return false;
 }
 
+// The truth of `o`; false where asking for it raised.
+bool flag(PyObject *o, int &value) {
+    value = PyObject_IsTrue(o);
+    return value >= 0;
+}
+
 bool arguments(Py_ssize_t n, Py_ssize_t want) {
     if (n == want) return true;
     PyErr_Format(PyExc_TypeError, "%zd arguments: %zd are needed", n, want);
@@ -201,8 +207,7 @@ PyObject *rope(PyObject *, PyObject *const *v, Py_ssize_t n) {
     lora_rope_desc d{};
     const Tensor *out = tensor(v[5], "out", true);
     Tensor y = rotated(x, positions, table, out, w, d);
-    d.interleaved = PyObject_IsTrue(v[3]);
-    d.inverse = PyObject_IsTrue(v[4]);
+    if (!flag(v[3], d.interleaved) || !flag(v[4], d.inverse)) return nullptr;
     if (!done(g_rope(&d, w.stream))) return nullptr;
     if (out) written(y);
     return THPVariable_Wrap(std::move(y));
@@ -242,7 +247,7 @@ PyObject *rope_append(PyObject *, PyObject *const *v, Py_ssize_t n) {
     check_cache(kc, vc, w, type, k.size(1), k.size(2));
     const Tensor *out = tensor(v[9], "out", true);
     Tensor y = rotated(q, positions, table, out, w, d);
-    d.interleaved = PyObject_IsTrue(v[8]);
+    if (!flag(v[8], d.interleaved)) return nullptr;
     d.k = k.const_data_ptr();
     d.k_token = k.stride(0);
     d.k_head = k.stride(1);

@@ -240,3 +240,16 @@ def test_rope_table_zero_is_not_a_default(ops):  # noqa: F811
         for kw in (dict(low_freq=0), dict(low_freq=0.0, high_freq=4.0), dict(high_freq=0), dict(original=0)):
             with pytest.raises(B.LoraError):
                 ops.rope_table(10, 64, scaling=scaling, factor=2.0, **{"original": 4096, **kw})
+
+
+def test_flags_without_a_truth_value(ops):  # noqa: F811
+    """A flag whose truth raises: that error, and nothing is queued."""
+    import torch
+    q, k, v, pos, kc, vc, slots = _rope_inputs(4, 4, 2, 64, 64, "bf16")
+    table, two = ops.rope_table(500, 64), torch.tensor([0, 1])
+    out = torch.full_like(q, 3.0)
+    for call in (lambda: ops.rope(q, pos, table, interleaved=two, out=out), lambda: ops.rope(q, pos, table, inverse=two, out=out),
+                 lambda: ops.rope_append(q, k, v, pos, table, kc, vc, slots, interleaved=two, out=out)):
+        with pytest.raises(RuntimeError, match="ambiguous"):
+            call()
+    assert (out == 3.0).all() and (kc == 7.0).all()
