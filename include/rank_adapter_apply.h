@@ -588,7 +588,8 @@ int lora_apply_static_scratch(const void *x, void *y, const int32_t *token_slot_
  * nothing. What can only be seen on the device (positions, cache slots, page
  * ids, lengths, tree parents, token ids) never leads to an access outside the
  * arrays: each call says what it does with an entry out of range.
- * Outputs must not overlap inputs, except where a call allows it.
+ * Outputs must not overlap inputs, except where a call allows it, and the rows
+ * of an output (and of the caches that lora_rope writes) not each other.
  */
 
 /*

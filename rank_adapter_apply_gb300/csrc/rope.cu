@@ -312,6 +312,14 @@ extern "C" int lora_rope(const lora_rope_desc *d, void *stream) {
     if (!d->positions || (!d->table && d->n_positions > 0) || (d->n_heads > 0 && (!d->q || !d->q_out)) ||
         (append && (!d->k || !d->v || !d->k_cache || !d->v_cache || !d->slots)))
         return fail(LORA_ERR_ARG, "rope: NULL pointer argument");
+    if (!rows_apart(d->n_tokens, d->q_out_token, d->n_heads, d->q_out_head, d->head_dim))
+        return fail(LORA_ERR_ARG, "rope: the rows of q_out overlap (strides %lld, %lld)", (long long)d->q_out_token,
+                    (long long)d->q_out_head);
+    if (append && (!rows_apart(d->n_pages, d->cache_page, d->page_size, d->cache_slot, d->head_dim) ||
+                   !rows_apart(d->n_pages, d->cache_page, d->n_kv_heads, d->cache_head, d->head_dim) ||
+                   !rows_apart(d->page_size, d->cache_slot, d->n_kv_heads, d->cache_head, d->head_dim)))
+        return fail(LORA_ERR_ARG, "rope: rows of the caches overlap (strides %lld, %lld, %lld)", (long long)d->cache_page,
+                    (long long)d->cache_slot, (long long)d->cache_head);
     RopeArgs a{d->q,       d->k,         d->v,          d->q_out,       d->k_cache,     d->v_cache,   d->slots,
                d->positions, d->table,   d->q_token,    d->q_head,      d->q_out_token, d->q_out_head, d->k_token,
                d->k_head,  d->v_token,   d->v_head,     d->cache_page,  d->cache_slot,  d->cache_head,

@@ -65,6 +65,22 @@ inline cudaError_t launch_step(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
 }
 
 inline bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Whether rows of `len` elements at i * s0 + j * s1, i < n0 and j < n1, lie apart: the rows of an output that one call
+// writes in no order.
+inline bool rows_apart(long long n0, long long s0, long long n1, long long s1, long long len) {
+    using wide = __int128;
+    if (n0 < 1 || n1 < 1) return true;
+    const wide a = s0 < 0 ? -(wide)s0 : s0, b = s1 < 0 ? -(wide)s1 : s1;
+    if ((n0 > 1 && a < len) || (n1 > 1 && b < len)) return false;
+    if (n0 == 1 || n1 == 1 || a >= (n1 - 1) * b + len || b >= (n0 - 1) * a + len) return true;
+    for (wide j = 1; j < n1; ++j) {                        // neither inside the other: the rows next to i = 0's j-th
+        const wide i = j * b / a;
+        if ((i < n0 && j * b - i * a < len) || (i + 1 < n0 && (i + 1) * a - j * b < len)) return false;
+    }
+    return true;
+}
+
 inline bool known_dtype(int dtype) { return dtype == LORA_DTYPE_F32 || dtype == LORA_DTYPE_BF16; }
 
 __device__ __forceinline__ float to_f32(float v) { return v; }

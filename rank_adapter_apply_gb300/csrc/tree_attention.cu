@@ -608,6 +608,9 @@ extern "C" int lora_tree_attention(const lora_tree_attention_desc *d, void *stre
     if (!ok)
         return fail(LORA_ERR_ARG, "tree_attention: q, out and cache pointers and strides must be multiples of 16 bytes, "
                                   "no stride negative");
+    if (!rows_apart(d->n_tokens, d->out_token, d->n_heads, d->out_head, d->head_dim))
+        return fail(LORA_ERR_ARG, "tree_attention: the rows of out overlap (strides %lld, %lld)", (long long)d->out_token,
+                    (long long)d->out_head);
     const size_t need = lora_tree_attention_workspace_bytes(d->n_requests, d->n_tokens, d->n_heads, d->n_kv_heads,
                                                             d->head_dim, d->dtype);
     if (!d->workspace || d->workspace_bytes < need || reinterpret_cast<uintptr_t>(d->workspace) % 256)
