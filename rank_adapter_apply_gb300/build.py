@@ -49,14 +49,19 @@ def _stale(target: str, deps: list[str]) -> bool:
 
 
 # The tensor form of the drafted-token step's calls: a Python module of its own,
-# which the library does not depend on (and the sanitizer build leaves out).
+# which the library does not depend on (the sanitizer build leaves it out, and so
+# does a build without torch).
 TENSOR_CALLS = os.path.join(BUILD, "_tensor_calls.so")
 TENSOR_CALLS_SOURCE = os.path.join(CSRC, "tensor_calls.cpp")
 
 
-def _tensor_calls_command(out: str) -> list[str]:
+def _torch_dir() -> str | None:
     from importlib.util import find_spec
-    torch = os.path.dirname(find_spec("torch").origin)
+    spec = find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _tensor_calls_command(torch: str, out: str) -> list[str]:
     cuda = os.path.dirname(os.path.dirname(_nvcc())) if os.path.isabs(_nvcc()) else "/usr/local/cuda"
     include = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
                os.path.join(torch, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
@@ -65,6 +70,19 @@ def _tensor_calls_command(out: str) -> list[str]:
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D_GLIBCXX_USE_CXX11_ABI=1",
             *[f"-I{d}" for d in include], TENSOR_CALLS_SOURCE, "-o", out, f"-L{lib}", "-ltorch_python", "-ltorch_cuda",
             "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{lib}"]
+
+
+def _tensor_calls_made_of(torch: str) -> str:
+    """What the module was built with, kept beside it: its interface is torch's C++ one, which a version may change."""
+    with open(os.path.join(torch, "version.py")) as f:
+        return "\n".join([*_tensor_calls_command(torch, TENSOR_CALLS), f.read()])
+
+
+def _tensor_calls_stale(torch: str, deps: list[str]) -> bool:
+    if _stale(TENSOR_CALLS, deps) or not os.path.exists(TENSOR_CALLS + ".made_of"):
+        return True
+    with open(TENSOR_CALLS + ".made_of") as f:
+        return f.read() != _tensor_calls_made_of(torch)
 
 
 SANITIZE_FLAGS = ["-Xcompiler", "-fsanitize=address,-fsanitize=undefined,-fno-omit-frame-pointer", "-g"]
@@ -90,9 +108,10 @@ def build(force: bool = False, verbose: bool = False, sanitize: bool = False) ->
             jobs.append(cmd)
     objects = bool(jobs)
     calls_tmp = TENSOR_CALLS + f".tmp{os.getpid()}"
-    calls = not sanitize and (force or _stale(TENSOR_CALLS, [TENSOR_CALLS_SOURCE, common_deps[-1]]))
+    torch = None if sanitize else _torch_dir()
+    calls = torch is not None and (force or _tensor_calls_stale(torch, [TENSOR_CALLS_SOURCE, common_deps[-1]]))
     if calls:
-        jobs.insert(0, _tensor_calls_command(calls_tmp))
+        jobs.insert(0, _tensor_calls_command(torch, calls_tmp))
 
     def run(cmd):
         if verbose:
@@ -108,6 +127,8 @@ def build(force: bool = False, verbose: bool = False, sanitize: bool = False) ->
                 print(err, flush=True)
     if calls:
         os.replace(calls_tmp, TENSOR_CALLS)
+        with open(TENSOR_CALLS + ".made_of", "w") as f:
+            f.write(_tensor_calls_made_of(torch))
     if force or objects or _stale(lib_path, objs):
         tmp = lib_path + f".tmp{os.getpid()}"
         link_extra = ["-Xcompiler", "-fsanitize=address,-fsanitize=undefined"] if sanitize else []
