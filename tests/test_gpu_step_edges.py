@@ -2,8 +2,9 @@
 import numpy as np
 import pytest
 
-from tests.test_gpu_step import (_check_tree, _check_verify, _dev, _dt, _linear_inputs, _rope_inputs, _run_tree,  # noqa: F401
-                                 _run_verify, _tree_case, _verify_case, ops)
+from tests import step_reference as ref
+from tests.test_gpu_step import (ROUND, _check_linear, _check_tree, _check_verify, _close, _dev, _dt, _linear_inputs,  # noqa: F401
+                                 _np, _rope_inputs, _run_tree, _run_verify, _tree_case, _verify_case, ops)
 
 pytestmark = pytest.mark.gpu
 
@@ -253,3 +254,42 @@ def test_flags_without_a_truth_value(ops):  # noqa: F811
         with pytest.raises(RuntimeError, match="ambiguous"):
             call()
     assert (out == 3.0).all() and (kc == 7.0).all()
+
+
+# ---- base_linear: prompts -----------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tokens,d_in,d_out,group,zeros", [(257, 640, 200, 128, True), (1000, 96, 130, 32, False),
+                                                            (4096, 512, 129, 64, True)])
+def test_base_linear_prompts(ops, tokens, d_in, d_out, group, zeros, dtype):  # noqa: F811
+    """Many tiles of tokens, with rows that TMA takes and with rows at odd elements."""
+    import torch
+    x, qw, sc, z = _linear_inputs(tokens, d_in, d_out, group, zeros, dtype, seed=tokens)
+    _check_linear(ops.base_linear(x, qw, sc, z), x, qw, sc, z, group, dtype)
+    wide = torch.full((tokens, d_in + 9), float("nan"), dtype=x.dtype, device=x.device)
+    wide[:, 5:5 + d_in] = x
+    _check_linear(ops.base_linear(wide[:, 5:5 + d_in], qw, sc, z), x, qw, sc, z, group, dtype)
+
+
+# ---- rope: the inverse ----------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim,rot,kw", [
+    (128, 128, {}), (80, 64, dict(scaling="linear", factor=4.0)), (30, 10, {}),
+    (64, 64, dict(scaling="yarn", factor=16.0, original=4096)), (36, 20, dict(scaling="yarn", factor=8.0, original=1024))])
+def test_rope_inverse_is_the_gradient(ops, dim, rot, kw, interleaved, dtype):  # noqa: F811
+    """The rotation by the negative angle, with the table's magnitude (above 1 with "yarn"): for y = m R x it is m R^T, the
+    gradient, and undoes y only where m is 1."""
+    r = np.random.default_rng(dim + rot)
+    g = _dev(r.standard_normal((50, 3, dim)), _dt(dtype))
+    pos = _dev(r.integers(0, 500, 50).astype(np.int32))
+    table = ops.rope_table(500, rot, **kw)
+    got = _np(ops.rope(g, pos, table, interleaved=interleaved, inverse=True))
+    tab, p = _np(table), pos.cpu().numpy()
+    want, mass = ref.rope(_np(g), tab[p, :rot // 2], -tab[p, rot // 2:], interleaved)
+    m = max(1.0, np.hypot(tab[0, 0], tab[0, rot // 2]))
+    _close(got, want, (mass > 0) * (ROUND[dtype] * np.abs(want) + 2.0 ** -22 * mass * m))
+    x = r.standard_normal((50, 3, dim))
+    turned, _ = ref.rope(x, tab[p, :rot // 2], tab[p, rot // 2:], interleaved)
+    both = (turned * _np(g)).sum(), (x * want).sum()                        # <m R x, g> = <x, m R^T g>
+    assert abs(both[0] - both[1]) <= 1e-9 * np.abs(turned * _np(g)).sum()
+    assert (m > 1.05) == (kw.get("scaling") == "yarn")
