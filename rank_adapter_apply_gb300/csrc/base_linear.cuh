@@ -57,8 +57,8 @@ int active_clusters(Kernel kernel, int threads, size_t smem, int c, ActiveCluste
     return n;
 }
 
-// On the 5th-generation tensor cores (base_linear_tc.cu): whether TMA can load x in bf16 (fp32 it takes as it is), and the
-// launch.
+// On the 5th-generation tensor cores (base_linear_tc.cu): whether TMA can load an x of several rows in bf16 (fp32 it takes
+// as it is), and the launch.
 bool tc_takes(const LinearArgs &a);
 cudaError_t launch_tc(const LinearArgs &a, int dtype, int sms, cudaStream_t st);
 // CTAs whose bounded waits gave up.

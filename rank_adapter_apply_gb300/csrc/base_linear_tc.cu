@@ -518,7 +518,7 @@ cudaError_t launch_group(const LinearArgs &a, int sms, cudaStream_t st) {
 cudaError_t read_timeouts(unsigned *count) { return cudaMemcpyFromSymbol(count, g_gave_up, sizeof *count); }
 
 bool tc_takes(const LinearArgs &a) {
-    return aligned16(a.x) && (a.n_tokens == 1 || (a.x_stride % 8 == 0 && a.x_stride < 1ll << 38));
+    return aligned16(a.x) && a.x_stride % 8 == 0 && a.x_stride < 1ll << 38;
 }
 
 cudaError_t launch_tc(const LinearArgs &a, int dtype, int sms, cudaStream_t st) {
