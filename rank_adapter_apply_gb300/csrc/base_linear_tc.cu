@@ -9,8 +9,9 @@
 // no weight is ever rounded.
 //
 // An x in fp32 is cut by eight more warps into three bf16 parts of eight bits each that
-// sum to it exactly; they lie side by side as three times the tokens in one product, and
-// their sums meet in the row's accumulators.
+// sum to it exactly from 2^-103 on, where all three are normal numbers; of a smaller x
+// less than 2^-125 is lost. They lie side by side as three times the tokens in one
+// product, and their sums meet in the row's accumulators.
 //
 // S sets of four warps take units of up to 128 columns in turn, each with its own A and
 // D in tensor memory, so the reads, the conversion, the products and the sums of S units
@@ -109,8 +110,8 @@ struct Unit {
     static constexpr int kPieces = k4 ? 4 : k2 ? 2 : GU;
 };
 
-// Eight fp32 values (zeros where !there) as three bf16 each that sum to them exactly: the upper eight significand bits,
-// cut, the eight after them, and the rest. An infinity or NaN is the first part alone.
+// Eight fp32 values (zeros where !there) as three bf16 each that sum to them (exactly from 2^-103 on): the upper eight
+// significand bits, cut, the eight after them, and the rest. An infinity or NaN is the first part alone.
 __device__ __forceinline__ void cut(const float (&v)[8], bool there, uint4 (&part)[3]) {
     uint32_t h[3][8];
 #pragma unroll

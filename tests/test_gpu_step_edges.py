@@ -293,3 +293,19 @@ def test_rope_inverse_is_the_gradient(ops, dim, rot, kw, interleaved, dtype):  #
     both = (turned * _np(g)).sum(), (x * want).sum()                        # <m R x, g> = <x, m R^T g>
     assert abs(both[0] - both[1]) <= 1e-9 * np.abs(turned * _np(g)).sum()
     assert (m > 1.05) == (kw.get("scaling") == "yarn")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tokens", [1, 20])
+@pytest.mark.parametrize("power", [-100, -103, -112, -122])
+def test_base_linear_small_activations(ops, power, tokens, dtype):  # noqa: F811
+    """Activations near the smallest normal numbers: an fp32 x loses less than 2^-125 of itself where its parts are
+    subnormal, a bf16 x nothing; sums of 64ths may lose a few 2^-149 each."""
+    x, qw, sc, z = _linear_inputs(tokens, 256, 70, 64, True, dtype, seed=7)
+    x = (x.double() * 2.0 ** power).to(x.dtype)
+    want, mass = ref.linear(_np(x), qw.cpu().numpy(), _np(sc), z.cpu().numpy(), 64)
+    _, weights = ref.linear(np.ones((1, 256)), qw.cpu().numpy(), _np(sc), z.cpu().numpy(), 64)
+    lost = 2.0 ** -125 if dtype == "f32" else 2.0 ** -133
+    small = 2.0 ** -134 if dtype == "bf16" else 2.0 ** -149               # a result's own rounding below the normal numbers
+    _close(_np(ops.base_linear(x, qw, sc, z)), want,
+           ROUND[dtype] * np.abs(want) + 2.0 ** -22 * mass + lost * weights + 256 * 64 * 2.0 ** -149 + small)
