@@ -584,10 +584,12 @@ int lora_apply_static_scratch(const void *x, void *y, const int32_t *token_slot_
  * each before a capture: it loads the device code). All pointers are device
  * pointers; strides are in elements and the last dimension is contiguous.
  * dtype is a lora_dtype: LORA_DTYPE_BF16 computes in fp32 with one final
- * rounding to bf16. A count of zero (tokens, requests) is LORA_OK and queues
- * nothing. What can only be seen on the device (positions, cache slots, page
- * ids, lengths, tree parents, token ids) never leads to an access outside the
- * arrays: each call says what it does with an entry out of range.
+ * rounding to bf16, but for the softmax weights of lora_tree_attention, which
+ * are rounded to bf16 for their product with the values (their sum is not; with
+ * LORA_DTYPE_F32 nothing is). A count of zero (tokens, requests) is LORA_OK
+ * and queues nothing. What can only be seen on the device (positions, cache
+ * slots, page ids, lengths, tree parents, token ids) never leads to an access
+ * outside the arrays: each call says what it does with an entry out of range.
  * Outputs must not overlap inputs, except where a call allows it, and the rows
  * of an output (and of the caches that lora_rope writes) not each other.
  */
@@ -643,9 +645,11 @@ int lora_rope_table(float *table, int n_positions, int rot_dim, int scaling, dou
  * of the token's position: the pair (a, b) becomes (a cos - b sin, a sin + b
  * cos); pairs are elements (2j, 2j + 1) when interleaved, else (j, j + rot_dim /
  * 2). Elements past rot_dim are copied. inverse != 0 rotates by the negative
- * angle: the gradient of the forward rotation (and its undoing). With k, the
- * rotated k and the unchanged v of token t are written to slot slots[t] of the
- * paged cache: page slots[t] / page_size, place slots[t] % page_size.
+ * angle: the gradient of the forward rotation, whatever the table's magnitude (and
+ * its undoing where that is 1: not with LORA_ROPE_YARN and a factor above 1).
+ * With k, the rotated k and the unchanged v of token t are written to slot
+ * slots[t] of the paged cache: page slots[t] / page_size, place slots[t] %
+ * page_size.
  * A token whose position is outside the table has none of its rows written; a
  * slot outside [0, n_pages * page_size) writes no cache row (its q row is).
  * Two tokens with one slot: which of them stays is not defined. q_out may be q
@@ -715,7 +719,8 @@ typedef struct {
     int n_requests, n_tokens, n_heads, n_kv_heads, head_dim, dtype;
 } lora_tree_attention_desc;
 
-/* Bytes of workspace of a lora_tree_attention call (0 for sizes it refuses). */
+/* Bytes of workspace of a lora_tree_attention call (0 for sizes it refuses,
+ * 42.6 MB for all others: one workspace serves calls of any size). */
 size_t lora_tree_attention_workspace_bytes(int n_requests, int n_tokens, int n_heads, int n_kv_heads,
                                            int head_dim, int dtype);
 

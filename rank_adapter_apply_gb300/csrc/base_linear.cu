@@ -343,8 +343,8 @@ cudaError_t launch_group(const LinearArgs &a, int sms, cudaStream_t st) {
 // aligned rows), measured for 4096x4096, 5120x8192 and 4096x14336 (d_in x d_out), W from memory: 2 tokens 6.3 / 10.6 / 11.4
 // us here and 6.5 / 10.0 / 11.6 there, 4 tokens 6.5 / 10.4 / 12.0 and 6.5 / 10.0 / 11.6, 8 tokens 6.9 / 10.8 / 12.7 and 6.6 /
 // 10.0 / 11.6; from L2, 16 tokens 8.3 / 12.7 / 14.9 and 6.3 / 9.5 / 11.5, 64 tokens 15.1 / 29.9 / 32.3 and 8.0 / 12.5 /
-// 13.4. fp32 always goes there (with three products for each here, 1 token 8.8 / 16.5 / 19.0 us against 7.7 / 13.3 / 16.9, 64
-// tokens 41 / 71 / 88 against 17.7 / 37.7 / 58.6). Here, up to 16 tokens: two CTAs of eight warps to an SM. Above, the
+// 13.4. fp32 always goes there (with three products for each here, 1 token 8.8 / 16.5 / 19.0 us against 7.6 / 13.0 / 16.5, 64
+// tokens 41 / 71 / 88 against 16.6 / 34.9 / 55.5). Here, up to 16 tokens: two CTAs of eight warps to an SM. Above, the
 // accumulators want the registers of twelve warps to an SM, in one CTA, whose copy of x then serves more rows (48 tokens:
 // 12.5 / 23.4 / 26.2 us, against 14.1 / 25.5 / 32.1 with two CTAs of eight).
 cudaError_t launch_linear(const LinearArgs &a, int dtype, int sms, cudaStream_t st) {

@@ -141,9 +141,10 @@ __global__ void __launch_bounds__(256) rope_rows_kernel(RopeArgs a) {
 // and 2u + 1; past rot_dim (and in v): two neighbours to copy. A block has `units`
 // lanes for a row (unit = threadIdx.x) times blockDim.y rows; a thread takes its
 // unit of kRows rows of one token, whose cosines and sines it reads once, with all
-// loads in flight before the first is used. Bound by memory: 16384 tokens of 32 + 8 heads
-// of 128, with the append, 109 us, 6.2 TB/s; 1021 tokens in fp32 5.7 us, 4.1 TB/s (the
-// launch is 1.5 of them); 8 tokens 1.8 us, a launch and one round of reads.
+// loads in flight before the first is used. Bound by memory: 16384 tokens of 64 + 8 heads
+// of 128, with the append, 110 us, 6.2 TB/s; 1021 tokens of 28 + 4 heads of 80 in fp32 6.9
+// us from memory, 3.5 TB/s (the launch is 1.5 of them); 8 tokens of 32 + 8 heads 1.6 us in a
+// graph, a launch and one round of reads.
 __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }

@@ -498,10 +498,12 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan, i
 constexpr int kMaxRows = 128;
 constexpr int kMaxCtas = 2 * 160;
 
-// The row tile by the average rows (nodes times query heads of a key/value head) of a request. 8 requests, ctx 4096, 32
-// heads over 8, tiles of 16 / 32 / 128 rows: 8 rows 34.6 / 35.4 / 35.6 us, 16 rows 36.0 / 36.3 / 35.5, 24 rows 45.1 / 38.0 /
-// 36.8, 32 rows 45.5 / 38.2 / 37.4, 48 rows 58.9 / 50.9 / 38.9, 128 rows 119 / 80 / 47. For few keys 32 beats 128 up to 32
-// rows: 1x8 ctx 777 12.7 and 14.8, 4x8 ctx 500 13.6 and 17.7.
+// The row tile by the average rows (nodes times query heads of a key/value head) of a request: how they are spread over
+// the requests only the device knows, so one wide tree among many single nodes goes in many small tiles (64 requests, ctx
+// 4096, 32 heads over 8: all of one node 176 us, one of them of 64 nodes 234). Measured with equal requests: 8, ctx 4096,
+// 32 heads over 8, tiles of 16 / 32 / 128 rows: 8 rows 34.6 / 35.4 / 35.6 us, 16 rows 36.0 / 36.3 / 35.5, 24 rows 45.1 /
+// 38.0 / 36.8, 32 rows 45.5 / 38.2 / 37.4, 48 rows 58.9 / 50.9 / 38.9, 128 rows 119 / 80 / 47. For few keys 32 beats 128
+// up to 32 rows: 1x8 ctx 777 12.7 and 14.8, 4x8 ctx 500 13.6 and 17.7.
 int rows_of_tile(const TreeArgs &a) {
     const double rows = (double)a.n_tokens * (a.n_heads / a.n_kv) / a.n_requests;
     return rows <= 16.0 ? 16 : rows <= 32.0 || !tc_takes(a) ? 32 : 128;

@@ -7,7 +7,7 @@
 // rows (a shared-memory wavefront feeds 8 or more FMA instructions); for few rows
 // 16 are taken, so that little is computed for rows that do not exist. The split of the
 // work and the join are those of the tensor-core kernels. Two CTAs of an SM load
-// and compute in turn. 64 nodes, 64 heads over 8, ctx 32768: 1.54 ms, 45 TFLOP/s.
+// and compute in turn. 64 nodes, 64 heads over 8, ctx 32768: 1.55 ms, 44 TFLOP/s.
 #include "tree_common.cuh"
 
 #include <atomic>

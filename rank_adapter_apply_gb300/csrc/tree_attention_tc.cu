@@ -21,8 +21,8 @@
 // clear the rows that are not finite, and the rows that see one of them add it in
 // fp32 at the end of the unit.
 //
-// What bounds it: 4 requests of up to 64 nodes, ctx 32768, 64 heads over 8 take 200 us
-// with the join, 982 TFLOP/s. The product pipe is busy for 63 % of it (64 keys at a time,
+// What bounds it: 4 requests of up to 64 nodes, ctx 32768, 64 heads over 8 take 202 us
+// with the join in a graph, 971 TFLOP/s. The product pipe is busy for 63 % of it (64 keys at a time,
 // Q is read from shared memory again for each), and a CTA's chain scores, softmax, weights
 // to tensor memory, second product, next scores is as long as the two CTAs of an SM can
 // hide. 32 requests of up to 16 nodes, ctx 4096, 32 heads over 8: 89 us, 4.7 TB/s of keys

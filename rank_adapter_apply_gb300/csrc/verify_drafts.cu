@@ -41,9 +41,9 @@ struct Shared {
 // rejection that is followed by another sibling.
 //
 // What bounds it: for large batches memory (256 requests of 8 nodes, vocabulary 131072, two
-// fp32 rows and the noise: 79 us, 5.1 TB/s of what one pass reads, and a rejection reads
-// more); for few the chain of passes, each a round of reads and two cluster barriers (32x13
-// of 100003 17.3 us, 1x5 of 32000 5.7 us).
+// fp32 rows and the noise: 78 us in a graph, 5.1 TB/s of what one pass reads, 86-90 us in a
+// stream of calls, and a rejection reads more); for few the chain of passes, each a round of
+// reads and two cluster barriers (32x13 of 100003 18 us, 1x5 of 32000 6 us).
 // Visit a CTA's part of a row: f(v, p[v], q[v], noise[v]) for every index v, in
 // rising order within a thread. Whole 16-byte vectors of p, at whatever element
 // the row's first one starts, are dealt to the cluster; the elements before and

@@ -12,7 +12,9 @@ call's time is the host's. Every function checks its tensors (``ValueError``; wh
 library refuses raises ``binding.LoraError``), queues its kernels on torch's current stream of the current
 device and returns without waiting. Outputs and workspace come from torch's
 allocator on that stream. A tensor made on another stream needs the caller's own
-ordering (an event or ``wait_stream``), as for any kernel.
+ordering (an event or ``wait_stream``), as for any kernel. No gradient is recorded: a
+tensor that requires one, or has a forward-mode tangent, is refused. What a call writes
+in place (``out``, the caches) has a new version afterwards.
 """
 from __future__ import annotations
 
@@ -83,7 +85,8 @@ def rope_table(n_positions, rot_dim, base=10000.0, scaling=None, factor=1.0, ori
 def rope(x, positions, table, interleaved=False, inverse=False, out=None):
     """Rotate the first table.shape[1] elements of every head of x [tokens, heads, head_dim].
 
-    positions int32 [tokens]; inverse=True turns back (the gradient of the forward rotation). ``out`` may be x."""
+    positions int32 [tokens]; inverse=True turns by the negative angle: the gradient of the forward rotation (its undoing
+    only where the table's magnitude is 1, so not with "yarn" and a factor above 1). ``out`` may be x."""
     return _rope(x, positions, table, interleaved, inverse, out)
 
 
