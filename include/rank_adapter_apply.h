@@ -688,8 +688,8 @@ int lora_rope(const lora_rope_desc *desc, void *stream);
  * without a tree_mask, the nodes 0..i (a chain; one node: a decode step).
  *   out = sum_p softmax_p(scale q.k_p) v_p,   lse = ln sum_p exp(scale q.k_p)
  * over the keys it sees; a row that sees none (or only scores of -inf) gets out
- * = 0, lse = -inf, and a NaN among a row's scores makes its out and lse NaN. Head
- * h reads key/value head h / (n_heads / n_kv_heads). Keys past the page table's
+ * = 0, lse = -inf, and a NaN or +inf among a row's scores makes its out and lse
+ * NaN. Head h reads key/value head h / (n_heads / n_kv_heads). Keys past the page table's
  * row or on a page id outside [0, n_pages) are not seen; what lies there, and
  * in cache rows that no query sees, has no effect, NaN and infinities included.
  * A context length below 0 counts as 0; node_starts are clamped to
