@@ -679,6 +679,26 @@ typedef struct {
 int lora_rope(const lora_rope_desc *desc, void *stream);
 
 /*
+ * lora_rope with a norm of every query and key head in front of the rotation, in
+ * the same pass:
+ *   y = x / sqrt(sum(x^2) / head_dim + eps) * weight
+ * over the head's head_dim elements, then the first rot_dim of y are turned and
+ * the rest copied; v is only copied. Squares are summed in fp32, and one rounding
+ * comes at the end: none between norm and rotation. q_weight and k_weight (type
+ * dtype) hold head_dim values for every head (stride 0: the same for all), or are
+ * NULL: ones. rope.inverse is 0. eps >= 0, finite: with eps 0 a head of zeros is
+ * NaN. All else is as lora_rope says, and q_out may be q itself with the same strides.
+ */
+typedef struct {
+    lora_rope_desc rope;
+    const void *q_weight, *k_weight;
+    int64_t q_weight_head, k_weight_head;  /* strides between the heads' weights, not negative */
+    float eps;
+} lora_norm_rope_desc;
+
+int lora_norm_rope(const lora_norm_rope_desc *desc, void *stream);
+
+/*
  * Attention of drafted trees over a paged cache. Request b owns the query rows
  * (nodes) node_starts[b] .. node_starts[b + 1) and the cache rows of its page
  * table: key p is place p % page_size of page page_table[b][p / page_size].
@@ -725,6 +745,37 @@ size_t lora_tree_attention_workspace_bytes(int n_requests, int n_tokens, int n_h
                                            int head_dim, int dtype);
 
 int lora_tree_attention(const lora_tree_attention_desc *desc, void *stream);
+
+/*
+ * lora_tree_attention for requests that share prefixes: the requests
+ * group_starts[g] .. group_starts[g + 1) of group g see, besides all that
+ * lora_tree_attention shows them (their own context, which starts after the
+ * prefix, and their trees), keys 0 .. prefix_lens[g] - 1 of the group: key p is place
+ * p % page_size of page prefix_table[g][p / page_size] of the same caches. A group's
+ * keys are read once for all its rows. Softmax and log-sum-exp go over all keys
+ * that a row sees; requests that belong to no group have their own keys alone.
+ * A prefix length below 0 counts as 0, keys past the prefix table's row or on a
+ * page id outside [0, n_pages) are not seen, group_starts are clamped to
+ * [0, n_requests]. Where starts (node_starts, group_starts) fall, the rows between
+ * the first and the last are not defined. tree.workspace:
+ * lora_prefix_attention_workspace_bytes(...). A call queues two or three kernels.
+ * All else is as lora_tree_attention says.
+ */
+typedef struct {
+    lora_tree_attention_desc tree;
+    const int32_t *prefix_table; /* [n_groups][prefix_pages], rows prefix_stride apart */
+    int64_t prefix_stride;
+    const int32_t *prefix_lens;  /* [n_groups] */
+    const int32_t *group_starts; /* [n_groups + 1], not decreasing */
+    int n_groups, prefix_pages;
+} lora_prefix_attention_desc;
+
+/* Bytes of workspace of a lora_prefix_attention call (0 for sizes it refuses): 85 MB, and
+ * 1072 bytes for each of n_tokens * n_heads rows (560 up to head_dim 64). */
+size_t lora_prefix_attention_workspace_bytes(int n_requests, int n_groups, int n_tokens, int n_heads, int n_kv_heads,
+                                             int head_dim, int dtype);
+
+int lora_prefix_attention(const lora_prefix_attention_desc *desc, void *stream);
 
 /* *count = thread blocks of lora_base_linear and lora_tree_attention on the
  * current device whose bounded device-side waits gave up so far; their rows are
@@ -775,6 +826,42 @@ typedef struct {
 } lora_verify_desc;
 
 int lora_verify_drafts(const lora_verify_desc *desc, void *stream);
+
+/*
+ * Draw the next token of every row from its logits x, from given random numbers.
+ * p = softmax(x / temperature); in the order of falling logits (of equal ones the
+ * lowest index first)
+ *   top_k keeps the first top_k tokens,
+ *   top_p the tokens whose predecessors have a mass below top_p (the fewest that
+ *         reach it, and always the first),
+ *   min_p the tokens with p >= min_p * (the largest p), and always the first;
+ * each filter looks at p itself, not at what another one left, and a token stays if
+ * all keep it. The token drawn is the kept one with the largest p / noise (the lowest
+ * index on a tie): with noise from the exponential distribution, tokens are
+ * distributed as the kept p. tokens[r] is its index, logprobs[r] = ln p of it, of
+ * all tokens, not of the kept ones alone.
+ * The filters are one value for each row, NULL where no row has one. temperature
+ * <= 0 or NaN: the first token, with logprobs at temperature 1. top_k <= 0, top_p >= 1
+ * (or NaN) and min_p <= 0 (or NaN) keep all. A logit of NaN counts as -inf, and +inf as
+ * the largest fp32 number; tokens of p = 0 are not drawn. A row of -inf alone has
+ * token -1 and logprob -inf. Noise that is negative or NaN keeps its token from being
+ * drawn; if that is so of all kept ones, the first token is drawn. Sums are fp32, put
+ * together in a fixed order.
+ */
+typedef struct {
+    const void *logits;       /* [n_rows][vocab], rows logits_row apart, type dtype */
+    int64_t logits_row;
+    const float *noise;       /* [n_rows][vocab], rows noise_row apart, > 0 */
+    int64_t noise_row;
+    const float *temperature; /* [n_rows], or NULL: 1 */
+    const int32_t *top_k;     /* [n_rows], or NULL */
+    const float *top_p, *min_p; /* [n_rows], or NULL */
+    int32_t *tokens;          /* [n_rows] */
+    float *logprobs;          /* [n_rows], or NULL */
+    int n_rows, vocab, dtype;
+} lora_sample_desc;
+
+int lora_sample_tokens(const lora_sample_desc *desc, void *stream);
 
 /* Message for the last failed call on this thread ("" if none; error reporting
  * only, no counterpart on the source pages). */

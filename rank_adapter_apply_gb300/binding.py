@@ -39,7 +39,8 @@ EXPORTED = [
     "lora_selftest_wait_timeout", "lora_assign_tokens", "lora_sync_host", "lora_abort_load",
     "lora_register_host_adapters", "lora_set_warm_set", "lora_serve_step",
     "lora_base_linear", "lora_rope_table", "lora_rope", "lora_tree_attention_workspace_bytes",
-    "lora_tree_attention", "lora_step_wait_timeouts", "lora_verify_drafts",
+    "lora_tree_attention", "lora_step_wait_timeouts", "lora_verify_drafts", "lora_norm_rope",
+    "lora_prefix_attention_workspace_bytes", "lora_prefix_attention", "lora_sample_tokens",
 ]
 
 
@@ -91,6 +92,20 @@ class LoraVerifyDesc(ctypes.Structure):
     _fields_ = _fields("target:p target_row:l draft:p draft_row:l tokens:p parents:p node_starts:p uniforms:p noise:p "
                        "noise_row:l path:p n_accepted:p next_token:p max_path:i n_requests:i n_nodes:i vocab:i "
                        "dtype:i")
+
+
+class LoraNormRopeDesc(ctypes.Structure):
+    _fields_ = [("rope", LoraRopeDesc)] + _fields("q_weight:p k_weight:p q_weight_head:l k_weight_head:l eps:f")
+
+
+class LoraPrefixAttentionDesc(ctypes.Structure):
+    _fields_ = [("tree", LoraTreeAttentionDesc)] + _fields("prefix_table:p prefix_stride:l prefix_lens:p group_starts:p "
+                                                           "n_groups:i prefix_pages:i")
+
+
+class LoraSampleDesc(ctypes.Structure):
+    _fields_ = _fields("logits:p logits_row:l noise:p noise_row:l temperature:p top_k:p top_p:p min_p:p tokens:p "
+                       "logprobs:p n_rows:i vocab:i dtype:i")
 
 
 LORA_ROPE_PLAIN, LORA_ROPE_LINEAR, LORA_ROPE_BASE, LORA_ROPE_PIECES, LORA_ROPE_YARN = range(5)
@@ -166,6 +181,10 @@ def load(path: str = LIB_PATH):
         "lora_tree_attention": (i32, [P(LoraTreeAttentionDesc), vp]),
         "lora_step_wait_timeouts": (i32, [P(u64)]),
         "lora_verify_drafts": (i32, [P(LoraVerifyDesc), vp]),
+        "lora_norm_rope": (i32, [P(LoraNormRopeDesc), vp]),
+        "lora_prefix_attention_workspace_bytes": (sz, [i32] * 7),
+        "lora_prefix_attention": (i32, [P(LoraPrefixAttentionDesc), vp]),
+        "lora_sample_tokens": (i32, [P(LoraSampleDesc), vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -491,3 +510,20 @@ def lora_step_wait_timeouts():
 
 def lora_verify_drafts(desc, stream):
     return check(load().lora_verify_drafts(desc, stream))
+
+
+def lora_norm_rope(desc, stream):
+    return check(load().lora_norm_rope(desc, stream))
+
+
+def lora_prefix_attention_workspace_bytes(n_requests, n_groups, n_tokens, n_heads, n_kv_heads, head_dim, dtype):
+    return int(load().lora_prefix_attention_workspace_bytes(n_requests, n_groups, n_tokens, n_heads, n_kv_heads, head_dim,
+                                                            dtype))
+
+
+def lora_prefix_attention(desc, stream):
+    return check(load().lora_prefix_attention(desc, stream))
+
+
+def lora_sample_tokens(desc, stream):
+    return check(load().lora_sample_tokens(desc, stream))

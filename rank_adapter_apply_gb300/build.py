@@ -26,9 +26,10 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "librank_adapter_apply.so")
 SOURCES = ["lora_abi.cu", "group.cu", "decode.cu", "decode_cluster.cu", "static_scratch.cu",
            "prefill_tc.cu", "upload.cu", "base_linear.cu", "base_linear_tc.cu", "rope.cu", "tree_attention.cu",
-           "tree_attention_tc.cu", "tree_attention_f32.cu", "verify_drafts.cu", "slot_table.cpp"]
+           "tree_attention_tc.cu", "tree_attention_f32.cu", "verify_drafts.cu", "norm_rope.cu", "prefix_attention.cu",
+           "sample_tokens.cu", "slot_table.cpp"]
 HEADERS = ["kernels.cuh", "slot_table.h", "device_util.cuh", "tc_util.cuh", "step_util.cuh", "tree_common.cuh",
-           "base_linear.cuh", "tensor_map.cuh"]
+           "base_linear.cuh", "tensor_map.cuh", "rope_common.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          f"-I{os.path.join(ROOT, 'include')}"]
@@ -48,7 +49,7 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-# The tensor form of the drafted-token step's calls: a Python module of its own,
+# The tensor form of the calls of a step: a Python module of its own,
 # which the library does not depend on (the sanitizer build leaves it out, and so
 # does a build without torch).
 TENSOR_CALLS = os.path.join(BUILD, "_tensor_calls.so")

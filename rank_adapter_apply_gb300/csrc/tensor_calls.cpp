@@ -1,4 +1,5 @@
-// Python module _tensor_calls: the drafted-token step's calls on torch tensors.
+// Python module _tensor_calls: the calls of a decoding step and of a step over
+// drafted tokens on torch tensors.
 //
 // It checks the tensors, fills the descriptors of include/rank_adapter_apply.h,
 // allocates outputs and workspace with torch's allocator and calls the C entry
@@ -32,6 +33,10 @@ decltype(&lora_rope) g_rope;
 decltype(&lora_tree_attention) g_tree;
 decltype(&lora_tree_attention_workspace_bytes) g_tree_bytes;
 decltype(&lora_verify_drafts) g_verify;
+decltype(&lora_norm_rope) g_norm;
+decltype(&lora_prefix_attention) g_prefix;
+decltype(&lora_prefix_attention_workspace_bytes) g_prefix_bytes;
+decltype(&lora_sample_tokens) g_sample;
 PyObject *g_raise;          // called with a status that is not LORA_OK
 
 using at::Tensor;
@@ -224,16 +229,11 @@ void check_cache(const Tensor &k, const Tensor &v, const Where &w, at::ScalarTyp
                       "k_cache and v_cache need one shape and one set of strides");
 }
 
-// rope_append(q, k, v, positions, table, k_cache, v_cache, slots, interleaved, out)
-PyObject *rope_append(PyObject *, PyObject *const *v, Py_ssize_t n) {
-    HANDLE_TH_ERRORS
-    if (!arguments(n, 10)) return nullptr;
-    const Tensor &q = *tensor(v[0], "q"), &k = *tensor(v[1], "k"), &val = *tensor(v[2], "v");
-    const Tensor &positions = *tensor(v[3], "positions"), &table = *tensor(v[4], "table");
-    const Tensor &kc = *tensor(v[5], "k_cache"), &vc = *tensor(v[6], "v_cache"), &slots = *tensor(v[7], "slots");
-    const Where w = start(q, "q");
+// What rope_append and norm_rope_append share: k, v and the caches, and what rotated() does.
+Tensor appended(const Tensor &q, const Tensor &k, const Tensor &val, const Tensor &positions, const Tensor &table,
+                const Tensor &kc, const Tensor &vc, const Tensor &slots, const Tensor *out, const Where &w,
+                lora_rope_desc &d) {
     const auto type = q.scalar_type();
-    lora_rope_desc d{};
     same(k, w, type, "k");
     same(val, w, type, "v");
     unit(k, 3, "k");
@@ -245,9 +245,7 @@ PyObject *rope_append(PyObject *, PyObject *const *v, Py_ssize_t n) {
     TORCH_CHECK_VALUE(slots.size(0) == q.size(0), "slots holds ", slots.size(0), " entries: one for each of ", q.size(0),
                       " tokens is needed");
     check_cache(kc, vc, w, type, k.size(1), k.size(2));
-    const Tensor *out = tensor(v[9], "out", true);
     Tensor y = rotated(q, positions, table, out, w, d);
-    if (!flag(v[8], d.interleaved)) return nullptr;
     d.k = k.const_data_ptr();
     d.k_token = k.stride(0);
     d.k_head = k.stride(1);
@@ -263,6 +261,21 @@ PyObject *rope_append(PyObject *, PyObject *const *v, Py_ssize_t n) {
     d.n_pages = kc.size(0);
     d.page_size = count(kc.size(1), "page_size");
     d.n_kv_heads = count(k.size(1), "kv_heads");
+    return y;
+}
+
+// rope_append(q, k, v, positions, table, k_cache, v_cache, slots, interleaved, out)
+PyObject *rope_append(PyObject *, PyObject *const *v, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 10)) return nullptr;
+    const Tensor &q = *tensor(v[0], "q"), &k = *tensor(v[1], "k"), &val = *tensor(v[2], "v");
+    const Tensor &positions = *tensor(v[3], "positions"), &table = *tensor(v[4], "table");
+    const Tensor &kc = *tensor(v[5], "k_cache"), &vc = *tensor(v[6], "v_cache"), &slots = *tensor(v[7], "slots");
+    const Where w = start(q, "q");
+    lora_rope_desc d{};
+    const Tensor *out = tensor(v[9], "out", true);
+    Tensor y = appended(q, k, val, positions, table, kc, vc, slots, out, w, d);
+    if (!flag(v[8], d.interleaved)) return nullptr;
     if (!done(g_rope(&d, w.stream))) return nullptr;
     if (out) written(y);
     written(kc);
@@ -271,14 +284,79 @@ PyObject *rope_append(PyObject *, PyObject *const *v, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// tree_attention(q, k_cache, v_cache, page_table, ctx_lens, node_starts, tree_mask, scale, out)
-PyObject *tree_attention(PyObject *, PyObject *const *v, Py_ssize_t n) {
+// A norm's weight, [head_dim] or [heads, head_dim], or None; its stride from head to head.
+const void *weight_of(const Tensor *t, int64_t heads, int64_t dim, const Where &w, at::ScalarType type, const char *name,
+                      int64_t &stride) {
+    stride = 0;
+    if (!t) return nullptr;
+    same(*t, w, type, name);
+    TORCH_CHECK_VALUE((t->dim() == 1 || (t->dim() == 2 && t->size(0) == heads)) && t->size(-1) == dim, name, " ", t->sizes(),
+                      ": [", dim, "] or [", heads, ", ", dim, "] is needed");
+    unit(*t, t->dim(), name);
+    if (t->dim() == 2) stride = t->stride(0);
+    return t->const_data_ptr();
+}
+
+bool number(PyObject *o, float &value) {
+    value = (float)PyFloat_AsDouble(o);
+    return !PyErr_Occurred();
+}
+
+// norm_rope(x, weight, positions, table, eps, interleaved, out)
+PyObject *norm_rope(PyObject *, PyObject *const *v, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (!arguments(n, 9)) return nullptr;
+    if (!arguments(n, 7)) return nullptr;
+    const Tensor &x = *tensor(v[0], "x"), *weight = tensor(v[1], "weight", true);
+    const Tensor &positions = *tensor(v[2], "positions"), &table = *tensor(v[3], "table");
+    const Where w = start(x, "x");
+    lora_norm_rope_desc d{};
+    const Tensor *out = tensor(v[6], "out", true);
+    Tensor y = rotated(x, positions, table, out, w, d.rope);
+    d.q_weight = weight_of(weight, x.size(1), x.size(2), w, x.scalar_type(), "weight", d.q_weight_head);
+    if (!number(v[4], d.eps) || !flag(v[5], d.rope.interleaved)) return nullptr;
+    if (!done(g_norm(&d, w.stream))) return nullptr;
+    if (out) written(y);
+    return THPVariable_Wrap(std::move(y));
+    END_HANDLE_TH_ERRORS
+}
+
+// norm_rope_append(q, k, v, q_weight, k_weight, positions, table, k_cache, v_cache, slots, eps, interleaved, out)
+PyObject *norm_rope_append(PyObject *, PyObject *const *v, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 13)) return nullptr;
+    const Tensor &q = *tensor(v[0], "q"), &k = *tensor(v[1], "k"), &val = *tensor(v[2], "v");
+    const Tensor *qw = tensor(v[3], "q_weight", true), *kw = tensor(v[4], "k_weight", true);
+    const Tensor &positions = *tensor(v[5], "positions"), &table = *tensor(v[6], "table");
+    const Tensor &kc = *tensor(v[7], "k_cache"), &vc = *tensor(v[8], "v_cache"), &slots = *tensor(v[9], "slots");
+    const Where w = start(q, "q");
+    lora_norm_rope_desc d{};
+    const Tensor *out = tensor(v[12], "out", true);
+    Tensor y = appended(q, k, val, positions, table, kc, vc, slots, out, w, d.rope);
+    d.q_weight = weight_of(qw, q.size(1), q.size(2), w, q.scalar_type(), "q_weight", d.q_weight_head);
+    d.k_weight = weight_of(kw, k.size(1), k.size(2), w, q.scalar_type(), "k_weight", d.k_weight_head);
+    if (!number(v[10], d.eps) || !flag(v[11], d.rope.interleaved)) return nullptr;
+    if (!done(g_norm(&d, w.stream))) return nullptr;
+    if (out) written(y);
+    written(kc);
+    written(vc);
+    return THPVariable_Wrap(std::move(y));
+    END_HANDLE_TH_ERRORS
+}
+
+// What tree_attention and prefix_attention share: v holds q, k_cache, v_cache, and page_table, ctx_lens, node_starts,
+// tree_mask, scale, out from v[table_at] on. The workspace is left to the caller.
+struct Tree {
+    Where w;
+    const Tensor *out;
+    Tensor y, lse;
+};
+
+bool tree_of(PyObject *const *v, int table_at, lora_tree_attention_desc &d, Tree &r) {
     const Tensor &q = *tensor(v[0], "q"), &kc = *tensor(v[1], "k_cache"), &vc = *tensor(v[2], "v_cache");
-    const Tensor &table = *tensor(v[3], "page_table"), &ctx = *tensor(v[4], "ctx_lens");
-    const Tensor &starts = *tensor(v[5], "node_starts");
-    const Tensor *mask = tensor(v[6], "tree_mask", true), *out = tensor(v[8], "out", true);
+    v += table_at;
+    const Tensor &table = *tensor(v[0], "page_table"), &ctx = *tensor(v[1], "ctx_lens");
+    const Tensor &starts = *tensor(v[2], "node_starts");
+    const Tensor *mask = tensor(v[3], "tree_mask", true), *out = tensor(v[5], "out", true);
     const Where w = start(q, "q");
     const auto type = q.scalar_type();
     same(q, w, type, "q");
@@ -294,7 +372,6 @@ PyObject *tree_attention(PyObject *, PyObject *const *v, Py_ssize_t n) {
     const int64_t requests = ctx.size(0), tokens = q.size(0);
     TORCH_CHECK_VALUE(table.size(0) == requests && starts.size(0) == requests + 1, "page_table ", table.sizes(),
                       ", ctx_lens ", ctx.sizes(), ", node_starts ", starts.sizes(), " do not fit");
-    lora_tree_attention_desc d{};
     if (mask) {
         same(*mask, w, at::kLong, "tree_mask");
         whole(*mask, 2, "tree_mask");
@@ -303,12 +380,10 @@ PyObject *tree_attention(PyObject *, PyObject *const *v, Py_ssize_t n) {
         d.tree_mask = static_cast<const uint64_t *>(mask->const_data_ptr());
         d.mask_words = count(mask->size(1), "mask words");
     }
-    if (v[7] == Py_None) {
+    if (v[4] == Py_None)
         d.scale = q.size(2) > 0 ? 1.0f / std::sqrt((float)q.size(2)) : 1.0f;
-    } else {
-        d.scale = (float)PyFloat_AsDouble(v[7]);
-        if (PyErr_Occurred()) return nullptr;
-    }
+    else if (!number(v[4], d.scale))
+        return false;
     d.n_requests = count(requests, "requests");
     d.n_tokens = count(tokens, "tokens");
     d.n_heads = count(q.size(1), "heads");
@@ -318,9 +393,6 @@ PyObject *tree_attention(PyObject *, PyObject *const *v, Py_ssize_t n) {
     Tensor y = output(out, q.sizes(), type, w);
     const int64_t lse_size[] = {tokens, q.size(1)};
     Tensor lse = fresh(lse_size, at::kFloat, w);
-    const size_t bytes = g_tree_bytes(d.n_requests, d.n_tokens, d.n_heads, d.n_kv_heads, d.head_dim, d.dtype);
-    const int64_t ws_size[] = {(int64_t)bytes};
-    Tensor ws = fresh(ws_size, at::kByte, w);
     d.q = q.const_data_ptr();
     d.q_token = q.stride(0);
     d.q_head = q.stride(1);
@@ -340,11 +412,108 @@ PyObject *tree_attention(PyObject *, PyObject *const *v, Py_ssize_t n) {
     d.out_token = y.stride(0);
     d.out_head = y.stride(1);
     d.lse = static_cast<float *>(lse.mutable_data_ptr());
+    r = {w, out, std::move(y), std::move(lse)};
+    return true;
+}
+
+Tensor workspace(size_t bytes, lora_tree_attention_desc &d, const Where &w) {
+    const int64_t size[] = {(int64_t)bytes};
+    Tensor ws = fresh(size, at::kByte, w);
     d.workspace = ws.mutable_data_ptr();
     d.workspace_bytes = bytes;
-    if (!done(g_tree(&d, w.stream))) return nullptr;
-    if (out) written(y);
-    PyObject *a = THPVariable_Wrap(std::move(y)), *b = THPVariable_Wrap(std::move(lse));
+    return ws;
+}
+
+PyObject *results(Tree &r) {
+    if (r.out) written(r.y);
+    PyObject *a = THPVariable_Wrap(std::move(r.y)), *b = THPVariable_Wrap(std::move(r.lse));
+    return a && b ? Py_BuildValue("(NN)", a, b) : nullptr;
+}
+
+// tree_attention(q, k_cache, v_cache, page_table, ctx_lens, node_starts, tree_mask, scale, out)
+PyObject *tree_attention(PyObject *, PyObject *const *v, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 9)) return nullptr;
+    lora_tree_attention_desc d{};
+    Tree r{{c10::Device(c10::kCPU), 0, nullptr}, nullptr, {}, {}};
+    if (!tree_of(v, 3, d, r)) return nullptr;
+    const Tensor ws = workspace(g_tree_bytes(d.n_requests, d.n_tokens, d.n_heads, d.n_kv_heads, d.head_dim, d.dtype), d, r.w);
+    if (!done(g_tree(&d, r.w.stream))) return nullptr;
+    return results(r);
+    END_HANDLE_TH_ERRORS
+}
+
+// prefix_attention(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, page_table, ctx_lens, node_starts,
+// tree_mask, scale, out)
+PyObject *prefix_attention(PyObject *, PyObject *const *v, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 12)) return nullptr;
+    lora_prefix_attention_desc d{};
+    Tree r{{c10::Device(c10::kCPU), 0, nullptr}, nullptr, {}, {}};
+    if (!tree_of(v, 6, d.tree, r)) return nullptr;
+    const Tensor &table = *tensor(v[3], "prefix_table"), &lens = *tensor(v[4], "prefix_lens");
+    const Tensor &starts = *tensor(v[5], "group_starts");
+    same(table, r.w, at::kInt, "prefix_table");
+    same(lens, r.w, at::kInt, "prefix_lens");
+    same(starts, r.w, at::kInt, "group_starts");
+    unit(table, 2, "prefix_table");
+    whole(lens, 1, "prefix_lens");
+    whole(starts, 1, "group_starts");
+    TORCH_CHECK_VALUE(table.size(0) == lens.size(0) && starts.size(0) == lens.size(0) + 1, "prefix_table ", table.sizes(),
+                      ", prefix_lens ", lens.sizes(), ", group_starts ", starts.sizes(), " do not fit");
+    d.prefix_table = static_cast<const int32_t *>(table.const_data_ptr());
+    d.prefix_stride = table.stride(0);
+    d.prefix_pages = count(table.size(1), "prefix_table columns");
+    d.prefix_lens = static_cast<const int32_t *>(lens.const_data_ptr());
+    d.group_starts = static_cast<const int32_t *>(starts.const_data_ptr());
+    d.n_groups = count(lens.size(0), "groups");
+    const auto &t = d.tree;
+    const Tensor ws = workspace(g_prefix_bytes(t.n_requests, d.n_groups, t.n_tokens, t.n_heads, t.n_kv_heads, t.head_dim,
+                                               t.dtype), d.tree, r.w);
+    if (!done(g_prefix(&d, r.w.stream))) return nullptr;
+    return results(r);
+    END_HANDLE_TH_ERRORS
+}
+
+// sample_tokens(logits, noise, temperature, top_k, top_p, min_p)
+PyObject *sample_tokens(PyObject *, PyObject *const *v, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 6)) return nullptr;
+    const Tensor &logits = *tensor(v[0], "logits"), &noise = *tensor(v[1], "noise");
+    const Where w = start(logits, "logits");
+    same(logits, w, logits.scalar_type(), "logits");
+    unit(logits, 2, "logits");
+    same(noise, w, at::kFloat, "noise");
+    unit(noise, 2, "noise");
+    TORCH_CHECK_VALUE(noise.sizes() == logits.sizes(), "noise ", noise.sizes(), ": logits' shape ", logits.sizes(),
+                      " is needed");
+    const int64_t rows = logits.size(0), each[] = {rows};
+    auto value = [&](PyObject *o, at::ScalarType type, const char *name) -> const void * {
+        const Tensor *t = tensor(o, name, true);
+        if (!t) return nullptr;
+        same(*t, w, type, name);
+        whole(*t, 1, name);
+        TORCH_CHECK_VALUE(t->size(0) == rows, name, " holds ", t->size(0), " values: one for each of ", rows,
+                          " rows is needed");
+        return t->const_data_ptr();
+    };
+    lora_sample_desc d{};
+    d.temperature = static_cast<const float *>(value(v[2], at::kFloat, "temperature"));
+    d.top_k = static_cast<const int32_t *>(value(v[3], at::kInt, "top_k"));
+    d.top_p = static_cast<const float *>(value(v[4], at::kFloat, "top_p"));
+    d.min_p = static_cast<const float *>(value(v[5], at::kFloat, "min_p"));
+    Tensor tokens = fresh(each, at::kInt, w), logprobs = fresh(each, at::kFloat, w);
+    d.logits = logits.const_data_ptr();
+    d.logits_row = logits.stride(0);
+    d.noise = static_cast<const float *>(noise.const_data_ptr());
+    d.noise_row = noise.stride(0);
+    d.tokens = static_cast<int32_t *>(tokens.mutable_data_ptr());
+    d.logprobs = static_cast<float *>(logprobs.mutable_data_ptr());
+    d.n_rows = count(rows, "rows");
+    d.vocab = count(logits.size(1), "vocab");
+    d.dtype = w.dtype;
+    if (!done(g_sample(&d, w.stream))) return nullptr;
+    PyObject *a = THPVariable_Wrap(std::move(tokens)), *b = THPVariable_Wrap(std::move(logprobs));
     return a && b ? Py_BuildValue("(NN)", a, b) : nullptr;
     END_HANDLE_TH_ERRORS
 }
@@ -414,11 +583,13 @@ PyObject *verify_drafts(PyObject *, PyObject *const *v, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// bind(base_linear, rope, tree_attention, tree_attention_workspace_bytes, verify_drafts addresses, raise)
+// bind(the addresses of base_linear, rope, tree_attention, tree_attention_workspace_bytes, verify_drafts, norm_rope,
+// prefix_attention, prefix_attention_workspace_bytes, sample_tokens; raise)
 PyObject *bind(PyObject *, PyObject *const *v, Py_ssize_t n) {
-    if (!arguments(n, 6)) return nullptr;
-    void *p[5];
-    for (int i = 0; i < 5; ++i) {
+    constexpr int kCalls = 9;
+    if (!arguments(n, kCalls + 1)) return nullptr;
+    void *p[kCalls];
+    for (int i = 0; i < kCalls; ++i) {
         p[i] = PyLong_AsVoidPtr(v[i]);
         if (!p[i]) return PyErr_Occurred() ? nullptr : PyErr_Format(PyExc_ValueError, "address %d is NULL", i);
     }
@@ -427,15 +598,21 @@ PyObject *bind(PyObject *, PyObject *const *v, Py_ssize_t n) {
     g_tree = reinterpret_cast<decltype(g_tree)>(p[2]);
     g_tree_bytes = reinterpret_cast<decltype(g_tree_bytes)>(p[3]);
     g_verify = reinterpret_cast<decltype(g_verify)>(p[4]);
-    Py_INCREF(v[5]);
+    g_norm = reinterpret_cast<decltype(g_norm)>(p[5]);
+    g_prefix = reinterpret_cast<decltype(g_prefix)>(p[6]);
+    g_prefix_bytes = reinterpret_cast<decltype(g_prefix_bytes)>(p[7]);
+    g_sample = reinterpret_cast<decltype(g_sample)>(p[8]);
+    Py_INCREF(v[kCalls]);
     Py_XDECREF(g_raise);
-    g_raise = v[5];
+    g_raise = v[kCalls];
     Py_RETURN_NONE;
 }
 
 #define CALL(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {CALL(bind),           CALL(base_linear),    CALL(rope), CALL(rope_append),
-                         CALL(tree_attention), CALL(verify_drafts), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {CALL(bind),           CALL(base_linear),      CALL(rope),
+                         CALL(rope_append),    CALL(norm_rope),        CALL(norm_rope_append),
+                         CALL(tree_attention), CALL(prefix_attention), CALL(sample_tokens),
+                         CALL(verify_drafts),  {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -40,7 +40,7 @@ struct Tile {
     static constexpr int kStart = kValid + kRing * 8, kSmem = kStart + (kScratch + kThreads / 32) * 8;
 };
 
-template <int DP, int WM, int WN>
+template <int DP, int WM, int WN, bool kPrefix>
 __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan plan) {
     using T = Tile<DP, WM, WN>;
     constexpr int kPieces = DP / 8;                     // 16-byte pieces of a row
@@ -54,16 +54,16 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
 
     grid_dependency_wait();
     grid_launch_dependents();                            // the join kernel waits for this grid's end itself
-    if (tid == 0) plan.seg[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (!kPrefix && tid == 0) plan.seg[blockIdx.x] = make_int4(0, 0, 0, 0);
     Share share;
-    if (!find_share<T::kThreads>(a, T::M, scratch, share)) return;
+    if (!find_share<T::kThreads, kPrefix>(a, T::M, scratch, share)) return;
     Cursor load = share.start;
     Cursor c = load;                                     // the tile being computed; `load` runs ahead of it
     Cursor look = load;                                  // the tile whose page ids are being read: one further ahead
     const int n_tiles = (int)(share.hi - share.lo);
 
     // Offsets of tile i's keys: read into a register by threads 0..63, stored to the ring at the end of the step.
-    auto read_off = [&](const Cursor &u) -> long long { return tid < kTileKeys ? key_offset(a, u, tid) : -1; };
+    auto read_off = [&](const Cursor &u) -> long long { return tid < kTileKeys ? key_offset<kPrefix>(a, u, tid) : -1; };
     auto store_off = [&](int i, long long off) {
         if (tid >= kTileKeys) return;
         offs[i % T::kRing * kTileKeys + tid] = off;
@@ -92,14 +92,14 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
     for (int i = 0; i < kStages - 1; ++i) {
         if (i < n_tiles) {
             store_off(i, read_off(look));
-            next_tile(a, look, T::M);
+            next_tile<kPrefix>(a, look, T::M);
         }
     }
     __syncthreads();
     for (int i = 0; i < kStages - 1; ++i) {
         if (i < n_tiles) {
             issue(i, load);
-            next_tile(a, load, T::M);
+            next_tile<kPrefix>(a, load, T::M);
         }
         cp_async_commit();
     }
@@ -145,8 +145,8 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
         __syncthreads();                                 // tile i is here, and everyone is done with tile i - 1
         if (i + kStages - 1 < n_tiles) {
             issue(i + kStages - 1, load);
-            next_tile(a, load, T::M);
-            next_tile(a, look, T::M);
+            next_tile<kPrefix>(a, load, T::M);
+            next_tile<kPrefix>(a, look, T::M);
         }
         cp_async_commit();
         if (i + kStages < n_tiles) pending = read_off(look);
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
                     const int r = wm * 16 + g4 + hrow * 8;
                     const int row = c.row_tile * T::M + r, node = row / group;
                     if (node >= c.r.nodes) continue;
-                    if (starts && ends) {
+                    if (!kPrefix && starts && ends) {
                         const long long token = c.r.start + node;
                         const int head = c.head * group + row % group;
                         const float inv = l[hrow] > 0.f ? 1.f / l[hrow] : l[hrow];
@@ -346,21 +346,27 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
                     } else {
                         const long long slot = 2ll * blockIdx.x + (starts ? 1 : 0);
                         float *part = plan.part + (slot * T::M + r) * DP;
+                        float2 *stat = plan.stat + slot * T::M + r;
+                        if constexpr (kPrefix) {
+                            const size_t at = row_index(a, c, c.r.start + node, c.head * group + row % group);
+                            if (starts && ends) part = a.row_o + at * DP, stat = a.row_ml + at;
+                            if (starts && t4 == 0) name_parts(a, at, ends ? 0 : parts_of(share, c, i), r);
+                        }
 #pragma unroll
                         for (int d = 0; d < DP / 8; ++d)
                             *reinterpret_cast<float2 *>(part + d * 8 + t4 * 2) =
                                 make_float2(o[d][hrow * 2], o[d][hrow * 2 + 1]);
-                        if (t4 == 0) plan.stat[slot * T::M + r] = make_float2(m[hrow], l[hrow]);
+                        if (t4 == 0) *stat = make_float2(m[hrow], l[hrow]);
                     }
                 }
             }
-            if (tid == 0 && starts && !ends) {
+            if (!kPrefix && tid == 0 && starts && !ends) {
                 plan.seg[blockIdx.x] = make_int4(c.b, c.row_tile, c.head, parts_of(share, c, i));
             }
             fresh = true;
         }
         if (i + kStages < n_tiles) store_off(i + kStages, pending);
-        next_tile(a, c, T::M);
+        next_tile<kPrefix>(a, c, T::M);
     }
 }
 
@@ -372,41 +378,6 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
 // 13.0 / 12.6 / 13.8). (One row to a warp and four: 1x8 ctx 777 12.7 and 16.0 us,
 // 32x16 ctx 4096 89.4 and 89.0. 38 parts, 1x6 ctx 3000: 24.5 us row after row, 17.6
 // so.)
-template <int DP>
-struct Joined {
-    static constexpr int V = DP / 32;                    // columns of a lane
-    float o[V], m = -INFINITY, l = 0.f;
-    __device__ __forceinline__ void add(float2 ml, const float (&v)[V]) {
-        const float t = fmaxf(m, ml.x), b = t == -INFINITY ? 0.f : t;
-        const float f = exp2_fast(m - b), h = exp2_fast(ml.x - b);
-        m = t;
-        l = l * f + ml.y * h;
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = o[e] * f + v[e] * h;
-    }
-};
-
-template <typename T, int DP>
-__device__ __forceinline__ void store_joined(const TreeArgs &a, const int4 &seg, int start, int row, const Joined<DP> &j) {
-    constexpr int V = Joined<DP>::V;
-    const int lane = threadIdx.x & 31, group = a.n_heads / a.n_kv, head = seg.z * group + row % group;
-    const long long token = start + row / group;
-    const bool none = j.l == 0.f;                        // m is -inf for a row of NaN scores, too
-    const float inv = j.l > 0.f ? 1.f / j.l : j.l;       // a NaN stays one
-    T *out = static_cast<T *>(a.out) + token * a.o_token + (long long)head * a.o_head + lane * V;
-    if (lane * V < a.head_dim) {
-#pragma unroll
-        for (int e = 0; e < V; e += 2) {
-            const float x = none ? 0.f : j.o[e] * inv, y = none ? 0.f : j.o[e + 1] * inv;
-            if constexpr (sizeof(T) == 2)
-                *reinterpret_cast<uint32_t *>(out + e) = pack_bf16(x, y);
-            else
-                *reinterpret_cast<float2 *>(out + e) = make_float2(x, y);
-        }
-    }
-    if (a.lse && lane == 0) a.lse[token * a.n_heads + head] = none ? -INFINITY : j.m * 0.6931471805599453f + logf(j.l);
-}
-
 template <typename T, int DP, int M, int kR>
 __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan, int m_rows) {
     constexpr int V = Joined<DP>::V, kAhead = kR == 1 ? 8 : 2, kMany = 24, kShared = kR == 1 ? 8 : 1;
@@ -419,6 +390,9 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan, i
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = a.n_heads / a.n_kv;
     const int start = node_start(a, seg.x);
     const int rows = min((node_start(a, seg.x + 1) - start) * group - seg.y * m_rows, m_rows);
+    auto store = [&](int row, const Joined<DP> &j) {
+        store_joined<T, DP>(a, start + row / group, seg.z * group + row % group, j);
+    };
     auto read = [&](int part, int r, float2 &ml, float (&v)[V]) {
         const long long slot = part == 0 ? 2ll * blockIdx.x + 1 : 2ll * (blockIdx.x + part);
         ml = plan.stat[slot * M + r];
@@ -465,7 +439,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan, i
                 for (int e = 0; e < V; ++e) v[e] = so[w][warp][lane * V + e];
                 all.add(sm[w][warp], v);
             }
-            store_joined<T, DP>(a, seg, start, seg.y * m_rows + r0 + warp, all);
+            store(seg.y * m_rows + r0 + warp, all);
             return;
         }
     }
@@ -492,31 +466,13 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan, i
     }
 #pragma unroll
     for (int k = 0; k < kR; ++k)
-        if (r0 + k < rows) store_joined<T, DP>(a, seg, start, seg.y * m_rows + r0 + k, j[k]);
+        if (r0 + k < rows) store(seg.y * m_rows + r0 + k, j[k]);
 }
 
-constexpr int kMaxRows = 128;
-constexpr int kMaxCtas = 2 * 160;
-
-// The row tile by the average rows (nodes times query heads of a key/value head) of a request: how they are spread over
-// the requests only the device knows, so one wide tree among many single nodes goes in many small tiles (64 requests, ctx
-// 4096, 32 heads over 8: all of one node 176 us, one of them of 64 nodes 234). Measured with equal requests: 8, ctx 4096,
-// 32 heads over 8, tiles of 16 / 32 / 128 rows: 8 rows 34.6 / 35.4 / 35.6 us, 16 rows 36.0 / 36.3 / 35.5, 24 rows 45.1 /
-// 38.0 / 36.8, 32 rows 45.5 / 38.2 / 37.4, 48 rows 58.9 / 50.9 / 38.9, 128 rows 119 / 80 / 47. For few keys 32 beats 128
-// up to 32 rows: 1x8 ctx 777 12.7 and 14.8, 4x8 ctx 500 13.6 and 17.7.
-int rows_of_tile(const TreeArgs &a) {
-    const double rows = (double)a.n_tokens * (a.n_heads / a.n_kv) / a.n_requests;
-    return rows <= 16.0 ? 16 : rows <= 32.0 || !tc_takes(a) ? 32 : 128;
-}
-
-size_t plan_bytes(int ctas) {
-    return (size_t)ctas * sizeof(int4) + 2 * (size_t)ctas * kMaxRows * (128 * sizeof(float) + sizeof(float2));
-}
-
-template <int DP, int WM>
+template <int DP, int WM, bool kPrefix>
 cudaError_t launch_tiles(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
     using T = Tile<DP, WM, 4 / WM>;
-    auto kernel = tree_tiles_kernel<DP, WM, 4 / WM>;
+    auto kernel = tree_tiles_kernel<DP, WM, 4 / WM, kPrefix>;
     static std::atomic<uint64_t> ready{0};
     if (!device_bit(ready)) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
@@ -539,19 +495,15 @@ cudaError_t launch_join(const TreeArgs &a, const Plan &plan, int m_rows, cudaStr
 
 template <int DP>
 cudaError_t launch_bf16(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
-    const int rows = rows_of_tile(a);
-    cudaError_t e = cudaErrorNotSupported;
+    const int rows = rows_of_tile((double)a.n_tokens * (a.n_heads / a.n_kv) / a.n_requests, tc_takes(a));
     if (rows == 128) {
-        e = launch_tc(a, plan, st);
+        const cudaError_t e = launch_tc(a, plan, st);
         if (e == cudaSuccess) return launch_join<__nv_bfloat16, DP, 128>(a, plan, tc_rows(a), st);
+        if (e != cudaErrorNotSupported) return e;
     }
-    if (rows == 16) {
-        e = launch_tiles<DP, 1>(a, plan, st);
-        return e != cudaSuccess ? e : launch_join<__nv_bfloat16, DP, 16>(a, plan, 16, st);
-    }
-    if (e != cudaErrorNotSupported) return e;
-    e = launch_tiles<DP, 2>(a, plan, st);
-    return e != cudaSuccess ? e : launch_join<__nv_bfloat16, DP, 32>(a, plan, 32, st);
+    const cudaError_t e = launch_mma(a, plan, rows == 16 ? 16 : 32, st);
+    if (e != cudaSuccess) return e;
+    return rows == 16 ? launch_join<__nv_bfloat16, DP, 16>(a, plan, 16, st) : launch_join<__nv_bfloat16, DP, 32>(a, plan, 32, st);
 }
 
 template <int DP>
@@ -564,43 +516,73 @@ cudaError_t launch_fp32(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
     return rows == 16 ? launch_join<float, DP, 16>(a, plan, 16, st) : launch_join<float, DP, 64>(a, plan, 64, st);
 }
 
+}  // namespace
+
+namespace tree {
+
 bool shape_ok(int n_requests, int n_tokens, int n_heads, int n_kv, int head_dim, int dtype) {
     return known_dtype(dtype) && n_requests >= 0 && n_tokens >= 0 && n_heads >= 1 && n_heads <= 65535 && n_kv >= 1 &&
            n_heads % n_kv == 0 && head_dim >= 8 && head_dim <= 128 && head_dim % 8 == 0;
 }
 
-}  // namespace
-}  // namespace lora
-
-using namespace lora;
-using namespace lora::step;
-
-extern "C" size_t lora_tree_attention_workspace_bytes(int n_requests, int n_tokens, int n_heads, int n_kv_heads,
-                                                      int head_dim, int dtype) {
-    if (!shape_ok(n_requests, n_tokens, n_heads, n_kv_heads, head_dim, dtype)) return 0;
-    // the largest grid of any GPU this library is built for: the size does not depend on the device
-    return plan_bytes(kMaxCtas);
+size_t plan_bytes() {
+    // of the largest grid of any GPU this library is built for: the size does not depend on the device
+    return (size_t)kMaxCtas * sizeof(int4) + 2 * (size_t)kMaxCtas * kMaxRows * (128 * sizeof(float) + sizeof(float2));
 }
 
-extern "C" int lora_tree_attention(const lora_tree_attention_desc *d, void *stream) {
-    if (!d) return fail(LORA_ERR_ARG, "tree_attention: NULL descriptor");
+int grid_of_device() {
+    const int sms = sm_count();
+    return sms < 1 ? 0 : std::min(std::max(2 * sms, 64), kMaxCtas);    // 64: a group of every class fits
+}
+
+Plan plan_at(void *workspace, int ctas) {
+    Plan plan;
+    plan.ctas = ctas;
+    plan.part = static_cast<float *>(workspace);
+    plan.stat = reinterpret_cast<float2 *>(plan.part + 2 * (size_t)ctas * kMaxRows * 128);
+    plan.seg = reinterpret_cast<int4 *>(plan.stat + 2 * (size_t)ctas * kMaxRows);
+    return plan;
+}
+
+// The row tile by the average rows (nodes times query heads of a key/value head) of a request: how they are spread over
+// the requests only the device knows, so one wide tree among many single nodes goes in many small tiles (64 requests, ctx
+// 4096, 32 heads over 8: all of one node 176 us, one of them of 64 nodes 234). Measured with equal requests: 8, ctx 4096,
+// 32 heads over 8, tiles of 16 / 32 / 128 rows: 8 rows 34.6 / 35.4 / 35.6 us, 16 rows 36.0 / 36.3 / 35.5, 24 rows 45.1 /
+// 38.0 / 36.8, 32 rows 45.5 / 38.2 / 37.4, 48 rows 58.9 / 50.9 / 38.9, 128 rows 119 / 80 / 47. For few keys 32 beats 128
+// up to 32 rows: 1x8 ctx 777 12.7 and 14.8, 4x8 ctx 500 13.6 and 17.7.
+int rows_of_tile(double rows, bool wide) { return rows <= 16.0 ? 16 : rows <= 32.0 || !wide ? 32 : 128; }
+
+
+cudaError_t launch_mma(const TreeArgs &a, const Plan &plan, int m_rows, cudaStream_t st) {
+    const bool prefix = a.row_o != nullptr;
+    if (a.head_dim <= 64) {
+        if (m_rows == 16) return prefix ? launch_tiles<64, 1, true>(a, plan, st) : launch_tiles<64, 1, false>(a, plan, st);
+        return prefix ? launch_tiles<64, 2, true>(a, plan, st) : launch_tiles<64, 2, false>(a, plan, st);
+    }
+    if (m_rows == 16) return prefix ? launch_tiles<128, 1, true>(a, plan, st) : launch_tiles<128, 1, false>(a, plan, st);
+    return prefix ? launch_tiles<128, 2, true>(a, plan, st) : launch_tiles<128, 2, false>(a, plan, st);
+}
+
+int check(const lora_tree_attention_desc *d, const char *name, size_t need, bool *nothing) {
+    *nothing = false;
     if (!shape_ok(d->n_requests, d->n_tokens, d->n_heads, d->n_kv_heads, d->head_dim, d->dtype))
         return fail(LORA_ERR_ARG,
-                    "tree_attention: dtype %d, n_requests %d, n_tokens %d, n_heads %d (a multiple of n_kv_heads %d), "
+                    "%s: dtype %d, n_requests %d, n_tokens %d, n_heads %d (a multiple of n_kv_heads %d), "
                     "head_dim %d (a multiple of 8, 8..128)",
-                    d->dtype, d->n_requests, d->n_tokens, d->n_heads, d->n_kv_heads, d->head_dim);
+                    name, d->dtype, d->n_requests, d->n_tokens, d->n_heads, d->n_kv_heads, d->head_dim);
     if (d->page_size < 1 || d->table_pages < 0 || d->n_pages < 0 || d->mask_words < 0)
-        return fail(LORA_ERR_ARG, "tree_attention: page_size %d, table_pages %d, n_pages %lld, mask_words %d",
-                    d->page_size, d->table_pages, (long long)d->n_pages, d->mask_words);
+        return fail(LORA_ERR_ARG, "%s: page_size %d, table_pages %d, n_pages %lld, mask_words %d",
+                    name, d->page_size, d->table_pages, (long long)d->n_pages, d->mask_words);
     if ((long long)d->n_tokens * d->n_heads > (1 << 30))
-        return fail(LORA_ERR_ARG, "tree_attention: n_tokens %d times n_heads %d is above 2^30", d->n_tokens,
+        return fail(LORA_ERR_ARG, "%s: n_tokens %d times n_heads %d is above 2^30", name, d->n_tokens,
                     d->n_heads);
-    if (!std::isfinite(d->scale)) return fail(LORA_ERR_ARG, "tree_attention: scale is not finite");
-    if (d->n_tokens == 0 || d->n_requests == 0) return LORA_OK;
+    if (!std::isfinite(d->scale)) return fail(LORA_ERR_ARG, "%s: scale is not finite", name);
+    *nothing = d->n_tokens == 0 || d->n_requests == 0;
+    if (*nothing) return LORA_OK;
     if (!d->q || !d->out || !d->ctx_lens || !d->node_starts || (d->table_pages > 0 && !d->page_table) ||
         (d->n_pages > 0 && (!d->k_cache || !d->v_cache)))
-        return fail(LORA_ERR_ARG, "tree_attention: NULL pointer argument");
-    if (d->tree_mask && d->mask_words == 0) return fail(LORA_ERR_ARG, "tree_attention: mask_words is 0");
+        return fail(LORA_ERR_ARG, "%s: NULL pointer argument", name);
+    if (d->tree_mask && d->mask_words == 0) return fail(LORA_ERR_ARG, "%s: mask_words is 0", name);
     const long long eb = d->dtype == LORA_DTYPE_F32 ? 4 : 2;
     const long long strides[] = {(long long)d->q_token,   (long long)d->q_head,     (long long)d->cache_page,
                                  (long long)d->cache_slot, (long long)d->cache_head, (long long)d->out_token,
@@ -608,27 +590,45 @@ extern "C" int lora_tree_attention(const lora_tree_attention_desc *d, void *stre
     bool ok = aligned16(d->q) && aligned16(d->out) && aligned16(d->k_cache) && aligned16(d->v_cache);
     for (long long s : strides) ok = ok && s >= 0 && s * eb % 16 == 0;
     if (!ok)
-        return fail(LORA_ERR_ARG, "tree_attention: q, out and cache pointers and strides must be multiples of 16 bytes, "
-                                  "no stride negative");
+        return fail(LORA_ERR_ARG, "%s: q, out and cache pointers and strides must be multiples of 16 bytes, "
+                                  "no stride negative",
+                    name);
     if (!rows_apart(d->n_tokens, d->out_token, d->n_heads, d->out_head, d->head_dim))
-        return fail(LORA_ERR_ARG, "tree_attention: the rows of out overlap (strides %lld, %lld)", (long long)d->out_token,
+        return fail(LORA_ERR_ARG, "%s: the rows of out overlap (strides %lld, %lld)", name, (long long)d->out_token,
                     (long long)d->out_head);
-    const size_t need = lora_tree_attention_workspace_bytes(d->n_requests, d->n_tokens, d->n_heads, d->n_kv_heads,
-                                                            d->head_dim, d->dtype);
     if (!d->workspace || d->workspace_bytes < need || reinterpret_cast<uintptr_t>(d->workspace) % 256)
-        return fail(LORA_ERR_ARG, "tree_attention: workspace of %zu bytes, 256-byte aligned, is needed", need);
-    TreeArgs a{d->q,       d->k_cache,   d->v_cache,   d->out,       d->lse,       d->page_table, d->ctx_lens,
+        return fail(LORA_ERR_ARG, "%s: workspace of %zu bytes, 256-byte aligned, is needed", name, need);
+    return LORA_OK;
+}
+
+TreeArgs arguments(const lora_tree_attention_desc *d) {
+    return {d->q,       d->k_cache,   d->v_cache,   d->out,       d->lse,       d->page_table, d->ctx_lens,
                d->node_starts, d->tree_mask, d->q_token, d->q_head,  d->cache_page, d->cache_slot, d->cache_head,
                d->out_token, d->out_head, d->table_stride, d->n_pages, d->scale,   d->page_size,  d->table_pages,
                d->mask_words, d->n_requests, d->n_tokens, d->n_heads, d->n_kv_heads, d->head_dim};
+}
+
+}  // namespace tree
+}  // namespace lora
+
+using namespace lora;
+using namespace lora::step;
+
+extern "C" size_t lora_tree_attention_workspace_bytes(int n_requests, int n_tokens, int n_heads, int n_kv_heads,
+                                                      int head_dim, int dtype) {
+    return tree::shape_ok(n_requests, n_tokens, n_heads, n_kv_heads, head_dim, dtype) ? tree::plan_bytes() : 0;
+}
+
+extern "C" int lora_tree_attention(const lora_tree_attention_desc *d, void *stream) {
+    if (!d) return fail(LORA_ERR_ARG, "tree_attention: NULL descriptor");
+    bool nothing;
+    const int rc = tree::check(d, "tree_attention", tree::plan_bytes(), &nothing);
+    if (rc != LORA_OK || nothing) return rc;
+    const TreeArgs a = tree::arguments(d);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int sms = sm_count();
-    if (sms < 1) return fail(LORA_ERR_CUDA, "tree_attention: no CUDA device");
-    Plan plan;
-    plan.ctas = std::min(std::max(2 * sms, 64), kMaxCtas);          // 64: a group of every class fits
-    plan.part = static_cast<float *>(d->workspace);
-    plan.stat = reinterpret_cast<float2 *>(plan.part + 2 * (size_t)plan.ctas * kMaxRows * 128);
-    plan.seg = reinterpret_cast<int4 *>(plan.stat + 2 * (size_t)plan.ctas * kMaxRows);
+    const int ctas = tree::grid_of_device();
+    if (ctas < 1) return fail(LORA_ERR_CUDA, "tree_attention: no CUDA device");
+    const Plan plan = tree::plan_at(d->workspace, ctas);
     cudaError_t e;
     if (d->dtype == LORA_DTYPE_BF16)
         e = d->head_dim <= 64 ? launch_bf16<64>(a, plan, st) : launch_bf16<128>(a, plan, st);

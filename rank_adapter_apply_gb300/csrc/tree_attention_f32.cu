@@ -1,4 +1,4 @@
-// lora_tree_attention in fp32: tiles of M rows and 64 keys on the FMA units.
+// lora_tree_attention and lora_prefix_attention in fp32: tiles of M rows and 64 keys on the FMA units.
 //
 // 128 threads; a half-warp (16 lanes) owns M / 8 rows. Scores: a lane has those rows
 // against keys lane, lane + 16, + 32, + 48, so a row's maximum and sum are a
@@ -29,7 +29,7 @@ struct F32 {
     static constexpr int kSmem = (M * kRow + kKeys + kTileKeys * DP) * 4;
 };
 
-template <int DP, int M>
+template <int DP, int M, bool kPrefix>
 __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(TreeArgs a, Plan plan) {
     using T = F32<DP, M>;
     constexpr int R = T::R, C = T::C, kPieces = DP / 4;
@@ -41,9 +41,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(TreeArgs a, Plan 
     const int group = a.n_heads / a.n_kv, row0 = half * R;     // this half-warp's rows of the tile
     grid_dependency_wait();
     grid_launch_dependents();                                  // the join kernel waits for this grid's end itself
-    if (tid == 0) plan.seg[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (!kPrefix && tid == 0) plan.seg[blockIdx.x] = make_int4(0, 0, 0, 0);
     Share share;
-    if (!find_share<kThreads>(a, M, scratch, share)) return;
+    if (!find_share<kThreads, kPrefix>(a, M, scratch, share)) return;
     Cursor c = share.start;
     const int n_tiles = (int)(share.hi - share.lo);
     const float c2 = a.scale * 1.4426950408889634f;            // scores in powers of two
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(TreeArgs a, Plan 
         const bool first = i == 0 || c.tile == 0;
         __syncthreads();                                       // everyone is done with the tile before
         if (tid < kTileKeys) {
-            const long long off = key_offset(a, c, tid);
+            const long long off = key_offset<kPrefix>(a, c, tid);
             offs[tid] = off;
             const uint32_t ok = __ballot_sync(0xffffffffu, off >= 0);
             if (lane == 0) valid[warp] = ok;
@@ -197,10 +197,16 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(TreeArgs a, Plan 
                 const long long token = c.r.start + node;
                 const int head = c.head * group + row % group;
                 // a row without keys is 0; one whose scores are all NaN also has m = -inf, but its l is NaN
-                const bool none = l[r] == 0.f, done = starts && ends;
+                const bool none = l[r] == 0.f, done = !kPrefix && starts && ends;
                 const float inv = !done ? 1.f : l[r] > 0.f ? 1.f / l[r] : l[r];
                 float *dst = done ? static_cast<float *>(a.out) + token * a.o_token + (long long)head * a.o_head
                                   : plan.part + (slot * M + row0 + r) * DP;
+                float2 *stat = plan.stat + slot * M + row0 + r;
+                if constexpr (kPrefix) {
+                    const size_t at = row_index(a, c, token, head);
+                    if (starts && ends) dst = a.row_o + at * DP, stat = a.row_ml + at;
+                    if (starts && l16 == 0) name_parts(a, at, ends ? 0 : parts_of(share, c, i), row0 + r);
+                }
 #pragma unroll
                 for (int e = 0; e < C; e += 4) {
                     const int col = (e / 4) * 64 + l16 * 4;
@@ -211,22 +217,22 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(TreeArgs a, Plan 
                 }
                 if (l16 == 0) {
                     if (!done)
-                        plan.stat[slot * M + row0 + r] = make_float2(m[r], l[r]);
+                        *stat = make_float2(m[r], l[r]);
                     else if (a.lse)
                         a.lse[token * a.n_heads + head] = none ? -INFINITY : m[r] * 0.6931471805599453f + logf(l[r]);
                 }
             }
-            if (tid == 0 && starts && !ends)
+            if (!kPrefix && tid == 0 && starts && !ends)
                 plan.seg[blockIdx.x] = make_int4(c.b, c.row_tile, c.head, parts_of(share, c, i));
         }
-        next_tile(a, c, M);
+        next_tile<kPrefix>(a, c, M);
     }
 }
 
-template <int DP, int M>
+template <int DP, int M, bool kPrefix>
 cudaError_t launch(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0};
-    auto kernel = tree_f32_kernel<DP, M>;
+    auto kernel = tree_f32_kernel<DP, M, kPrefix>;
     if (!device_bit(ready)) {
         const cudaError_t e =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F32<DP, M>::kSmem);
@@ -236,11 +242,16 @@ cudaError_t launch(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
     return launch_step(kernel, dim3(plan.ctas), dim3(kThreads), F32<DP, M>::kSmem, 1, st, a, plan);
 }
 
+template <int DP, int M>
+cudaError_t launch_call(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
+    return a.row_o ? launch<DP, M, true>(a, plan, st) : launch<DP, M, false>(a, plan, st);
+}
+
 }  // namespace
 
 cudaError_t launch_f32(const TreeArgs &a, const Plan &plan, int m_rows, cudaStream_t st) {
-    if (a.head_dim <= 64) return m_rows == 16 ? launch<64, 16>(a, plan, st) : launch<64, 64>(a, plan, st);
-    return m_rows == 16 ? launch<128, 16>(a, plan, st) : launch<128, 64>(a, plan, st);
+    if (a.head_dim <= 64) return m_rows == 16 ? launch_call<64, 16>(a, plan, st) : launch_call<64, 64>(a, plan, st);
+    return m_rows == 16 ? launch_call<128, 16>(a, plan, st) : launch_call<128, 64>(a, plan, st);
 }
 
 }  // namespace tree

@@ -1,4 +1,4 @@
-// lora_tree_attention, row tiles of 128 on the 5th-generation tensor cores.
+// lora_tree_attention and lora_prefix_attention, row tiles of 128 on the 5th-generation tensor cores.
 //
 // Scores S = Q K^T (128 rows x 64 keys) and O += P V are tcgen05 products with
 // their accumulators in tensor memory; P goes back into S's columns in bf16 and is
@@ -85,6 +85,7 @@ __device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile 
 
 // o[0..31] += the weight times V of every key of tiles first .. c.tile that row
 // `node` sees and whose V row is not finite (columns d .. d + 31).
+template <bool kPrefix>
 __device__ __noinline__ void add_poison(const TreeArgs &a, const Cursor &c, int first, int node, int head, int d, float c2,
                                         float m, float *o) {
     const __nv_bfloat16 *q =
@@ -93,7 +94,7 @@ __device__ __noinline__ void add_poison(const TreeArgs &a, const Cursor &c, int 
     for (at.tile = first; at.tile <= c.tile; ++at.tile) {
         const uint64_t seen = seen_keys(a, c.r, node, at.tile * kTileKeys);
         for (int k = 0; k < kTileKeys; ++k) {
-            const long long off = seen >> k & 1 ? key_offset(a, at, k) : -1;
+            const long long off = seen >> k & 1 ? key_offset<kPrefix>(a, at, k) : -1;
             if (off < 0) continue;
             const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(a.k_cache) + off + (long long)c.head * a.c_head;
             const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.v_cache) + off + (long long)c.head * a.c_head;
@@ -164,7 +165,7 @@ __device__ __forceinline__ bool odd_piece(const uint4 &v) {
              ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u)) & 0x80008000u) != 0;
 }
 
-template <int DP>
+template <int DP, bool kPrefix>
 __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_constant__ TcArgs args) {
     using C = Tc<DP>;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -182,9 +183,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
     const int rows = kRows / group * group;            // of a tile
     grid_dependency_wait();
     grid_launch_dependents();                          // the join kernel waits for this grid's end itself
-    if (tid == 0) plan.seg[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (!kPrefix && tid == 0) plan.seg[blockIdx.x] = make_int4(0, 0, 0, 0);
     Share share;
-    if (!find_share<kThreads>(a, rows, scratch, share)) return;
+    if (!find_share<kThreads, kPrefix>(a, rows, scratch, share)) return;
     const int n_tiles = (int)(share.hi - share.lo);
     if (tid == 0) {
         for (int i = 0; i < kItems; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
         auto read_run = [&](int run) -> Run {
             // unsigned: the run after the last may begin past 2^31
             const uint32_t p = ((uint32_t)run * 32 + lane) * (uint32_t)args.box, at = p / (uint32_t)a.page_size;
-            return {p < (uint32_t)u.r.keys ? a.page_table[u.b * a.table_stride + at] : -1, (int)(p - at * (uint32_t)a.page_size)};
+            return {p < (uint32_t)u.r.keys ? table_row<kPrefix>(a, u.b)[at] : -1, (int)(p - at * (uint32_t)a.page_size)};
         };
         int run_b = -1, run_at = 0;                    // request, and number of the run in use
         Run now{}, ahead{}, head_run{};
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
             }
             if (i > 0 && !load(&args.v, last)) break;
             last = here;
-            next_tile(a, u, rows);
+            next_tile<kPrefix>(a, u, rows);
         }
         if (i == n_tiles) load(&args.v, last);
         // no copy is in flight when the CTA ends
@@ -475,11 +476,17 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
                 if (!together(wait(&pv_done[i & 1], (uint32_t)(i >> 1)))) break;
                 tc::fence_after_sync();
                 // a row without keys is 0; one whose scores are all NaN also has m = -inf, but its l is NaN
-                const bool mine = node < c.r.nodes, none = l == 0.f, done = starts && ends;
+                const bool mine = node < c.r.nodes, none = l == 0.f, done = !kPrefix && starts && ends;
                 const long long token = c.r.start + node, slot = 2ll * blockIdx.x + (starts ? 1 : 0);
                 const float inv = !done ? 1.f : l > 0.f ? 1.f / l : l;
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + token * a.o_token + head * a.o_head;
                 float *part = plan.part + (slot * kRows + tid) * DP;
+                float2 *stat = plan.stat + slot * kRows + tid;
+                if constexpr (kPrefix) {
+                    const size_t at = mine ? row_index(a, c, token, head) : 0;
+                    if (starts && ends) part = a.row_o + at * DP, stat = a.row_ml + at;
+                    if (mine && starts) name_parts(a, at, ends ? 0 : parts_of(share, c, i), tid);
+                }
 #pragma unroll 1
                 for (int d = 0; d < DP; d += 32) {
                     uint32_t o[32];
@@ -488,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
                         float t[32];
 #pragma unroll
                         for (int k = 0; k < 32; ++k) t[k] = __uint_as_float(o[k]);
-                        add_poison(a, c, max(seg_first, min(c.r.ctx, c.r.keys) / kTileKeys), node, head, d, c2, m, t);
+                        add_poison<kPrefix>(a, c, max(seg_first, min(c.r.ctx, c.r.keys) / kTileKeys), node, head, d, c2, m, t);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(t[k]);
                     }
@@ -512,13 +519,13 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
                 }
                 if (mine && done && a.lse)
                     a.lse[token * a.n_heads + head] = none ? -INFINITY : m * 0.6931471805599453f + logf(l);
-                if (mine && !done) plan.stat[slot * kRows + tid] = make_float2(m, l);
-                if (tid == 0 && starts && !ends)
+                if (mine && !done) *stat = make_float2(m, l);
+                if (!kPrefix && tid == 0 && starts && !ends)
                     plan.seg[blockIdx.x] = make_int4(c.b, c.row_tile, c.head, parts_of(share, c, i));
                 tc::fence_before_sync();
             }
             __syncwarp();
-            next_tile(a, c, rows);
+            next_tile<kPrefix>(a, c, rows);
         }
     }
     tc::fence_before_sync();
@@ -550,12 +557,12 @@ int box_of(int page_size) {
     return box;
 }
 
-template <int DP>
+template <int DP, bool kPrefix>
 cudaError_t launch(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
     static std::atomic<uint64_t> ready{0};
     if (!device_bit(ready)) {
         const cudaError_t e =
-            cudaFuncSetAttribute(tree_tc_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<DP>::kSmem);
+            cudaFuncSetAttribute(tree_tc_kernel<DP, kPrefix>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<DP>::kSmem);
         if (e != cudaSuccess) return e;
         set_device_bit(ready);
     }
@@ -577,7 +584,7 @@ cudaError_t launch(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
     if (!encode(&args.q, a.q, 3, q_dims, q_strides, q_box) || !encode(&args.k, a.k_cache, 4, c_dims, c_strides, c_box) ||
         !encode(&args.v, a.v_cache, 4, c_dims, c_strides, c_box))
         return cudaErrorNotSupported;
-    return launch_step(tree_tc_kernel<DP>, dim3(plan.ctas), dim3(kThreads), Tc<DP>::kSmem, 1, st, args);
+    return launch_step(tree_tc_kernel<DP, kPrefix>, dim3(plan.ctas), dim3(kThreads), Tc<DP>::kSmem, 1, st, args);
 }
 
 }  // namespace
@@ -611,7 +618,8 @@ bool tc_takes(const TreeArgs &a) {
 int tc_rows(const TreeArgs &a) { return kRows / (a.n_heads / a.n_kv) * (a.n_heads / a.n_kv); }
 
 cudaError_t launch_tc(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
-    return a.head_dim <= 64 ? launch<64>(a, plan, st) : launch<128>(a, plan, st);
+    if (a.row_o) return a.head_dim <= 64 ? launch<64, true>(a, plan, st) : launch<128, true>(a, plan, st);
+    return a.head_dim <= 64 ? launch<64, false>(a, plan, st) : launch<128, false>(a, plan, st);
 }
 
 }  // namespace tree

@@ -1,5 +1,6 @@
-// Shared by the tensor-core kernels of lora_tree_attention (tree_attention.cu,
-// tree_attention_tc.cu): arguments, the units of work and their split.
+// Shared by the kernels of lora_tree_attention and lora_prefix_attention
+// (tree_attention.cu, tree_attention_tc.cu, tree_attention_f32.cu,
+// prefix_attention.cu): arguments, the units of work and their split.
 #pragma once
 
 #include "step_util.cuh"
@@ -18,6 +19,16 @@ struct TreeArgs {
     long long q_token, q_head, c_page, c_slot, c_head, o_token, o_head, table_stride, n_pages;
     float scale;
     int page_size, table_pages, mask_words, n_requests, n_tokens, n_heads, n_kv, head_dim;
+    // lora_prefix_attention alone. Its work is that of n_groups + n_requests entries: a group's rows are those of its
+    // requests and its keys the prefix; then the requests with their own keys. A launch does `count` of them from `first`
+    // on. Results of a row go to row_o, row_ml (of a group's entry, then of a request's: [2][n_tokens * n_heads]) or
+    // to the parts that row_at names.
+    const int32_t *prefix_table, *prefix_lens, *group_starts;
+    long long prefix_stride;
+    int n_groups, prefix_pages, first, count;
+    float *row_o;             // [..][DP] unnormalised O; nullptr: a call of lora_tree_attention
+    float2 *row_ml;           // (m, l)
+    int4 *row_at;             // (CTA of the first part, parts: 0 is row_o, row of the tile, token * n_heads + head)
 };
 
 __device__ __forceinline__ int node_start(const TreeArgs &a, int b) {
@@ -62,16 +73,45 @@ struct Request {
     int start, nodes, row_tiles, key_tiles, ctx, keys;
 };
 
+// The entries of a launch, and entry b's row of page ids. kPrefix: a call of lora_prefix_attention.
+template <bool kPrefix>
+__device__ __forceinline__ int entries(const TreeArgs &a) {
+    return kPrefix ? a.count : a.n_requests;
+}
+template <bool kPrefix>
+__device__ __forceinline__ bool is_group(const TreeArgs &a, int b) {
+    return kPrefix && a.first + b < a.n_groups;
+}
+template <bool kPrefix>
+__device__ __forceinline__ const int32_t *table_row(const TreeArgs &a, int b) {
+    if (is_group<kPrefix>(a, b)) return a.prefix_table + (a.first + b) * a.prefix_stride;
+    return a.page_table + (kPrefix ? a.first + b - a.n_groups : b) * a.table_stride;
+}
+// First request of group g.
+__device__ __forceinline__ int group_start(const TreeArgs &a, int g) {
+    return min(max(a.group_starts[g], 0), a.n_requests);
+}
+
 // Not inlined, like everything that a tile in the middle of a unit does not need: a warp of a role runs alone on its
 // scheduler, and straight code that does not fit the instruction cache would be its pace.
+template <bool kPrefix>
 __device__ __noinline__ inline Request request(const TreeArgs &a, int b, int m_rows) {
     Request r;
-    r.start = node_start(a, b);
-    r.nodes = max(node_start(a, b + 1) - r.start, 0);
+    const bool shared = is_group<kPrefix>(a, b);
+    int n = b;
+    if constexpr (kPrefix) n = shared ? a.first + b : a.first + b - a.n_groups;
+    if (shared) {
+        r.start = node_start(a, group_start(a, n));
+        r.nodes = max(node_start(a, group_start(a, n + 1)) - r.start, 0);
+        r.ctx = max(a.prefix_lens[n], 0);
+    } else {
+        r.start = node_start(a, n);
+        r.nodes = max(node_start(a, n + 1) - r.start, 0);
+        r.ctx = max(a.ctx_lens[n], 0);
+    }
     // keys that fit the page table; the largest count is a multiple of the tile below 2^31
-    const long long room = min((long long)a.table_pages * a.page_size, 0x7fffffc0ll);
-    r.ctx = max(a.ctx_lens[b], 0);
-    r.keys = (int)min((long long)r.ctx + r.nodes, room);
+    const long long room = min((long long)(shared ? a.prefix_pages : a.table_pages) * a.page_size, 0x7fffffc0ll);
+    r.keys = (int)min((long long)r.ctx + (shared ? 0 : r.nodes), room);
     r.row_tiles = (r.nodes * (a.n_heads / a.n_kv) + m_rows - 1) / m_rows;
     r.key_tiles = max((r.keys + kTileKeys - 1) / kTileKeys, 1);   // one for rows without keys, too
     return r;
@@ -90,22 +130,24 @@ struct Cursor {
     int b, row_tile, head, tile, k, row;
 };
 
+template <bool kPrefix>
 __device__ __noinline__ inline void next_unit(const TreeArgs &a, Cursor &c, int m_rows) {
     c.tile = 0;
     if (++c.head < a.n_kv) return;
     c.head = 0;
     if (c.k == kMaxClass && (c.row_tile += kMaxClass) / kMaxClass < c.r.row_tiles / kMaxClass) return;
     do {
-        if (++c.b >= a.n_requests) return;
-        c.r = request(a, c.b, m_rows);
+        if (++c.b >= entries<kPrefix>(a)) return;
+        c.r = request<kPrefix>(a, c.b, m_rows);
     } while (blocks_of(c.r.row_tiles, c.k) == 0);
     c.row_tile = (c.k == kMaxClass ? 0 : c.r.row_tiles - c.k) + c.row;
 }
 
+template <bool kPrefix>
 __device__ __forceinline__ void next_tile(const TreeArgs &a, Cursor &c, int m_rows) {
     if (++c.tile < c.r.key_tiles) return;
     Cursor next = c;                                     // c itself stays in registers
-    next_unit(a, next, m_rows);
+    next_unit<kPrefix>(a, next, m_rows);
     c = next;
 }
 
@@ -142,14 +184,14 @@ __device__ __forceinline__ long long scaled(long long x, long long y, long long 
     return (p | z) >> 32 == 0 ? (long long)((uint32_t)p / (uint32_t)z) : p / z;
 }
 
-template <int kThreads>
+template <int kThreads, bool kPrefix>
 __device__ inline bool find_share(const TreeArgs &a, int m_rows, long long *scratch, Share &s) {
     constexpr int kWarps = kThreads / 32;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_entries = entries<kPrefix>(a);
     long long *columns = scratch + 2, *sums = scratch + kScratch;    // of class k at k - 1; of the warps' requests
     // Up to 32 requests: every warp finds it all for itself, a lane to a request. What the warps write to shared memory
     // is the same, and none waits for another.
-    const bool few = a.n_requests <= 32;
+    const bool few = n_entries <= 32;
     const int each = few ? 32 : kThreads, me = few ? lane : tid;
     if (!few) {
         if (tid < kScratch) scratch[tid] = tid == 0 ? -1 : 0;
@@ -157,10 +199,10 @@ __device__ inline bool find_share(const TreeArgs &a, int m_rows, long long *scra
     }
     Request mine{};                                          // request `me`: the only ones in most calls
     long long my_columns = 0;                                // few: of class lane + 1
-    for (int b0 = 0; b0 < a.n_requests; b0 += each) {
+    for (int b0 = 0; b0 < n_entries; b0 += each) {
         const int b = b0 + me;
         Request r{};
-        if (b < a.n_requests) r = request(a, b, m_rows);
+        if (b < n_entries) r = request<kPrefix>(a, b, m_rows);
         if (b0 == 0) mine = r;
         const uint32_t some = __reduce_or_sync(0xffffffffu, (r.row_tiles % kMaxClass ? 1u << r.row_tiles % kMaxClass : 0u) |
                                                                 (r.row_tiles >= kMaxClass ? 1u << kMaxClass : 0u));
@@ -250,10 +292,10 @@ __device__ inline bool find_share(const TreeArgs &a, int m_rows, long long *scra
                      __shfl_sync(0xffffffffu, mine.row_tiles, b), __shfl_sync(0xffffffffu, mine.key_tiles, b),
                      __shfl_sync(0xffffffffu, mine.ctx, b),       __shfl_sync(0xffffffffu, mine.keys, b)};
     } else {
-        for (int b0 = 0; b0 < a.n_requests; b0 += kThreads) {    // ends in the chunk that holds column lo < total
+        for (int b0 = 0; b0 < n_entries; b0 += kThreads) {    // ends in the chunk that holds column lo < total
             const int b = b0 + tid;
-            if (b0 > 0 && b < a.n_requests) mine = request(a, b, m_rows);
-            const long long n = b < a.n_requests ? (long long)blocks_of(mine.row_tiles, k) * mine.key_tiles * a.n_kv : 0;
+            if (b0 > 0 && b < n_entries) mine = request<kPrefix>(a, b, m_rows);
+            const long long n = b < n_entries ? (long long)blocks_of(mine.row_tiles, k) * mine.key_tiles * a.n_kv : 0;
             long long upto = scan(n);
             if (lane == 31) sums[warp] = upto;
             __syncthreads();
@@ -267,7 +309,7 @@ __device__ inline bool find_share(const TreeArgs &a, int m_rows, long long *scra
         if (scratch[0] < 0) return false;                    // not reached
         before = scratch[1];
         s.start.b = (int)scratch[0];
-        s.start.r = request(a, s.start.b, m_rows);
+        s.start.r = request<kPrefix>(a, s.start.b, m_rows);
     }
     const long long at = s.lo - before, unit = scaled(at, 1, s.start.r.key_tiles), block = scaled(unit, 1, a.n_kv);
     s.start.tile = (int)(at - unit * s.start.r.key_tiles);
@@ -286,12 +328,75 @@ __device__ __forceinline__ int parts_of(const Share &s, const Cursor &c, int i) 
 }
 
 // Element offset of key `key` of the cursor's tile in the caches, -1: nobody sees it.
+template <bool kPrefix>
 __device__ __forceinline__ long long key_offset(const TreeArgs &a, const Cursor &u, int key) {
     const int p = u.tile * kTileKeys + key;
     if (p >= u.r.keys) return -1;
-    const int at = p / a.page_size, id = a.page_table[u.b * a.table_stride + at];
+    const int at = p / a.page_size, id = table_row<kPrefix>(a, u.b)[at];
     return id >= 0 && id < a.n_pages ? id * a.c_page + (p - at * a.page_size) * a.c_slot : -1;
 }
+
+// Where a row's result goes in a call of lora_prefix_attention: the index of row_o and row_ml for one that is whole, and
+// row_at's entry of the unit that starts in this CTA's share.
+__device__ __forceinline__ size_t row_index(const TreeArgs &a, const Cursor &c, long long token, int head) {
+    const size_t rows = (size_t)a.n_tokens * a.n_heads, row = (size_t)token * a.n_heads + head;
+    return is_group<true>(a, c.b) ? row : rows + row;
+}
+__device__ __forceinline__ void name_parts(const TreeArgs &a, size_t index, int parts, int r) {
+    const size_t rows = (size_t)a.n_tokens * a.n_heads;
+    a.row_at[index] = make_int4(blockIdx.x, parts, r, (int)(index < rows ? index : index - rows));
+}
+
+// O, maximum (in powers of two) and sum of a row, a lane's columns, joined part by part.
+template <int DP>
+struct Joined {
+    static constexpr int V = DP / 32;                    // columns of a lane
+    float o[V], m = -INFINITY, l = 0.f;
+    __device__ __forceinline__ void add(float2 ml, const float (&v)[V]) {
+        const float t = fmaxf(m, ml.x), b = t == -INFINITY ? 0.f : t;
+        const float f = exp2_fast(m - b), h = exp2_fast(ml.x - b);
+        m = t;
+        l = l * f + ml.y * h;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = o[e] * f + v[e] * h;
+    }
+};
+
+// A row's output and log-sum-exp, by a warp.
+template <typename T, int DP>
+__device__ __forceinline__ void store_joined(const TreeArgs &a, long long token, int head, const Joined<DP> &j) {
+    constexpr int V = Joined<DP>::V;
+    const int lane = threadIdx.x & 31;
+    const bool none = j.l == 0.f;                        // m is -inf for a row of NaN scores, too
+    const float inv = j.l > 0.f ? 1.f / j.l : j.l;       // a NaN stays one
+    T *out = static_cast<T *>(a.out) + token * a.o_token + (long long)head * a.o_head + lane * V;
+    if (lane * V < a.head_dim) {
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+            const float x = none ? 0.f : j.o[e] * inv, y = none ? 0.f : j.o[e + 1] * inv;
+            if constexpr (sizeof(T) == 2)
+                *reinterpret_cast<uint32_t *>(out + e) = pack_bf16(x, y);
+            else
+                *reinterpret_cast<float2 *>(out + e) = make_float2(x, y);
+        }
+    }
+    if (a.lse && lane == 0) a.lse[token * a.n_heads + head] = none ? -INFINITY : j.m * 0.6931471805599453f + logf(j.l);
+}
+
+constexpr int kMaxRows = 128;
+constexpr int kMaxCtas = 2 * 160;
+
+// tree_attention.cu: the checks of a call under its name (*nothing: there is nothing to do; need: the least workspace),
+// its arguments, CTAs of a kernel on the current device (0: there is none), a workspace's bytes for them.
+int check(const lora_tree_attention_desc *d, const char *name, size_t need, bool *nothing);
+bool shape_ok(int n_requests, int n_tokens, int n_heads, int n_kv, int head_dim, int dtype);
+TreeArgs arguments(const lora_tree_attention_desc *d);
+int grid_of_device();
+size_t plan_bytes();
+Plan plan_at(void *workspace, int ctas);
+// The rows of a tile for `rows` of an entry on average: 16, 32 or, where `wide`, 128. The kernel of 16 or 32.
+int rows_of_tile(double rows, bool wide);
+cudaError_t launch_mma(const TreeArgs &a, const Plan &plan, int m_rows, cudaStream_t st);
 
 // tree_attention_tc.cu: row tiles of up to 128 on the 5th-generation tensor cores,
 // for the calls that it takes; the rows of a tile. launch_tc returns

@@ -1,10 +1,13 @@
-"""Torch-tensor form of the drafted-token step's calls.
+"""Torch-tensor form of the calls of a decoding step and of a step over drafted tokens.
 
 Around the adapters' delta (``LoraSlots.apply_multi``) a step over drafted tokens
 needs the base model's product with 4-bit weights (``base_linear``), rotary
-positions with the append to a paged cache (``rope``, ``rope_append``), attention
-of the drafted trees over that cache (``tree_attention``) and the verification of
-the drafts (``verify_drafts``). Formulas, layouts and what happens to entries out
+positions with the append to a paged cache (``rope``, ``rope_append``; with norms of
+the query and key heads in front ``norm_rope``, ``norm_rope_append``), attention
+of the drafted trees over that cache (``tree_attention``; of requests that share
+prefixes ``prefix_attention``) and the verification of the drafts
+(``verify_drafts``), a plain decoding step the draw of the next token
+(``sample_tokens``). Formulas, layouts and what happens to entries out
 of range stand in include/rank_adapter_apply.h.
 
 The checks, descriptors and allocations are native (csrc/tensor_calls.cpp): a small
@@ -37,7 +40,8 @@ def _load():
     loader.exec_module(module)
     import ctypes
     names = ("lora_base_linear", "lora_rope", "lora_tree_attention", "lora_tree_attention_workspace_bytes",
-             "lora_verify_drafts")
+             "lora_verify_drafts", "lora_norm_rope", "lora_prefix_attention", "lora_prefix_attention_workspace_bytes",
+             "lora_sample_tokens")
     module.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names], B.check)
     return module
 
@@ -45,6 +49,8 @@ def _load():
 _calls = _load()
 _base_linear, _rope, _rope_append = _calls.base_linear, _calls.rope, _calls.rope_append
 _tree_attention, _verify_drafts = _calls.tree_attention, _calls.verify_drafts
+_norm_rope, _norm_rope_append = _calls.norm_rope, _calls.norm_rope_append
+_prefix_attention, _sample_tokens = _calls.prefix_attention, _calls.sample_tokens
 
 
 def base_linear(x, qweight, scales, zeros=None, out=None):
@@ -98,6 +104,20 @@ def rope_append(q, k, v, positions, table, k_cache, v_cache, slots, interleaved=
     return _rope_append(q, k, v, positions, table, k_cache, v_cache, slots, interleaved, out)
 
 
+def norm_rope(x, weight, positions, table, eps=1e-6, interleaved=False, out=None):
+    """Norm every head of x [tokens, heads, head_dim] and rotate it as rope does, in one pass.
+
+    y = x / sqrt(mean(x^2) + eps) * weight over a head's elements, weight [head_dim], [heads, head_dim] or None (ones), of
+    x's dtype. ``out`` may be x."""
+    return _norm_rope(x, weight, positions, table, eps, interleaved, out)
+
+
+def norm_rope_append(q, k, v, q_weight, k_weight, positions, table, k_cache, v_cache, slots, eps=1e-6,
+                     interleaved=False, out=None):
+    """rope_append with norm_rope's norm of the heads of q and k in front. Returns the rotated q (``out``, which may be q)."""
+    return _norm_rope_append(q, k, v, q_weight, k_weight, positions, table, k_cache, v_cache, slots, eps, interleaved, out)
+
+
 def tree_attention(q, k_cache, v_cache, page_table, ctx_lens, node_starts, tree_mask=None, scale=None, out=None):
     """Attention of drafted trees over the paged cache. Returns (out like q, lse fp32 [tokens, heads]).
 
@@ -106,6 +126,26 @@ def tree_attention(q, k_cache, v_cache, page_table, ctx_lens, node_starts, tree_
     key ctx_lens[b] + j of the cache; tree_mask int64 [tokens, words] (bit j % 64 of word j // 64: the row sees node
     j), None: node i sees nodes 0..i. scale: head_dim ** -0.5 by default."""
     return _tree_attention(q, k_cache, v_cache, page_table, ctx_lens, node_starts, tree_mask, scale, out)
+
+
+def prefix_attention(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, page_table, ctx_lens, node_starts,
+                     tree_mask=None, scale=None, out=None):
+    """tree_attention of requests that share prefixes. Returns (out like q, lse fp32 [tokens, heads]).
+
+    Group g is the requests group_starts[g] .. group_starts[g + 1] (int32 [groups + 1]); they see the prefix_lens[g]
+    (int32 [groups]) keys on the pages prefix_table[g] (int32 [groups, pages of a prefix]), read once for the group, in
+    front of what tree_attention shows them: ctx_lens and page_table do not contain the prefix."""
+    return _prefix_attention(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, page_table, ctx_lens, node_starts,
+                             tree_mask, scale, out)
+
+
+def sample_tokens(logits, noise, temperature=None, top_k=None, top_p=None, min_p=None):
+    """Draw a token for every row of logits [rows, vocab]. Returns (tokens int32 [rows], logprobs fp32 [rows]).
+
+    noise fp32 [rows, vocab], exponentially distributed; temperature, top_p, min_p fp32 [rows] and top_k int32 [rows], or
+    None. Each filter is taken of the softmax at the row's temperature, and a token stays if all keep it; temperature 0 is
+    the likeliest token. logprobs: of the token at the temperature (1 where it is 0), before the filters."""
+    return _sample_tokens(logits, noise, temperature, top_k, top_p, min_p)
 
 
 def verify_drafts(target, draft, tokens, parents, node_starts, uniforms, noise, max_path):
