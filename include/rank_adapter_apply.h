@@ -843,7 +843,7 @@ int lora_verify_drafts(const lora_verify_desc *desc, void *stream);
  * The filters are one value for each row, NULL where no row has one. temperature
  * <= 0 or NaN: the first token, with logprobs at temperature 1. top_k <= 0, top_p >= 1
  * (or NaN) and min_p <= 0 (or NaN) keep all. A logit of NaN counts as -inf, and +inf as
- * the largest fp32 number; tokens of p = 0 are not drawn. A row of -inf alone has
+ * the largest number of its type; tokens of p < 2^-126 are not drawn. A row of -inf alone has
  * token -1 and logprob -inf. Noise that is negative or NaN keeps its token from being
  * drawn; if that is so of all kept ones, the first token is drawn. Sums are fp32, put
  * together in a fixed order.
