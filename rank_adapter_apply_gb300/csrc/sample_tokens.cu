@@ -6,6 +6,7 @@
 #include <atomic>
 #include <cfloat>
 #include <climits>
+#include <type_traits>
 
 namespace lora {
 namespace {
@@ -14,6 +15,8 @@ using namespace step;
 
 constexpr int kMaxCluster = 8;
 constexpr int kSliceBytes = 64 * 1024;   // of a CTA's logits in shared memory: three CTAs fit an SM
+constexpr int kBins = 256;               // of 1/8: down to 2^-32 of the largest p
+constexpr int kListed = 512;              // tokens of a race that a CTA lists
 constexpr int kRejections = 6;           // races lost before the border is found by bisection
 
 struct SampleArgs {
@@ -26,12 +29,24 @@ struct SampleArgs {
     int n_rows, vocab, cluster, slots;       // slots: vectors of a CTA in shared memory
 };
 
-// What the CTAs of a cluster put together in a pass.
+// What the warps of a cluster put together in a pass: a race's winner (at < 0: none), its logit and noise; p of the
+// tokens but the maxima, which are counted, by the maximum of the warp's CTA.
 struct alignas(16) Part {
-    unsigned long long best;      // quotient's bits, then the complement of the index: the largest wins
-    float sum;                    // (first pass: the maximum)
-    uint32_t n;                   // (first pass: the bits of the lower bound)
+    int at;
+    float x, noise, most;
+    float sum;
+    uint32_t n;
+    uint32_t pad[2];
 };
+
+// Bits that order as the floats do, and back.
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t o) {
+    return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
 
 // A place in the row's order: largest logit first, of equal ones the lowest index.
 struct Place {
@@ -41,13 +56,10 @@ struct Place {
     __device__ __forceinline__ bool behind(float y, int v) const { return y > x || (y == x && v < i); }
     // places as numbers: the further to the front, the larger
     __device__ __forceinline__ unsigned long long number() const {
-        const uint32_t b = __float_as_uint(x);
-        return (unsigned long long)(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | (0xffffffffu - (unsigned)i);
+        return (unsigned long long)ordered(x) << 32 | (0xffffffffu - (unsigned)i);
     }
     __device__ __forceinline__ static Place of(unsigned long long n) {
-        const uint32_t o = (uint32_t)(n >> 32);
-        return {__uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o),
-                (int)min(0xffffffffu - (uint32_t)n, (uint32_t)INT_MAX)};
+        return {unordered((uint32_t)(n >> 32)), (int)min(0xffffffffu - (uint32_t)n, (uint32_t)INT_MAX)};
     }
 };
 
@@ -74,31 +86,50 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-__device__ __forceinline__ void st_peer_part(uint32_t cluster_addr, const Part &p) {
-    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"((uint32_t)p.best),
-                 "r"((uint32_t)(p.best >> 32)), "r"(__float_as_uint(p.sum)), "r"(p.n) : "memory");
+__device__ __forceinline__ void st_peer(uint32_t cluster_addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+__device__ __forceinline__ float warp_max(float v) { return unordered(__reduce_max_sync(0xffffffffu, ordered(v))); }
+
+// p / noise exactly, of a token with p >= min_p. Not inlined: few tokens come to it, and it would be in the loops' way.
+__device__ __noinline__ float quotient(float below_top, float inv_t, float min_p, float n) {
+    const float p = expf(below_top * inv_t);
+    return p >= min_p ? __fdiv_rn(p, n) : -1.f;
 }
 
 // The largest p / noise yet, and a little less: what is below it need not be divided.
 struct Race {
-    float top = 0.f, low = 0.f;
+    float top = 0.f, low = 0.f, x = 0.f, noise = 0.f;
     int at = -1;
-    __device__ __forceinline__ void enter(int v, float p, float n) {
-        const float key = __fdiv_rn(p, n);
+    __device__ __forceinline__ void enter(int v, float key, float xv, float nv) {
         // 2^-15: more than the fast exponential is off by
-        if (key > top || (key == top && v < at)) top = key, at = v, low = key * (1.f - 0x1p-15f);
+        if (key > top || (key == top && v < at))
+            top = key, at = v, x = xv, noise = nv, low = fmaxf(low, fminf(key, FLT_MAX) * (1.f - 0x1p-15f));
     }
-    // positive floats order as their bits do; the lower index wins a tie
-    __device__ __forceinline__ unsigned long long best() const {
-        return at < 0 ? 0ull : (unsigned long long)__float_as_uint(top) << 32 | (0xffffffffu - (unsigned)at);
+    // the warp's best in all lanes: positive floats order as their bits do, the lower index wins a tie
+    __device__ __forceinline__ void of_warp() {
+        const uint32_t key = at < 0 ? 0u : __float_as_uint(top), best = __reduce_max_sync(0xffffffffu, key);
+        const int first = __reduce_min_sync(0xffffffffu, key == best && at >= 0 ? at : INT_MAX);
+        const int src = __ffs(__ballot_sync(0xffffffffu, at == first && key == best)) - 1;
+        if (src < 0) {
+            at = -1;
+            return;
+        }
+        top = __shfl_sync(0xffffffffu, top, src);
+        x = __shfl_sync(0xffffffffu, x, src);
+        noise = __shfl_sync(0xffffffffu, noise, src);
+        at = first;
     }
 };
 
 // A row belongs to the CTAs of a cluster, which keep its logits in shared memory (what
 // is past 64 KB of a CTA is read again). Nothing is sorted:
 //
-//   1. the maximum; for top-k, a logit that at least k tokens reach: every warp takes the
-//      ceil(k / warps)-th of its lanes' maxima, and the lowest of these is one;
+//   1. the maximum; for top-k, a logit that at least k tokens reach: every CTA counts the
+//      maxima of its vectors by their distance from its largest, an eighth of a power of two
+//      of p to a bin, until ceil(k / CTAs) are there, and the lowest of these is one;
 //   2. the sum of p = exp((x - max) / t), and the race: the token with the largest
 //      p / noise among those that may win;
 //   3. the tokens in front of the winner are counted and their mass is summed. Each
@@ -112,9 +143,13 @@ struct Race {
 // is found by bisection of the order's places instead.
 template <typename T, int kThreads>
 __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(SampleArgs a) {
-    constexpr int N = 16 / sizeof(T), kWarps = kThreads / 32, kBatch = 16 / N;
+    constexpr int N = 16 / sizeof(T), kWarps = kThreads / 32, kBatch = 8 / N;
     extern __shared__ __align__(16) uint4 slice[];
-    __shared__ Part warps[2][kWarps], ctas[2][kMaxCluster];          // of passes in turn
+    __shared__ Part parts[2][kMaxCluster * kWarps];                  // of the cluster's warps, of passes in turn
+    __shared__ uint32_t bins[kBins];
+    __shared__ float of_cta[kWarps];
+    __shared__ float2 listed[kListed];               // (logit, index's bits) of tokens in the race
+    __shared__ int n_listed;
     static_assert(kSliceBytes / 16 % kThreads == 0, "the vectors past the slice begin at thread 0");
     const int cluster = a.cluster;
     const int row = blockIdx.x / cluster, rank = blockIdx.x % cluster, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -144,83 +179,126 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(Sample
     bool first_only = !(t > 0.f) || top_k == 1 || top_p <= 0.f || min_p > 1.f;
     const float inv_t = t > 0.f ? fminf(fmaxf(__fdiv_rn(1.f, t), FLT_MIN), FLT_MAX) : 1.f;
     // every token is in the race: its noise is read in vectors, and brought to L2 while the logits come
-    const int of_warp = (top_k - 1) / (kWarps * cluster) + 1;
-    const bool dense = !first_only && min_p == 0.f && of_warp > 32 && (reinterpret_cast<uintptr_t>(noise + base) & 15) == 0;
-    if (dense && tid == 0 && held > 0) prefetch_l2_bulk(noise + base, (uint32_t)held * N * 4u);
+    const bool dense_row = !first_only && min_p == 0.f && top_k >= a.vocab && (reinterpret_cast<uintptr_t>(noise + base) & 15) == 0;
+    if (dense_row && tid == 0 && held > 0) prefetch_l2_bulk(noise + base, (uint32_t)held * N * 4u);
 
     int passes = 0;
-    // The cluster's value from the threads': join(a, b) over lanes, warps and CTAs, in one order.
-    auto together = [&](Part mine, auto &&join) -> Part {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            mine = join(mine, Part{__shfl_xor_sync(0xffffffffu, mine.best, o), __shfl_xor_sync(0xffffffffu, mine.sum, o),
-                                   __shfl_xor_sync(0xffffffffu, mine.n, o)});
-        const int buf = passes++ & 1;                // written again only after the barriers of the pass in between
-        if (lane == 0) warps[buf][warp] = mine;
-        __syncthreads();
-        mine = warps[buf][0];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) mine = join(mine, warps[buf][w]);
-        if (cluster > 1) {
-            if (tid < cluster) st_peer_part(map_peer(smem_u32(&ctas[buf][rank]), tid), mine);
-            cluster_sync_all();
-            mine = ctas[buf][0];
-            for (int r = 1; r < cluster; ++r) mine = join(mine, ctas[buf][r]);
+    const int n_parts = cluster * kWarps;
+    // A warp's part to the CTAs of the cluster, and a barrier; a lane then has the parts `lane` and `lane + 32` of theirs.
+    auto exchange = [&](const Part &p) -> const Part * {
+        Part *buf = parts[passes++ & 1];             // written again only after the barrier of the pass in between
+        if (lane < cluster) {
+            const uint32_t at = smem_u32(&buf[rank * kWarps + warp]);
+            const uint32_t to = cluster > 1 ? map_peer(at, lane) : at;
+            st_peer(to, p.at, __float_as_uint(p.x), __float_as_uint(p.noise), __float_as_uint(p.most));
+            st_peer(to + 16, __float_as_uint(p.sum), p.n, 0, 0);
         }
-        return mine;
+        if (cluster > 1)
+            cluster_sync_all();
+        else
+            __syncthreads();
+        return buf;
     };
-    auto add = [](const Part &p, const Part &q) { return Part{p.best > q.best ? p.best : q.best, p.sum + q.sum, p.n + q.n}; };
     auto vector = [&](int j) -> uint4 {
         return j < held ? slice[j] : clean_vector<T>(*reinterpret_cast<const uint4 *>(logits + base + j * N));
     };
 
+    auto each = [&](int from, auto &&f) {            // f(vector's number, its logits) from vector `from` of the thread on
+        int j = from;
+#pragma unroll 4
+        for (; j < held; j += kThreads) {
+            float x[N];
+            unpack<T>(slice[j], x);
+            f(j, x);
+        }
+        for (; j < n_vec; j += kThreads) {
+            float x[N];
+            unpack<T>(vector(j), x);
+            f(j, x);
+        }
+    };
+
     // ---- 1: the maximum, and what at least top_k tokens reach
     cp_async_wait_all();
-    float most = odd_x;
-    bool unclean = false;
-    for (int j = tid; j < n_vec; j += kThreads) {
-        float x[N];
-        unpack<T>(vector(j), x);
+    float most = odd_x, nan = 0.f;
+    each(tid, [&](int, const float (&x)[N]) {
 #pragma unroll
         for (int e = 0; e < N; ++e) {
             most = fmaxf(most, x[e]);
-            unclean = unclean || x[e] != x[e];
+            nan = x[e] != x[e] ? 1.f : nan;
         }
-    }
-    if (unclean || most == INFINITY) {
+    });
+    if (nan > 0.f || most == INFINITY) {
         for (int j = tid; j < held; j += kThreads) slice[j] = clean_vector<T>(slice[j]);
         most = clean<T>(most);
     }
+    // the CTA's
+    const float of_warp = warp_max(most);
+    if (lane == 0) of_cta[warp] = of_warp;
+    const bool bounded = !first_only && top_k < a.vocab;
+    if (bounded)
+        for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
+    __syncthreads();
+    float top = of_cta[0];                           // of the CTA, then of the row
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, of_cta[w]);
+    const float c2 = fminf(inv_t * 1.4426950408889634f, FLT_MAX);    // logits to powers of two
     float reached = -INFINITY;
-    if (!first_only && of_warp <= 32) {              // the lanes' maxima sorted, the largest in lane 0
-        float v = most;
+    if (bounded && top > -INFINITY) {
+        const float largest = top;
+        each(tid, [&](int, const float (&x)[N]) {
+            float most_x = -INFINITY;
 #pragma unroll
-        for (int size = 2; size <= 32; size *= 2)
+            for (int e = 0; e < N; ++e) most_x = fmaxf(most_x, x[e]);
+            const float bin = (largest - most_x) * c2 * 8.f;
+            if (bin < (float)kBins) atomicAdd(&bins[(int)bin], 1u);
+        });
+        __syncthreads();
+        {
+            // every warp finds the bin for itself: lane's eight bins, then up to the lane
+            constexpr int kEach = kBins / 32;
+            const uint32_t need = (uint32_t)((top_k - 1) / cluster + 1);
+            uint32_t n[kEach], upto = 0;
 #pragma unroll
-            for (int o = size / 2; o > 0; o /= 2) {
-                const float w = __shfl_xor_sync(0xffffffffu, v, o);
-                v = ((lane & o) == 0) == ((lane & size) == 0) ? fmaxf(v, w) : fminf(v, w);
+            for (int i = 0; i < kEach; ++i) upto += n[i] = bins[lane * kEach + i];
+            uint32_t before = upto;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, before, o);
+                if (lane >= o) before += v;
             }
-        reached = __shfl_sync(0xffffffffu, v, of_warp - 1);
+            before -= upto;
+            int bin = kBins;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                before += n[i];
+                if (before >= need && bin == kBins) bin = lane * kEach + i;
+            }
+            bin = __reduce_min_sync(0xffffffffu, bin);
+            // the bin's far edge, and what the difference and its product may be off by
+            if (bin < kBins) reached = largest - (float)(bin + 1) * 1.0001f / (8.f * c2) - fabsf(largest) * 0x1p-22f;
+        }
     }
-    if (cluster > 1) cluster_wait_acquire();
-    const Part first = together(Part{0ull, most, (uint32_t)(Place{reached, 0}.number() >> 32)},
-                                [](const Part &p, const Part &q) {
-                                    return Part{0ull, fmaxf(p.sum, q.sum), min(p.n, q.n)};
-                                });
-    const float top = first.sum;
+    if (cluster > 1) cluster_wait_acquire();         // of the arrival at the start
     int token = -1;
     float logprob = -INFINITY;
-    if (top > -INFINITY) {
-        const float c2 = inv_t * 1.4426950408889634f;
-        auto prob = [&](float x) { return expf((x - top) * inv_t); };
-        auto about = [&](float x) { return exp2_fast((x - top) * c2); };     // within 2^-17 where it is not below 2^-126
-        Place limit = Place::of((unsigned long long)first.n << 32);          // only tokens in front of it are in the race
-        // and no logit below this has p >= min_p
+    Place limit{-INFINITY, INT_MAX};                 // only tokens in front of it are in the race
+    if (!dense_row) {
+        // the row's maximum and bound; where all tokens are in the race they are not needed before it
+        const Part *p = exchange(Part{0, 0.f, 0.f, top, reached, 0, {0, 0}});
+        float m = -INFINITY, r = INFINITY;
+        for (int i = lane; i < n_parts; i += 32) m = fmaxf(m, p[i].most), r = fminf(r, p[i].sum);
+        top = warp_max(m);
+        limit.x = -warp_max(-r);
+    }
+    if (dense_row || top > -INFINITY) {
+        // within 2^-17 where it is not below 2^-126; by the maximum that is known: the CTA's in a dense row's first round
+        auto about = [&](float x) { return exp2_fast((x - top) * c2); };
+        // no logit below this has p >= min_p
         const float floor_x = min_p > 0.f ? top + (logf(min_p) - 0.01f) / inv_t - fabsf(top) * 0x1p-22f : -INFINITY;
         const bool by_mass = top_p < 1.f, tested = !first_only && (by_mass || top_k < a.vocab);
-        float rest = 0.f, total = 0.f;               // p of all tokens but the maxima, which are 1 each, and of all
-        uint32_t tops = 0;
+        float rest = 0.f, total = 0.f, token_x = 0.f;    // p of all tokens but the maxima, which are 1 each, and of all
+        uint32_t tops = 0, in_race = 0;              // in_race: of later rounds
         bool found = false;                          // the border: the tokens in the race are the kept ones
         for (int round = 0;; ++round) {
             // ---- 2: the sum and the race
@@ -228,89 +306,178 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(Sample
             float sum = 0.f;
             uint32_t n = 0;
             const float gate = first_only ? top : fmaxf(limit.x, floor_x);
-            auto enter = [&](int v, float x) {       // exactly
-                if (first_only) {
-                    if (x == top) race.enter(v, 1.f, 1.f);
-                } else if (limit.behind(x, v)) {
-                    const float p = prob(x);
-                    if (p >= min_p) race.enter(v, p, noise[v]);
-                }
+            auto enter = [&](int v, float x, float nv) {                     // exactly, of tokens that may win
+                if (first_only ? x == top : limit.behind(x, v))
+                    race.enter(v, first_only ? 1.f : quotient(x - top, inv_t, min_p, nv), x, nv);
             };
-            if (odd >= 0) {
-                if (odd_x < top) sum = about(odd_x);
-                if (odd_x >= gate) enter(odd, odd_x);
-            }
-            if (dense && round == 0) {
-                for (int j0 = tid; j0 < held; j0 += kBatch * kThreads) {
-                    alignas(16) float nv[kBatch][N];
+            // All tokens, with their noise in vectors where it can be. A quotient is formed where a product says that it may
+            // be the largest yet of the warp's, which have a batch's bound from one another; the first batch's comes from
+            // quick quotients. (With a bound of its own, some lane divides in most steps.)
+            auto race_all = [&](auto gated) {
+                constexpr bool kGated = decltype(gated)::value;
+                const bool in_vectors = !kGated || (reinterpret_cast<uintptr_t>(noise + base) & 15) == 0;
+                const int end = kGated ? n_vec : held;
+                alignas(16) float nv[kBatch][N], next[kBatch][N];
+                auto load = [&](int j0) {
 #pragma unroll
                     for (int b = 0; b < kBatch; ++b) {
-                        const int j = j0 + b * kThreads;
-                        if (j < held)
+                        const int j = j0 + lane + b * kThreads;
+                        if (j >= end || first_only) continue;
+                        const float *src = noise + base + j * N;
+                        if (in_vectors) {
 #pragma unroll
-                            for (int e = 0; e < N; e += 4)
-                                *reinterpret_cast<float4 *>(&nv[b][e]) = *reinterpret_cast<const float4 *>(noise + base + j * N + e);
-                    }
+                            for (int e = 0; e < N; e += 4) *reinterpret_cast<float4 *>(&next[b][e]) = *reinterpret_cast<const float4 *>(src + e);
+                        } else {
 #pragma unroll
-                    for (int b = 0; b < kBatch; ++b) {
-                        const int j = j0 + b * kThreads;
-                        if (j >= held) break;
-                        float x[N];
-                        unpack<T>(slice[j], x);
-#pragma unroll
-                        for (int e = 0; e < N; ++e) {
-                            const float p = about(x[e]);
-                            sum += p;
-                            if (p > race.low * nv[b][e]) race.enter(base + j * N + e, prob(x[e]), nv[b][e]);
+                            for (int e = 0; e < N; ++e) next[b][e] = src[e];
                         }
                     }
-                }
-            }
-            for (int j = tid + (dense && round == 0 ? held + kThreads - 1 - (held + kThreads - 1) % kThreads : 0); j < n_vec;
-                 j += kThreads) {
-                float x[N], most_x = -INFINITY;
-                unpack<T>(vector(j), x);
+                };
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    if (round == 0) sum += about(x[e]);
-                    most_x = fmaxf(most_x, x[e]);
-                }
-                if (most_x >= gate)
+                for (int i = 0; i < kBatch * N; ++i) next[i / N][i % N] = 1.f;
+                load(tid - lane);
+                for (int j0 = tid - lane; j0 < end; j0 += kBatch * kThreads) {      // a warp's lanes together
 #pragma unroll
-                    for (int e = 0; e < N; ++e)
-                        if (x[e] >= gate) enter(base + j * N + e, x[e]);
-            }
-            if (round == 0 && most == top) {         // the maxima apart: 1 swallows what it is added to
-                sum = odd >= 0 && odd_x < top ? about(odd_x) : 0.f;
-                n = odd >= 0 && odd_x == top;
-                for (int j = tid; j < n_vec; j += kThreads) {
-                    float x[N];
-                    unpack<T>(vector(j), x);
+                    for (int i = 0; i < kBatch * N; ++i) nv[i / N][i % N] = next[i / N][i % N];
+                    load(j0 + kBatch * kThreads);
+                    float x[kBatch][N], p[kBatch][N];
 #pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        if (x[e] == top)
-                            ++n;
-                        else
-                            sum += about(x[e]);
+                    for (int b = 0; b < kBatch; ++b) {
+                        const int j = j0 + lane + b * kThreads;
+                        if (j < end) {
+                            unpack<T>(kGated ? vector(j) : slice[j], x[b]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < N; ++e) x[b][e] = -INFINITY;
+                        }
+#pragma unroll
+                        for (int e = 0; e < N; ++e) {
+                            p[b][e] = about(x[b][e]);
+                            if (!kGated) sum += p[b][e];
+                            if (kGated && !(x[b][e] >= gate)) p[b][e] = 0.f;
+                        }
+                    }
+                    if (!kGated && j0 < kThreads) {
+                        float quick = 0.f;
+#pragma unroll
+                        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+                            for (int e = 0; e < N; ++e)
+                                quick = fmaxf(quick, nv[b][e] >= FLT_MIN ? __fdividef(p[b][e], nv[b][e]) : 0.f);
+                        race.low = fmaxf(race.low, fminf(warp_max(quick), FLT_MAX) * (1.f - 0x1p-14f));
+                    }
+                    bool some = false;
+#pragma unroll
+                    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+                        for (int e = 0; e < N; ++e) some |= p[b][e] > race.low * nv[b][e];
+                    if (__any_sync(0xffffffffu, some)) {
+#pragma unroll
+                        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+                            for (int e = 0; e < N; ++e)
+                                if (p[b][e] > race.low * nv[b][e])
+                                    enter(base + (j0 + lane + b * kThreads) * N + e, x[b][e], nv[b][e]);
+                        race.low = warp_max(race.low);
                     }
                 }
+            };
+            const bool all_in = dense_row && round == 0;
+            if (top > -INFINITY) {                   // a CTA of a dense row may have nothing
+                if (odd >= 0) {
+                    if (odd_x < top) sum = about(odd_x);
+                    if (odd_x >= gate) enter(odd, odd_x, noise[odd]);
+                }
+                if (all_in) race_all(std::false_type{});
+                if (!all_in || n_vec > held) {
+                    int count = kListed + 1;
+                    if (in_race <= (uint32_t)(kListed / 2 * cluster)) {
+                        // few tokens are in the race: they are listed, and their noise is read by all threads at once
+                        if (tid == 0) n_listed = 0;
+                        __syncthreads();
+                        each(tid + (all_in ? held : 0), [&](int j, const float (&x)[N]) {
+                            float most_x = -INFINITY;
+#pragma unroll
+                            for (int e = 0; e < N; ++e) {
+                                if (round == 0) sum += about(x[e]);
+                                most_x = fmaxf(most_x, x[e]);
+                            }
+                            if (most_x >= gate) {
+#pragma unroll
+                                for (int e = 0; e < N; ++e) {
+                                    const int v = base + j * N + e;
+                                    if (x[e] < gate || (first_only ? x[e] < top : !limit.behind(x[e], v))) continue;
+                                    const int at = atomicAdd(&n_listed, 1);
+                                    if (at < kListed) listed[at] = make_float2(x[e], __int_as_float(v));
+                                }
+                            }
+                        });
+                        __syncthreads();
+                        count = n_listed;
+                    }
+                    if (count <= kListed) {
+                        for (int i = tid; i < count; i += kThreads) {
+                            const int v = __float_as_int(listed[i].y);
+                            enter(v, listed[i].x, first_only ? 1.f : noise[v]);
+                        }
+                    } else {
+                        race_all(std::true_type{});
+                    }
+                    __syncthreads();                 // nobody reads the list any more
+                }
+                if (round == 0 && most == top) {     // the maxima apart: 1 swallows what it is added to
+                    sum = odd >= 0 && odd_x < top ? about(odd_x) : 0.f;
+                    n = odd >= 0 && odd_x == top;
+                    each(tid, [&](int, const float (&x)[N]) {
+#pragma unroll
+                        for (int e = 0; e < N; ++e) {
+                            if (x[e] == top)
+                                ++n;
+                            else
+                                sum += about(x[e]);
+                        }
+                    });
+                }
             }
-            const Part all = together(Part{race.best(), sum, n}, add);
+            race.of_warp();
+            const Part *parts_of_all = exchange(Part{race.at, race.x, race.noise, top, warp_sum(sum), __reduce_add_sync(0xffffffffu, n), {0, 0}});
+            Race best;
+            float m = top;
+            if (all_in) {
+                for (int i = lane; i < n_parts; i += 32) m = fmaxf(m, parts_of_all[i].most);
+                m = warp_max(m);
+                if (m == -INFINITY) break;           // a row of -inf alone
+            }
+            top = m;
+            float of_rest = 0.f;
+            uint32_t of_tops = 0;
+            for (int i = lane; i < n_parts; i += 32) {
+                const Part p = parts_of_all[i];
+                if (p.most == top)
+                    of_rest += p.sum, of_tops += p.n;
+                else
+                    of_rest += (p.sum + (float)p.n) * exp2_fast((p.most - top) * c2);
+                if (p.at >= 0) best.enter(p.at, first_only ? 1.f : quotient(p.x - top, inv_t, min_p, p.noise), p.x, p.noise);
+            }
+            best.of_warp();
             if (round == 0) {
-                rest = all.sum;
-                tops = all.n;
+                rest = warp_sum(of_rest);
+                tops = __reduce_add_sync(0xffffffffu, of_tops);
                 total = rest + (float)tops;
             }
-            if (all.best == 0) {                     // no noise was a positive number: the first in the order
+            if (best.at < 0) {                       // no noise was a positive number: the first in the order
                 if (first_only) break;
                 first_only = true;
+                in_race = 0;
                 continue;
             }
-            token = (int)(0xffffffffu - (unsigned)(all.best & 0xffffffffu));
+            token = best.at;
+            token_x = best.x;
             if (!tested || found || first_only) break;
             // ---- 3: whether the winner is kept
-            Place at{clean<T>(to_f32(logits[token])), token};
-            unsigned long long no = 0, yes = 0;      // of the bisection: places not kept and kept
+            Place at{best.x, token};
+            unsigned long long no = 0, yes = 0;      // of the bisection: places not kept and kept,
+            uint32_t front_no = 0, front_yes = 0;    // and the tokens in front of them
             bool kept;
             for (;;) {
                 float mass = 0.f;
@@ -322,26 +489,36 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(Sample
                     }
                 };
                 if (odd >= 0) count(odd, odd_x);
-                for (int j = tid; j < n_vec; j += kThreads) {
-                    float x[N], most_x = -INFINITY;
-                    unpack<T>(vector(j), x);
+                each(tid, [&](int j, const float (&x)[N]) {
+                    float most_x = -INFINITY;
 #pragma unroll
                     for (int e = 0; e < N; ++e) most_x = fmaxf(most_x, x[e]);
-                    if (most_x >= at.x)
+                    if (most_x >= at.x) {
 #pragma unroll
                         for (int e = 0; e < N; ++e) count(base + j * N + e, x[e]);
-                }
-                const Part p = together(Part{0ull, mass, front}, add);
-                kept = p.n < (uint32_t)top_k && (!by_mass || p.sum < top_p * total);
+                    }
+                });
+                const Part *p = exchange(Part{0, 0.f, 0.f, 0.f, warp_sum(mass), __reduce_add_sync(0xffffffffu, front), {0, 0}});
+                mass = 0.f;
+                front = 0;
+                for (int i = lane; i < n_parts; i += 32) mass += p[i].sum, front += p[i].n;
+                mass = warp_sum(mass);
+                front = __reduce_add_sync(0xffffffffu, front);
+                kept = front < (uint32_t)top_k && (!by_mass || mass < top_p * total);
                 if (yes == 0) {                      // the winner's place
+                    in_race = front;
                     if (kept || round < kRejections) break;
-                    no = at.number();
-                    yes = Place{top, 0}.number();
+                    no = at.number(), front_no = front;
+                    yes = Place{top, 0}.number(), front_yes = 0;
+                } else if (kept) {
+                    yes = no + (yes - no) / 2, front_yes = front;
                 } else {
-                    (kept ? yes : no) = no + (yes - no) / 2;
+                    no = no + (yes - no) / 2, front_no = front;
                 }
-                if (yes - no <= 1) {
+                // at most one token between them: what is in front of it is in front of `yes`, so it is kept
+                if (front_no - front_yes <= 1) {
                     found = true;
+                    in_race = front_no;
                     break;
                 }
                 at = Place::of(no + (yes - no) / 2);
@@ -349,8 +526,10 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(Sample
             if (kept && yes == 0) break;
             limit = found ? Place::of(no) : at;
         }
-        logprob = -(logf((float)tops) + log1pf(rest / (float)tops));
-        if (token >= 0) logprob += (clean<T>(to_f32(logits[token])) - top) * inv_t;
+        if (top > -INFINITY) {
+            logprob = -(logf((float)tops) + log1pf(rest / (float)tops));
+            if (token >= 0) logprob += (token_x - top) * inv_t;
+        }
     }
     if (rank == 0 && tid == 0) {
         a.tokens[row] = token;
