@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(Sample
     __shared__ Part parts[2][kMaxCluster * kWarps];                  // of the cluster's warps, of passes in turn
     __shared__ uint32_t bins[kBins];
     __shared__ float of_cta[kWarps];
+    __shared__ uint32_t bound;                       // bits of a race's bound
     __shared__ float2 listed[kListed];               // (logit, index's bits) of tokens in the race
     __shared__ int n_listed;
     static_assert(kSliceBytes / 16 % kThreads == 0, "the vectors past the slice begin at thread 0");
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(Sample
     // the CTA's
     const float of_warp = warp_max(most);
     if (lane == 0) of_cta[warp] = of_warp;
+    if (tid == 0) bound = 0;
     const bool bounded = !first_only && top_k < a.vocab;
     if (bounded)
         for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
@@ -311,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(Sample
                     race.enter(v, first_only ? 1.f : quotient(x - top, inv_t, min_p, nv), x, nv);
             };
             // All tokens, with their noise in vectors where it can be. A quotient is formed where a product says that it may
-            // be the largest yet of the warp's, which have a batch's bound from one another; the first batch's comes from
-            // quick quotients. (With a bound of its own, some lane divides in most steps.)
+            // be the largest yet of the CTA's threads, which have the bound from one another; the first comes from quick
+            // quotients. (With a bound of its own, some lane of a warp divides in most steps.)
             auto race_all = [&](auto gated) {
                 constexpr bool kGated = decltype(gated)::value;
                 const bool in_vectors = !kGated || (reinterpret_cast<uintptr_t>(noise + base) & 15) == 0;
@@ -365,7 +367,9 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(Sample
                             for (int e = 0; e < N; ++e)
                                 quick = fmaxf(quick, nv[b][e] >= FLT_MIN ? __fdividef(p[b][e], nv[b][e]) : 0.f);
                         race.low = fmaxf(race.low, fminf(warp_max(quick), FLT_MAX) * (1.f - 0x1p-14f));
+                        if (lane == 0) atomicMax(&bound, __float_as_uint(race.low));
                     }
+                    if (!kGated) race.low = fmaxf(race.low, __uint_as_float(*reinterpret_cast<volatile uint32_t *>(&bound)));
                     bool some = false;
 #pragma unroll
                     for (int b = 0; b < kBatch; ++b)
@@ -379,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(Sample
                                 if (p[b][e] > race.low * nv[b][e])
                                     enter(base + (j0 + lane + b * kThreads) * N + e, x[b][e], nv[b][e]);
                         race.low = warp_max(race.low);
+                        if (!kGated && lane == 0) atomicMax(&bound, __float_as_uint(race.low));
                     }
                 }
             };
@@ -425,18 +430,27 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(Sample
                     }
                     __syncthreads();                 // nobody reads the list any more
                 }
-                if (round == 0 && most == top) {     // the maxima apart: 1 swallows what it is added to
-                    sum = odd >= 0 && odd_x < top ? about(odd_x) : 0.f;
-                    n = odd >= 0 && odd_x == top;
-                    each(tid, [&](int, const float (&x)[N]) {
+                if (round == 0) {
+                    // The maxima apart, for 1 swallows what it is added to: the lanes of a warp that has one sum its tokens
+                    // again together.
+                    if (most == top) {
+                        sum = odd >= 0 && odd_x < top ? about(odd_x) : 0.f;
+                        n = odd >= 0 && odd_x == top;
+                    }
+                    for (uint32_t left = __ballot_sync(0xffffffffu, most == top); left; left &= left - 1) {
+                        const int other = __ffs(left) - 1;
+                        for (int j = tid - lane + other + lane * kThreads; j < n_vec; j += 32 * kThreads) {
+                            float x[N];
+                            unpack<T>(vector(j), x);
 #pragma unroll
-                        for (int e = 0; e < N; ++e) {
-                            if (x[e] == top)
-                                ++n;
-                            else
-                                sum += about(x[e]);
+                            for (int e = 0; e < N; ++e) {
+                                if (x[e] == top)
+                                    ++n;
+                                else
+                                    sum += about(x[e]);
+                            }
                         }
-                    });
+                    }
                 }
             }
             race.of_warp();
