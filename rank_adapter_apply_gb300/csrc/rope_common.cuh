@@ -46,16 +46,19 @@ __device__ __forceinline__ Row<T> row_of(const RopeArgs &a, long long t, int r, 
     return w;
 }
 
-// Element offset of the token's place in the caches, -1: it has none.
-__device__ __forceinline__ long long cache_place(const RopeArgs &a, long long t) {
-    if (a.n_kv == 0) return -1;
-    const long long slot = a.slots[t];
+// Element offset of a slot in the caches, -1: it is none of theirs.
+__device__ __forceinline__ long long place_of(const RopeArgs &a, long long slot) {
     if (slot < 0 || slot >= a.n_slots) return -1;
     if ((slot >> 31) == 0) {                               // 32-bit division where it will do
         const uint32_t page = (uint32_t)slot / (uint32_t)a.page_size;
         return page * a.c_page + ((uint32_t)slot - page * (uint32_t)a.page_size) * a.c_slot;
     }
     return slot / a.page_size * a.c_page + slot % a.page_size * a.c_slot;
+}
+
+// Element offset of the token's place in the caches, -1: it has none.
+__device__ __forceinline__ long long cache_place(const RopeArgs &a, long long t) {
+    return a.n_kv == 0 ? -1 : place_of(a, a.slots[t]);
 }
 
 __device__ __forceinline__ uint4 pack(const float (&f)[4]) {

@@ -83,6 +83,39 @@ def test_norm_rope_layouts(ops, dim, rot, tokens, dtype):  # noqa: F811
     assert (out[:, :, 0] == 7.0).all() and (out[:, :, dim + 1:] == 7.0).all()
 
 
+@pytest.mark.parametrize("dtype,interleaved,tokens,heads,kv,dim,rot,kind", [
+    ("bf16", False, 2500, 32, 8, 128, 128, "one"), ("bf16", True, 2301, 42, 1, 80, 64, "each"),
+    ("f32", False, 3000, 28, 4, 80, 32, "one"), ("f32", True, 1100, 64, 16, 64, 64, "none"),
+    ("bf16", False, 1200, 64, 8, 256, 128, "each"), ("bf16", True, 9000, 9, 1, 512, 512, "one"),
+])
+def test_norm_rope_many_rows(ops, dtype, interleaved, tokens, heads, kv, dim, rot, kind):  # noqa: F811
+    """Batches whose blocks go over several tokens: rows with and without a vector for every lane, tokens in several
+    chunks of rows, positions and slots out of range among the others; in place, and alone as with the append."""
+    import torch
+    q, k, v, pos, kc, vc, slots = _rope_inputs(tokens, heads, kv, dim, rot, dtype, page=16, seed=7)
+    qw, kw = _weights(kind, heads, kv, dim, dtype)
+    table = ops.rope_table(500, rot)
+    bad = torch.arange(tokens, device="cuda") % 13 == 5
+    lost = torch.arange(tokens, device="cuda") % 17 == 3
+    pos = torch.where(bad, torch.where(torch.arange(tokens, device="cuda") % 2 == 0, -1, 500).int(), pos)
+    slots = torch.where(lost, kc.shape[0] * 16 + slots, slots)
+    out = torch.full((tokens, heads, dim), 5.0, dtype=q.dtype, device="cuda")
+    ops.norm_rope_append(q, k, v, qw, kw, pos, table, kc, vc, slots, interleaved=interleaved, out=out)
+    good, there = (~bad).cpu().numpy(), (~bad & ~lost).cpu().numpy()
+    tab, p, s = _np(table), pos.cpu().numpy()[good], slots.cpu().numpy()[there]
+    _check_norm(out[~bad], q[~bad], qw, tab[p, :rot // 2], tab[p, rot // 2:], interleaved, 1e-6, dtype)
+    assert (out[bad] == 5.0).all()
+    p = pos.cpu().numpy()[there]
+    _check_norm(kc[s // 16, s % 16], k[~bad & ~lost], kw, tab[p, :rot // 2], tab[p, rot // 2:], interleaved, 1e-6, dtype)
+    assert torch.equal(vc[s // 16, s % 16], v[~bad & ~lost])
+    rest = np.ones(kc.shape[:2], bool)
+    rest[s // 16, s % 16] = False
+    assert (kc[_dev(rest)] == 7.0).all() and (vc[_dev(rest)] == 9.0).all()
+    same = q.contiguous()
+    ops.norm_rope(same, qw, pos, table, interleaved=interleaved, out=same)
+    assert torch.equal(same[~bad], out[~bad]) and torch.equal(same[bad], q[bad])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("dim", [128, 50])
 def test_norm_rope_values(ops, dim, dtype):  # noqa: F811
