@@ -97,10 +97,11 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
 }
 
 // Entries [first, first + count) in tiles of `rows`, which become what the kernel took.
-cudaError_t launch_entries(TreeArgs a, bool bf16, const Plan &plan, int first, int count, int &rows, cudaStream_t st) {
+cudaError_t launch_entries(TreeArgs a, bool bf16, Plan &plan, int first, int count, int &rows, cudaStream_t st) {
     a.first = first;
     a.count = count;
     if (!bf16) return launch_f32(a, plan, rows, st);
+    if (rows == 16) return launch_rows(a, plan, st);
     if (rows == 128) {
         const cudaError_t e = launch_tc(a, plan, st);
         if (e != cudaErrorNotSupported) return e;
@@ -119,12 +120,12 @@ cudaError_t launch_prefix(const TreeArgs &a, const Plan &groups, const Plan &req
     cudaError_t e;
     if (kBf16 ? (of_groups == 128) == (of_requests == 128) : of_groups == of_requests) {
         of_requests = std::max(of_groups, of_requests);
-        join.plan[0] = requests;
-        e = launch_entries(a, kBf16, requests, 0, a.n_groups + a.n_requests, of_requests, st);
+        e = launch_entries(a, kBf16, join.plan[1], 0, a.n_groups + a.n_requests, of_requests, st);
         of_groups = of_requests;
+        join.plan[0] = join.plan[1];
     } else {
-        e = launch_entries(a, kBf16, groups, 0, a.n_groups, of_groups, st);
-        if (e == cudaSuccess) e = launch_entries(a, kBf16, requests, a.n_groups, a.n_requests, of_requests, st);
+        e = launch_entries(a, kBf16, join.plan[0], 0, a.n_groups, of_groups, st);
+        if (e == cudaSuccess) e = launch_entries(a, kBf16, join.plan[1], a.n_groups, a.n_requests, of_requests, st);
     }
     if (e != cudaSuccess) return e;
     join.m_rows[0] = of_groups;

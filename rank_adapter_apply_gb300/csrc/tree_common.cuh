@@ -69,6 +69,16 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// Four 8 x 8 matrices of 16-bit elements, plain and transposed.
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
 struct Request {
     int start, nodes, row_tiles, key_tiles, ctx, keys;
 };
@@ -397,6 +407,9 @@ Plan plan_at(void *workspace, int ctas);
 // The rows of a tile for `rows` of an entry on average: 16, 32 or, where `wide`, 128. The kernel of 16 or 32.
 int rows_of_tile(double rows, bool wide);
 cudaError_t launch_mma(const TreeArgs &a, const Plan &plan, int m_rows, cudaStream_t st);
+
+// prefix_decode.cu: row tiles of 16 by single warps, which become the plan's CTAs (lora_prefix_attention alone).
+cudaError_t launch_rows(const TreeArgs &a, Plan &plan, cudaStream_t st);
 
 // tree_attention_tc.cu: row tiles of up to 128 on the 5th-generation tensor cores,
 // for the calls that it takes; the rows of a tile. launch_tc returns
