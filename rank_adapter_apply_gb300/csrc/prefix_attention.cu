@@ -10,6 +10,7 @@
 #include "tree_common.cuh"
 
 #include <algorithm>
+#include <cmath>
 
 namespace lora {
 namespace {
@@ -17,83 +18,97 @@ namespace {
 using namespace step;
 using namespace tree;
 
+// Rows up to which eight warps, and two, join one.
+constexpr long long kJoin8 = 2400, kJoin2 = 9600;
+
 struct JoinArgs {
     TreeArgs a;
     Plan plan[2];                                        // of the groups' and of the requests' launch
     int m_rows[2];                                       // rows of their parts
 };
 
-// A warp joins a row, or the eight of a block, which have the parts dealt to them: few
-// rows are cut into many parts.
-template <typename T, int DP, bool kBlock>
+// kEach warps of a block join a row: its parts of the group's unit and of the request's, in a
+// row, are dealt to them. All that is read first is read at once; whether the group's entry is
+// the row's own is known only later. Latency: two rounds of reads where a warp has at most
+// kAhead parts.
+template <typename T, int DP, int kEach>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant__ JoinArgs args) {
     constexpr int V = Joined<DP>::V, kAhead = 4;
-    __shared__ float so[kBlock ? 8 : 1][DP];
-    __shared__ float2 sm[kBlock ? 8 : 1];
+    __shared__ float so[8][DP];
+    __shared__ float2 sm[8];
     const TreeArgs &a = args.a;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kEach;
     grid_dependency_wait();
     grid_launch_dependents();
-    const size_t rows = (size_t)a.n_tokens * a.n_heads, row = kBlock ? blockIdx.x : (size_t)blockIdx.x * 8 + warp;
-    if (row >= rows) return;
-    const int token = (int)(row / a.n_heads), head = (int)(row % a.n_heads);
-    if (token < node_start(a, 0) || token >= node_start(a, a.n_requests)) return;   // of no request
+    const size_t rows = (size_t)a.n_tokens * a.n_heads, row = (size_t)blockIdx.x * (8 / kEach) + warp / kEach;
+    const bool real = row < rows;
+    const int token = real ? (int)(row / a.n_heads) : 0, head = real ? (int)(row % a.n_heads) : 0;
+    int4 named[2];
+    named[0] = named[1] = make_int4(0, 0, 0, -1);
+    int g0 = 0, g1 = 0;
+    if (real) named[1] = a.row_at[rows + row];
+    if (real && a.n_groups > 0) {
+        named[0] = a.row_at[row];
+        g0 = group_start(a, 0);
+        g1 = group_start(a, a.n_groups);
+    }
+    const int first = node_start(a, 0), last = node_start(a, a.n_requests);
+    const bool mine = real && token >= first && token < last;            // of a request
+    if (a.n_groups > 0 && (token < node_start(a, g0) || token >= node_start(a, g1))) named[0].w = -1;   // of no group
+    int parts[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        // what starts that fall leave there leads nowhere
+        const int4 n = named[k];
+        const bool ok = mine && n.w == (int)row && n.y >= 0 && n.x >= 0 && n.x < args.plan[k].ctas &&
+                        n.y <= args.plan[k].ctas - n.x && n.z >= 0 && n.z < args.m_rows[k];
+        parts[k] = ok ? max(n.y, 1) : 0;
+    }
     Joined<DP> all;
 #pragma unroll
     for (int e = 0; e < V; ++e) all.o[e] = 0.f;
+    const int n_parts = parts[0] + parts[1];
+    for (int p0 = sub; p0 < n_parts; p0 += kEach * kAhead) {
+        alignas(4 * V) float v[kAhead][V];
+        float2 ml[kAhead];
 #pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-        if (kind == 0 && (a.n_groups == 0 || token < node_start(a, group_start(a, 0)) ||
-                          token >= node_start(a, group_start(a, a.n_groups))))
-            continue;                                    // of no group
-        const Plan &plan = args.plan[kind];
-        const size_t at = kind * rows + row;
-        const int4 named = a.row_at[at];
-        // what starts that fall leave there leads nowhere
-        if (named.w != (int)row || named.y < 0 || named.x < 0 || named.x >= plan.ctas || named.y > plan.ctas - named.x ||
-            named.z < 0 || named.z >= args.m_rows[kind])
-            continue;
-        const int parts = max(named.y, 1);
-        auto source = [&](int p) -> size_t {
-            return (size_t)(p == 0 ? 2 * named.x + 1 : 2 * (named.x + p)) * args.m_rows[kind] + named.z;
-        };
-        const float *from = named.y == 0 ? a.row_o + at * DP : plan.part;
-        const float2 *stat = named.y == 0 ? a.row_ml + at : plan.stat;
-        constexpr int kStep = kBlock ? 8 : 1;
-        for (int p0 = kBlock ? warp : 0; p0 < parts; p0 += kStep * kAhead) {
-            alignas(4 * V) float v[kAhead][V];
-            float2 ml[kAhead];
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int p = p0 + u * kStep;
-                if (p >= parts) break;
-                const size_t s = named.y == 0 ? 0 : source(p);
-                ml[u] = stat[s];
-                const float *src = from + s * DP + lane * V;
-                if constexpr (V == 4)
-                    *reinterpret_cast<float4 *>(v[u]) = *reinterpret_cast<const float4 *>(src);
-                else
-                    *reinterpret_cast<float2 *>(v[u]) = *reinterpret_cast<const float2 *>(src);
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = p0 + u * kEach;
+            if (i >= n_parts) break;
+            const int k = i < parts[0] ? 0 : 1, p = k == 0 ? i : i - parts[0];
+            const int4 n = k == 0 ? named[0] : named[1];
+            const float *o = a.row_o + ((size_t)k * rows + row) * DP;
+            const float2 *stat = a.row_ml + (size_t)k * rows + row;
+            if (n.y > 0) {
+                const size_t at = (size_t)(p == 0 ? 2 * n.x + 1 : 2 * (n.x + p)) * args.m_rows[k] + n.z;
+                o = args.plan[k].part + at * DP;
+                stat = args.plan[k].stat + at;
             }
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-                if (p0 + u * kStep < parts) all.add(ml[u], v[u]);
+            ml[u] = *stat;
+            if constexpr (V == 4)
+                *reinterpret_cast<float4 *>(v[u]) = *reinterpret_cast<const float4 *>(o + lane * V);
+            else
+                *reinterpret_cast<float2 *>(v[u]) = *reinterpret_cast<const float2 *>(o + lane * V);
         }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (p0 + u * kEach < n_parts) all.add(ml[u], v[u]);
     }
-    if constexpr (kBlock) {
+    if constexpr (kEach > 1) {
 #pragma unroll
         for (int e = 0; e < V; ++e) so[warp][lane * V + e] = all.o[e];
         if (lane == 0) sm[warp] = make_float2(all.m, all.l);
         __syncthreads();
-        if (warp > 0) return;
-        for (int w = 1; w < 8; ++w) {
+        if (sub > 0) return;
+#pragma unroll
+        for (int w = 1; w < kEach; ++w) {
             float v[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[e] = so[w][lane * V + e];
-            all.add(sm[w], v);
+            for (int e = 0; e < V; ++e) v[e] = so[warp + w][lane * V + e];
+            all.add(sm[warp + w], v);
         }
     }
-    store_joined<T, DP>(a, token, head, all);
+    if (mine) store_joined<T, DP>(a, token, head, all);
 }
 
 // Entries [first, first + count) in tiles of `rows`, which become what the kernel took.
@@ -101,25 +116,33 @@ cudaError_t launch_entries(TreeArgs a, bool bf16, Plan &plan, int first, int cou
     a.first = first;
     a.count = count;
     if (!bf16) return launch_f32(a, plan, rows, st);
-    if (rows == 16) return launch_rows(a, plan, st);
     if (rows == 128) {
         const cudaError_t e = launch_tc(a, plan, st);
         if (e != cudaErrorNotSupported) return e;
-        rows = 32;
+        rows = 16;
     }
-    return launch_mma(a, plan, rows, st);
+    return launch_rows(a, plan, st);
 }
 
 template <typename T, int DP>
 cudaError_t launch_prefix(const TreeArgs &a, const Plan &groups, const Plan &requests, cudaStream_t st) {
     constexpr bool kBf16 = sizeof(T) == 2;
-    const double all = (double)a.n_tokens * (a.n_heads / a.n_kv);
+    const double group = a.n_heads / a.n_kv;
     JoinArgs join{a, {groups, requests}, {0, 0}};
-    auto tile = [&](double rows) { return kBf16 ? rows_of_tile(rows, tc_takes(a)) : rows <= 16.0 ? 16 : 64; };
-    int of_requests = tile(all / a.n_requests), of_groups = a.n_groups > 0 ? tile(all / a.n_groups) : of_requests;
+    // Rows of a tile for n entries with up to `keys` keys. In bf16 the warps' tiles of 16 read the keys again for each tile,
+    // mostly from L2; the 5th-generation tensor cores read them once for 128 rows, but take another launch of some 20 us.
+    // Bytes read by the warps, and us with both kinds on 16 / with the wide one on 128: 55 MB (100x2 of 300) 43 / 62, 65 MB
+    // (16x1 of 4000 in 2 groups) 24 / 34, 98 MB (requests of 16x16 of 1000) 57 / 48, 201 MB (12x1 of 16384) 45 / 39
+    auto tile = [&](int n, double keys) {
+        const double rows = a.n_tokens * group / std::max(n, 1);
+        if (!kBf16) return rows <= 16.0 ? 16 : 64;
+        const double bytes = std::ceil(rows / 16.0) * n * a.n_kv * keys * a.head_dim * 4.0;
+        return rows <= 16.0 || bytes <= 80e6 || !tc_takes(a) ? 16 : 128;
+    };
+    int of_requests = tile(a.n_requests, (double)a.table_pages * a.page_size);
+    int of_groups = a.n_groups > 0 ? tile(a.n_groups, (double)a.prefix_pages * a.page_size) : of_requests;
     cudaError_t e;
-    if (kBf16 ? (of_groups == 128) == (of_requests == 128) : of_groups == of_requests) {
-        of_requests = std::max(of_groups, of_requests);
+    if (of_groups == of_requests) {
         e = launch_entries(a, kBf16, join.plan[1], 0, a.n_groups + a.n_requests, of_requests, st);
         of_groups = of_requests;
         join.plan[0] = join.plan[1];
@@ -131,9 +154,12 @@ cudaError_t launch_prefix(const TreeArgs &a, const Plan &groups, const Plan &req
     join.m_rows[0] = of_groups;
     join.m_rows[1] = of_requests;
     const long long rows = (long long)a.n_tokens * a.n_heads;
-    if (rows <= 8 * groups.ctas)
-        return launch_step(prefix_join_kernel<T, DP, true>, dim3((unsigned)rows), dim3(256), 0, 1, st, join);
-    return launch_step(prefix_join_kernel<T, DP, false>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, 1, st, join);
+    auto join_by = [&](auto kernel, int each) {
+        return launch_step(kernel, dim3((unsigned)((rows * each + 7) / 8)), dim3(256), 0, 1, st, join);
+    };
+    if (rows <= kJoin8) return join_by(prefix_join_kernel<T, DP, 8>, 8);
+    if (rows <= kJoin2) return join_by(prefix_join_kernel<T, DP, 2>, 2);
+    return join_by(prefix_join_kernel<T, DP, 1>, 1);
 }
 
 size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
