@@ -111,17 +111,11 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
     if (mine) store_joined<T, DP>(a, token, head, all);
 }
 
-// Entries [first, first + count) in tiles of `rows`, which become what the kernel took.
-cudaError_t launch_entries(TreeArgs a, bool bf16, Plan &plan, int first, int count, int &rows, cudaStream_t st) {
+// Entries [first, first + count).
+TreeArgs entries_of(TreeArgs a, int first, int count) {
     a.first = first;
     a.count = count;
-    if (!bf16) return launch_f32(a, plan, rows, st);
-    if (rows == 128) {
-        const cudaError_t e = launch_tc(a, plan, st);
-        if (e != cudaErrorNotSupported) return e;
-        rows = 16;
-    }
-    return launch_rows(a, plan, st);
+    return a;
 }
 
 template <typename T, int DP>
@@ -130,25 +124,51 @@ cudaError_t launch_prefix(const TreeArgs &a, const Plan &groups, const Plan &req
     const double group = a.n_heads / a.n_kv;
     JoinArgs join{a, {groups, requests}, {0, 0}};
     // Rows of a tile for n entries with up to `keys` keys. In bf16 the warps' tiles of 16 read the keys again for each tile,
-    // mostly from L2; the 5th-generation tensor cores read them once for 128 rows, but take another launch of some 20 us.
+    // mostly from L2; the 5th-generation tensor cores read them once for 128 rows, but their kernel takes some 20 us.
     // Bytes read by the warps, and us with both kinds on 16 / with the wide one on 128: 55 MB (100x2 of 300) 43 / 62, 65 MB
     // (16x1 of 4000 in 2 groups) 24 / 34, 98 MB (requests of 16x16 of 1000) 57 / 48, 201 MB (12x1 of 16384) 45 / 39
-    auto tile = [&](int n, double keys) {
-        const double rows = a.n_tokens * group / std::max(n, 1);
-        if (!kBf16) return rows <= 16.0 ? 16 : 64;
-        const double bytes = std::ceil(rows / 16.0) * n * a.n_kv * keys * a.head_dim * 4.0;
-        return rows <= 16.0 || bytes <= 80e6 || !tc_takes(a) ? 16 : 128;
+    auto rows_of = [&](int n) { return a.n_tokens * group / std::max(n, 1); };
+    auto bytes = [&](int n, double pages) {
+        return std::ceil(rows_of(n) / 16.0) * n * a.n_kv * pages * a.page_size * a.head_dim * 4.0;
     };
-    int of_requests = tile(a.n_requests, (double)a.table_pages * a.page_size);
-    int of_groups = a.n_groups > 0 ? tile(a.n_groups, (double)a.prefix_pages * a.page_size) : of_requests;
-    cudaError_t e;
-    if (of_groups == of_requests) {
-        e = launch_entries(a, kBf16, join.plan[1], 0, a.n_groups + a.n_requests, of_requests, st);
-        of_groups = of_requests;
-        join.plan[0] = join.plan[1];
+    auto tile = [&](int n, int pages) {
+        if (!kBf16) return rows_of(n) <= 16.0 ? 16 : 64;
+        return rows_of(n) <= 16.0 || bytes(n, pages) <= 80e6 || !tc_takes(a) ? 16 : 128;
+    };
+    int of_requests = tile(a.n_requests, a.table_pages);
+    int of_groups = a.n_groups > 0 ? tile(a.n_groups, a.prefix_pages) : of_requests;
+    const TreeArgs all = entries_of(a, 0, a.n_groups + a.n_requests), groups_alone = entries_of(a, 0, a.n_groups);
+    const TreeArgs requests_alone = entries_of(a, a.n_groups, a.n_requests);
+    Plan *const plan = join.plan;
+    cudaError_t e = cudaErrorNotSupported;
+    if (!kBf16) {
+        if (of_groups == of_requests) {
+            plan[0] = plan[1];
+            e = launch_f32(all, plan[1], of_requests, st);
+        } else {
+            e = launch_f32(groups_alone, plan[0], of_groups, st);
+            if (e == cudaSuccess) e = launch_f32(requests_alone, plan[1], of_requests, st);
+        }
     } else {
-        e = launch_entries(a, kBf16, join.plan[0], 0, a.n_groups, of_groups, st);
-        if (e == cudaSuccess) e = launch_entries(a, kBf16, join.plan[1], a.n_groups, a.n_requests, of_requests, st);
+        if (of_groups == 128 && of_requests == 128) {
+            e = launch_mixed(all, plan[1], entries_of(a, 0, 0), plan[0], st);
+            plan[0] = plan[1];
+        } else if (of_groups == 128) {
+            // The few rows of requests behind the groups' share in one launch save its latency; in their own they have eight
+            // warps of an SM with more registers, and shares that all begin at once. us in one / in two: 12x1 of 16384 (up to
+            // 13 MB of requests) 36 / 39, 64x1 of 8192 (285 MB) 78 / 82, 256x1 of 32768 (1.1 GB) 398 / 380
+            const bool apart = bytes(a.n_requests, a.table_pages) > 500e6;
+            Plan none = plan[1];
+            e = launch_mixed(groups_alone, plan[0], apart ? entries_of(a, 0, 0) : requests_alone, apart ? none : plan[1], st);
+            if (e == cudaSuccess && apart) e = launch_rows(requests_alone, plan[1], st);
+        } else if (of_requests == 128) {
+            e = launch_mixed(requests_alone, plan[1], groups_alone, plan[0], st);
+        }
+        if (e == cudaErrorNotSupported) {
+            of_groups = of_requests = 16;
+            e = launch_rows(all, plan[1], st);
+            plan[0] = plan[1];
+        }
     }
     if (e != cudaSuccess) return e;
     join.m_rows[0] = of_groups;

@@ -1,6 +1,5 @@
-// lora_prefix_attention in bf16, up to 16 rows of an entry: the single tokens and small
-// trees of a decoding step, whose keys are read for a few rows.
-//
+// Device code of lora_prefix_attention in bf16 for up to 16 rows of an entry
+// (prefix_rows.cu) and beside the 5th-generation tensor cores (tree_attention_tc.cu):
 // A warp works alone: row tiles of 16 on mma.sync, 16 keys a step, K and V by cp.async
 // through the page table into a ring of its own, O in registers, no barrier but the warp's.
 // The steps of all units (entry, head, row tile), in a row, with a few more for each unit's
@@ -8,25 +7,20 @@
 // many short units cost each warp alike. (Tiles of 64 keys shared by a block's four warps and dealt
 // without the units' own cost: 64 requests with contexts of up to 1000 take 64 us, the same
 // number of keys in contexts of 500 41.)
+#pragma once
+
 #include "tree_common.cuh"
 
-#include <algorithm>
-#include <atomic>
+#include <climits>
 
 namespace lora {
 namespace tree {
-namespace {
+namespace rows {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps, kRows = 16, kKeys = 16;
+constexpr int kRows = 16, kKeys = 16;
 constexpr int kStages = 3;
 constexpr int kUnitCost = 2;                   // steps that a unit's beginning and end are worth
 constexpr int kLeast = 4;                      // steps of a warp's share, at least
-
-template <int DP>
-struct Ring {
-    static constexpr int kRowBytes = DP * 2, kHalf = kKeys * kRowBytes, kStage = 2 * kHalf;
-    static constexpr int kSmem = kWarps * kStages * kStage;
-};
 
 // What a step's computation has to know of it.
 struct Step {
@@ -34,6 +28,16 @@ struct Step {
     int row_tile, head, step, there;           // there: the keys that are there
     int last, starts, ends, parts;             // last: of the warp's part of its unit, which has the unit's first or last step
     int group;                                 // whether the entry is a group
+};
+
+// Shared memory: the warps' rings, then what the shares are found with and the steps in the rings.
+template <int DP, int kWarps, int kThreads>
+struct Memory {
+    static constexpr int kRowBytes = DP * 2, kHalf = kKeys * kRowBytes, kStage = 2 * kHalf;
+    unsigned char rings[kWarps][kStages * kStage];
+    Step steps[kWarps][kStages + 1];
+    long long sums[kThreads / 32], first_of[kWarps];
+    int entry_of[kWarps];
 };
 
 // Where a warp is in the units' steps.
@@ -49,7 +53,7 @@ __device__ __forceinline__ long long cost_of(const TreeArgs &a, const Request &r
 }
 
 // The first unit after the one at p, at its first step.
-__device__ __noinline__ void next_place(const TreeArgs &a, Place &p) {
+__device__ __noinline__ inline void next_place(const TreeArgs &a, Place &p) {
     p.step = 0;
     if (++p.row_tile < p.r.row_tiles) return;
     p.row_tile = 0;
@@ -75,18 +79,18 @@ __device__ __forceinline__ bool advance(const TreeArgs &a, Place &p) {
     return p.col < p.hi;
 }
 
-template <int DP>
-__global__ void __launch_bounds__(kThreads, 1) prefix_rows_kernel(TreeArgs a, Plan plan) {
-    using R = Ring<DP>;
+// A CTA's work. kWarps of its kThreads / 32 warps have shares; all threads call it.
+template <int DP, int kWarps, int kThreads>
+__device__ __forceinline__ void work(const TreeArgs &a, const Plan &plan, unsigned char *smem) {
+    using R = Memory<DP, kWarps, kThreads>;
     constexpr int kPieces = DP / 8;                    // 16-byte pieces of a row
-    extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ Step steps[kWarps][kStages + 1];
-    __shared__ long long sums[kWarps], first_of[kWarps];
-    __shared__ int entry_of[kWarps];
+    R &sm = *reinterpret_cast<R *>(smem);
+    auto &steps = sm.steps;
+    auto &sums = sm.sums;
+    auto &first_of = sm.first_of;
+    auto &entry_of = sm.entry_of;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g4 = lane >> 2, t4 = lane & 3;
     const int group = a.n_heads / a.n_kv;
-    grid_dependency_wait();
-    grid_launch_dependents();
 
     // ---- the warps' shares: neighbours in different blocks
     auto scanned = [&](long long n) {                  // up to this thread, of the block
@@ -111,11 +115,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_rows_kernel(TreeArgs a, Pl
         __syncthreads();
         total += sums[0];
     }
-    const int worker = warp * gridDim.x + blockIdx.x;
+    const int worker = warp < kWarps ? warp * (int)gridDim.x + (int)blockIdx.x : INT_MAX;
     const long long workers = min((long long)plan.ctas, (total + kLeast - 1) / kLeast);
     const long long lo = worker < workers ? scaled(total, worker, workers) : total;
     const long long hi = worker < workers ? scaled(total, worker + 1, workers) : total;
-    if (lane == 0) first_of[warp] = lo, entry_of[warp] = -1;
+    if (lane == 0 && warp < kWarps) first_of[warp] = lo, entry_of[warp] = -1;
     __syncthreads();
     // the entry of each warp's first step
     long long before = 0;
@@ -159,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_rows_kernel(TreeArgs a, Pl
     int from = load.step;                              // the first step of the warp's part of the unit at `load`
     auto worker_of = [&](long long x) { return (int)scaled((x + 1) * workers - 1, 1, total); };
 
-    unsigned char *ring = smem + warp * (kStages * R::kStage);
+    unsigned char *ring = sm.rings[warp];
     const uint32_t ring_at = smem_u32(ring);
     // lane k < 16: element offset of the step's key k, -1: nobody sees it
     auto look = [&](const Place &p) -> long long {
@@ -375,25 +379,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_rows_kernel(TreeArgs a, Pl
     }
 }
 
-template <int DP>
-cudaError_t launch(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
-    static std::atomic<uint64_t> ready{0};
-    if (!device_bit(ready)) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(prefix_rows_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<DP>::kSmem);
-        if (e != cudaSuccess) return e;
-        set_device_bit(ready);
-    }
-    return launch_step(prefix_rows_kernel<DP>, dim3(plan.ctas / kWarps), dim3(kThreads), Ring<DP>::kSmem, 1, st, a, plan);
-}
-
-}  // namespace
-
-// plan.ctas becomes the number of warps: each has two parts of 16 rows.
-cudaError_t launch_rows(const TreeArgs &a, Plan &plan, cudaStream_t st) {
-    plan.ctas = plan.ctas / 2 * kWarps;
-    return a.head_dim <= 64 ? launch<64>(a, plan, st) : launch<128>(a, plan, st);
-}
-
+}  // namespace rows
 }  // namespace tree
 }  // namespace lora

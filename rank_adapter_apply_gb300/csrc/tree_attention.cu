@@ -32,7 +32,7 @@ struct Tile {
     static constexpr int kStart = kValid + kRing * 8, kSmem = kStart + (kScratch + kThreads / 32) * 8;
 };
 
-template <int DP, int WM, int WN, bool kPrefix>
+template <int DP, int WM, int WN>
 __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan plan) {
     using T = Tile<DP, WM, WN>;
     constexpr int kPieces = DP / 8;                     // 16-byte pieces of a row
@@ -46,16 +46,16 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
 
     grid_dependency_wait();
     grid_launch_dependents();                            // the join kernel waits for this grid's end itself
-    if (!kPrefix && tid == 0) plan.seg[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (tid == 0) plan.seg[blockIdx.x] = make_int4(0, 0, 0, 0);
     Share share;
-    if (!find_share<T::kThreads, kPrefix>(a, T::M, scratch, share)) return;
+    if (!find_share<T::kThreads, false>(a, T::M, scratch, share)) return;
     Cursor load = share.start;
     Cursor c = load;                                     // the tile being computed; `load` runs ahead of it
     Cursor look = load;                                  // the tile whose page ids are being read: one further ahead
-    const int n_tiles = (int)(share.hi - share.lo);
+    const int n_tiles = share.n_tiles;
 
     // Offsets of tile i's keys: read into a register by threads 0..63, stored to the ring at the end of the step.
-    auto read_off = [&](const Cursor &u) -> long long { return tid < kTileKeys ? key_offset<kPrefix>(a, u, tid) : -1; };
+    auto read_off = [&](const Cursor &u) -> long long { return tid < kTileKeys ? key_offset<false>(a, u, tid) : -1; };
     auto store_off = [&](int i, long long off) {
         if (tid >= kTileKeys) return;
         offs[i % T::kRing * kTileKeys + tid] = off;
@@ -84,14 +84,14 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
     for (int i = 0; i < kStages - 1; ++i) {
         if (i < n_tiles) {
             store_off(i, read_off(look));
-            next_tile<kPrefix>(a, look, T::M);
+            next_tile<false>(a, look, T::M);
         }
     }
     __syncthreads();
     for (int i = 0; i < kStages - 1; ++i) {
         if (i < n_tiles) {
             issue(i, load);
-            next_tile<kPrefix>(a, load, T::M);
+            next_tile<false>(a, load, T::M);
         }
         cp_async_commit();
     }
@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
         __syncthreads();                                 // tile i is here, and everyone is done with tile i - 1
         if (i + kStages - 1 < n_tiles) {
             issue(i + kStages - 1, load);
-            next_tile<kPrefix>(a, load, T::M);
-            next_tile<kPrefix>(a, look, T::M);
+            next_tile<false>(a, load, T::M);
+            next_tile<false>(a, look, T::M);
         }
         cp_async_commit();
         if (i + kStages < n_tiles) pending = read_off(look);
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
                     const int r = wm * 16 + g4 + hrow * 8;
                     const int row = c.row_tile * T::M + r, node = row / group;
                     if (node >= c.r.nodes) continue;
-                    if (!kPrefix && starts && ends) {
+                    if (starts && ends) {
                         const long long token = c.r.start + node;
                         const int head = c.head * group + row % group;
                         const float inv = l[hrow] > 0.f ? 1.f / l[hrow] : l[hrow];
@@ -338,27 +338,21 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
                     } else {
                         const long long slot = 2ll * blockIdx.x + (starts ? 1 : 0);
                         float *part = plan.part + (slot * T::M + r) * DP;
-                        float2 *stat = plan.stat + slot * T::M + r;
-                        if constexpr (kPrefix) {
-                            const size_t at = row_index(a, c, c.r.start + node, c.head * group + row % group);
-                            if (starts && ends) part = a.row_o + at * DP, stat = a.row_ml + at;
-                            if (starts && t4 == 0) name_parts(a, at, ends ? 0 : parts_of(share, c, i), r);
-                        }
 #pragma unroll
                         for (int d = 0; d < DP / 8; ++d)
                             *reinterpret_cast<float2 *>(part + d * 8 + t4 * 2) =
                                 make_float2(o[d][hrow * 2], o[d][hrow * 2 + 1]);
-                        if (t4 == 0) *stat = make_float2(m[hrow], l[hrow]);
+                        if (t4 == 0) plan.stat[slot * T::M + r] = make_float2(m[hrow], l[hrow]);
                     }
                 }
             }
-            if (!kPrefix && tid == 0 && starts && !ends) {
-                plan.seg[blockIdx.x] = make_int4(c.b, c.row_tile, c.head, parts_of(share, c, i));
+            if (tid == 0 && starts && !ends) {
+                plan.seg[blockIdx.x] = make_int4(c.b, c.row_tile, c.head, parts_of(share, c));
             }
             fresh = true;
         }
         if (i + kStages < n_tiles) store_off(i + kStages, pending);
-        next_tile<kPrefix>(a, c, T::M);
+        next_tile<false>(a, c, T::M);
     }
 }
 
@@ -461,10 +455,22 @@ __global__ void __launch_bounds__(256) tree_join_kernel(TreeArgs a, Plan plan, i
         if (r0 + k < rows) store(seg.y * m_rows + r0 + k, j[k]);
 }
 
-template <int DP, int WM, bool kPrefix>
+// The row tile by the average rows (nodes times query heads of a key/value head) of a request: how they are spread over
+// the requests only the device knows, so one wide tree among many single nodes goes in many small tiles (64 requests, ctx
+// 4096, 32 heads over 8: all of one node 176 us, one of them of 64 nodes 234). Measured with equal requests: 8, ctx 4096,
+// 32 heads over 8, tiles of 16 / 32 / 128 rows: 8 rows 34.6 / 35.4 / 35.6 us, 16 rows 36.0 / 36.3 / 35.5, 24 rows 45.1 /
+// 38.0 / 36.8, 32 rows 45.5 / 38.2 / 37.4, 48 rows 58.9 / 50.9 / 38.9, 128 rows 119 / 80 / 47. For few keys 32 beats 128
+// up to 32 rows: 1x8 ctx 777 12.7 and 14.8, 4x8 ctx 500 13.6 and 17.7.
+int rows_of_tile(const TreeArgs &a) {
+    const double rows = (double)a.n_tokens * (a.n_heads / a.n_kv) / a.n_requests;
+    return rows <= 16.0 ? 16 : rows <= 32.0 || !tc_takes(a) ? 32 : 128;
+}
+
+
+template <int DP, int WM>
 cudaError_t launch_tiles(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
     using T = Tile<DP, WM, 4 / WM>;
-    auto kernel = tree_tiles_kernel<DP, WM, 4 / WM, kPrefix>;
+    auto kernel = tree_tiles_kernel<DP, WM, 4 / WM>;
     static std::atomic<uint64_t> ready{0};
     if (!device_bit(ready)) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
@@ -487,13 +493,13 @@ cudaError_t launch_join(const TreeArgs &a, const Plan &plan, int m_rows, cudaStr
 
 template <int DP>
 cudaError_t launch_bf16(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
-    const int rows = rows_of_tile((double)a.n_tokens * (a.n_heads / a.n_kv) / a.n_requests, tc_takes(a));
+    const int rows = rows_of_tile(a);
     if (rows == 128) {
         const cudaError_t e = launch_tc(a, plan, st);
         if (e == cudaSuccess) return launch_join<__nv_bfloat16, DP, 128>(a, plan, tc_rows(a), st);
         if (e != cudaErrorNotSupported) return e;
     }
-    const cudaError_t e = launch_mma(a, plan, rows == 16 ? 16 : 32, st);
+    const cudaError_t e = rows == 16 ? launch_tiles<DP, 1>(a, plan, st) : launch_tiles<DP, 2>(a, plan, st);
     if (e != cudaSuccess) return e;
     return rows == 16 ? launch_join<__nv_bfloat16, DP, 16>(a, plan, 16, st) : launch_join<__nv_bfloat16, DP, 32>(a, plan, 32, st);
 }
@@ -534,25 +540,6 @@ Plan plan_at(void *workspace, int ctas) {
     plan.stat = reinterpret_cast<float2 *>(plan.part + 2 * (size_t)ctas * kMaxRows * 128);
     plan.seg = reinterpret_cast<int4 *>(plan.stat + 2 * (size_t)ctas * kMaxRows);
     return plan;
-}
-
-// The row tile by the average rows (nodes times query heads of a key/value head) of a request: how they are spread over
-// the requests only the device knows, so one wide tree among many single nodes goes in many small tiles (64 requests, ctx
-// 4096, 32 heads over 8: all of one node 176 us, one of them of 64 nodes 234). Measured with equal requests: 8, ctx 4096,
-// 32 heads over 8, tiles of 16 / 32 / 128 rows: 8 rows 34.6 / 35.4 / 35.6 us, 16 rows 36.0 / 36.3 / 35.5, 24 rows 45.1 /
-// 38.0 / 36.8, 32 rows 45.5 / 38.2 / 37.4, 48 rows 58.9 / 50.9 / 38.9, 128 rows 119 / 80 / 47. For few keys 32 beats 128
-// up to 32 rows: 1x8 ctx 777 12.7 and 14.8, 4x8 ctx 500 13.6 and 17.7.
-int rows_of_tile(double rows, bool wide) { return rows <= 16.0 ? 16 : rows <= 32.0 || !wide ? 32 : 128; }
-
-
-cudaError_t launch_mma(const TreeArgs &a, const Plan &plan, int m_rows, cudaStream_t st) {
-    const bool prefix = a.row_o != nullptr;
-    if (a.head_dim <= 64) {
-        if (m_rows == 16) return prefix ? launch_tiles<64, 1, true>(a, plan, st) : launch_tiles<64, 1, false>(a, plan, st);
-        return prefix ? launch_tiles<64, 2, true>(a, plan, st) : launch_tiles<64, 2, false>(a, plan, st);
-    }
-    if (m_rows == 16) return prefix ? launch_tiles<128, 1, true>(a, plan, st) : launch_tiles<128, 1, false>(a, plan, st);
-    return prefix ? launch_tiles<128, 2, true>(a, plan, st) : launch_tiles<128, 2, false>(a, plan, st);
 }
 
 int check(const lora_tree_attention_desc *d, const char *name, size_t need, bool *nothing) {

@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(TreeArgs a, Plan 
     Share share;
     if (!find_share<kThreads, kPrefix>(a, M, scratch, share)) return;
     Cursor c = share.start;
-    const int n_tiles = (int)(share.hi - share.lo);
+    const int n_tiles = share.n_tiles;
     const float c2 = a.scale * 1.4426950408889634f;            // scores in powers of two
 
     float o[R][C], m[R], l[R];
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(TreeArgs a, Plan 
                 if constexpr (kPrefix) {
                     const size_t at = row_index(a, c, token, head);
                     if (starts && ends) dst = a.row_o + at * DP, stat = a.row_ml + at;
-                    if (starts && l16 == 0) name_parts(a, at, ends ? 0 : parts_of(share, c, i), row0 + r);
+                    if (starts && l16 == 0) name_parts(a, at, ends ? 0 : parts_of(share, c), row0 + r);
                 }
 #pragma unroll
                 for (int e = 0; e < C; e += 4) {
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(TreeArgs a, Plan 
                 }
             }
             if (!kPrefix && tid == 0 && starts && !ends)
-                plan.seg[blockIdx.x] = make_int4(c.b, c.row_tile, c.head, parts_of(share, c, i));
+                plan.seg[blockIdx.x] = make_int4(c.b, c.row_tile, c.head, parts_of(share, c));
         }
         next_tile<kPrefix>(a, c, M);
     }

@@ -27,6 +27,7 @@
 // to tensor memory, second product, next scores is as long as the two CTAs of an SM can
 // hide. 32 requests of up to 16 nodes, ctx 4096, 32 heads over 8: 89 us, 4.7 TB/s of keys
 // and values, with half of the 128 lanes empty.
+#include "prefix_rows.cuh"
 #include "tree_common.cuh"
 #include "tc_util.cuh"
 #include "tensor_map.cuh"
@@ -41,6 +42,9 @@ constexpr int kRows = 128;                     // lanes of an accumulator; rows 
 constexpr int kThreads = 192;
 constexpr int kItems = 5;                      // ring of K and V items
 constexpr int kMeta = 4;                       // ring of the tiles' masks
+// Tiles that a unit's beginning and end are worth in lora_prefix_attention's shares. us with 0 / 2 / 4: requests of 16x16
+// of 1000 52 / 44 / 43, 37x7 of 3001 71 / 70 / 68, 64x1 of 8192 81 / 80 / 78. (6: 41, 65, 108.)
+constexpr int kUnitTiles = 4;
 constexpr uint32_t kWaitLimit = 1u << 18;       // polls, of some microseconds each: about a second
 
 template <int DP>
@@ -146,9 +150,8 @@ __device__ __forceinline__ bool odd_piece(const uint4 &v) {
 }
 
 template <int DP, bool kPrefix>
-__global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_constant__ TcArgs args) {
+__device__ __forceinline__ void tc_work(const TcArgs &args, unsigned char *smem) {
     using C = Tc<DP>;
-    extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ uint64_t full[kItems], empty[kItems], meta_full[kMeta], s_full[2], p_ready[2], pv_done[2], q_full, drained, looked;
     __shared__ int poison_at[2];                       // 1 + the last tile (even, odd) whose V had a row that is not finite
     __shared__ Meta meta[kMeta];
@@ -161,12 +164,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
     const Plan &plan = args.plan;
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), group = a.n_heads / a.n_kv;
     const int rows = kRows / group * group;            // of a tile
-    grid_dependency_wait();
-    grid_launch_dependents();                          // the join kernel waits for this grid's end itself
-    if (!kPrefix && tid == 0) plan.seg[blockIdx.x] = make_int4(0, 0, 0, 0);
+    const int cta = blockIdx.x;
+    if (!kPrefix && tid == 0) plan.seg[cta] = make_int4(0, 0, 0, 0);
     Share share;
-    if (!find_share<kThreads, kPrefix>(a, rows, scratch, share)) return;
-    const int n_tiles = (int)(share.hi - share.lo);
+    if (!find_share<kThreads, kPrefix, kPrefix ? kUnitTiles : 0>(a, rows, scratch, share)) return;
+    const int n_tiles = share.n_tiles;
     if (tid == 0) {
         for (int i = 0; i < kItems; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         for (int i = 0; i < kMeta; ++i) mbar_init(&meta_full[i], 1);
@@ -457,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
                 tc::fence_after_sync();
                 // a row without keys is 0; one whose scores are all NaN also has m = -inf, but its l is NaN
                 const bool mine = node < c.r.nodes, none = l == 0.f, done = !kPrefix && starts && ends;
-                const long long token = c.r.start + node, slot = 2ll * blockIdx.x + (starts ? 1 : 0);
+                const long long token = c.r.start + node, slot = 2ll * cta + (starts ? 1 : 0);
                 const float inv = !done ? 1.f : l > 0.f ? 1.f / l : l;
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + token * a.o_token + head * a.o_head;
                 float *part = plan.part + (slot * kRows + tid) * DP;
@@ -465,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
                 if constexpr (kPrefix) {
                     const size_t at = mine ? row_index(a, c, token, head) : 0;
                     if (starts && ends) part = a.row_o + at * DP, stat = a.row_ml + at;
-                    if (mine && starts) name_parts(a, at, ends ? 0 : parts_of(share, c, i), tid);
+                    if (mine && starts) name_parts(a, at, ends ? 0 : parts_of(share, c), tid);
                 }
 #pragma unroll 1
                 for (int d = 0; d < DP; d += 32) {
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
                     a.lse[token * a.n_heads + head] = none ? -INFINITY : m * 0.6931471805599453f + logf(l);
                 if (mine && !done) *stat = make_float2(m, l);
                 if (!kPrefix && tid == 0 && starts && !ends)
-                    plan.seg[blockIdx.x] = make_int4(c.b, c.row_tile, c.head, parts_of(share, c, i));
+                    plan.seg[cta] = make_int4(c.b, c.row_tile, c.head, parts_of(share, c));
                 tc::fence_before_sync();
             }
             __syncwarp();
@@ -515,6 +517,35 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, 256);
     }
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_constant__ TcArgs args) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    grid_dependency_wait();
+    grid_launch_dependents();                          // the join kernel waits for this grid's end itself
+    tc_work<DP, false>(args, smem);
+}
+
+// lora_prefix_attention: the wide row tiles, then, as each CTA is done with its share of them, the few rows of the other
+// entries: one launch, and nobody waits for the slowest share. (Wide and narrow CTAs side by side, so that one
+// kind's products overlap the other's reads, were slower: one CTA of this kernel on an SM has half the pace of two.)
+constexpr int kNarrowWarps = 4;
+struct MixedArgs {
+    TcArgs wide;
+    TreeArgs narrow;
+    Plan narrow_plan;
+};
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 2) prefix_mixed_kernel(const __grid_constant__ MixedArgs args) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    static_assert(sizeof(rows::Memory<DP, kNarrowWarps, kThreads>) <= Tc<DP>::kSmem, "the rings fit");
+    grid_dependency_wait();
+    grid_launch_dependents();
+    tc_work<DP, true>(args.wide, smem);
+    if (args.narrow.count == 0) return;
+    __syncthreads();                                   // shared memory changes hands
+    rows::work<DP, kNarrowWarps, kThreads>(args.narrow, args.narrow_plan, smem);
 }
 
 // A bf16 map of `rank` dimensions, boxes of 64 columns, 128-byte swizzle. The
@@ -537,17 +568,9 @@ int box_of(int page_size) {
     return box;
 }
 
-template <int DP, bool kPrefix>
-cudaError_t launch(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
-    static std::atomic<uint64_t> ready{0};
-    if (!device_bit(ready)) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(tree_tc_kernel<DP, kPrefix>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<DP>::kSmem);
-        if (e != cudaSuccess) return e;
-        set_device_bit(ready);
-    }
+// The maps of a call's tensors; false: the driver refuses one.
+bool fill(const TreeArgs &a, const Plan &plan, TcArgs &args) {
     const int group = a.n_heads / a.n_kv;
-    TcArgs args;
     args.a = a;
     args.plan = plan;
     args.box = box_of(a.page_size);
@@ -561,10 +584,19 @@ cudaError_t launch(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
     const cuuint64_t c_dims[] = {(cuuint64_t)a.head_dim, sf ? places : heads, sf ? heads : places, (cuuint64_t)a.n_pages};
     const long long c_strides[] = {sf ? a.c_slot : a.c_head, sf ? a.c_head : a.c_slot, a.c_page};
     const cuuint32_t c_box[] = {64, sf ? box : 1, sf ? 1 : box, 1};
-    if (!encode(&args.q, a.q, 3, q_dims, q_strides, q_box) || !encode(&args.k, a.k_cache, 4, c_dims, c_strides, c_box) ||
-        !encode(&args.v, a.v_cache, 4, c_dims, c_strides, c_box))
-        return cudaErrorNotSupported;
-    return launch_step(tree_tc_kernel<DP, kPrefix>, dim3(plan.ctas), dim3(kThreads), Tc<DP>::kSmem, 1, st, args);
+    return encode(&args.q, a.q, 3, q_dims, q_strides, q_box) && encode(&args.k, a.k_cache, 4, c_dims, c_strides, c_box) &&
+           encode(&args.v, a.v_cache, 4, c_dims, c_strides, c_box);
+}
+
+template <int DP, typename Kernel, typename Args>
+cudaError_t launch(Kernel kernel, const Args &args, int ctas, cudaStream_t st) {
+    static std::atomic<uint64_t> ready{0};
+    if (!device_bit(ready)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc<DP>::kSmem);
+        if (e != cudaSuccess) return e;
+        set_device_bit(ready);
+    }
+    return launch_step(kernel, dim3(ctas), dim3(kThreads), Tc<DP>::kSmem, 1, st, args);
 }
 
 }  // namespace
@@ -598,8 +630,21 @@ bool tc_takes(const TreeArgs &a) {
 int tc_rows(const TreeArgs &a) { return kRows / (a.n_heads / a.n_kv) * (a.n_heads / a.n_kv); }
 
 cudaError_t launch_tc(const TreeArgs &a, const Plan &plan, cudaStream_t st) {
-    if (a.row_o) return a.head_dim <= 64 ? launch<64, true>(a, plan, st) : launch<128, true>(a, plan, st);
-    return a.head_dim <= 64 ? launch<64, false>(a, plan, st) : launch<128, false>(a, plan, st);
+    TcArgs args;
+    if (!fill(a, plan, args)) return cudaErrorNotSupported;
+    return a.head_dim <= 64 ? launch<64>(tree_tc_kernel<64>, args, plan.ctas, st)
+                            : launch<128>(tree_tc_kernel<128>, args, plan.ctas, st);
+}
+
+cudaError_t launch_mixed(const TreeArgs &wide, const Plan &wide_plan, const TreeArgs &narrow, Plan &narrow_plan,
+                         cudaStream_t st) {
+    MixedArgs args;
+    if (!fill(wide, wide_plan, args.wide)) return cudaErrorNotSupported;
+    args.narrow = narrow;
+    narrow_plan.ctas = wide_plan.ctas * kNarrowWarps;
+    args.narrow_plan = narrow_plan;
+    return wide.head_dim <= 64 ? launch<64>(prefix_mixed_kernel<64>, args, wide_plan.ctas, st)
+                               : launch<128>(prefix_mixed_kernel<128>, args, wide_plan.ctas, st);
 }
 
 }  // namespace tree

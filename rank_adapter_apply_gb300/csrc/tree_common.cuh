@@ -179,12 +179,13 @@ __device__ __noinline__ inline uint64_t seen_keys(const TreeArgs &a, const Reque
     return seen;
 }
 
-// A CTA's share of its class's columns: [lo, hi) of total, dealt to `used` groups of which its is number `group`, and
-// where it starts. false: it has none. scratch: kScratch words and one for each warp. Every thread calls it.
+// A CTA's share of its class's columns: [lo, hi) of total, dealt to `used` groups of which its is number `group`, the
+// tiles in it and where it starts. false: it has none. scratch: kScratch words and one for each warp. Every thread calls
+// it. kUnit: columns without a tile that follow a unit's, for what its beginning and end cost.
 constexpr int kScratch = 2 + kMaxClass;
 struct Share {
     long long lo, hi, total, used;
-    int group;
+    int group, n_tiles;
     Cursor start;
 };
 
@@ -194,7 +195,7 @@ __device__ __forceinline__ long long scaled(long long x, long long y, long long 
     return (p | z) >> 32 == 0 ? (long long)((uint32_t)p / (uint32_t)z) : p / z;
 }
 
-template <int kThreads, bool kPrefix>
+template <int kThreads, bool kPrefix, int kUnit = 0>
 __device__ inline bool find_share(const TreeArgs &a, int m_rows, long long *scratch, Share &s) {
     constexpr int kWarps = kThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_entries = entries<kPrefix>(a);
@@ -218,7 +219,7 @@ __device__ inline bool find_share(const TreeArgs &a, int m_rows, long long *scra
                                                                 (r.row_tiles >= kMaxClass ? 1u << kMaxClass : 0u));
         for (uint32_t left = some; left; left &= left - 1) {
             const int k = __ffs(left) - 1;
-            const long long n = (long long)blocks_of(r.row_tiles, k) * r.key_tiles * a.n_kv;
+            const long long n = (long long)blocks_of(r.row_tiles, k) * (r.key_tiles + kUnit) * a.n_kv;
             const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)n & 0xffffffu);
             const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(n >> 24));
             const unsigned long long sum = lo + ((unsigned long long)hi << 24);
@@ -292,47 +293,87 @@ __device__ inline bool find_share(const TreeArgs &a, int m_rows, long long *scra
         }
         return n;
     };
+    // of an entry with `units` units before it and its columns from `first` on: columns without a tile before column x
+    auto idle = [&](long long x, long long first, long long units, int key_tiles) -> long long {
+        const long long at = x - first, unit = scaled(at, 1, key_tiles + kUnit), rest = at - unit * (key_tiles + kUnit);
+        return (units + unit) * kUnit + max(rest - key_tiles, 0ll);
+    };
     long long before = 0;                                    // columns of the requests before the share's first
+    long long idle_lo = 0, idle_hi = 0;
     if (few) {
-        const long long n = (long long)blocks_of(mine.row_tiles, k) * mine.key_tiles * a.n_kv, upto = scan(n);
+        const long long units = (long long)blocks_of(mine.row_tiles, k) * a.n_kv, n = units * (mine.key_tiles + kUnit);
+        const long long upto = scan(n);
         const int b = __ffs(__ballot_sync(0xffffffffu, upto - n <= s.lo && s.lo < upto)) - 1;
         before = __shfl_sync(0xffffffffu, upto - n, b);
         s.start.b = b;
         s.start.r = {__shfl_sync(0xffffffffu, mine.start, b),     __shfl_sync(0xffffffffu, mine.nodes, b),
                      __shfl_sync(0xffffffffu, mine.row_tiles, b), __shfl_sync(0xffffffffu, mine.key_tiles, b),
                      __shfl_sync(0xffffffffu, mine.ctx, b),       __shfl_sync(0xffffffffu, mine.keys, b)};
+        if constexpr (kUnit > 0) {
+            const long long units_before = scan(units) - units;
+            const int e = __ffs(__ballot_sync(0xffffffffu, upto - n < s.hi && s.hi <= upto)) - 1;
+            idle_lo = idle(s.lo, before, __shfl_sync(0xffffffffu, units_before, b), s.start.r.key_tiles);
+            idle_hi = idle(s.hi, __shfl_sync(0xffffffffu, upto - n, e), __shfl_sync(0xffffffffu, units_before, e),
+                           __shfl_sync(0xffffffffu, mine.key_tiles, e));
+        }
     } else {
-        for (int b0 = 0; b0 < n_entries; b0 += kThreads) {    // ends in the chunk that holds column lo < total
+        long long units_before = 0;
+        if constexpr (kUnit > 0) {                           // the columns have been read: their place is free
+            __syncthreads();
+            if (tid == 0) scratch[3] = -1;
+            __syncthreads();
+        }
+        for (int b0 = 0; b0 < n_entries; b0 += kThreads) {    // ends in the chunk that holds the share's last column
             const int b = b0 + tid;
             if (b0 > 0 && b < n_entries) mine = request<kPrefix>(a, b, m_rows);
-            const long long n = b < n_entries ? (long long)blocks_of(mine.row_tiles, k) * mine.key_tiles * a.n_kv : 0;
+            const long long units = b < n_entries ? (long long)blocks_of(mine.row_tiles, k) * a.n_kv : 0;
+            const long long n = units * (mine.key_tiles + kUnit);
             long long upto = scan(n);
             if (lane == 31) sums[warp] = upto;
             __syncthreads();
             for (int w = 0; w < warp; ++w) upto += sums[w];
             upto += before;
-            if (upto - n <= s.lo && s.lo < upto) scratch[0] = b, scratch[1] = upto - n;
+            const bool first = upto - n <= s.lo && s.lo < upto, last = upto - n < s.hi && s.hi <= upto;
+            if (first) scratch[0] = b, scratch[1] = upto - n;
             for (int w = 0; w < kWarps; ++w) before += sums[w];
             __syncthreads();
-            if (scratch[0] >= 0) break;
+            if constexpr (kUnit > 0) {
+                long long u = scan(units);
+                if (lane == 31) sums[warp] = u;
+                __syncthreads();
+                for (int w = 0; w < warp; ++w) u += sums[w];
+                u += units_before - units;
+                if (first) scratch[2] = idle(s.lo, upto - n, u, mine.key_tiles);
+                if (last) scratch[3] = idle(s.hi, upto - n, u, mine.key_tiles);
+                for (int w = 0; w < kWarps; ++w) units_before += sums[w];
+                __syncthreads();
+                if (scratch[3] >= 0) break;
+            } else if (scratch[0] >= 0) {
+                break;
+            }
         }
         if (scratch[0] < 0) return false;                    // not reached
+        if constexpr (kUnit > 0) idle_lo = scratch[2], idle_hi = scratch[3];
         before = scratch[1];
         s.start.b = (int)scratch[0];
         s.start.r = request<kPrefix>(a, s.start.b, m_rows);
     }
-    const long long at = s.lo - before, unit = scaled(at, 1, s.start.r.key_tiles), block = scaled(unit, 1, a.n_kv);
-    s.start.tile = (int)(at - unit * s.start.r.key_tiles);
+    s.n_tiles = (int)(s.hi - s.lo - (idle_hi - idle_lo));
+    if (s.n_tiles == 0) return false;
+    const int wide = s.start.r.key_tiles + kUnit;
+    const long long at = s.lo - before, unit = scaled(at, 1, wide), block = scaled(unit, 1, a.n_kv);
+    s.start.tile = (int)(at - unit * wide);
     s.start.head = (int)(unit - block * a.n_kv);
     s.start.row_tile = (k == kMaxClass ? (int)block * kMaxClass : s.start.r.row_tiles - k) + s.start.row;
+    if (kUnit > 0 && s.start.tile >= s.start.r.key_tiles) next_unit<kPrefix>(a, s.start, m_rows);
     return true;
 }
 
-// Parts of the unit at cursor c whose tile is the share's tile i and the last of
-// the share: group floor(((x + 1) used - 1) / total) has column x. The CTAs of
-// neighbouring groups with the same row are neighbours.
-__device__ __forceinline__ int parts_of(const Share &s, const Cursor &c, int i) {
-    const long long x = s.lo + i + (c.r.key_tiles - 1 - c.tile);
+// Parts of the unit at cursor c whose tile is the share's last, and not the unit's:
+// group floor(((x + 1) used - 1) / total) has column x. The CTAs of neighbouring
+// groups with the same row are neighbours.
+__device__ __forceinline__ int parts_of(const Share &s, const Cursor &c) {
+    const long long x = s.hi - 1 + (c.r.key_tiles - 1 - c.tile);
     const long long p = (x + 1) * s.used - 1;
     return (int)scaled(p, 1, s.total) - s.group + 1;
 }
@@ -404,11 +445,8 @@ TreeArgs arguments(const lora_tree_attention_desc *d);
 int grid_of_device();
 size_t plan_bytes();
 Plan plan_at(void *workspace, int ctas);
-// The rows of a tile for `rows` of an entry on average: 16, 32 or, where `wide`, 128. The kernel of 16 or 32.
-int rows_of_tile(double rows, bool wide);
-cudaError_t launch_mma(const TreeArgs &a, const Plan &plan, int m_rows, cudaStream_t st);
 
-// prefix_decode.cu: row tiles of 16 by single warps, which become the plan's CTAs (lora_prefix_attention alone).
+// prefix_rows.cu: row tiles of 16 by single warps, which become the plan's CTAs (lora_prefix_attention alone).
 cudaError_t launch_rows(const TreeArgs &a, Plan &plan, cudaStream_t st);
 
 // tree_attention_tc.cu: row tiles of up to 128 on the 5th-generation tensor cores,
@@ -417,6 +455,10 @@ cudaError_t launch_rows(const TreeArgs &a, Plan &plan, cudaStream_t st);
 bool tc_takes(const TreeArgs &a);
 int tc_rows(const TreeArgs &a);
 cudaError_t launch_tc(const TreeArgs &a, const Plan &plan, cudaStream_t st);
+// lora_prefix_attention: the entries of `wide` on that kernel, then, where there are any, those of `narrow` by single warps
+// of the same CTAs, which become its plan's CTAs.
+cudaError_t launch_mixed(const TreeArgs &wide, const Plan &wide_plan, const TreeArgs &narrow, Plan &narrow_plan,
+                         cudaStream_t st);
 // CTAs of its kernel on the current device whose bounded waits gave up so far.
 cudaError_t read_timeouts(unsigned *count);
 
