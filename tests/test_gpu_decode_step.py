@@ -258,6 +258,52 @@ def test_prefix_attention(ops, case, dtype):  # noqa: F811
     _check_prefix(c, *_run_prefix(ops, c))
 
 
+def _widen(c, group_bytes, request_bytes):
+    """Tables as wide as contexts of so many bytes, read 16 rows at a time, would need: entries with more than 16 rows then
+    go to the tiles of 128 (80 MB), and requests with fewer to a launch of their own (500 MB)."""
+    (tokens, heads, dim), (_, page, kv, _) = c["q"].shape, c["kc"].shape
+
+    def wide(table, n, size):
+        each = max(1, -(-tokens * heads // kv // max(n, 1) // 16)) * max(n, 1) * kv * page * dim * 4
+        return np.pad(table, ((0, 0), (0, int(size // each))), constant_values=-1)
+    return dict(c, ptable=wide(c["ptable"], len(c["prefix"]), group_bytes), table=wide(c["table"], len(c["ctx"]), request_bytes))
+
+
+@pytest.mark.parametrize("widths", [(2e8, 0), (2e8, 2e8), (0, 2e8), (2e8, 7e8)])
+@pytest.mark.parametrize("case", PREFIXES[3:], ids=lambda c: f"{len(c[2])}of{c[0]}")
+def test_prefix_attention_wide_tables(ops, case, widths):  # noqa: F811
+    c = _widen(_prefix_case(*case, "bf16", seed=9), *widths)
+    _check_prefix(c, *_run_prefix(ops, c))
+
+
+@pytest.mark.parametrize("members", [9, 30])
+@pytest.mark.parametrize("nodes", [1, 20])
+@pytest.mark.parametrize("widths", [(2e8, 0), (2e8, 2e8), (2e8, 7e8)])
+def test_prefix_attention_wide_tables_edges(ops, widths, nodes, members):  # noqa: F811
+    """Entries without keys or rows, page ids and lengths out of range, values that are not finite, on the same routes."""
+    import torch
+    n = members + 7
+    c = _widen(_prefix_case([150, 0, 700, 90], [members, 2, 1, 2], [20, 0, 64] * (n // 3) + [1] * (n % 3),
+                            [nodes, 1, 0] * (n // 3) + [1] * (n % 3), 8, 1, 64, 16, "bf16", seed=10, first=1, spare_rows=3), *widths)
+    c["ptable"][0, 1], c["ptable"][2, 4], c["ptable"][3, 2] = -1, c["kc"].shape[0], 1 << 30
+    c["mask"][0] = False
+    c["bits"][0] = 0
+    want = _run_prefix(ops, c)
+    _check_prefix(c, *want)
+    c["ctx"][0] = -3
+    _check_prefix(c, *_run_prefix(ops, c))
+    c["ctx"][0] = 20
+    d = dict(c, vc=c["vc"].clone())
+    d["vc"][int(c["ptable"][0, 0]), 3, 0, 5] = float("inf")
+    out, lse = _run_prefix(ops, d)
+    rows = slice(int(c["starts"][1]), int(c["starts"][1 + members]))
+    assert (out[rows, :, 5] == float("inf")).all() and torch.equal(lse[:-3], want[1][:-3])
+    keep = torch.ones_like(out, dtype=torch.bool)
+    keep[rows, :, 5] = False
+    keep[-3:] = False
+    assert ((out - want[0]).abs()[keep] <= 2.0 ** -6 * (1 + want[0].abs()[keep])).all()     # both near the same values
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("case", [PREFIXES[6], PREFIXES[8], PREFIXES[11]], ids=lambda c: f"{len(c[2])}of{c[0]}")
 def test_prefix_attention_chain(ops, case, dtype):  # noqa: F811
