@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
             fresh = true;
         }
         if (i + kStages < n_tiles) store_off(i + kStages, pending);
-        next_tile<false>(a, c, T::M);
+        if (i + 1 < n_tiles) next_tile<false>(a, c, T::M);
     }
 }
 

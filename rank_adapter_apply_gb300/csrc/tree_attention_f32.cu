@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_f32_kernel(TreeArgs a, Plan 
             if (!kPrefix && tid == 0 && starts && !ends)
                 plan.seg[blockIdx.x] = make_int4(c.b, c.row_tile, c.head, parts_of(share, c));
         }
-        next_tile<kPrefix>(a, c, M);
+        if (i + 1 < n_tiles) next_tile<kPrefix>(a, c, M);
     }
 }
 

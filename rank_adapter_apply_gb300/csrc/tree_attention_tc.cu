@@ -42,9 +42,10 @@ constexpr int kRows = 128;                     // lanes of an accumulator; rows 
 constexpr int kThreads = 192;
 constexpr int kItems = 5;                      // ring of K and V items
 constexpr int kMeta = 4;                       // ring of the tiles' masks
-// Tiles that a unit's beginning and end are worth in lora_prefix_attention's shares. us with 0 / 2 / 4: requests of 16x16
-// of 1000 52 / 44 / 43, 37x7 of 3001 71 / 70 / 68, 64x1 of 8192 81 / 80 / 78. (6: 41, 65, 108.)
-constexpr int kUnitTiles = 4;
+// Tiles that a unit's beginning and end are worth in lora_prefix_attention's shares. us with 4 / 8 / 12: requests of 16x16
+// of 1000 30.8 / 31.2 / 29.8, 37x7 of 3001 36.2 / 35.9 / 38.8, 64x1 of 8192 76.9 / 73.9 / 73.7, 256x1 of 32768
+// 374 / 375 / 377.
+constexpr int kUnitTiles = 8;
 constexpr uint32_t kWaitLimit = 1u << 18;       // polls, of some microseconds each: about a second
 
 template <int DP>
@@ -165,10 +166,6 @@ __device__ __forceinline__ void tc_work(const TcArgs &args, unsigned char *smem)
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), group = a.n_heads / a.n_kv;
     const int rows = kRows / group * group;            // of a tile
     const int cta = blockIdx.x;
-    if (!kPrefix && tid == 0) plan.seg[cta] = make_int4(0, 0, 0, 0);
-    Share share;
-    if (!find_share<kThreads, kPrefix, kPrefix ? kUnitTiles : 0>(a, rows, scratch, share)) return;
-    const int n_tiles = share.n_tiles;
     if (tid == 0) {
         for (int i = 0; i < kItems; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         for (int i = 0; i < kMeta; ++i) mbar_init(&meta_full[i], 1);
@@ -183,10 +180,32 @@ __device__ __forceinline__ void tc_work(const TcArgs &args, unsigned char *smem)
         tc::prefetch_tensormap(&args.k);
         tc::prefetch_tensormap(&args.v);
     }
+    // An SM takes its second CTA only when the first has given up the right to allocate, here and not after the share is
+    // found, 4 us later: a CTA without a share gave it up only at its end, and the second one began 44 us late. Kernels
+    // that come after may allocate only when all of this one's CTAs have, before launch_dependents: each could have what
+    // the other waits for.
+    grid_dependency_wait();
     if (warp == 5) {
         tc::tmem_alloc(&tmem_base, 256);
         tc::tmem_relinquish();
+        grid_launch_dependents();                      // the join kernel waits for this grid's end itself
     }
+    if (!kPrefix && tid == 0) plan.seg[cta] = make_int4(0, 0, 0, 0);
+    Share share;
+    const bool any = find_share<kThreads, kPrefix, kPrefix ? kUnitTiles : 0>(a, rows, scratch, share);
+    auto free_tmem = [&]() {
+        tc::fence_before_sync();
+        __syncthreads();
+        if (warp == 5) {
+            tc::fence_after_sync();
+            tc::tmem_dealloc(tmem_base, 256);
+        }
+    };
+    if (!any) {
+        free_tmem();
+        return;
+    }
+    const int n_tiles = share.n_tiles;
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -288,7 +307,7 @@ __device__ __forceinline__ void tc_work(const TcArgs &args, unsigned char *smem)
             }
             if (i > 0 && !load(&args.v, last)) break;
             last = here;
-            next_tile<kPrefix>(a, u, rows);
+            if (i + 1 < n_tiles) next_tile<kPrefix>(a, u, rows);
         }
         if (i == n_tiles) load(&args.v, last);
         // no copy is in flight when the CTA ends
@@ -494,8 +513,10 @@ __device__ __forceinline__ void tc_work(const TcArgs &args, unsigned char *smem)
                         }
                     } else if (mine) {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            *reinterpret_cast<uint4 *>(part + d + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                        for (int k = 0; k < 32; k += 8)       // whole sectors: a thread writes a row
+                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(part + d + k),
+                                         "r"(o[k]), "r"(o[k + 1]), "r"(o[k + 2]), "r"(o[k + 3]), "r"(o[k + 4]),
+                                         "r"(o[k + 5]), "r"(o[k + 6]), "r"(o[k + 7]) : "memory");
                     }
                     __syncwarp();
                 }
@@ -507,23 +528,16 @@ __device__ __forceinline__ void tc_work(const TcArgs &args, unsigned char *smem)
                 tc::fence_before_sync();
             }
             __syncwarp();
-            next_tile<kPrefix>(a, c, rows);
+            if (i + 1 < n_tiles) next_tile<kPrefix>(a, c, rows);
         }
     }
-    tc::fence_before_sync();
-    __syncthreads();
+    free_tmem();
     if (tid == 0 && error) atomicAdd(&g_gave_up, 1u);
-    if (warp == 5) {
-        tc::fence_after_sync();
-        tc::tmem_dealloc(tmem, 256);
-    }
 }
 
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_constant__ TcArgs args) {
     extern __shared__ __align__(1024) unsigned char smem[];
-    grid_dependency_wait();
-    grid_launch_dependents();                          // the join kernel waits for this grid's end itself
     tc_work<DP, false>(args, smem);
 }
 
@@ -540,8 +554,6 @@ template <int DP>
 __global__ void __launch_bounds__(kThreads, 2) prefix_mixed_kernel(const __grid_constant__ MixedArgs args) {
     extern __shared__ __align__(1024) unsigned char smem[];
     static_assert(sizeof(rows::Memory<DP, kNarrowWarps, kThreads>) <= Tc<DP>::kSmem, "the rings fit");
-    grid_dependency_wait();
-    grid_launch_dependents();
     tc_work<DP, true>(args.wide, smem);
     if (args.narrow.count == 0) return;
     __syncthreads();                                   // shared memory changes hands

@@ -140,16 +140,30 @@ struct Cursor {
     int b, row_tile, head, tile, k, row;
 };
 
+// The next request of the class is looked for by the whole warp, 32 at a time: one after the other they took 18 us of a
+// CTA whose class has few requests among 41. All lanes call it with the same cursor.
 template <bool kPrefix>
 __device__ __noinline__ inline void next_unit(const TreeArgs &a, Cursor &c, int m_rows) {
     c.tile = 0;
     if (++c.head < a.n_kv) return;
     c.head = 0;
     if (c.k == kMaxClass && (c.row_tile += kMaxClass) / kMaxClass < c.r.row_tiles / kMaxClass) return;
-    do {
-        if (++c.b >= entries<kPrefix>(a)) return;
-        c.r = request<kPrefix>(a, c.b, m_rows);
-    } while (blocks_of(c.r.row_tiles, c.k) == 0);
+    const int n = entries<kPrefix>(a), lane = threadIdx.x & 31;
+    uint32_t found = 0;
+    for (int b0 = c.b + 1; found == 0; b0 += 32) {
+        if (b0 >= n) {
+            c.b = n;
+            return;
+        }
+        Request r{};
+        if (b0 + lane < n) r = request<kPrefix>(a, b0 + lane, m_rows);
+        found = __ballot_sync(0xffffffffu, blocks_of(r.row_tiles, c.k) > 0);
+        const int at = __ffs(found) - 1;                     // -1, of nobody: any lane
+        c.b = b0 + at;
+        c.r = {__shfl_sync(0xffffffffu, r.start, at),     __shfl_sync(0xffffffffu, r.nodes, at),
+               __shfl_sync(0xffffffffu, r.row_tiles, at), __shfl_sync(0xffffffffu, r.key_tiles, at),
+               __shfl_sync(0xffffffffu, r.ctx, at),       __shfl_sync(0xffffffffu, r.keys, at)};
+    }
     c.row_tile = (c.k == kMaxClass ? 0 : c.r.row_tiles - c.k) + c.row;
 }
 
