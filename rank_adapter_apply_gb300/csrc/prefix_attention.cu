@@ -123,16 +123,21 @@ cudaError_t launch_prefix(const TreeArgs &a, const Plan &groups, const Plan &req
     constexpr bool kBf16 = sizeof(T) == 2;
     const double group = a.n_heads / a.n_kv;
     JoinArgs join{a, {groups, requests}, {0, 0}};
-    // Rows of a tile for n entries with up to `keys` keys. In bf16 the warps' tiles of 16 read the keys again for each tile,
-    // mostly from L2; the 5th-generation tensor cores read them once for 128 rows, but their kernel takes some 20 us.
-    // Bytes read by the warps, and us with both kinds on 16 / with the wide one on 128: 55 MB (100x2 of 300) 43 / 62, 65 MB
-    // (16x1 of 4000 in 2 groups) 24 / 34, 98 MB (requests of 16x16 of 1000) 57 / 48, 201 MB (12x1 of 16384) 45 / 39
+    // Rows of a tile for n entries with up to so many pages of keys. In bf16 the warps' tiles of 16 read the keys again for
+    // each tile, mostly from L2; the 5th-generation tensor cores read them once for 128 rows, but their kernel takes some
+    // 20 us. Bytes read by the warps, and us with both kinds on 16 / with the wide one on 128: 55 MB (100x2 of 300) 43 / 62,
+    // 65 MB (16x1 of 4000 in 2 groups) 24 / 29, 98 MB (requests of 16x16 of 1000) 57 / 31, 201 MB (12x1 of 16384) 45 / 36.
+    // In fp32 tiles of 64 rows feed the FMA units better, and take a launch of their own beside 16: all wide entries take
+    // them, or none. us with 16 / 64: 8 MB (8x4 of
+    // 500) 15 / 29, 20 MB (24x2 of 1024) 28 / 32, 50 MB (32x2 of 2000) 46 / 45, 262 MB (32x4 of 4000) 153 / 91
     auto rows_of = [&](int n) { return a.n_tokens * group / std::max(n, 1); };
     auto bytes = [&](int n, double pages) {
-        return std::ceil(rows_of(n) / 16.0) * n * a.n_kv * pages * a.page_size * a.head_dim * 4.0;
+        return std::ceil(rows_of(n) / 16.0) * n * a.n_kv * pages * a.page_size * a.head_dim * 2.0 * sizeof(T);
     };
+    auto wide_bytes = [&](int n, int pages) { return rows_of(n) <= 16.0 ? 0.0 : bytes(n, pages); };
+    const double wide = wide_bytes(a.n_groups, a.prefix_pages) + wide_bytes(a.n_requests, a.table_pages);
     auto tile = [&](int n, int pages) {
-        if (!kBf16) return rows_of(n) <= 16.0 ? 16 : 64;
+        if (!kBf16) return rows_of(n) <= 16.0 || wide <= 30e6 ? 16 : 64;
         return rows_of(n) <= 16.0 || bytes(n, pages) <= 80e6 || !tc_takes(a) ? 16 : 128;
     };
     int of_requests = tile(a.n_requests, a.table_pages);
@@ -156,7 +161,7 @@ cudaError_t launch_prefix(const TreeArgs &a, const Plan &groups, const Plan &req
         } else if (of_groups == 128) {
             // The few rows of requests behind the groups' share in one launch save its latency; in their own they have eight
             // warps of an SM with more registers, and shares that all begin at once. us in one / in two: 12x1 of 16384 (up to
-            // 13 MB of requests) 36 / 39, 64x1 of 8192 (285 MB) 78 / 82, 256x1 of 32768 (1.1 GB) 398 / 380
+            // 13 MB of requests) 36 / 39, 64x1 of 8192 (285 MB) 74 / 78, 256x1 of 32768 (1.1 GB) 392 / 375
             const bool apart = bytes(a.n_requests, a.table_pages) > 500e6;
             Plan none = plan[1];
             e = launch_mixed(groups_alone, plan[0], apart ? entries_of(a, 0, 0) : requests_alone, apart ? none : plan[1], st);
