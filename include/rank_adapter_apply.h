@@ -758,7 +758,8 @@ int lora_tree_attention(const lora_tree_attention_desc *desc, void *stream);
  * page id outside [0, n_pages) are not seen, group_starts are clamped to
  * [0, n_requests]. Where starts (node_starts, group_starts) fall, the rows between
  * the first and the last are not defined. tree.workspace:
- * lora_prefix_attention_workspace_bytes(...). A call queues two or three kernels.
+ * lora_prefix_attention_workspace_bytes(...). A call queues two or three kernels,
+ * chosen by the mean rows of an entry and by how many keys the tables hold room for.
  * All else is as lora_tree_attention says.
  */
 typedef struct {
@@ -777,8 +778,8 @@ size_t lora_prefix_attention_workspace_bytes(int n_requests, int n_groups, int n
 
 int lora_prefix_attention(const lora_prefix_attention_desc *desc, void *stream);
 
-/* *count = thread blocks of lora_base_linear and lora_tree_attention on the
- * current device whose bounded device-side waits gave up so far; their rows are
+/* *count = thread blocks of lora_base_linear, lora_tree_attention and
+ * lora_prefix_attention on the current device whose bounded device-side waits gave up so far; their rows are
  * wrong (never expected). Synchronises the device, all streams. */
 int lora_step_wait_timeouts(uint64_t *count);
 

