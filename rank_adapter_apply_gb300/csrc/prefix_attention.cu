@@ -9,11 +9,11 @@
 // O = sum 2^(m_i - m) O_i, l = sum 2^(m_i - m) l_i, m = max m_i, out = O / l.
 //
 // 64 requests behind two prefixes of 8192, own contexts of up to 1000, 32 heads over 8 of 128:
-// 74 us; keys and values are read in 29. Of it the prefixes take 25, the requests' keys 30
-// at 5 TB/s, the rest are the beginnings of the three parts and the join. 256 requests behind
-// 32768 keys, 64 heads over 8: 375 us, the products alone 148; the prefix's part runs at 650
+// 69 us; keys and values are read in 29. Of it the prefixes take 25, the requests' keys some
+// 25 at 5 TB/s, the rest are the beginnings of the three parts and the join. 256 requests behind
+// 32768 keys, 64 heads over 8: 374 us, the products alone 148; the prefix's part runs at 650
 // TFLOP/s (a unit's chain of scores, softmax, second product), the requests' 0.5 GB at 5 TB/s.
-// 3 requests behind 777: 13.5 us, two launches and five dependent reads.
+// 3 requests behind 777: 12.6 us, two launches and five dependent reads.
 #include "tree_common.cuh"
 
 #include <algorithm>
@@ -166,13 +166,7 @@ cudaError_t launch_prefix(const TreeArgs &a, const Plan &groups, const Plan &req
             e = launch_mixed(all, plan[1], entries_of(a, 0, 0), plan[0], st);
             plan[0] = plan[1];
         } else if (of_groups == 128) {
-            // The few rows of requests behind the groups' share in one launch save its latency; in their own they have eight
-            // warps of an SM with more registers, and shares that all begin at once. us in one / in two: 12x1 of 16384 (up to
-            // 13 MB of requests) 36 / 39, 64x1 of 8192 (285 MB) 74 / 78, 256x1 of 32768 (1.1 GB) 392 / 375
-            const bool apart = bytes(a.n_requests, a.table_pages) > 500e6;
-            Plan none = plan[1];
-            e = launch_mixed(groups_alone, plan[0], apart ? entries_of(a, 0, 0) : requests_alone, apart ? none : plan[1], st);
-            if (e == cudaSuccess && apart) e = launch_rows(requests_alone, plan[1], st);
+            e = launch_mixed(groups_alone, plan[0], requests_alone, plan[1], st);
         } else if (of_requests == 128) {
             e = launch_mixed(requests_alone, plan[1], groups_alone, plan[0], st);
         }

@@ -544,9 +544,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_tc_kernel(const __grid_const
 }
 
 // lora_prefix_attention: the wide row tiles, then, as each CTA is done with its share of them, the few rows of the other
-// entries: one launch, and nobody waits for the slowest share. (Wide and narrow CTAs side by side, so that one
-// kind's products overlap the other's reads, were slower: one CTA of this kernel on an SM has half the pace of two.)
-constexpr int kNarrowWarps = 4;
+// entries by all six warps: one launch, and nobody waits for the slowest share. us in one launch / in two: 12x1 of 16384
+// (up to 13 MB of requests) 36 / 39, 64x1 of 8192 (285 MB) 69 / 77, 256x1 of 32768 (1.1 GB) 373 / 375; with four warps 36,
+// 73 and 390. (Wide and narrow CTAs side by side, so that one kind's products overlap the other's reads, were slower:
+// one CTA of this kernel on an SM has half the pace of two.)
+constexpr int kNarrowWarps = 6;
 struct MixedArgs {
     TcArgs wide;
     TreeArgs narrow;

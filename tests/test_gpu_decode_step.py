@@ -260,7 +260,7 @@ def test_prefix_attention(ops, case, dtype):  # noqa: F811
 
 def _widen(c, group_bytes, request_bytes):
     """Tables as wide as contexts of so many bytes, read 16 rows at a time, would need: entries with more than 16 rows then
-    go to the tiles of 128 (80 MB), and requests with fewer to a launch of their own (500 MB)."""
+    go to the tiles of 128 (80 MB)."""
     (tokens, heads, dim), (_, page, kv, _) = c["q"].shape, c["kc"].shape
 
     def wide(table, n, size):
