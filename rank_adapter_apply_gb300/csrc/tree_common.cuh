@@ -348,7 +348,12 @@ __device__ inline bool find_share(const TreeArgs &a, int m_rows, long long *scra
             for (int w = 0; w < warp; ++w) upto += sums[w];
             upto += before;
             const bool first = upto - n <= s.lo && s.lo < upto, last = upto - n < s.hi && s.hi <= upto;
-            if (first) scratch[0] = b, scratch[1] = upto - n;
+            if (first) {
+                scratch[0] = b, scratch[1] = upto - n;
+                const int words[] = {mine.start, mine.nodes, mine.row_tiles, mine.key_tiles, mine.ctx, mine.keys};
+#pragma unroll
+                for (int i = 0; i < 6; ++i) reinterpret_cast<int *>(scratch + 4)[i] = words[i];
+            }
             for (int w = 0; w < kWarps; ++w) before += sums[w];
             __syncthreads();
             if constexpr (kUnit > 0) {
@@ -370,7 +375,8 @@ __device__ inline bool find_share(const TreeArgs &a, int m_rows, long long *scra
         if constexpr (kUnit > 0) idle_lo = scratch[2], idle_hi = scratch[3];
         before = scratch[1];
         s.start.b = (int)scratch[0];
-        s.start.r = request<kPrefix>(a, s.start.b, m_rows);
+        const int *r = reinterpret_cast<const int *>(scratch + 4);
+        s.start.r = {r[0], r[1], r[2], r[3], r[4], r[5]};
     }
     s.n_tiles = (int)(s.hi - s.lo - (idle_hi - idle_lo));
     if (s.n_tiles == 0) return false;
