@@ -11,8 +11,8 @@
 // 64 requests behind two prefixes of 8192, own contexts of up to 1000, 32 heads over 8 of 128:
 // 69 us; keys and values are read in 29. Of it the prefixes take 25, the requests' keys some
 // 25 at 5 TB/s, the rest are the beginnings of the three parts and the join. 256 requests behind
-// 32768 keys, 64 heads over 8: 374 us, the products alone 148; the prefix's part runs at 650
-// TFLOP/s (a unit's chain of scores, softmax, second product), the requests' 0.5 GB at 5 TB/s.
+// 32768 keys, 64 heads over 8: 370 us, the products alone 148; the prefix's part runs at 1.2
+// PFLOP/s (the chain of scores, softmax, second product), the requests' 0.5 GB at 5 TB/s.
 // 3 requests behind 777: 12.6 us, two launches and five dependent reads.
 #include "tree_common.cuh"
 

@@ -284,6 +284,21 @@ def test_prefix_attention_wide_tables_fp32(ops, case, widths):  # noqa: F811
     _check_prefix(c, *_run_prefix(ops, c))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nodes,request_bytes", [(1, 0), (5, 2e8)])
+def test_prefix_attention_many_entries(ops, nodes, request_bytes, dtype):  # noqa: F811
+    """More entries than threads of any block that finds its share among them; some have no rows."""
+    import torch
+    n = 290
+    sizes = [0 if i % 29 == 7 else nodes + i % 2 for i in range(n)]
+    c = _widen(_prefix_case([70, 0, 33] * 20, [4, 3, 5] * 20, [(7 * i) % 90 for i in range(n)], sizes, 4, 1, 64, 16, dtype,
+                            seed=12, first=20), 2e8, request_bytes)
+    out, lse = _run_prefix(ops, c)
+    _check_prefix(c, out, lse)
+    again, _ = _run_prefix(ops, c)
+    assert torch.equal(out, again)
+
+
 @pytest.mark.parametrize("members", [9, 30])
 @pytest.mark.parametrize("nodes", [1, 20])
 @pytest.mark.parametrize("widths", [(2e8, 0), (2e8, 2e8), (2e8, 7e8)])
