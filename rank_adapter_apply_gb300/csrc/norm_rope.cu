@@ -7,8 +7,8 @@
 // between the norm and the rotation nothing is rounded or written. A row is read once
 // and written once, as in lora_rope, whose layout of threads it keeps.
 //
-// 16384 tokens, 64 + 8 + 8 heads of 128 in bf16: 128 us, 5.3 TB/s of 6.8 (100 us); issue slots
-// are busy for 63 % and waits for the arithmetic's own results are the first stall. 8 tokens
+// 16384 tokens, 64 + 8 + 8 heads of 128 in bf16: 123 us, 5.5 TB/s of 6.8 (100 us); issue slots
+// are busy for two thirds and waits for the arithmetic's own results are the first stall. 8 tokens
 // 2.2 us in a graph, the launch and one chain of reads.
 #include "rope_common.cuh"
 
@@ -254,9 +254,10 @@ __global__ void __launch_bounds__(256) norm_vectors_kernel(NormArgs n) {
 // Many rows: a block goes over tokens, `rounds` rows of a token to a thread, with the rows and
 // angles of the next kStages - 1 tokens on their way to shared memory. Rows do not wait for
 // the token's position, which is read a token earlier than its angles. (Blocks of one token each
-// wait for position, rows and angles in turn: 145 us for 16384 tokens of 64 + 8 heads.) kTail: a
-// row has fewer than two vectors for each of its lanes.
-constexpr int kStages = 2, kStreamThreads = 160, kStreamBlocks = 4;   // blocks of an SM
+// wait for position, rows and angles in turn: 145 us for 16384 tokens of 64 + 8 heads.) Threads x
+// blocks of an SM for the same: 96 x 5 124 us, 128 x 4 126, 128 x 5 123, 160 x 4 128, 192 x 4 156,
+// 320 x 2 157. kTail: a row has fewer than two vectors for each of its lanes.
+constexpr int kStages = 2, kStreamThreads = 128, kStreamBlocks = 5;   // blocks of an SM
 
 struct Stream {
     int rounds, chunk;                                     // chunk: rows of a token that a block takes
@@ -404,7 +405,9 @@ cudaError_t launch_stream(const NormArgs &n, int units, int sms, cudaStream_t st
     how.rounds = rounds;
     how.chunk = per;
     how.stage_bytes = rounds * y * units * 32 + n.r.rot_dim * 4;
-    const int blocks = std::max(std::min(n.r.n_tokens, kStreamBlocks * sms / chunks), 1);
+    // as many blocks as run at once: of the largest stages four fit an SM's 228 KB, each with 1 KB of the system's
+    const int fit = std::min(kStreamBlocks, 228 * 1024 / (kStages * how.stage_bytes + 1024 + 128));
+    const int blocks = std::max(std::min(n.r.n_tokens, fit * sms / chunks), 1);
     return launch_step(kernel, dim3(blocks, chunks), dim3(units, y), (size_t)kStages * how.stage_bytes, 1, st, n, how);
 }
 
@@ -416,9 +419,9 @@ cudaError_t launch_norm(const NormArgs &n, int sms, cudaStream_t st) {
     while (units < (a.head_dim / (int)(16 / sizeof(T)) + 1) / 2) units *= 2;
     if (units <= 32 && by_vectors<T>(a, kInterleaved) && weights_by_vectors<T>(n)) {
         // The stream's blocks need a few tokens each, and a token two rounds. In bf16, 32 + 8 heads of 128, rows one by one /
-        // streamed: 512 tokens 4.9 / 5.0 us, 1024 8.1 / 8.7, 2048 17.0 / 16.7, 4096 33.0 / 28.1, 8192 68 / 54; 8 + 2 heads of
-        // 64, 4096 tokens 5.9 / 9.7
-        if (rows <= 600ll * sms || (a.n_heads + 2 * a.n_kv) * units < 256) return launch_vectors<T, kInterleaved>(n, units, st);
+        // streamed: 512 tokens 4.9 / 5.1 us, 1024 8.1 / 8.1, 2048 17.0 / 13.9, 4096 33.0 / 24.9, 8192 68 / 45; 16 + 4 heads of
+        // 256, 2000 tokens 16.9 / 14.1; 8 + 2 heads of 64, 4096 tokens 5.9 / 9.7
+        if (rows <= 300ll * sms || (a.n_heads + 2 * a.n_kv) * units < 256) return launch_vectors<T, kInterleaved>(n, units, st);
         return units * 2 * (int)(16 / sizeof(T)) == a.head_dim ? launch_stream<T, kInterleaved, false>(n, units, sms, st)
                                                                : launch_stream<T, kInterleaved, true>(n, units, sms, st);
     }
