@@ -132,11 +132,11 @@ cudaError_t launch_prefix(const TreeArgs &a, const Plan &groups, const Plan &req
     JoinArgs join{a, {groups, requests}, {0, 0}};
     // Rows of a tile for n entries with up to so many pages of keys. In bf16 the warps' tiles of 16 read the keys again for
     // each tile, mostly from L2; the 5th-generation tensor cores read them once for 128 rows, but their kernel takes some
-    // 20 us. Bytes read by the warps, and us with both kinds on 16 / with the wide one on 128: 55 MB (100x2 of 300) 43 / 62,
-    // 65 MB (16x1 of 4000 in 2 groups) 24 / 29, 98 MB (requests of 16x16 of 1000) 57 / 31, 201 MB (12x1 of 16384) 45 / 36.
+    // 20 us. Bytes read by the warps, and us with both kinds on 16 / with the wide one on 128: 55 MB (100x2 of 300) 40 / 62,
+    // 65 MB (16x1 of 4000 in 2 groups) 23 / 29, 142 MB (requests of 16x16 of 1000) 49 / 31, 201 MB (12x1 of 16384) 45 / 36.
     // In fp32 tiles of 64 rows feed the FMA units better, and take a launch of their own beside 16: all wide entries take
-    // them, or none. us with 16 / 64: 8 MB (8x4 of
-    // 500) 15 / 29, 20 MB (24x2 of 1024) 28 / 32, 50 MB (32x2 of 2000) 46 / 45, 262 MB (32x4 of 4000) 153 / 91
+    // them, or none. us with 16 / 64: 8 MB (8x4 of 500) 15 / 29, 20 MB (24x2 of 1024) 28 / 32, 50 MB (32x2 of 2000)
+    // 46 / 45, 262 MB (32x4 of 4000) 153 / 91
     auto rows_of = [&](int n) { return a.n_tokens * group / std::max(n, 1); };
     auto bytes = [&](int n, double pages) {
         return std::ceil(rows_of(n) / 16.0) * n * a.n_kv * pages * a.page_size * a.head_dim * 2.0 * sizeof(T);

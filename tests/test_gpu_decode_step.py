@@ -806,3 +806,30 @@ def test_tensor_form_refusals(ops):  # noqa: F811
         att(q[:, :3], kc, vc, *s["prefix"])
     with pytest.raises(LoraError, match="vocab"):
         draw(s["logits"][:, :0], s["noise"][:, :0])
+
+
+def test_wide_prefixes_on_two_streams_and_replayed(ops):  # noqa: F811
+    """Calls that fill the SMs' tensor memory, eager on two streams at once beside a graph of others: all as alone."""
+    import torch
+    cases = [_widen(_prefix_case([500, 90], [20, 9], [40, 0, 7] * 10, [nodes] * 30, 8, 1, 64, 16, "bf16", seed=20 + nodes),
+                    2e8, size) for nodes, size in ((1, 0), (3, 2e8), (5, 0))]
+    i32 = lambda a: _dev(np.asarray(a, np.int32))  # noqa: E731
+    args = [(c["q"], c["kc"], c["vc"], i32(c["ptable"]), i32(c["prefix"]), i32(c["groups"]), i32(c["table"]), i32(c["ctx"]),
+             i32(c["starts"]), c["bits"]) for c in cases]
+    want = [ops.prefix_attention(*a) for a in args]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        replayed = [ops.prefix_attention(*a) for a in args * 4]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    graph.replay()
+    eager = []
+    for turn in range(6):
+        for s, first in zip(streams, (0, 1)):
+            with torch.cuda.stream(s):
+                eager.append((first, ops.prefix_attention(*args[first])))
+    torch.cuda.synchronize()
+    for i, (out, lse) in enumerate(replayed):
+        assert torch.equal(out, want[i % 3][0]) and torch.equal(lse, want[i % 3][1])
+    for i, (out, lse) in eager:
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
