@@ -93,20 +93,22 @@ __device__ __forceinline__ void st_peer(uint32_t cluster_addr, uint32_t a, uint3
 
 __device__ __forceinline__ float warp_max(float v) { return unordered(__reduce_max_sync(0xffffffffu, ordered(v))); }
 
-// p / noise exactly, of a token with p >= min_p. Not inlined: few tokens come to it, and it would be in the loops' way.
+// p / noise exactly, of a token that may be drawn: with p >= min_p, and 2^-126 (the loops' exponential flushes what is
+// smaller, so that a limit is needed that holds wherever a token is looked at). Not inlined: few tokens come to it, and it
+// would be in the loops' way.
 __device__ __noinline__ float quotient(float below_top, float inv_t, float min_p, float n) {
     const float p = expf(below_top * inv_t);
-    return p >= min_p ? __fdiv_rn(p, n) : -1.f;
+    return p >= fmaxf(min_p, FLT_MIN) ? __fdiv_rn(p, n) : -1.f;
 }
 
-// The largest p / noise yet, and a little less: what is below it need not be divided.
+// The largest p / noise yet, and twice a little less: what has a 2 p / noise below it need not be divided.
 struct Race {
     float top = 0.f, low = 0.f, x = 0.f, noise = 0.f;
     int at = -1;
     __device__ __forceinline__ void enter(int v, float key, float xv, float nv) {
-        // 2^-15: more than the fast exponential is off by
+        // 2^-15: more than the fast exponential and quotient's are apart
         if (key > top || (key == top && v < at))
-            top = key, at = v, x = xv, noise = nv, low = fmaxf(low, fminf(key, FLT_MAX) * (1.f - 0x1p-15f));
+            top = key, at = v, x = xv, noise = nv, low = fmaxf(low, fminf(key, 0.5f * FLT_MAX) * (2.f - 0x1p-14f));
     }
     // the warp's best in all lanes: positive floats order as their bits do, the lower index wins a tie
     __device__ __forceinline__ void of_warp() {
@@ -123,6 +125,17 @@ struct Race {
         at = first;
     }
 };
+
+// What p / noise of a token above the limit, of parts whose winners are below it, stays under: p of their winners is below
+// 2^-126, and no p / noise of theirs is above the winner's.
+__device__ __noinline__ float most_behind(const Part *parts, int n_parts, float top, float inv_t) {
+    float most = 0.f;
+    for (int i = threadIdx.x & 31; i < n_parts; i += 32) {
+        const Part p = parts[i];
+        if (p.at >= 0 && quotient(p.x - top, inv_t, 0.f, p.noise) < 0.f) most = fmaxf(most, __fdiv_rn(2.f * FLT_MIN, p.noise));
+    }
+    return warp_max(most);
+}
 
 // A row belongs to the CTAs of a cluster, which keep its logits in shared memory (what
 // is past 64 KB of a CTA is read again). Nothing is sorted:
@@ -303,8 +316,13 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(Sample
         limit.x = -warp_max(-r);
     }
     if (dense_row || top > -INFINITY) {
-        // within 2^-17 where it is not below 2^-126; by the maximum that is known: the CTA's in a dense row's first round
+        // By the maximum that is known: the CTA's in a dense row's first round. The roundings of the difference, of 1 / t, of
+        // c2 and of the product move the argument by 2^-24 of itself each, and p by as much of |ln p|: with the constant's and
+        // the exponential's own, p is within 2^-24 (5 |ln p| + 4) where it is not below 2^-126. quotient's argument shares the
+        // first two: for |ln p| up to 87.4 the two are apart by less than 2^-15.5.
         auto about = [&](float x) { return exp2_fast((x - top) * c2); };
+        // 2 p as near: not flushed for any p that quotient takes
+        auto twice = [&](float x) { return exp2_fast(fmaf(x - top, c2, 1.f)); };
         // no logit below this has p >= min_p
         const float floor_x = min_p > 0.f ? top + (logf(min_p) - 0.01f) / inv_t - fabsf(top) * 0x1p-22f : -INFINITY;
         const bool by_mass = top_p < 1.f, tested = !first_only && (by_mass || top_k < a.vocab);
@@ -329,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(Sample
                 const bool in_vectors = !kGated || (reinterpret_cast<uintptr_t>(noise + base) & 15) == 0;
                 const int end = kGated ? n_vec : held;
                 alignas(16) float nv[kBatch][N], next[kBatch][N];
+                if (!kGated) sum *= 2.f;                     // so are the p that are added
                 auto load = [&](int j0) {
 #pragma unroll
                     for (int b = 0; b < kBatch; ++b) {
@@ -351,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(Sample
 #pragma unroll
                     for (int i = 0; i < kBatch * N; ++i) nv[i / N][i % N] = next[i / N][i % N];
                     load(j0 + kBatch * kThreads);
-                    float x[kBatch][N], p[kBatch][N];
+                    float x[kBatch][N], p[kBatch][N];        // p: twice p
 #pragma unroll
                     for (int b = 0; b < kBatch; ++b) {
                         const int j = j0 + lane + b * kThreads;
@@ -363,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(Sample
                         }
 #pragma unroll
                         for (int e = 0; e < N; ++e) {
-                            p[b][e] = about(x[b][e]);
+                            p[b][e] = twice(x[b][e]);
                             if (!kGated) sum += p[b][e];
                             if (kGated && !(x[b][e] >= gate)) p[b][e] = 0.f;
                         }
@@ -395,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(Sample
                         if (!kGated && lane == 0) atomicMax(&bound, __float_as_uint(race.low));
                     }
                 }
+                if (!kGated) sum *= 0.5f;
             };
             const bool all_in = dense_row && round == 0;
             if (top > -INFINITY) {                   // a CTA of a dense row may have nothing
@@ -474,13 +494,17 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(Sample
             top = m;
             float of_rest = 0.f;
             uint32_t of_tops = 0;
+            bool far = false;                        // a part's winner is below the limit
             for (int i = lane; i < n_parts; i += 32) {
                 const Part p = parts_of_all[i];
                 if (p.most == top)
                     of_rest += p.sum, of_tops += p.n;
                 else
                     of_rest += (p.sum + (float)p.n) * exp2_fast((p.most - top) * c2);
-                if (p.at >= 0) best.enter(p.at, first_only ? 1.f : quotient(p.x - top, inv_t, min_p, p.noise), p.x, p.noise);
+                if (p.at < 0) continue;
+                const float key = first_only ? 1.f : quotient(p.x - top, inv_t, min_p, p.noise);
+                best.enter(p.at, key, p.x, p.noise);
+                far = far || key < 0.f;
             }
             best.of_warp();
             if (round == 0) {
@@ -488,10 +512,15 @@ __global__ void __launch_bounds__(kThreads, 768 / kThreads) sample_kernel(Sample
                 tops = __reduce_add_sync(0xffffffffu, of_tops);
                 total = rest + (float)tops;
             }
-            if (best.at < 0) {                       // no noise was a positive number: the first in the order
+            // In a dense row a CTA's winner may be below the limit of the row's maximum, which the CTA did not know, in front of
+            // a token above it that could win: the race is run again by the row's maximum. Noise of the exponential
+            // distribution is never as small as that needs.
+            const bool again =
+                round == 0 && __any_sync(0xffffffffu, far) && most_behind(parts_of_all, n_parts, top, inv_t) >= best.top;
+            if (best.at < 0 || again) {              // not again: no noise was a positive number, the first in the order
                 if (first_only) break;
-                first_only = true;
-                in_race = 0;
+                first_only = !again;
+                in_race = again ? UINT32_MAX : 0;
                 continue;
             }
             token = best.at;
