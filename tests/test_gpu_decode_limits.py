@@ -3,7 +3,8 @@ could keep them differently."""
 import numpy as np
 import pytest
 
-from tests.test_gpu_step import _dev, _dt, ops  # noqa: F401
+from tests.test_gpu_decode_step import _run_sample, _sample_case
+from tests.test_gpu_step import _close, _dev, _dt, _np, ops  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +88,93 @@ def test_sample_tokens_far_token_before_a_likelier_one(ops, best, dtype):  # noq
         assert _drawn(ops, x, noise, dtype) == near
         assert _drawn(ops, x, noise, dtype, top_k=3) == near
         assert _drawn(ops, x, noise, dtype, top_p=0.5) == 17000
+
+
+def _settled(c):
+    """(tokens, settled, logprobs, tol) of a case: the 64-bit draw of every row, and whether fp32 has to find the same.
+
+    In units of 2^-24, with z = ln p + a row's constant <= 0. A key p / noise: a rounding of z for the difference, for 1 / t
+    and for the product, a unit (2) of exp and the division's 1: 3 |z| + 3, 4 allowed. A mass of some p: of each 5 |z| + 4
+    (difference, 1 / t, the factor to powers of two, its constant, the product; exponential), weighted 5 E|z| + 4 of the
+    total, and an addition for each of a thread's at most vocab / 256 + 1 tokens and 20 levels above them; the mass in front
+    and the total are both off by that, and their border's product by 1. ln p: 3 |z| + 2 for z, the total's error, the logarithms'
+    units."""
+    x, noise = _np(c["logits"]), _np(c["noise"])
+    rows, vocab = x.shape
+    tokens, settled, logprobs, tol = np.zeros(rows, int), np.zeros(rows, bool), np.zeros(rows), np.zeros(rows)
+    for r in range(rows):
+        t, k, top_p, min_p = (float(c[n][r]) for n in ("temperature", "top_k", "top_p", "min_p"))
+        z = (x[r] - x[r].max()) / (t if t > 0 else 1.0)
+        p = np.exp(z)
+        total, reach = p.sum(), (p * np.abs(z)).sum() / p.sum()
+        of_key = 2.0 ** -24 * (3 * np.abs(z) + 4)
+        of_mass = 2.0 ** -24 * (2 * (5 * reach + 4 + vocab / 256 + 21) + 1)
+        order = np.argsort(-x[r], kind="stable")
+        front = np.empty(vocab)
+        front[order] = np.cumsum(p[order]) - p[order]
+        rank = np.empty(vocab, int)
+        rank[order] = np.arange(vocab)
+        kept, near = np.ones(vocab, bool), np.zeros(vocab, bool)
+        if k > 0:
+            kept &= rank < k
+        if top_p < 1:
+            kept &= front < top_p * total
+            near |= np.abs(front / total - top_p) < of_mass
+        if min_p > 0:
+            kept &= p >= min_p
+            near |= np.abs(p / min_p - 1) < of_key
+        kept[order[0]], near[order[0]] = True, False
+        if t <= 0:
+            kept, near = rank == 0, np.zeros(vocab, bool)
+        key = np.where(kept, p / noise[r], -1.0)
+        tokens[r] = best = int(key.argmax())
+        rivals = kept & (key > key[best] * (1 - of_key - of_key[best]))
+        rivals[best] = False
+        unsure = near & (p / noise[r] > key[best] * (1 - of_key - of_key[best]))
+        settled[r] = not rivals.any() and not unsure.any() and not near[best]
+        logprobs[r] = z[best] - np.log(total)
+        tol[r] = 2.0 ** -24 * (3 * abs(z[best]) + 2 + 5 * reach + 4 + vocab / 256 + 21 + 4 * (1 + np.log(total)))
+    return tokens, settled, logprobs, tol
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,vocab", [(5, 301), (3, 40001), (400, 1003), (64, 20011)])
+@pytest.mark.parametrize("at", [(0, 0), (3, 1), (0, 1), (5, 2), (1, 3), (7, 0)])
+def test_sample_tokens_row_by_row_at_different_offsets(ops, at, rows, vocab, dtype):  # noqa: F811
+    """Wherever rows start, each settled one gives its token, and every row whose tokens are alike nearly the same ln p."""
+    import torch
+    c = _sample_case(rows, vocab, dtype, ["none", "all", "p", "k", "m"], seed=4)
+    tokens, settled, logprobs, tol = _settled(c)
+    assert (~settled).sum() <= 1 + rows // 20
+    want = _run_sample(ops, c)
+    for i, name in enumerate(("logits", "noise")):
+        wide = torch.full((rows, vocab + 11 + i), float("nan"), dtype=c[name].dtype, device="cuda")
+        wide[:, at[i]:at[i] + vocab] = c[name]
+        c[name] = wide[:, at[i]:at[i] + vocab]
+    got = _run_sample(ops, c)
+    for drawn, ln_p in (want, got):
+        assert (drawn.cpu().numpy()[settled] == tokens[settled]).all()
+        _close(_np(ln_p)[settled], logprobs[settled], tol[settled])
+    alike = (want[0] == got[0]).cpu().numpy()
+    _close(_np(got[1])[alike], _np(want[1])[alike], 2 * tol[alike])
+
+
+@pytest.mark.parametrize("sharp", [1.0, 30.0])
+def test_sample_tokens_arguments_up_to_the_limit(ops, sharp):  # noqa: F811
+    """Low temperatures, where ln p of the tokens that decide goes up to 87: the border of what fp32 tells apart goes with it."""
+    c = _sample_case(200, 2003, "f32", ["none", "p", "m", "k"], seed=6, sharp=sharp)
+    c["temperature"][:] = np.geomspace(0.05, 1.0, 200)
+    r = np.random.default_rng(6)
+    far = r.integers(0, 2003, 200)
+    noise = c["noise"].cpu().numpy()
+    noise[np.arange(200), far] = 1e-36                # tokens far down that may win
+    c["noise"] = _dev(noise)
+    z = (_np(c["logits"]) - _np(c["logits"]).max(1, keepdims=True)) / c["temperature"][:, None]
+    keep = (np.abs(z[np.arange(200), far] + 87.3) > 0.1)  # not next to the limit of 2^-126
+    tokens, settled, logprobs, tol = _settled(c)
+    got, ln_p = _run_sample(ops, c)
+    below = z[np.arange(200), tokens] < -87.3         # the definition in 64 bits has no such limit
+    settled &= keep & ~below
+    assert settled.sum() > 100
+    assert (got.cpu().numpy()[settled] == tokens[settled]).all()
+    _close(_np(ln_p)[settled], logprobs[settled], tol[settled])
