@@ -300,9 +300,12 @@ __device__ __forceinline__ void work(const TreeArgs &a, const Plan &plan, unsign
             top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], x));
             top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], x));
         }
-        const float base0 = top[0] == -INFINITY ? 0.f : top[0] * c2, base1 = top[1] == -INFINITY ? 0.f : top[1] * c2;
+        // The products are rounded by themselves: a row whose maximum stands is kept by a factor of exactly 1, whatever the
+        // others do.
+        const float base0 = top[0] == -INFINITY ? 0.f : __fmul_rn(top[0], c2);
+        const float base1 = top[1] == -INFINITY ? 0.f : __fmul_rn(top[1], c2);
         if (__any_sync(0xffffffffu, top[0] != m[0] || top[1] != m[1])) {
-            const float k0 = exp2_fast(fmaf(m[0], c2, -base0)), k1 = exp2_fast(fmaf(m[1], c2, -base1));
+            const float k0 = exp2_fast(__fmul_rn(m[0], c2) - base0), k1 = exp2_fast(__fmul_rn(m[1], c2) - base1);
             l[0] *= k0;
             l[1] *= k1;
 #pragma unroll
