@@ -194,9 +194,12 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
             top[hrow] = fmaxf(top[hrow], __shfl_xor_sync(0xffffffffu, top[hrow], 2));
         }
         const bool moved = top[0] != m[0] || top[1] != m[1];
-        const float base0 = top[0] == -INFINITY ? 0.f : top[0] * c2, base1 = top[1] == -INFINITY ? 0.f : top[1] * c2;
+        // The products are rounded by themselves: a row whose maximum stands is kept by a factor of exactly 1, whatever the
+        // others do.
+        const float base0 = top[0] == -INFINITY ? 0.f : __fmul_rn(top[0], c2);
+        const float base1 = top[1] == -INFINITY ? 0.f : __fmul_rn(top[1], c2);
         if (__any_sync(0xffffffffu, moved)) {
-            const float k0 = exp2_fast(fmaf(m[0], c2, -base0)), k1 = exp2_fast(fmaf(m[1], c2, -base1));
+            const float k0 = exp2_fast(__fmul_rn(m[0], c2) - base0), k1 = exp2_fast(__fmul_rn(m[1], c2) - base1);
             l[0] *= k0;
             l[1] *= k1;
 #pragma unroll
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
             for (int hrow = 0; hrow < 2; ++hrow) {
                 l[hrow] += __shfl_xor_sync(0xffffffffu, l[hrow], 1);
                 l[hrow] += __shfl_xor_sync(0xffffffffu, l[hrow], 2);
-                m[hrow] = m[hrow] == -INFINITY ? -INFINITY : m[hrow] * c2;
+                m[hrow] = m[hrow] == -INFINITY ? -INFINITY : __fmul_rn(m[hrow], c2);
             }
             if constexpr (WN > 1) {
                 // the warps that share rows, through the stage just consumed (the next copies into it are issued

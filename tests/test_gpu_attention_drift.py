@@ -51,3 +51,9 @@ def test_prefix_attention_maximum_of_other_rows(ops, dtype):  # noqa: F811
     none = torch.zeros((0, 1), dtype=torch.int32, device="cuda")
     _check(c, *ops.prefix_attention(c["q"], c["k"], c["v"], none, none[:, 0], torch.zeros(1, dtype=torch.int32, device="cuda"),
                                     c["table"], c["ctx"], c["starts"], scale=1.0))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tree_attention_maximum_of_other_rows(ops, dtype):  # noqa: F811
+    c = _inputs(dtype)
+    _check(c, *ops.tree_attention(c["q"], c["k"], c["v"], c["table"], c["ctx"], c["starts"], scale=1.0))
