@@ -446,8 +446,10 @@ extern "C" int lora_norm_rope(const lora_norm_rope_desc *d, void *stream) {
         return fail(LORA_ERR_ARG, "norm_rope: the weights' strides %lld, %lld are negative", (long long)d->q_weight_head,
                     (long long)d->k_weight_head);
     if (nothing) return LORA_OK;
-    const NormArgs n{arguments(&d->rope), d->q_weight, d->k_weight, d->q_weight_head, d->k_weight_head, d->eps,
-                     1.f / (float)d->rope.head_dim};
+    NormArgs n{arguments(&d->rope), nullptr, nullptr, 0, 0, d->eps, 1.f / (float)d->rope.head_dim};
+    // a weight of no heads is not looked at, not even for its alignment
+    if (d->rope.n_heads > 0) n.q_weight = d->q_weight, n.q_weight_head = d->q_weight_head;
+    if (d->rope.n_kv_heads > 0) n.k_weight = d->k_weight, n.k_weight_head = d->k_weight_head;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int sms = sm_count();
     if (sms < 1) return fail(LORA_ERR_CUDA, "norm_rope: no CUDA device");

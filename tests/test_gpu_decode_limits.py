@@ -178,3 +178,29 @@ def test_sample_tokens_arguments_up_to_the_limit(ops, sharp):  # noqa: F811
     assert settled.sum() > 100
     assert (got.cpu().numpy()[settled] == tokens[settled]).all()
     _close(_np(ln_p)[settled], logprobs[settled], tol[settled])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tokens", [5, 3000])
+def test_norm_rope_weights_of_no_heads(ops, tokens, dtype):  # noqa: F811
+    """A weight whose rows do not exist is not looked at: the same bits as without it, wherever it points."""
+    import ctypes
+
+    import torch
+    from rank_adapter_apply_gb300 import binding as B
+    heads, dim = 32, 128
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    x = torch.randn((tokens, heads, dim), generator=gen, device="cuda").to(_dt(dtype))
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda") % 500
+    table, spare = ops.rope_table(500, dim), torch.zeros(2 * dim, dtype=x.dtype, device="cuda")
+    out = []
+    for weight in (None, spare.data_ptr() + spare.element_size()):
+        y = torch.empty_like(x)
+        rope = B.LoraRopeDesc(q=x.data_ptr(), q_token=heads * dim, q_head=dim, q_out=y.data_ptr(), q_out_token=heads * dim,
+                              q_out_head=dim, positions=pos.data_ptr(), table=table.data_ptr(), n_positions=500, page_size=1,
+                              n_tokens=tokens, n_heads=heads, head_dim=dim, rot_dim=dim,
+                              dtype=B.LORA_DTYPE_BF16 if dtype == "bf16" else B.LORA_DTYPE_F32)
+        d = B.LoraNormRopeDesc(rope=rope, k_weight=weight, eps=1e-6)
+        B.lora_norm_rope(ctypes.byref(d), torch.cuda.current_stream().cuda_stream)
+        out.append(y)
+    assert torch.equal(out[0], out[1])
