@@ -752,8 +752,13 @@ int lora_tree_attention(const lora_tree_attention_desc *desc, void *stream);
  * lora_tree_attention shows them (their own context, which starts after the
  * prefix, and their trees), keys 0 .. prefix_lens[g] - 1 of the group: key p is place
  * p % page_size of page prefix_table[g][p / page_size] of the same caches. A group's
- * keys are read once for all its rows. Softmax and log-sum-exp go over all keys
- * that a row sees; requests that belong to no group have their own keys alone.
+ * keys are read once for each tile of its rows of a key/value head, not for each
+ * request: in bf16 a tile is 128 rows for large groups and long prefixes, 16 for small
+ * ones (whose second reading comes from cache), in fp32 64 or 16. The tiles of 128 need
+ * a page_size that is a multiple of 8, caches whose pages are outermost, tokens of q
+ * outside its heads, and at most 128 query heads to a key/value head; other
+ * layouts have tiles of 16 at any size. Softmax and
+ * log-sum-exp go over all keys that a row sees; requests that belong to no group have their own keys alone.
  * A prefix length below 0 counts as 0, keys past the prefix table's row or on a
  * page id outside [0, n_pages) are not seen, group_starts are clamped to
  * [0, n_requests]. Where starts (node_starts, group_starts) fall, the rows between

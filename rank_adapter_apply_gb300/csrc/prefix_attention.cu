@@ -1,7 +1,7 @@
 // lora_prefix_attention: attention of requests that share a prefix of their context.
 //
 // Entries are of two kinds: a group, whose rows are those of all its requests and whose
-// keys are the prefix, read once for them all, and a request with its own keys. In bf16
+// keys are the prefix, read once for each tile of its rows, and a request with its own keys. In bf16
 // few rows go to single warps (prefix_rows.cuh) and many to tiles of 128 on the
 // 5th-generation tensor cores (tree_attention_tc.cu, which takes up the few rows as its
 // CTAs are done); fp32 goes to the FMA units (tree_attention_f32.cu). A row's two
@@ -132,7 +132,8 @@ cudaError_t launch_prefix(const TreeArgs &a, const Plan &groups, const Plan &req
     JoinArgs join{a, {groups, requests}, {0, 0}};
     // Rows of a tile for n entries with up to so many pages of keys. In bf16 the warps' tiles of 16 read the keys again for
     // each tile, mostly from L2; the 5th-generation tensor cores read them once for 128 rows, but their kernel takes some
-    // 20 us. Bytes read by the warps, and us with both kinds on 16 / with the wide one on 128: 55 MB (100x2 of 300) 40 / 62,
+    // 20 us, and layouts that it does not take stay on 16 (256x1 of 8192, 64 heads over 8: 133 us with pages of 64, 584 with
+    // pages of 12). Bytes read by the warps, and us with both kinds on 16 / with the wide one on 128: 55 MB (100x2 of 300) 40 / 62,
     // 65 MB (16x1 of 4000 in 2 groups) 23 / 29, 142 MB (requests of 16x16 of 1000) 49 / 31, 201 MB (12x1 of 16384) 45 / 36.
     // In fp32 tiles of 64 rows feed the FMA units better, and take a launch of their own beside 16: all wide entries take
     // them, or none. us with 16 / 64: 8 MB (8x4 of 500) 15 / 29, 20 MB (24x2 of 1024) 28 / 32, 50 MB (32x2 of 2000)

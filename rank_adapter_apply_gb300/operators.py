@@ -133,8 +133,9 @@ def prefix_attention(q, k_cache, v_cache, prefix_table, prefix_lens, group_start
     """tree_attention of requests that share prefixes. Returns (out like q, lse fp32 [tokens, heads]).
 
     Group g is the requests group_starts[g] .. group_starts[g + 1] (int32 [groups + 1]); they see the prefix_lens[g]
-    (int32 [groups]) keys on the pages prefix_table[g] (int32 [groups, pages of a prefix]), read once for the group, in
-    front of what tree_attention shows them: ctx_lens and page_table do not contain the prefix."""
+    (int32 [groups]) keys on the pages prefix_table[g] (int32 [groups, pages of a prefix]), in front of what tree_attention
+    shows them: ctx_lens and page_table do not contain the prefix. It is read once for each tile of up to 128 rows of the
+    group; a page size that is not a multiple of 8 leaves tiles of 16."""
     return _prefix_attention(q, k_cache, v_cache, prefix_table, prefix_lens, group_starts, page_table, ctx_lens, node_starts,
                              tree_mask, scale, out)
 
