@@ -686,8 +686,9 @@ int lora_rope(const lora_rope_desc *desc, void *stream);
  * the rest copied; v is only copied. Squares are summed in fp32, and one rounding
  * comes at the end: none between norm and rotation. q_weight and k_weight (type
  * dtype) hold head_dim values for every head (stride 0: the same for all), or are
- * NULL: ones. rope.inverse is 0. eps >= 0, finite: with eps 0 a head of zeros is
- * NaN. All else is as lora_rope says, and q_out may be q itself with the same strides.
+ * NULL: ones (of no heads, they are not looked at). rope.inverse is 0. eps >= 0, finite:
+ * with eps 0 a head of zeros is NaN. Where the sum of squares passes fp32's range (elements
+ * of some 10^19), the head's finite elements become 0. All else is as lora_rope says, and q_out may be q itself with the same strides.
  */
 typedef struct {
     lora_rope_desc rope;
@@ -842,17 +843,19 @@ int lora_verify_drafts(const lora_verify_desc *desc, void *stream);
  *         reach it, and always the first),
  *   min_p the tokens with p >= min_p * (the largest p), and always the first;
  * each filter looks at p itself, not at what another one left, and a token stays if
- * all keep it. The token drawn is the kept one with the largest p / noise (the lowest
+ * all keep it. (Where a row has both top_k and top_p, taking the mass of top_p from what
+ * top_k left, made to sum to 1 again, would keep fewer.) The token drawn is the kept one with the largest p / noise (the lowest
  * index on a tie): with noise from the exponential distribution, tokens are
  * distributed as the kept p. tokens[r] is its index, logprobs[r] = ln p of it, of
  * all tokens, not of the kept ones alone.
  * The filters are one value for each row, NULL where no row has one. temperature
  * <= 0 or NaN: the first token, with logprobs at temperature 1. top_k <= 0, top_p >= 1
  * (or NaN) and min_p <= 0 (or NaN) keep all. A logit of NaN counts as -inf, and +inf as
- * the largest number of its type; tokens of p < 2^-126 are not drawn. A row of -inf alone has
- * token -1 and logprob -inf. Noise that is negative or NaN keeps its token from being
- * drawn; if that is so of all kept ones, the first token is drawn. Sums are fp32, put
- * together in a fixed order.
+ * the largest number of its type; tokens of p < 2^-126 of the largest are not drawn, whatever their
+ * noise. A row of -inf alone has token -1 and logprob -inf. Noise that is negative, infinite
+ * or NaN keeps its token from being drawn; if that is so of all kept ones, the first token is
+ * drawn. Sums are fp32, put together in an order that goes by the sizes and by where a row
+ * starts within 16 bytes alone.
  */
 typedef struct {
     const void *logits;       /* [n_rows][vocab], rows logits_row apart, type dtype */

@@ -13,7 +13,7 @@
 // 25 at 5 TB/s, the rest are the beginnings of the three parts and the join. 256 requests behind
 // 32768 keys, 64 heads over 8: 370 us, the products alone 148; the prefix's part runs at 1.2
 // PFLOP/s (the chain of scores, softmax, second product), the requests' 0.5 GB at 5 TB/s.
-// 3 requests behind 777: 12.6 us, two launches and five dependent reads.
+// 3 requests behind 777: 12.5 us in a graph, 13.2 a call: two launches and five dependent reads.
 #include "tree_common.cuh"
 
 #include <algorithm>
@@ -25,7 +25,10 @@ namespace {
 using namespace step;
 using namespace tree;
 
-// Rows up to which eight warps, and two, join one.
+// Rows up to which eight warps, and two, join one. Calls with eight / two / one warps, us, a group behind 1000 keys with
+// contexts of up to 300: 96 rows 13.0 / 16.8 / 22.0, 768 17.8 / 19.5 / 23.1, 2048 30.0 / 27.4 / 29.3, 2400 33.8 / 29.7 / 31.0, 4096 56 /
+// 49.6 / 47.7, 9600 80 / 61.7 / 58.5, 16384 122 / 91 / 85. (Eight are right below some 1200 rows, two up to some 3000: what
+// lies between these and the limits below loses 2 to 4 us.)
 constexpr long long kJoin8 = 2400, kJoin2 = 9600;
 
 struct JoinArgs {

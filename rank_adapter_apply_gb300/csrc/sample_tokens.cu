@@ -16,8 +16,13 @@ using namespace step;
 constexpr int kMaxCluster = 8;
 constexpr int kSliceBytes = 64 * 1024;   // of a CTA's logits in shared memory: three CTAs fit an SM
 constexpr int kBins = 256;               // of 1/8: down to 2^-32 of the largest p
-constexpr int kListed = 512;              // tokens of a race that a CTA lists
-constexpr int kRejections = 6;           // races lost before the border is found by bisection
+// Tokens of a race that a CTA lists. us with 128 / 512 / 1024: 1 row of 32000 8.2 / 7.5 / 7.5, 77 of 65537 with top-k 23.3 / 20.0 /
+// 20.1, 256 of 131072 102 / 102 / 122 (three CTAs no longer fit an SM), 64 of 100003 with k = 1000 49 / 39 / 39.
+constexpr int kListed = 512;
+// Races lost before the border is found by bisection, a pass for each halving. us with 2 / 6 / 12: 64 rows of 32000 nearly equal logits,
+// top-p 0.5 72 / 32 / 32, top-p 0.1 129 / 84 / 54, k = 50 166 / 155 / 132; 64 of 100003 with k = 20 71 / 33 / 33; the others
+// alike. A race that is lost in vain costs two passes.
+constexpr int kRejections = 6;
 
 struct SampleArgs {
     const void *logits;
@@ -156,11 +161,13 @@ __device__ __noinline__ float most_behind(const Part *parts, int n_parts, float 
 // is found by bisection of the order's places instead.
 //
 // A row is a cluster's: its logits are read from memory once and stay in shared memory. 256 rows
-// of 131072 in fp32, filters of all kinds: 102 us, where logits and the noise that is asked for
+// of 131072 in fp32, top-p alone: 102 us, where logits and noise, which every row then reads whole,
 // take 40 from memory: three passes over shared memory, exponentials and exchanges between
 // CTAs follow one another, with three CTAs on an SM to fill the gaps (barriers, the
 // arithmetic's own results and shared memory are the stalls, issue slots are busy for 40 %). 32 rows
-// of 100003 17 us, one of 32000 7.9: a launch and a chain of five exchanges. (A maximum of
+// of 100003 with filters of all kinds 18 us, one of 32000 7.5: a launch and a chain of five exchanges. 64
+// rows of 151936 in fp32, top-p alone: 60 us, 78 MB: the tokens past a CTA's 64 KB are listed in vain
+// and gone over again. (A maximum of
 // each vector in place of its tokens for top-k's bound 149 -> 107 us; 384 or 512 threads,
 // 16 CTAs to a cluster and rows brought to L2 ahead were slower.)
 template <typename T, int kThreads>

@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(128, 2) tree_tiles_kernel(TreeArgs a, Plan pla
             const float e2 = exp2_fast(fmaf(s[n][2], c2, -base1)), e3 = exp2_fast(fmaf(s[n][3], c2, -base1));
             l[0] += e0 + e1;
             l[1] += e2 + e3;
-            // weights to bf16 for the second product: 2^-9 relative, below the output's own rounding; their sum
-            // l stays in fp32 and unrounded
+            // weights to bf16 for the second product: half a step, 2^-8 relative at most, of either sign from key to key, so that
+            // a row of many keys is off by less than its output's own rounding; their sum l stays in fp32 and unrounded
             pf[n][0] = pack_bf16(e0, e1);
             pf[n][1] = pack_bf16(e2, e3);
         }

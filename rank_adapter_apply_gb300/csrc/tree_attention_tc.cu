@@ -435,8 +435,8 @@ __device__ __forceinline__ void tc_work(const TcArgs &args, unsigned char *smem)
                     e0 = exp2_fast(e0);
                     e1 = exp2_fast(e1);
                     sums[k & 1] = add2(sums[k & 1], pair(e0, e1));
-                    // weights to bf16 for the second product: 2^-9 relative, below the output's own rounding; their sum
-                    // l stays in fp32 and unrounded
+                    // weights to bf16 for the second product: half a step, 2^-8 relative at most, of either sign from key to key, so that
+                    // a row of many keys is off by less than its output's own rounding; their sum l stays in fp32 and unrounded
                     p[k] = pack_bf16(e0, e1);
                 }
                 float l0, l1;

@@ -204,3 +204,18 @@ def test_norm_rope_weights_of_no_heads(ops, tokens, dtype):  # noqa: F811
         B.lora_norm_rope(ctypes.byref(d), torch.cuda.current_stream().cuda_stream)
         out.append(y)
     assert torch.equal(out[0], out[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tokens", [3, 3000])
+@pytest.mark.parametrize("dim", [50, 128])
+def test_norm_rope_squares_out_of_range(ops, dim, tokens, dtype):  # noqa: F811
+    """A head whose squares pass fp32's range is 0, and no other head is touched; one just below it is normed."""
+    import torch
+    x = torch.ones((tokens, 8, dim), dtype=_dt(dtype), device="cuda")
+    x[1, 3], x[1, 4], x[2, 0, 1] = 2.0 ** 66, 2.0 ** 59, 2.0 ** 65
+    pos, table = torch.zeros(tokens, dtype=torch.int32, device="cuda"), ops.rope_table(4, dim // 4 * 2)
+    y = ops.norm_rope(x, None, pos, table).float()
+    assert not y[1, 3].any() and not y[2, 0].any()
+    y[1, 3] = y[2, 0] = 1.0
+    assert (y - 1).abs().max() <= 2.0 ** -8      # 1 / sqrt(1 + 1e-6), rounded
