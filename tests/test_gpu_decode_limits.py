@@ -76,11 +76,12 @@ def test_sample_tokens_next_to_the_limit(ops, temperature):  # noqa: F811
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("best", [1.0, float("nan")])
-def test_sample_tokens_far_token_before_a_likelier_one(ops, best, dtype):  # noqa: F811
+@pytest.mark.parametrize("vocab", [40003, 300007])
+def test_sample_tokens_far_token_before_a_likelier_one(ops, vocab, best, dtype):  # noqa: F811
     """A token below the limit that would win among its neighbours does not hide one above it; only the row's maximum,
     which lies elsewhere, tells them apart."""
-    vocab = 40003
-    for near, far in ((30001, 30002), (30002, 30001), (vocab - 2, vocab - 1), (1, 0)):
+    most = vocab // 4 * 3
+    for near, far in ((most, most + 1), (most + 1, most), (vocab - 2, vocab - 1), (1, 0)):
         x, noise = np.full(vocab, -400.0), np.ones(vocab)
         x[17000], noise[17000] = 0.0, best
         x[near], noise[near] = -87.0, 1e-40
