@@ -757,9 +757,10 @@ int lora_tree_attention(const lora_tree_attention_desc *desc, void *stream);
  * request: in bf16 a tile is 128 rows for large groups and long prefixes, 16 for small
  * ones (whose second reading comes from cache), in fp32 64 or 16. The tiles of 128 need
  * a page_size that is a multiple of 8, caches whose pages are outermost, tokens of q
- * outside its heads, and at most 128 query heads to a key/value head; other
- * layouts have tiles of 16 at any size. Softmax and
- * log-sum-exp go over all keys that a row sees; requests that belong to no group have their own keys alone.
+ * outside its heads, and at most 128 query heads to a key/value head; other layouts
+ * have tiles of 16 at any size.
+ * Softmax and log-sum-exp go over all keys that a row sees; requests that belong to no
+ * group have their own keys alone.
  * A prefix length below 0 counts as 0, keys past the prefix table's row or on a
  * page id outside [0, n_pages) are not seen, group_starts are clamped to
  * [0, n_requests]. Where starts (node_starts, group_starts) fall, the rows between
@@ -851,11 +852,11 @@ int lora_verify_drafts(const lora_verify_desc *desc, void *stream);
  * The filters are one value for each row, NULL where no row has one. temperature
  * <= 0 or NaN: the first token, with logprobs at temperature 1. top_k <= 0, top_p >= 1
  * (or NaN) and min_p <= 0 (or NaN) keep all. A logit of NaN counts as -inf, and +inf as
- * the largest number of its type; tokens of p < 2^-126 of the largest are not drawn, whatever their
- * noise. A row of -inf alone has token -1 and logprob -inf. Noise that is negative, infinite
- * or NaN keeps its token from being drawn; if that is so of all kept ones, the first token is
- * drawn. Sums are fp32, put together in an order that goes by the sizes and by where a row
- * starts within 16 bytes alone.
+ * the largest number of its type; tokens of p < 2^-126 of the largest are not drawn,
+ * whatever their noise. A row of -inf alone has token -1 and logprob -inf. Noise that is
+ * negative, infinite or NaN keeps its token from being drawn; if that is so of all kept
+ * ones, the first token is drawn. Sums are fp32, put together in an order that goes by the
+ * sizes and by where a row starts within 16 bytes alone.
  */
 typedef struct {
     const void *logits;       /* [n_rows][vocab], rows logits_row apart, type dtype */
